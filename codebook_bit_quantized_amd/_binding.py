@@ -31,7 +31,7 @@ EXPORTED = ("cbq_rotate_quantize", "cbq_rotate_quantize_ex", "cbq_rotate_dense_w
             "cbq_moe_route_gather_noalloc", "cbq_prepack_bytes", "cbq_prepack_weights",
             "cbq_gemm_workspace", "cbq_codebook_lut_gemm", "cbq_moe_combine",
             "cbq_kmeans_codebooks", "cbq_refit_codebooks", "cbq_cpu_lut_gemm", "cbq_status_string", "cbq_last_error",
-            "cbq_version")
+            "cbq_version", "cbq_norm_rotate_quantize", "cbq_combine_norm_residual")
 
 
 class CbqError(RuntimeError):
@@ -49,6 +49,15 @@ class cbq_weights(ctypes.Structure):
                 ("layout", ctypes.c_int32)]
 
 
+TYPE_F32, TYPE_BF16 = 0, 1
+
+
+class cbq_norm(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("eps", ctypes.c_float), ("had_block", ctypes.c_int32),
+                ("act_bits", ctypes.c_int32), ("normed", ctypes.c_void_p), ("ldn", ctypes.c_int64),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -63,6 +72,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib = ctypes.CDLL(path)
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     W = ctypes.POINTER(cbq_weights)
+    f32, Nrm = ctypes.c_float, ctypes.POINTER(cbq_norm)
     sig = {
         "cbq_rotate_quantize": (ctypes.c_int, [vp, i64, i32, i64, i32, i32, vp, vp, vp, vp]),
         "cbq_rotate_quantize_ex": (ctypes.c_int, [vp, i64, i32, i64, i32, i32, vp, vp, vp, vp, vp,
@@ -84,6 +94,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "cbq_kmeans_codebooks": (ctypes.c_int, [vp, i64, i32, i64, i32, i32, vp, vp, vp, vp]),
         "cbq_refit_codebooks": (ctypes.c_int, [vp, i64, i32, i64, i32, vp, vp, i32, i64, vp, vp]),
         "cbq_cpu_lut_gemm": (ctypes.c_int, [vp, vp, i32, i64, W, vp, i64, i32, i32]),
+        "cbq_norm_rotate_quantize": (ctypes.c_int, [vp, i64, i32, i64, Nrm, vp]),
+        "cbq_combine_norm_residual": (ctypes.c_int, [vp, i32, i64, vp, vp, i64, i32, i32, i32, vp, f32, vp, i64,
+                                                     f32, vp, i64, vp, i64, Nrm, vp]),
         "cbq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "cbq_last_error": (ctypes.c_char_p, []),
         "cbq_version": (ctypes.c_int, []),
@@ -117,6 +130,43 @@ def _require_gpu(*ts: Optional[torch.Tensor]):
     for t in ts:
         if t is not None and not t.is_cuda:
             raise ValueError("cbq operates on device tensors only")
+
+
+def _on_stream(dev: torch.device, stream, call):
+    """call(stream handle) with `dev` current and what it allocates belonging to the stream it
+    launches on: the given one, or dev's current one."""
+    if stream is None and dev.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream().cuda_stream)
+    st = stream if stream is not None else torch.cuda.current_stream(dev)
+    if not hasattr(st, "cuda_stream"):
+        st = torch.cuda.ExternalStream(int(st), device=dev)
+    if st.device != dev:
+        raise ValueError(f"the stream is on {st.device}, the tensors are on {dev}")
+    with torch.cuda.device(dev), torch.cuda.stream(st):
+        return call(st.cuda_stream)
+
+
+def _tensor(name: str, t: Optional[torch.Tensor], dev: torch.device, dtype, shape=None,
+            rows: bool = False, contiguous: bool = False):
+    """Checks an argument tensor's place, type, shape and layout; None passes."""
+    if t is None:
+        return
+    if t.device != dev or dev.type != "cuda":
+        raise ValueError(f"{name} must be on the same GPU as the other tensors (got {t.device}, {dev})")
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if rows and t.numel() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Elements between rows of a [T][K] tensor (its width where there is at most one row,
+    whose stride torch leaves open)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 8 * ((t.shape[1] + 7) // 8))
 
 
 @dataclass
@@ -325,6 +375,108 @@ def moe_combine(expert_out: torch.Tensor, slot_of: torch.Tensor, topk_w: torch.T
     _check(lib.cbq_moe_combine(_ptr(expert_out), _ptr(slot_of), _ptr(topk_w), T, topk, H, n_shared,
                                _ptr(y), _stream(stream)))
     return y
+
+
+def _norm_outputs(T: int, K: int, dev, act_bits: int, normed, codes, scales, want_normed: bool = True):
+    if normed is None and want_normed:
+        normed = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
+    if act_bits:
+        if codes is None:
+            codes = torch.empty((T, K * act_bits // 8), dtype=torch.uint8, device=dev)
+        if scales is None:
+            scales = torch.empty((T,), dtype=torch.float32, device=dev)
+    return normed, codes, scales
+
+
+def _norm_struct(weight, eps, had_block, act_bits, normed, codes, scales) -> cbq_norm:
+    return cbq_norm(weight.data_ptr(), eps, had_block, act_bits, None if normed is None else normed.data_ptr(),
+                    0 if normed is None else _row_stride(normed), codes.data_ptr() if act_bits else None,
+                    scales.data_ptr() if act_bits else None)
+
+
+def _check_norm_args(T, K, dev, weight, act_bits, normed, codes, scales):
+    _tensor("weight", weight, dev, torch.float32, (K,), contiguous=True)
+    _tensor("normed", normed, dev, torch.bfloat16, (T, K), rows=True)
+    if act_bits:
+        _tensor("codes", codes, dev, torch.uint8, (T, K * act_bits // 8), contiguous=True)
+        _tensor("scales", scales, dev, torch.float32, (T,), contiguous=True)
+
+
+def norm_rotate_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, act_bits: int = 4,
+                         had_block: int = 0, want_normed: bool = True, normed: Optional[torch.Tensor] = None,
+                         codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None, stream=None):
+    """RMS norm of x (bf16 [T][K]) with weight (fp32 [K]), fused with rotate_quantize of its
+    bf16 result: returns (normed, codes, scales).  act_bits = 0 leaves out the codes (codes
+    and scales are None), want_normed = False the normed rows (cbq_norm_rotate_quantize)."""
+    lib = load_library()
+    _require_gpu(x)
+    T, K = x.shape
+    dev = x.device
+    _tensor("x", x, dev, torch.bfloat16, rows=True)
+    _check_norm_args(T, K, dev, weight, act_bits, normed, codes, scales)
+
+    def call(st):
+        n, c, s = _norm_outputs(T, K, dev, act_bits, normed, codes, scales, want_normed)
+        nrm = _norm_struct(weight, eps, had_block, act_bits, n, c, s)
+        _check(lib.cbq_norm_rotate_quantize(x.data_ptr(), T, K, _row_stride(x), ctypes.byref(nrm), st))
+        return (n, c, s) if act_bits else (n, None, None)
+
+    return _on_stream(dev, stream, call)
+
+
+def combine_norm_residual(rows: torch.Tensor, residual: torch.Tensor, slot_of: Optional[torch.Tensor] = None,
+                          topk_w: Optional[torch.Tensor] = None, n_shared: Optional[int] = None,
+                          post_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                          gate: Optional[torch.Tensor] = None, scale: float = 1.0,
+                          next_weight: Optional[torch.Tensor] = None, act_bits: int = 0, had_block: int = 0,
+                          out: Optional[torch.Tensor] = None, normed: Optional[torch.Tensor] = None,
+                          codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None, stream=None):
+    """out = residual + scale * gate * norm(combined rows), bf16 [T][H]; with next_weight also
+    the next block's norm of out: returns out, or (out, normed, codes, scales)
+    (cbq_combine_norm_residual).
+
+    rows: fp32 or bf16 [T*topk + n_shared*T][H] with slot_of and topk_w [T][topk] from
+    moe_route_gather, or a block's output [T][H] without them.  post_weight (fp32 [H]) norms
+    the combined row; gate is bf16 [T][H], or [H] / [1][H] for all tokens.  out may be
+    residual.  act_bits = 0 leaves out the codes.  eps serves both norms."""
+    lib = load_library()
+    _require_gpu(rows, residual)
+    dev = residual.device
+    T, H = residual.shape
+    if (slot_of is None) != (topk_w is None):
+        raise ValueError("slot_of and topk_w go together")
+    topk = 0 if slot_of is None else slot_of.shape[1]
+    if n_shared is None:
+        n_shared = 0 if topk else 1
+    _tensor("residual", residual, dev, torch.bfloat16, rows=True)
+    _tensor("rows", rows, dev, (torch.float32, torch.bfloat16), (T * topk + n_shared * T, H), rows=True)
+    _tensor("slot_of", slot_of, dev, torch.int32, (T, topk), contiguous=True)
+    _tensor("topk_w", topk_w, dev, torch.float32, (T, topk), contiguous=True)
+    _tensor("post_weight", post_weight, dev, torch.float32, (H,), contiguous=True)
+    _tensor("out", out, dev, torch.bfloat16, (T, H), rows=True)
+    ldg = 0
+    if gate is not None:
+        shared_gate = gate.dim() == 1 or gate.shape[0] == 1 and T != 1
+        _tensor("gate", gate, dev, torch.bfloat16, (H,) if gate.dim() == 1 else (1 if shared_gate else T, H), rows=True)
+        ldg = 0 if shared_gate else _row_stride(gate)
+    if next_weight is not None:
+        _check_norm_args(T, H, dev, next_weight, act_bits, normed, codes, scales)
+
+    def call(st):
+        o = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if out is None else out
+        nrm = None
+        if next_weight is not None:
+            n, c, s = _norm_outputs(T, H, dev, act_bits, normed, codes, scales)
+            nrm = ctypes.byref(_norm_struct(next_weight, eps, had_block, act_bits, n, c, s))
+        _check(lib.cbq_combine_norm_residual(
+            rows.data_ptr(), TYPE_F32 if rows.dtype == torch.float32 else TYPE_BF16, _row_stride(rows), _ptr(slot_of),
+            _ptr(topk_w), T, topk, n_shared, H, _ptr(post_weight), eps, _ptr(gate), ldg, scale, residual.data_ptr(),
+            _row_stride(residual), o.data_ptr(), _row_stride(o), nrm, st))
+        if next_weight is None:
+            return o
+        return (o, n, c, s) if act_bits else (o, n, None, None)
+
+    return _on_stream(dev, stream, call)
 
 
 def kmeans_codebooks(w: torch.Tensor, bits: int, max_iters: int = 50, idx: Optional[torch.Tensor] = None,

@@ -3,6 +3,8 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <cmath>
+
 #include "../../include/cbq.h"
 #include "cpu_lut.hpp"
 #include "cbq_internal.hpp"
@@ -38,6 +40,35 @@ int check_weights(const cbq_weights* W, int i) {
   if (W->bits < 2 || W->bits > 4) return fail(CBQ_EUNSUPPORTED, "W[%d]: bits must be 2, 3 or 4 (got %d)", i, W->bits);
   if (W->layout != CBQ_LAYOUT_ROWS && W->layout != CBQ_LAYOUT_BLOCKED)
     return fail(CBQ_EINVAL, "W[%d]: unknown index layout %d", i, W->layout);
+  return CBQ_OK;
+}
+
+// the argument rules that cbq_norm_rotate_quantize and cbq_combine_norm_residual share; fills
+// a's norm part and *b, the rotation block
+int check_norm(const cbq_norm* n, int32_t K, cbq::NormArgs* a, int* b) {
+  if (!n->weight || !aligned16(n->weight)) return fail(CBQ_EINVAL, "norm weight must be non-null and 16-byte aligned");
+  if (!(n->eps > 0.0f) || !std::isfinite(n->eps)) return fail(CBQ_EINVAL, "norm eps must be finite and > 0");
+  if (!n->normed && !n->codes) return fail(CBQ_EINVAL, "a norm needs normed or codes to write");
+  if (n->normed && (!aligned16(n->normed) || n->ldn < K || n->ldn % 8))
+    return fail(CBQ_EINVAL, "normed must be 16-byte aligned with ldn >= K and a multiple of 8 (got %lld)", (long long)n->ldn);
+  *b = 1;
+  if (n->codes) {
+    if (n->act_bits != 4 && n->act_bits != 8) return fail(CBQ_EINVAL, "act_bits must be 4 or 8 (got %d)", n->act_bits);
+    *b = n->had_block == 0 ? (K & -K) : n->had_block;
+    if (!pow2(*b) || K % *b) return fail(CBQ_EINVAL, "had_block must be 0 or a power of two dividing K (got %d)", n->had_block);
+    if (!n->scales) return fail(CBQ_EINVAL, "scales must be non-null with codes");
+    if (!aligned16(n->codes)) return fail(CBQ_EINVAL, "codes must be 16-byte aligned");
+  }
+  a->weight = n->weight; a->eps = n->eps; a->normed = n->normed; a->ldn = n->ldn;
+  a->codes = n->codes; a->scales = n->scales; a->act_bits = n->act_bits;
+  return CBQ_OK;
+}
+
+int check_norm_sizes(int64_t T, int32_t K, const char* name) {
+  if (T < 0) return fail(CBQ_EINVAL, "T must be >= 0 (got %lld)", (long long)T);
+  if (T > 0x7FFFFFFF) return fail(CBQ_EUNSUPPORTED, "T must be < 2^31");
+  if (K < 32 || K % 32) return fail(CBQ_EINVAL, "%s must be a positive multiple of 32 (got %d)", name, K);
+  if (K > 16384) return fail(CBQ_EUNSUPPORTED, "%s must be <= 16384 (got %d)", name, K);
   return CBQ_OK;
 }
 
@@ -354,6 +385,62 @@ CBQ_EXPORT int cbq_cpu_lut_gemm(const uint8_t* codes, const float* scales, int32
   if (!cbq::cpu_lut_supported()) return fail(CBQ_EUNSUPPORTED, "the CPU kernel needs AVX2, FMA, F16C and BMI2");
   cbq::cpu_lut_gemm_impl(codes, scales, act_bits, T, W->N, W->K, W->bits, W->idx, W->codebook, out,
                          ldo, n_threads, (flags & CBQ_CPU_NO_AVX512) == 0);
+  return CBQ_OK;
+}
+
+CBQ_EXPORT int cbq_norm_rotate_quantize(const uint16_t* x, int64_t T, int32_t K, int64_t ldx,
+                                        const cbq_norm* norm, void* stream) {
+  g_err[0] = 0;
+  if (int rc = check_norm_sizes(T, K, "K")) return rc;
+  if (ldx < K || ldx % 8) return fail(CBQ_EINVAL, "ldx must be >= K and a multiple of 8 (got %lld)", (long long)ldx);
+  if (!norm) return fail(CBQ_EINVAL, "norm must be non-null");
+  if (T == 0) return CBQ_OK;
+  cbq::NormArgs a{};
+  int b = 1;
+  if (int rc = check_norm(norm, K, &a, &b)) return rc;
+  if (!x || !aligned16(x)) return fail(CBQ_EINVAL, "x must be non-null and 16-byte aligned");
+  a.x = x; a.ldx = ldx; a.T = T; a.K = K;
+  hipError_t e = cbq::launch_norm_quantize(a, cbq::kNormX, b, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "norm_rotate_quantize launch");
+  return CBQ_OK;
+}
+
+CBQ_EXPORT int cbq_combine_norm_residual(const void* rows, int32_t rows_type, int64_t ldr,
+                                         const int32_t* slot_of, const float* topk_w, int64_t T,
+                                         int32_t topk, int32_t n_shared, int32_t H,
+                                         const float* post_weight, float post_eps,
+                                         const uint16_t* gate, int64_t ldg, float scale,
+                                         const uint16_t* residual, int64_t ldres, uint16_t* out,
+                                         int64_t ldo, const cbq_norm* next, void* stream) {
+  g_err[0] = 0;
+  if (int rc = check_norm_sizes(T, H, "H")) return rc;
+  if (rows_type != CBQ_TYPE_F32 && rows_type != CBQ_TYPE_BF16) return fail(CBQ_EINVAL, "unknown rows_type %d", rows_type);
+  if (topk < 0 || topk > 8) return fail(CBQ_EINVAL, "topk must be in [0, 8] (got %d)", topk);
+  if (n_shared < 0 || n_shared > 8) return fail(CBQ_EINVAL, "n_shared must be in [0, 8] (got %d)", n_shared);
+  if (topk + n_shared < 1) return fail(CBQ_EINVAL, "topk + n_shared must be >= 1");
+  if (ldr < H || ldr % (rows_type == CBQ_TYPE_F32 ? 4 : 8))
+    return fail(CBQ_EINVAL, "ldr must be >= H and keep rows 16-byte aligned (got %lld)", (long long)ldr);
+  if (ldres < H || ldres % 8 || ldo < H || ldo % 8)
+    return fail(CBQ_EINVAL, "ldres and ldo must be >= H and multiples of 8");
+  if (gate && ldg != 0 && (ldg < H || ldg % 8))
+    return fail(CBQ_EINVAL, "ldg must be 0, or >= H and a multiple of 8 (got %lld)", (long long)ldg);
+  if (post_weight && (!(post_eps > 0.0f) || !std::isfinite(post_eps)))
+    return fail(CBQ_EINVAL, "post_eps must be finite and > 0");
+  if (T == 0) return CBQ_OK;
+  cbq::NormArgs a{};
+  int b = 1;
+  if (next)
+    if (int rc = check_norm(next, H, &a, &b)) return rc;
+  if (!rows || !residual || !out) return fail(CBQ_EINVAL, "rows, residual and out must be non-null");
+  if (topk > 0 && (!slot_of || !topk_w)) return fail(CBQ_EINVAL, "slot_of and topk_w must be non-null when topk > 0");
+  if (!aligned16(rows) || !aligned16(residual) || !aligned16(out) || !aligned16(post_weight) || !aligned16(gate))
+    return fail(CBQ_EINVAL, "rows, residual, out, post_weight and gate must be 16-byte aligned");
+  a.x = residual; a.ldx = ldres; a.rows = rows; a.ldr = ldr; a.slot_of = slot_of; a.topk_w = topk_w;
+  a.topk = topk; a.n_shared = n_shared; a.post_weight = post_weight; a.post_eps = post_eps;
+  a.gate = gate; a.ldg = ldg; a.scale = scale; a.out = out; a.ldo = ldo; a.T = T; a.K = H;
+  hipError_t e = cbq::launch_norm_quantize(a, rows_type == CBQ_TYPE_F32 ? cbq::kNormF32 : cbq::kNormBF16, b,
+                                           (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "combine_norm_residual launch");
   return CBQ_OK;
 }
 

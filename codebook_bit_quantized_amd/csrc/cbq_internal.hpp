@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "cbq_device.hpp"
 
@@ -42,6 +43,38 @@ hipError_t launch_rotate_quantize(const uint16_t* x, int64_t T, int K, int64_t l
                                   int act_bits, const float* smooth, const uint8_t* signs,
                                   uint8_t* codes, float* scales, uint32_t* precond,
                                   hipStream_t stream);
+
+// Norms around a block (norm_quantize.hip).  Pointers may be null where the comment says so.
+enum { kNormX = 0, kNormF32 = 1, kNormBF16 = 2 };   // what is normed: x, or combined rows of that type
+struct NormArgs {
+  const uint16_t* x;          // bf16 [T][ldx]: the row, or the residual stream beside rows
+  int64_t ldx;
+  const void* rows;           // fp32 or bf16 [T*topk + n_shared*T][ldr]
+  int64_t ldr;
+  const int32_t* slot_of;     // [T][topk]
+  const float* topk_w;        // [T][topk]
+  int topk, n_shared;
+  const float* post_weight;   // [K] or null: no norm of the combined row
+  float post_eps;
+  const uint16_t* gate;       // bf16 [T][ldg] (ldg 0: one row for all) or null
+  int64_t ldg;
+  float scale;
+  uint16_t* out;              // bf16 [T][ldo]
+  int64_t ldo;
+  const float* weight;        // [K] or null: nothing after out
+  float eps;
+  uint16_t* normed;           // bf16 [T][ldn] or null
+  int64_t ldn;
+  uint8_t* codes;             // packed codes or null
+  float* scales;
+  int act_bits;
+  int64_t T;
+  int K;
+  int logb;                   // set by the launcher, as the next two
+  float c_b;
+  double inv_K;
+};
+hipError_t launch_norm_quantize(NormArgs a, int src, int b, hipStream_t stream);
 
 // Compute units of the current device (cached per device after the first query).
 hipError_t device_cu_count(int* out);

@@ -339,6 +339,80 @@ int cbq_moe_combine(const float* expert_out, const int32_t* slot_of, const float
                     int64_t T, int32_t topk, int32_t H, int32_t n_shared, float* y,
                     void* stream);
 
+/* Element types of tensors that may be fp32 or bf16 */
+enum {
+  CBQ_TYPE_F32 = 0,
+  CBQ_TYPE_BF16 = 1
+};
+
+/*
+ * cbq_norm - an RMS norm and what is taken from it: the normed row, its rotated and
+ * quantised codes, or both.
+ *
+ *  weight     : fp32 [K] (16-byte aligned).
+ *  eps        : finite and > 0.
+ *  normed     : optional bf16 [T][ldn] (ldn >= K, ldn % 8 == 0, 16-byte aligned):
+ *               n = bf16(fp32(v * w / sqrt(mean(v^2) + eps))), evaluated in fp64 and
+ *               rounded to fp32, then to bf16 (both to nearest even).
+ *  codes      : optional [T][K*act_bits/8] bytes, 16-byte aligned: the codes that
+ *               cbq_rotate_quantize(n, had_block, act_bits) gives, with
+ *  scales     : fp32 [T], its scales.  Without codes, scales, had_block and act_bits are
+ *               not read.
+ *  At least one of normed and codes is given.  A row of zeros gives n = 0, codes 0 and
+ *  scale 0.
+ */
+typedef struct {
+  const float* weight;
+  float eps;
+  int32_t had_block, act_bits;
+  uint16_t* normed;
+  int64_t ldn;
+  uint8_t* codes;
+  float* scales;
+} cbq_norm;
+
+/*
+ * cbq_norm_rotate_quantize - the norm before a block fused with cbq_rotate_quantize.
+ * Passage: CodeQuant2, Figure 1 (the rotation and the per-channel scales sit between the
+ * model's norm and its quantised linears).
+ *
+ *  x    : bf16 [T][ldx] (ldx >= K, ldx % 8 == 0, 16-byte aligned), the residual stream.
+ *  norm : the norm and its outputs (host pointer, read during the call only); normed may
+ *         be x itself (with ldn == ldx).
+ *  Requires K % 32 == 0, 32 <= K <= 16384, T < 2^31.
+ */
+int cbq_norm_rotate_quantize(const uint16_t* x, int64_t T, int32_t K, int64_t ldx,
+                             const cbq_norm* norm, void* stream);
+
+/*
+ * cbq_combine_norm_residual - after a block: the combine of cbq_moe_combine, an optional
+ * norm of its result, an optional gate, the addition to the residual stream, and
+ * optionally the next block's norm with its codes, in one pass.
+ *
+ *  rows, rows_type : fp32 or bf16 (CBQ_TYPE_*) [T*topk + n_shared*T][ldr] expert outputs
+ *               in row order as cbq_moe_combine takes them (ldr >= H, 16-byte aligned rows:
+ *               ldr % 4 == 0 for fp32, % 8 for bf16).  A plain block output [T][H] is
+ *               topk = 0, n_shared = 1.
+ *  slot_of, topk_w : [T][topk] from cbq_moe_route_gather (not read when topk == 0).  Every
+ *               entry of slot_of must be a row of rows (caller's contract).
+ *               y[t] = sum_j topk_w[t][j] rows[slot_of[t][j]] + sum_s rows[T*topk + s*T + t].
+ *  post_weight, post_eps : optional fp32 [H] (16-byte aligned): y is RMS-normed with it.
+ *  gate, ldg  : optional bf16 [T][ldg] (16-byte aligned, ldg >= H and a multiple of 8), or
+ *               ldg == 0: one row [H] for all tokens.  Multiplies the (normed) y.
+ *  residual   : bf16 [T][ldres] (ldres >= H, % 8, 16-byte aligned).
+ *  out        : bf16 [T][ldo] (as residual; may be residual itself with ldo == ldres):
+ *               out = bf16(fp32(residual + scale * gate * y)), evaluated in fp64 and
+ *               rounded to fp32, then to bf16.
+ *  next       : NULL, or the norm taken of out (as cbq_norm_rotate_quantize of it).
+ *  0 <= topk <= 8, 0 <= n_shared <= 8, topk + n_shared >= 1; H as K above.
+ */
+int cbq_combine_norm_residual(const void* rows, int32_t rows_type, int64_t ldr,
+                              const int32_t* slot_of, const float* topk_w, int64_t T,
+                              int32_t topk, int32_t n_shared, int32_t H,
+                              const float* post_weight, float post_eps, const uint16_t* gate,
+                              int64_t ldg, float scale, const uint16_t* residual, int64_t ldres,
+                              uint16_t* out, int64_t ldo, const cbq_norm* next, void* stream);
+
 /*
  * cbq_kmeans_codebooks - offline codebook construction, one 1-D K-means per weight row.
  * Passage: CodeQuant2, Figure 3 (right: K-means initialises the centroid matrix and the

@@ -1,0 +1,58 @@
+"""Host-side checks of the calls around a block: invalid arguments give the documented status
+before any HIP call, so every refusal runs on a machine without a GPU."""
+import ctypes
+import os
+
+import pytest
+
+cbq = pytest.importorskip("codebook_bit_quantized_amd")
+
+P, U = ctypes.c_void_p(0x1000), ctypes.c_void_p(0x1004)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(cbq.LIB_PATH):
+        pytest.skip("libcbq.so not built")
+    return cbq.load_library()
+
+
+def _norm(weight=0x1000, eps=1e-6, had_block=0, act_bits=4, normed=0x1000, ldn=256, codes=0x1000, scales=0x1000):
+    return ctypes.byref(cbq._binding.cbq_norm(weight, eps, had_block, act_bits, normed, ldn, codes, scales))
+
+
+def test_norm_rotate_quantize_refusals(lib):
+    f = lib.cbq_norm_rotate_quantize
+    assert f(P, -1, 256, 256, _norm(), None) == cbq.CBQ_EINVAL
+    assert f(P, 1 << 31, 256, 256, _norm(), None) == cbq.CBQ_EUNSUPPORTED
+    assert f(P, 4, 250, 256, _norm(), None) == cbq.CBQ_EINVAL
+    assert f(P, 4, 32768, 32768, _norm(), None) == cbq.CBQ_EUNSUPPORTED
+    assert f(P, 4, 256, 248, _norm(), None) == cbq.CBQ_EINVAL
+    assert f(P, 4, 256, 260, _norm(), None) == cbq.CBQ_EINVAL
+    assert f(P, 4, 256, 256, None, None) == cbq.CBQ_EINVAL
+    assert f(None, 4, 256, 256, _norm(), None) == cbq.CBQ_EINVAL
+    assert f(U, 4, 256, 256, _norm(), None) == cbq.CBQ_EINVAL
+    for bad in (dict(weight=None), dict(weight=0x1004), dict(eps=0.0), dict(eps=-1.0), dict(eps=float("nan")),
+                dict(eps=float("inf")), dict(normed=None, codes=None), dict(normed=0x1008), dict(ldn=248),
+                dict(ldn=260), dict(act_bits=5), dict(had_block=3), dict(had_block=512), dict(had_block=-2),
+                dict(scales=None), dict(codes=0x1004)):
+        assert f(P, 4, 256, 256, _norm(**bad), None) == cbq.CBQ_EINVAL, bad
+        assert lib.cbq_last_error()
+    assert f(None, 0, 256, 256, _norm(), None) == cbq.CBQ_OK
+
+
+def test_combine_norm_residual_refusals(lib):
+    def f(rows=P, rows_type=0, ldr=256, slot_of=P, topk_w=P, T=4, topk=2, n_shared=1, H=256, post_weight=P,
+          post_eps=1e-6, gate=P, ldg=256, scale=1.0, residual=P, ldres=256, out=P, ldo=256, nxt=None):
+        return lib.cbq_combine_norm_residual(rows, rows_type, ldr, slot_of, topk_w, T, topk, n_shared, H, post_weight,
+                                             post_eps, gate, ldg, scale, residual, ldres, out, ldo, nxt, None)
+
+    for bad in (dict(T=-1), dict(H=250), dict(rows_type=2), dict(topk=9), dict(topk=-1), dict(n_shared=9),
+                dict(topk=0, n_shared=0), dict(ldr=252), dict(ldr=258), dict(rows_type=1, ldr=260), dict(ldres=248),
+                dict(ldo=260), dict(ldg=8), dict(ldg=260), dict(post_eps=0.0), dict(rows=None), dict(residual=None),
+                dict(out=None), dict(slot_of=None), dict(topk_w=None), dict(rows=U), dict(residual=U), dict(out=U),
+                dict(post_weight=U), dict(gate=U), dict(nxt=_norm(eps=0.0)), dict(nxt=_norm(normed=None, codes=None))):
+        assert f(**bad) == cbq.CBQ_EINVAL, bad
+        assert lib.cbq_last_error()
+    assert f(H=32768, ldr=32768, ldres=32768, ldo=32768, ldg=0) == cbq.CBQ_EUNSUPPORTED
+    assert f(T=0, rows=None, residual=None, out=None) == cbq.CBQ_OK
