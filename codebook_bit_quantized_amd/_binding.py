@@ -24,6 +24,7 @@ PATH_PAGES_PRODUCTS, PATH_PAGES_BUCKETS = 3, 4   # the table forms (4-bit, A4; n
 PATH_REG_TABLES = 0x10   # flags: where 2-/3-bit codebooks are looked up (default: per path)
 PATH_LDS_TABLES = 0x20
 AUTO_MAX_LUT_ROWS = 32
+FEW_MAX_TOKENS = 32
 
 # every symbol include/cbq.h declares
 EXPORTED = ("cbq_rotate_quantize", "cbq_rotate_quantize_ex", "cbq_rotate_dense_workspace",
@@ -31,7 +32,8 @@ EXPORTED = ("cbq_rotate_quantize", "cbq_rotate_quantize_ex", "cbq_rotate_dense_w
             "cbq_moe_route_gather_noalloc", "cbq_prepack_bytes", "cbq_prepack_weights",
             "cbq_gemm_workspace", "cbq_codebook_lut_gemm", "cbq_moe_combine",
             "cbq_kmeans_codebooks", "cbq_refit_codebooks", "cbq_cpu_lut_gemm", "cbq_status_string", "cbq_last_error",
-            "cbq_version", "cbq_norm_rotate_quantize", "cbq_combine_norm_residual")
+            "cbq_version", "cbq_norm_rotate_quantize", "cbq_combine_norm_residual", "cbq_moe_few_workspace",
+            "cbq_moe_ffn_few")
 
 
 class CbqError(RuntimeError):
@@ -97,6 +99,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "cbq_norm_rotate_quantize": (ctypes.c_int, [vp, i64, i32, i64, Nrm, vp]),
         "cbq_combine_norm_residual": (ctypes.c_int, [vp, i32, i64, vp, vp, i64, i32, i32, i32, vp, f32, vp, i64,
                                                      f32, vp, i64, vp, i64, Nrm, vp]),
+        "cbq_moe_few_workspace": (sz, [i64, i32, i32, i32, i32, i32]),
+        "cbq_moe_ffn_few": (ctypes.c_int, [vp, vp, i32, vp, i64, i32, i32, i32, i32, W, W, W, vp, i32, i64, vp, sz, vp]),
         "cbq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "cbq_last_error": (ctypes.c_char_p, []),
         "cbq_version": (ctypes.c_int, []),
@@ -187,6 +191,15 @@ class CodebookWeights:
     @property
     def N(self) -> int:
         return self.idx.shape[1]
+
+    def _check(self, dev: torch.device, name: str):
+        """The tensors as the C struct describes them: on dev, packed, of these sizes."""
+        kp = self.K if self.layout == LAYOUT_ROWS else (self.K + 127) // 128 * 128
+        _tensor(name + ".idx", self.idx, dev, torch.uint8, (self.E, self.N, kp * self.bits // 8), contiguous=True)
+        if self.codebook.element_size() != 2:
+            raise ValueError(f"{name}.codebook must hold 16-bit fp16 patterns (got {self.codebook.dtype})")
+        _tensor(name + ".codebook", self.codebook, dev, self.codebook.dtype, (self.E, self.N, 1 << self.bits),
+                contiguous=True)
 
     def c_struct(self) -> cbq_weights:
         return cbq_weights(self.idx.data_ptr(), self.codebook.data_ptr(), self.E, self.N, self.K,
@@ -475,6 +488,52 @@ def combine_norm_residual(rows: torch.Tensor, residual: torch.Tensor, slot_of: O
         if next_weight is None:
             return o
         return (o, n, c, s) if act_bits else (o, n, None, None)
+
+    return _on_stream(dev, stream, call)
+
+
+def moe_few_workspace(T: int, topk: int, n_shared: int, H: int, F: int, act_bits: int = 4) -> int:
+    """Bytes of device workspace moe_ffn_few needs (cbq_moe_few_workspace)."""
+    return int(load_library().cbq_moe_few_workspace(T, topk, n_shared, H, F, act_bits))
+
+
+def moe_ffn_few(codes: torch.Tensor, scales: torch.Tensor, logits: torch.Tensor, gate: CodebookWeights,
+                up: CodebookWeights, down: CodebookWeights, topk: int, n_shared: int = 0, act_bits: int = 4,
+                renormalize: bool = True, y: Optional[torch.Tensor] = None, y_dtype: torch.dtype = torch.bfloat16,
+                ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The whole MoE FFN layer for at most FEW_MAX_TOKENS quantised tokens (cbq_moe_ffn_few):
+    codes and scales from rotate_quantize or norm_rotate_quantize, router logits fp32 [T][E],
+    gate/up/down of E + n_shared experts.  Returns y [T][H] in y_dtype (bf16 or fp32).
+
+    h stays fp32 up to its quantiser, where moe_ffn rounds it to bf16.  ws: optional uint8
+    device workspace of moe_few_workspace(...) bytes; calls that overlap need one each."""
+    lib = load_library()
+    _require_gpu(codes, scales, logits)
+    dev = codes.device
+    T, E = logits.shape
+    H, F = gate.K, gate.N
+    _tensor("codes", codes, dev, torch.uint8, (T, H * act_bits // 8), contiguous=True)
+    _tensor("scales", scales, dev, torch.float32, (T,), contiguous=True)
+    _tensor("logits", logits, dev, torch.float32, contiguous=True)
+    for name, w in (("gate", gate), ("up", up), ("down", down)):
+        w._check(dev, name)
+    if y is not None:
+        y_dtype = y.dtype
+    if y_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"y must be float32 or bfloat16 (got {y_dtype})")
+    _tensor("y", y, dev, y_dtype, (T, H), rows=True)
+    _tensor("ws", ws, dev, torch.uint8, contiguous=True)
+
+    def call(st):
+        o = torch.empty((T, H), dtype=y_dtype, device=dev) if y is None else y
+        w = ws if ws is not None else torch.empty((moe_few_workspace(T, topk, n_shared, H, F, act_bits),),
+                                                  dtype=torch.uint8, device=dev)
+        _check(lib.cbq_moe_ffn_few(codes.data_ptr(), scales.data_ptr(), act_bits, logits.data_ptr(), T, E, topk,
+                                   int(bool(renormalize)), n_shared, ctypes.byref(gate.c_struct()),
+                                   ctypes.byref(up.c_struct()), ctypes.byref(down.c_struct()), o.data_ptr(),
+                                   TYPE_F32 if y_dtype == torch.float32 else TYPE_BF16, _row_stride(o), w.data_ptr(),
+                                   w.numel(), st))
+        return o
 
     return _on_stream(dev, stream, call)
 

@@ -444,6 +444,64 @@ CBQ_EXPORT int cbq_combine_norm_residual(const void* rows, int32_t rows_type, in
   return CBQ_OK;
 }
 
+CBQ_EXPORT size_t cbq_moe_few_workspace(int64_t T, int32_t topk, int32_t n_shared, int32_t H, int32_t F,
+                                        int32_t act_bits) {
+  if (T <= 0 || T > CBQ_FEW_MAX_TOKENS || topk < 1 || topk > 8 || n_shared < 0 || n_shared > 8 || H < 32 ||
+      H > 16384 || F < 32 || F > 16384 || (act_bits != 4 && act_bits != 8))
+    return 0;
+  return cbq::moe_few_workspace_bytes(T, topk, n_shared, H, F, act_bits);
+}
+
+CBQ_EXPORT int cbq_moe_ffn_few(const uint8_t* codes, const float* scales, int32_t act_bits,
+                               const float* logits, int64_t T, int32_t E, int32_t topk,
+                               int32_t renormalize, int32_t n_shared, const cbq_weights* gate,
+                               const cbq_weights* up, const cbq_weights* down, void* y,
+                               int32_t y_type, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  if (T < 0) return fail(CBQ_EINVAL, "T must be >= 0 (got %lld)", (long long)T);
+  if (T > CBQ_FEW_MAX_TOKENS)
+    return fail(CBQ_EUNSUPPORTED, "at most %d tokens (got %lld)", CBQ_FEW_MAX_TOKENS, (long long)T);
+  if (E < 1 || E > 256) return fail(CBQ_EUNSUPPORTED, "E must be in [1, 256] (got %d)", E);
+  if (topk < 1 || topk > 8 || topk > E) return fail(CBQ_EINVAL, "topk must be in [1, min(E, 8)] (got %d)", topk);
+  if (n_shared < 0 || n_shared > 8) return fail(CBQ_EINVAL, "n_shared must be in [0, 8] (got %d)", n_shared);
+  if (renormalize != 0 && renormalize != 1) return fail(CBQ_EINVAL, "renormalize must be 0 or 1");
+  if (act_bits != 4 && act_bits != 8) return fail(CBQ_EINVAL, "act_bits must be 4 or 8 (got %d)", act_bits);
+  if (!gate || !up || !down) return fail(CBQ_EINVAL, "gate, up and down must be non-null");
+  const cbq_weights* W[3] = {gate, up, down};
+  for (int i = 0; i < 3; ++i) {
+    if (int rc = check_weights(W[i], i)) return rc;
+    if (W[i]->E != E + n_shared)
+      return fail(CBQ_EINVAL, "W[%d]: E must be the router's %d experts and %d shared ones (got %d)", i, E, n_shared, W[i]->E);
+    if ((int64_t)W[i]->N * cbq::index_row_bytes(W[i]->K, W[i]->bits, W[i]->layout == CBQ_LAYOUT_BLOCKED) >= (int64_t(1) << 31))
+      return fail(CBQ_EUNSUPPORTED, "one expert's index block must be smaller than 2 GiB");
+  }
+  const int H = gate->K, F = gate->N;
+  if (up->N != F || up->K != H || up->bits != gate->bits || up->layout != gate->layout)
+    return fail(CBQ_EINVAL, "gate and up weights must have equal N, K, bits and layout");
+  if (down->N != H || down->K != F) return fail(CBQ_EINVAL, "down must have N = %d and K = %d (got %d, %d)", H, F, down->N, down->K);
+  if (H > 16384 || F > 16384) return fail(CBQ_EUNSUPPORTED, "H and F must be <= 16384 (got %d, %d)", H, F);
+  if (y_type != CBQ_TYPE_F32 && y_type != CBQ_TYPE_BF16) return fail(CBQ_EINVAL, "unknown y_type %d", y_type);
+  if (ldy < H || ldy % 4) return fail(CBQ_EINVAL, "ldy must be >= H and a multiple of 4 (got %lld)", (long long)ldy);
+  if (T == 0) return CBQ_OK;
+  if (!codes || !scales || !logits || !y) return fail(CBQ_EINVAL, "codes, scales, logits and y must be non-null");
+  if (!aligned16(codes) || !aligned16(y)) return fail(CBQ_EINVAL, "codes and y must be 16-byte aligned");
+  const size_t need = cbq::moe_few_workspace_bytes(T, topk, n_shared, H, F, act_bits);
+  if (!ws || ws_bytes < need)
+    return fail(CBQ_EWORKSPACE, "workspace of %zu bytes required (got %zu)", need, ws ? ws_bytes : (size_t)0);
+  if (!aligned16(ws)) return fail(CBQ_EINVAL, "ws must be 16-byte aligned");
+  cbq::MoeFewArgs m{};
+  m.codes = codes; m.scales = scales; m.logits = logits; m.T = (int)T; m.E = E; m.topk = topk;
+  m.n_shared = n_shared; m.renormalize = renormalize; m.act_bits = act_bits; m.H = H; m.F = F;
+  m.gate = cbq::GemmW{gate->idx, gate->codebook}; m.up = cbq::GemmW{up->idx, up->codebook};
+  m.down = cbq::GemmW{down->idx, down->codebook};
+  m.bits_gu = gate->bits; m.bits_d = down->bits;
+  m.blocked_gu = gate->layout == CBQ_LAYOUT_BLOCKED; m.blocked_d = down->layout == CBQ_LAYOUT_BLOCKED;
+  m.y = y; m.ldy = ldy; m.y_bf16 = y_type == CBQ_TYPE_BF16; m.ws = ws;
+  hipError_t e = cbq::launch_moe_few(m, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "moe_ffn_few launch");
+  return CBQ_OK;
+}
+
 CBQ_EXPORT int cbq_moe_combine(const float* expert_out, const int32_t* slot_of, const float* topk_w,
                                int64_t T, int32_t topk, int32_t H, int32_t n_shared, float* y,
                                void* stream) {

@@ -45,7 +45,9 @@ hipError_t launch_rotate_quantize(const uint16_t* x, int64_t T, int K, int64_t l
                                   hipStream_t stream);
 
 // Norms around a block (norm_quantize.hip).  Pointers may be null where the comment says so.
-enum { kNormX = 0, kNormF32 = 1, kNormBF16 = 2 };   // what is normed: x, or combined rows of that type
+// What is normed: x, or combined rows of that type; or fp32 rows rotated and quantised as they
+// are (no norm).
+enum { kNormX = 0, kNormF32 = 1, kNormBF16 = 2, kRotateF32 = 3 };
 struct NormArgs {
   const uint16_t* x;          // bf16 [T][ldx]: the row, or the residual stream beside rows
   int64_t ldx;
@@ -75,6 +77,32 @@ struct NormArgs {
   double inv_K;
 };
 hipError_t launch_norm_quantize(NormArgs a, int src, int b, hipStream_t stream);
+
+// The few-token MoE layer (moe_few.hip).  FewArgs: one of its grouped GEMMs.
+struct FewArgs {
+  const float* logits;        // [T][E]
+  int32_t* ids;               // [T][topk]: written by the gate/up kernel, read by the down kernel
+  int T, E, topk, n_shared;
+  const uint8_t* codes;       // code rows: tokens (gate/up) or choices (down)
+  const float* scales;
+  GemmW w[2];
+  int N, K, blocked;
+  float* out;                 // fp32 [T*topk + n_shared*T][N]
+};
+struct MoeFewArgs {
+  const uint8_t* codes;
+  const float* scales;
+  const float* logits;
+  int T, E, topk, n_shared, renormalize, act_bits, H, F;
+  GemmW gate, up, down;
+  int bits_gu, bits_d, blocked_gu, blocked_d;
+  void* y;
+  int64_t ldy;
+  int y_bf16;
+  void* ws;
+};
+size_t moe_few_workspace_bytes(int64_t T, int topk, int n_shared, int H, int F, int act_bits);
+hipError_t launch_moe_few(const MoeFewArgs& m, hipStream_t stream);
 
 // Compute units of the current device (cached per device after the first query).
 hipError_t device_cu_count(int* out);

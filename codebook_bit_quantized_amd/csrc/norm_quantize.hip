@@ -111,7 +111,8 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, bool store, const double
 }  // namespace
 
 // SRC: where the normed row comes from.  kNormX: the bf16 row x; kNormF32 / kNormBF16: the
-// block's rows of that type, combined and added to the residual.
+// block's rows of that type, combined and added to the residual; kRotateF32: no norm, fp32
+// rows (whose transform then rounds like any fp64 sum).
 template <int CPT, int NT, int SRC>
 __global__ void __launch_bounds__(NT)
 norm_quantize_kernel(NormArgs a) {
@@ -126,7 +127,9 @@ norm_quantize_kernel(NormArgs a) {
   const bool act = c0 < a.K;                 // K is a multiple of 32, so whole threads
   float f[CPT];                              // the row that is normed and quantised
 
-  if constexpr (SRC == kNormX) {
+  if constexpr (SRC == kRotateF32) {
+    if (act) load_f32<CPT>(static_cast<const float*>(a.rows) + t * a.ldr + c0, f);
+  } else if constexpr (SRC == kNormX) {
     if (act) load_bf16<CPT>(a.x + t * a.ldx + c0, f);
   } else {
     using Row = std::conditional_t<SRC == kNormF32, float, uint16_t>;
@@ -199,7 +202,7 @@ norm_quantize_kernel(NormArgs a) {
 
   // ---- RMS norm ----
   double v[CPT];
-  {
+  if constexpr (SRC != kRotateF32) {
     double ss = 0.0;
 #pragma unroll
     for (int i = 0; i < CPT; ++i) ss = __builtin_fma((double)f[i], (double)f[i], ss);
@@ -323,7 +326,8 @@ static void launch_nt(const NormArgs& a, int src, unsigned threads, size_t lds, 
   const dim3 grid((unsigned)a.T), block(threads);
   if (src == kNormX) hipLaunchKernelGGL((norm_quantize_kernel<CPT, NT, kNormX>), grid, block, lds, stream, a);
   else if (src == kNormF32) hipLaunchKernelGGL((norm_quantize_kernel<CPT, NT, kNormF32>), grid, block, lds, stream, a);
-  else hipLaunchKernelGGL((norm_quantize_kernel<CPT, NT, kNormBF16>), grid, block, lds, stream, a);
+  else if (src == kNormBF16) hipLaunchKernelGGL((norm_quantize_kernel<CPT, NT, kNormBF16>), grid, block, lds, stream, a);
+  else hipLaunchKernelGGL((norm_quantize_kernel<CPT, NT, kRotateF32>), grid, block, lds, stream, a);
 }
 
 hipError_t launch_norm_quantize(NormArgs a, int src, int b, hipStream_t stream) {

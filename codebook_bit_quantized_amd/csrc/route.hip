@@ -15,18 +15,9 @@
 #include <mutex>
 
 #include "cbq_internal.hpp"
+#include "route_device.hpp"
 
 namespace cbq {
-
-__device__ __forceinline__ uint32_t order_bits(float f) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, f + 0.0f);   // -0 -> +0
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-
-__device__ __forceinline__ float from_order_bits(uint32_t o) {
-  const uint32_t u = (o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o;
-  return __builtin_bit_cast(float, u);
-}
 
 // value of the lane n places down the same row of 16 (DPP row rotate)
 template <int N>

@@ -414,6 +414,40 @@ int cbq_combine_norm_residual(const void* rows, int32_t rows_type, int64_t ldr,
                               uint16_t* out, int64_t ldo, const cbq_norm* next, void* stream);
 
 /*
+ * cbq_moe_ffn_few - the whole MoE FFN layer for the few tokens of a decode batch.
+ * Passages: those of cbq_moe_route_gather, cbq_codebook_lut_gemm, cbq_rotate_quantize and
+ * cbq_moe_combine, whose sequence it replaces.
+ *
+ *  codes, scales : the quantised layer input: codes [T][H*act_bits/8] (16-byte aligned),
+ *               scales fp32 [T], from cbq_rotate_quantize or cbq_norm_rotate_quantize.
+ *  logits     : fp32 [T][E] router logits; E, topk, renormalize, n_shared as for
+ *               cbq_moe_route_gather (the chosen experts and their weights are the same).
+ *  gate, up   : weight sets of E + n_shared experts, N = F, K = H, equal bits and layout.
+ *  down       : E + n_shared experts, N = H, K = F; its own bits and layout.
+ *  y, y_type  : fp32 or bf16 (CBQ_TYPE_*) [T][ldy] (ldy >= H, ldy % 4 == 0, 16-byte
+ *               aligned): y[t] = sum_j w_j out_j + the shared experts' outputs, summed in
+ *               fp32 (j ascending, then the shared experts).
+ *  ws, ws_bytes : device workspace of cbq_moe_few_workspace(...) bytes, 16-byte aligned;
+ *               rewritten by every call, so it needs no clearing; calls that overlap in
+ *               time need one each.
+ *
+ *  Per chosen expert: g, u from the codes, h = silu(g) * u kept in fp32, its codes by the
+ *  transform and quantiser of cbq_rotate_quantize with F's own block (F & -F), and down's
+ *  product of those codes.  (The sequence of single calls rounds h to bf16 first, so its
+ *  codes of h differ now and then.)  Deterministic: no result depends on the order of atomics.
+ *  Limits: 0 <= T <= CBQ_FEW_MAX_TOKENS (CBQ_EUNSUPPORTED above: use the single calls),
+ *  H % 32 == 0, F % 32 == 0, H, F <= 16384, one expert's index block below 2 GiB.
+ */
+#define CBQ_FEW_MAX_TOKENS 32
+size_t cbq_moe_few_workspace(int64_t T, int32_t topk, int32_t n_shared, int32_t H, int32_t F,
+                             int32_t act_bits);
+int cbq_moe_ffn_few(const uint8_t* codes, const float* scales, int32_t act_bits,
+                    const float* logits, int64_t T, int32_t E, int32_t topk, int32_t renormalize,
+                    int32_t n_shared, const cbq_weights* gate, const cbq_weights* up,
+                    const cbq_weights* down, void* y, int32_t y_type, int64_t ldy, void* ws,
+                    size_t ws_bytes, void* stream);
+
+/*
  * cbq_kmeans_codebooks - offline codebook construction, one 1-D K-means per weight row.
  * Passage: CodeQuant2, Figure 3 (right: K-means initialises the centroid matrix and the
  * per-row assignment matrices); CodeQuant abstract (weight outliers absorbed into

@@ -56,3 +56,39 @@ def test_combine_norm_residual_refusals(lib):
         assert lib.cbq_last_error()
     assert f(H=32768, ldr=32768, ldres=32768, ldo=32768, ldg=0) == cbq.CBQ_EUNSUPPORTED
     assert f(T=0, rows=None, residual=None, out=None) == cbq.CBQ_OK
+
+
+def _w(E=10, N=96, K=128, bits=4, layout=0, idx=0x1000, cb=0x1000):
+    return ctypes.byref(cbq.cbq_weights(idx, cb, E, N, K, bits, layout))
+
+
+def test_moe_ffn_few_refusals(lib):
+    need = lib.cbq_moe_few_workspace(4, 2, 2, 128, 96, 4)
+    assert need > 0
+
+    def f(codes=P, scales=P, act_bits=4, logits=P, T=4, E=8, topk=2, renorm=1, n_shared=2, gate=_w(), up=_w(),
+          down=_w(N=128, K=96), y=P, y_type=0, ldy=128, ws=P, n=None):
+        return lib.cbq_moe_ffn_few(codes, scales, act_bits, logits, T, E, topk, renorm, n_shared, gate, up, down, y,
+                                   y_type, ldy, ws, need if n is None else n, None)
+
+    for bad in (dict(T=-1), dict(topk=0), dict(topk=9), dict(E=1, n_shared=9), dict(n_shared=-1), dict(renorm=2),
+                dict(act_bits=16), dict(gate=None), dict(up=None), dict(down=None), dict(gate=_w(E=9)),
+                dict(up=_w(N=80)), dict(up=_w(bits=3)), dict(up=_w(layout=1)), dict(down=_w(N=96, K=128)),
+                dict(gate=_w(idx=None)), dict(gate=_w(cb=0x1004)), dict(gate=_w(layout=7)), dict(y_type=2),
+                dict(ldy=124), dict(ldy=130), dict(codes=None), dict(scales=None), dict(logits=None), dict(y=None),
+                dict(codes=U), dict(y=U), dict(ws=U)):
+        assert f(**bad) == cbq.CBQ_EINVAL, bad
+        assert lib.cbq_last_error()
+    assert f(T=33) == cbq.CBQ_EUNSUPPORTED
+    assert f(E=257) == cbq.CBQ_EUNSUPPORTED
+    assert f(gate=_w(bits=5)) == cbq.CBQ_EUNSUPPORTED
+    assert f(ws=None) == cbq.CBQ_EWORKSPACE and f(n=need - 1) == cbq.CBQ_EWORKSPACE
+    assert f(T=0, codes=None, logits=None, y=None, ws=None) == cbq.CBQ_OK
+    wide = dict(gate=_w(N=16384 + 32), up=_w(N=16384 + 32), down=_w(N=128, K=16384 + 32))
+    assert f(**wide) == cbq.CBQ_EUNSUPPORTED
+
+
+def test_moe_few_workspace_sizes(lib):
+    f = lib.cbq_moe_few_workspace
+    assert f(0, 2, 0, 128, 96, 4) == 0 and f(33, 2, 0, 128, 96, 4) == 0 and f(1, 9, 0, 128, 96, 4) == 0
+    assert f(32, 8, 8, 16384, 16384, 8) >= 32 * 16 * (4 + 1 + 4) * 16384
