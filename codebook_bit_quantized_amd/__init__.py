@@ -20,13 +20,14 @@ from ._binding import (AUTO_MAX_LUT_ROWS, CBQ_EHIP, CBQ_EINVAL, CBQ_EUNSUPPORTED
                        refit_codebooks,
                        rotate_dense_workspace, rotate_quantize, rotate_quantize_dense,
                        route_workspace, gemm_workspace, norm_rotate_quantize,
-                       combine_norm_residual, moe_ffn_few, moe_few_workspace, FEW_MAX_TOKENS, TYPE_F32, TYPE_BF16)
+                       combine_norm_residual, moe_ffn_few, moe_few_workspace, FEW_MAX_TOKENS,
+                       codebook_adapter_gemm, adapter_workspace, TYPE_F32, TYPE_BF16)
 
 __all__ = [
     "rotate_quantize", "moe_route_gather", "moe_route_gather_noalloc", "prepack_weights", "LAYOUT_ROWS", "LAYOUT_BLOCKED",
     "codebook_lut_gemm", "moe_combine", "moe_ffn",
     "route_workspace", "gemm_workspace", "kmeans_codebooks", "refit_codebooks", "cpu_lut_gemm", "rotate_quantize_dense",
-    "rotate_dense_workspace", "norm_rotate_quantize", "combine_norm_residual", "moe_ffn_few", "moe_few_workspace", "FEW_MAX_TOKENS", "TYPE_F32", "TYPE_BF16",
+    "rotate_dense_workspace", "norm_rotate_quantize", "combine_norm_residual", "moe_ffn_few", "moe_few_workspace", "FEW_MAX_TOKENS", "codebook_adapter_gemm", "adapter_workspace", "TYPE_F32", "TYPE_BF16",
     "CodebookWeights", "CbqError", "load_library", "LIB_PATH", "EXPORTED", "cbq_weights",
     "EPI_F32", "EPI_SWIGLU_BF16", "PATH_AUTO", "PATH_LUT", "PATH_MFMA", "PATH_PAGES_PRODUCTS", "PATH_PAGES_BUCKETS", "PATH_REG_TABLES", "PATH_LDS_TABLES", "AUTO_MAX_LUT_ROWS",
     "CBQ_OK", "CBQ_EINVAL", "CBQ_EUNSUPPORTED", "CBQ_EWORKSPACE", "CBQ_EHIP",

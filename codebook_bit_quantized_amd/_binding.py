@@ -33,7 +33,7 @@ EXPORTED = ("cbq_rotate_quantize", "cbq_rotate_quantize_ex", "cbq_rotate_dense_w
             "cbq_gemm_workspace", "cbq_codebook_lut_gemm", "cbq_moe_combine",
             "cbq_kmeans_codebooks", "cbq_refit_codebooks", "cbq_cpu_lut_gemm", "cbq_status_string", "cbq_last_error",
             "cbq_version", "cbq_norm_rotate_quantize", "cbq_combine_norm_residual", "cbq_moe_few_workspace",
-            "cbq_moe_ffn_few")
+            "cbq_moe_ffn_few", "cbq_adapter_workspace", "cbq_codebook_adapter_gemm")
 
 
 class CbqError(RuntimeError):
@@ -101,6 +101,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                                      f32, vp, i64, vp, i64, Nrm, vp]),
         "cbq_moe_few_workspace": (sz, [i64, i32, i32, i32, i32, i32]),
         "cbq_moe_ffn_few": (ctypes.c_int, [vp, vp, i32, vp, i64, i32, i32, i32, i32, W, W, W, vp, i32, i64, vp, sz, vp]),
+        "cbq_adapter_workspace": (sz, [i64, i32]),
+        "cbq_codebook_adapter_gemm": (ctypes.c_int, [vp, vp, i32, i64, W, vp, i64, vp, vp, vp, i32, i32, vp, vp, i64, vp,
+                                                     sz, vp]),
         "cbq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "cbq_last_error": (ctypes.c_char_p, []),
         "cbq_version": (ctypes.c_int, []),
@@ -533,6 +536,50 @@ def moe_ffn_few(codes: torch.Tensor, scales: torch.Tensor, logits: torch.Tensor,
                                    ctypes.byref(up.c_struct()), ctypes.byref(down.c_struct()), o.data_ptr(),
                                    TYPE_F32 if y_dtype == torch.float32 else TYPE_BF16, _row_stride(o), w.data_ptr(),
                                    w.numel(), st))
+        return o
+
+    return _on_stream(dev, stream, call)
+
+
+def adapter_workspace(T: int, rank: int) -> int:
+    """Bytes of device workspace codebook_adapter_gemm needs (cbq_adapter_workspace)."""
+    return int(load_library().cbq_adapter_workspace(T, rank))
+
+
+def codebook_adapter_gemm(codes: torch.Tensor, scales: torch.Tensor, act_bits: int, weights: CodebookWeights,
+                          x: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor, adapter_of: torch.Tensor,
+                          adapter_scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                          ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """A dense codebook projection with each token's low-rank adapter beside it
+    (cbq_codebook_adapter_gemm): fp32 [T][N] = scale * q W^T + s_a (x A_a^T) B_a^T.
+
+    x: bf16 [T][K], the unrotated activations; lora_a: bf16 [n][rank][K]; lora_b: bf16
+    [n][N][rank]; adapter_of: int32 [T], -1 (or any id outside the set) for none;
+    adapter_scale: fp32 [n] or None.  ws: optional uint8 device workspace of
+    adapter_workspace(T, rank) bytes; calls that overlap need one each."""
+    lib = load_library()
+    _require_gpu(codes, scales, x)
+    dev = codes.device
+    T, K, N = x.shape[0], weights.K, weights.N
+    n_ad, rank = lora_a.shape[0], lora_a.shape[1]
+    _tensor("codes", codes, dev, torch.uint8, (T, K * act_bits // 8), contiguous=True)
+    _tensor("scales", scales, dev, torch.float32, (T,), contiguous=True)
+    weights._check(dev, "weights")
+    _tensor("x", x, dev, torch.bfloat16, (T, K), rows=True)
+    _tensor("lora_a", lora_a, dev, torch.bfloat16, (n_ad, rank, K), contiguous=True)
+    _tensor("lora_b", lora_b, dev, torch.bfloat16, (n_ad, N, rank), contiguous=True)
+    _tensor("adapter_of", adapter_of, dev, torch.int32, (T,), contiguous=True)
+    _tensor("adapter_scale", adapter_scale, dev, torch.float32, (n_ad,), contiguous=True)
+    _tensor("out", out, dev, torch.float32, (T, N), rows=True)
+    _tensor("ws", ws, dev, torch.uint8, contiguous=True)
+
+    def call(st):
+        o = torch.empty((T, N), dtype=torch.float32, device=dev) if out is None else out
+        w = ws if ws is not None else torch.empty((adapter_workspace(T, rank),), dtype=torch.uint8, device=dev)
+        _check(lib.cbq_codebook_adapter_gemm(
+            codes.data_ptr(), scales.data_ptr(), act_bits, T, ctypes.byref(weights.c_struct()), x.data_ptr(),
+            _row_stride(x), lora_a.data_ptr(), lora_b.data_ptr(), _ptr(adapter_scale), n_ad, rank,
+            adapter_of.data_ptr(), o.data_ptr(), _row_stride(o), w.data_ptr(), w.numel(), st))
         return o
 
     return _on_stream(dev, stream, call)

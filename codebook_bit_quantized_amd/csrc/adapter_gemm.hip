@@ -1,0 +1,202 @@
+// A shared codebook projection with low-rank adapters of many requests beside it:
+//   out[t] = scale_t * sum_k q[t][k] W[n][k]  +  s_a * B_a (A_a x[t]),   a = adapter_of[t].
+//
+// CodeQuant2, Figure 3 (the projection's codebook weights); the adapters are full-precision
+// updates trained beside frozen quantised weights.
+//
+// Two launches.  The first forms u[t] = s_a A_a x[t] (fp32, [T][rank]) for every token that
+// has an adapter; the second is the projection, whose epilogue adds B_a u[t] before the only
+// store of out, so the adapters cost no pass over out.  Nothing is sorted: a tile of 16 or 32
+// tokens works through the distinct adapters among its own tokens (one or two where requests
+// are contiguous, up to one a token in a decode batch), with results taken only for the
+// tokens of that adapter, so another adapter's infinities never reach a token.
+#include "cbq_internal.hpp"
+#include "few_device.hpp"
+
+namespace cbq {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// u = s_a A_a x for 16 tokens and RT * 16 rank rows.  Workgroup (tile, y, z): the distinct
+// adapters y, y + gridDim.y, ... of the tile; rank rows from 16 RT z on; the waves split K and
+// their sums meet in LDS in wave order.  Bound by the latency of one pass over the adapter's
+// rows in a decode batch, by reading x in a prefill batch.
+template <int RT>
+__global__ void __launch_bounds__(512)
+adapter_shrink_kernel(AdapterArgs a, const uint16_t* __restrict__ x, int64_t ldx, const uint16_t* __restrict__ lora_a,
+                      const float* __restrict__ adapter_scale, int64_t T, int K, float* __restrict__ u) {
+  __shared__ f32x4 red[7][RT][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+  const int m = lane & 15, g = lane >> 4;
+  const int64_t t0 = (int64_t)blockIdx.x * 16;
+  const int of = t0 + m < T ? a.of[t0 + m] : -1;
+  const int r0 = (int)blockIdx.z * 16 * RT;
+  const int nc = K >> 5, cpw = (nc + nw - 1) / nw;
+  const int k0 = wave * cpw, k1 = min(nc, k0 + cpw);
+
+  uint32_t todo = (uint32_t)__ballot((uint32_t)of < (uint32_t)a.n_adapters) & 0xFFFFu;
+  for (int i = 0; todo != 0; ++i) {
+    const int ad = __builtin_amdgcn_readlane(of, __builtin_ctz(todo));
+    const uint32_t mine = (uint32_t)__ballot(of == ad) & 0xFFFFu;
+    todo &= ~mine;
+    if (i % (int)gridDim.y != (int)blockIdx.y) continue;
+    const bool row = (mine >> m) & 1u;
+    const uint16_t* px = x + (row ? (t0 + m) * ldx : 0) + 8 * g;
+    const uint16_t* pa = lora_a + ((int64_t)ad * a.rank + r0) * K + 8 * g;
+    f32x4 acc[RT];
+#pragma unroll
+    for (int q = 0; q < RT; ++q) acc[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int UN = RT >= 4 ? 2 : 4;      // 32-channel steps in flight
+    for (int k = k0; k < k1; k += UN) {
+      u32x4 xv[UN], av[UN][RT];
+#pragma unroll
+      for (int j = 0; j < UN; ++j) {
+        const bool in = k + j < k1;
+        xv[j] = in && row ? *reinterpret_cast<const u32x4*>(px + (k + j) * 32) : u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int q = 0; q < RT; ++q) {
+          const int r = q * 16 + m;
+          av[j][q] = in && r0 + r < a.rank ? *reinterpret_cast<const u32x4*>(pa + (int64_t)r * K + (k + j) * 32)
+                                           : u32x4{0, 0, 0, 0};
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < UN; ++j)
+#pragma unroll
+        for (int q = 0; q < RT; ++q)
+          acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv[j]),
+                                                           __builtin_bit_cast(bf16x8, av[j][q]), acc[q], 0, 0, 0);
+    }
+    if (wave > 0) {
+#pragma unroll
+      for (int q = 0; q < RT; ++q) red[wave - 1][q][lane] = acc[q];
+    }
+    lds_barrier();
+    if (wave == 0) {
+      const float s = adapter_scale != nullptr ? adapter_scale[ad] : 1.0f;
+#pragma unroll
+      for (int q = 0; q < RT; ++q) {
+        for (int w = 0; w < nw - 1; ++w) acc[q] += red[w][q][lane];
+        const int r = r0 + q * 16 + m;       // lane holds D[4 g + i][m]
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (((mine >> (4 * g + i)) & 1u) && r < a.rank) u[(t0 + 4 * g + i) * a.rank + r] = s * acc[q][i];
+      }
+    }
+    lds_barrier();                           // red is free for the next adapter
+  }
+}
+
+// The projection of at most 32 tokens, a decode batch: the sweep of few_device.hpp over CW
+// column tiles and SK splits of K, and in each wave its share of the adapters' rank (groups of
+// 8, dealt to the splits), both reduced in split order.  Every lane forms its own outputs'
+// adapter terms, so tokens with different adapters cost no more than tokens with one.
+template <int BITS, int ABITS, bool BLK, int DEPTH>
+__global__ void __launch_bounds__(1024)
+few_adapter_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales, GemmW w, int T, int N, int K,
+                   int blocked, AdapterArgs a, float* __restrict__ out, int64_t ldo, int CW, int SK) {
+  extern __shared__ f32x4 red[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cw = wave / SK, sk = wave - cw * SK;
+  const int m = lane & 15, g = lane >> 4;
+  const int n0 = (blockIdx.x * CW + cw) * 16;
+  const int nchunks = (K + 127) >> 7;
+  const int cpw = (nchunks + SK - 1) / SK;
+  const int c0 = sk * cpw, c1 = min(nchunks, c0 + cpw);
+  FewWeights<BITS, 1> W;
+  W.init(&w, 0, n0, N, K, blocked, lane);
+  uint32_t ring[DEPTH][1][BITS];
+#pragma unroll
+  for (int i = 0; i < DEPTH; ++i) W.load(c0 + i, c1, ring[i]);
+  f32x4 acc[1][2], low[1][2];
+  uint32_t aoff[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    acc[0][s] = low[0][s] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    aoff[s] = s * 16 + m < T ? (uint32_t)((s * 16 + m) * ((int64_t)K * ABITS / 8)) + (uint32_t)(g * 4 * ABITS) : kOffNone;
+  }
+  const __amdgpu_buffer_rsrc_t cres = make_rsrc(codes, 0x7FFFFFFFu);
+  if (T > 16) few_sweep<BITS, ABITS, 1, BLK, 2, DEPTH>(W, ring, cres, aoff, c0, c1, acc);
+  else few_sweep<BITS, ABITS, 1, BLK, 1, DEPTH>(W, ring, cres, aoff, c0, c1, acc);
+  if (n0 < N) {
+    const int n = n0 + m;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = s * 16 + 4 * g + i;
+        const int ad = t < T ? a.of[t] : -1;
+        if ((uint32_t)ad >= (uint32_t)a.n_adapters) continue;
+        const uint16_t* b = a.lora_b + ((int64_t)ad * N + n) * a.rank;
+        const float* u = a.u + (int64_t)t * a.rank;
+        for (int r = sk * 8; r < a.rank; r += SK * 8) {
+          const u32x4 bv = *reinterpret_cast<const u32x4*>(b + r);
+          const f32x4 u0 = *reinterpret_cast<const f32x4*>(u + r), u1 = *reinterpret_cast<const f32x4*>(u + r + 4);
+          float d = low[0][s][i];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float lo = __builtin_bit_cast(float, bv[j] << 16), hi = __builtin_bit_cast(float, bv[j] & 0xFFFF0000u);
+            d = __builtin_fmaf(j < 2 ? u0[2 * j] : u1[2 * j - 4], lo, d);
+            d = __builtin_fmaf(j < 2 ? u0[2 * j + 1] : u1[2 * j - 3], hi, d);
+          }
+          low[0][s][i] = d;
+        }
+      }
+    }
+  }
+  const int nsub = T > 16 ? 2 : 1;
+  few_reduce<1>(red, cw, sk, SK, nsub, lane, acc);
+  few_reduce<1>(red + (size_t)(SK - 1) * CW * 2 * 64, cw, sk, SK, nsub, lane, low);
+  if (sk != 0 || n0 >= N) return;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = s * 16 + 4 * g + i;
+      if (t < T) out[t * ldo + n0 + m] = __builtin_fmaf(scales[t], acc[0][s][i], low[0][s][i]);
+    }
+  }
+}
+
+template <int BITS, int ABITS, bool BLK>
+static hipError_t launch_few_adapter(const GemmArgs& a, const AdapterArgs& ad, hipStream_t stream) {
+  const int tiles = a.N / 16, nchunks = (a.K + 127) / 128;
+  int SK = 1;
+  while (SK < 16 && (int64_t)tiles * SK < 2048 && SK * 8 <= nchunks) SK *= 2;
+  const int CW = SK < 4 ? 4 / SK : 1;
+  const dim3 grid((unsigned)((tiles + CW - 1) / CW)), block((unsigned)(64 * CW * SK));
+  const size_t lds = (size_t)(SK - 1) * CW * 2 * 2 * 64 * sizeof(f32x4);
+  hipLaunchKernelGGL((few_adapter_kernel<BITS, ABITS, BLK, 4>), grid, block, lds, stream, a.codes, a.scales, a.w[0],
+                     (int)a.n_rows, a.N, a.K, a.blocked, ad, static_cast<float*>(a.out), a.ldo, CW, SK);
+  return hipGetLastError();
+}
+
+size_t adapter_workspace_bytes(int64_t T, int rank) { return ((size_t)T * rank * sizeof(float) + 255) / 256 * 256; }
+
+hipError_t launch_adapter_gemm(const GemmArgs& a, AdapterArgs ad, const uint16_t* x, int64_t ldx,
+                               const uint16_t* lora_a, const float* adapter_scale, float* u, hipStream_t stream) {
+  ad.u = u;
+  const int64_t T = a.n_rows;
+  const int rt = (ad.rank + 15) / 16;
+  const int RT = rt >= 4 ? 4 : rt >= 2 ? 2 : 1;
+  // a decode batch's tile may hold 16 adapters, one a workgroup; in larger batches, where
+  // requests span tiles, a tile's workgroups take turns
+  const dim3 grid((unsigned)((T + 15) / 16), T <= 256 ? (unsigned)(T < 16 ? T : 16) : 2u, (unsigned)((rt + RT - 1) / RT));
+  if (RT == 4) hipLaunchKernelGGL(adapter_shrink_kernel<4>, grid, dim3(512), 0, stream, ad, x, ldx, lora_a, adapter_scale, T, a.K, u);
+  else if (RT == 2) hipLaunchKernelGGL(adapter_shrink_kernel<2>, grid, dim3(512), 0, stream, ad, x, ldx, lora_a, adapter_scale, T, a.K, u);
+  else hipLaunchKernelGGL(adapter_shrink_kernel<1>, grid, dim3(512), 0, stream, ad, x, ldx, lora_a, adapter_scale, T, a.K, u);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (T > kFewRows) return launch_mfma_prefill_adapter(a, ad, stream);
+  if (a.act_bits == 4) {
+    if (a.bits == 4) return launch_few_adapter<4, 4, false>(a, ad, stream);
+    if (a.bits == 2) return launch_few_adapter<2, 4, false>(a, ad, stream);
+    return a.blocked ? launch_few_adapter<3, 4, true>(a, ad, stream) : launch_few_adapter<3, 4, false>(a, ad, stream);
+  }
+  if (a.bits == 4) return launch_few_adapter<4, 8, false>(a, ad, stream);
+  if (a.bits == 2) return launch_few_adapter<2, 8, false>(a, ad, stream);
+  return a.blocked ? launch_few_adapter<3, 8, true>(a, ad, stream) : launch_few_adapter<3, 8, false>(a, ad, stream);
+}
+
+}  // namespace cbq

@@ -502,6 +502,57 @@ CBQ_EXPORT int cbq_moe_ffn_few(const uint8_t* codes, const float* scales, int32_
   return CBQ_OK;
 }
 
+CBQ_EXPORT size_t cbq_adapter_workspace(int64_t T, int32_t rank) {
+  if (T <= 0 || T > 0x7FFFFFFF || rank < 8 || rank > 128 || rank % 8) return 0;
+  return cbq::adapter_workspace_bytes(T, rank);
+}
+
+CBQ_EXPORT int cbq_codebook_adapter_gemm(const uint8_t* codes, const float* scales, int32_t act_bits,
+                                         int64_t T, const cbq_weights* W, const uint16_t* x,
+                                         int64_t ldx, const uint16_t* lora_a, const uint16_t* lora_b,
+                                         const float* adapter_scale, int32_t n_adapters, int32_t rank,
+                                         const int32_t* adapter_of, float* out, int64_t ldo, void* ws,
+                                         size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  if (!W) return fail(CBQ_EINVAL, "W must be non-null");
+  if (int rc = check_weights(W, 0)) return rc;
+  if (W->E != 1) return fail(CBQ_EINVAL, "the projection takes one weight matrix (E = 1, got %d)", W->E);
+  if (W->K > 16384) return fail(CBQ_EUNSUPPORTED, "K must be <= 16384 (got %d)", W->K);
+  if (act_bits != 4 && act_bits != 8) return fail(CBQ_EINVAL, "act_bits must be 4 or 8 (got %d)", act_bits);
+  if (T < 0) return fail(CBQ_EINVAL, "T must be >= 0 (got %lld)", (long long)T);
+  if (T > 0x7FFFFFFF) return fail(CBQ_EUNSUPPORTED, "T must be < 2^31");
+  if (ldx < W->K || ldx % 8) return fail(CBQ_EINVAL, "ldx must be >= K and a multiple of 8 (got %lld)", (long long)ldx);
+  if (ldo < W->N || ldo % 4) return fail(CBQ_EINVAL, "ldo must be >= N and a multiple of 4 (got %lld)", (long long)ldo);
+  if (n_adapters < 1) return fail(CBQ_EINVAL, "n_adapters must be >= 1 (got %d)", n_adapters);
+  if (rank < 8 || rank > 128 || rank % 8) return fail(CBQ_EINVAL, "rank must be a multiple of 8 in [8, 128] (got %d)", rank);
+  if (T == 0) return CBQ_OK;
+  if (T > (int64_t(1) << 30) / (ldo * 4) || T * ldo * 4 >= (int64_t(1) << 30))
+    return fail(CBQ_EUNSUPPORTED, "output must be smaller than 1 GiB per call (T * ldo * 4 bytes)");
+  if (T * ((int64_t)W->K * act_bits / 8) >= (int64_t(1) << 31)) return fail(CBQ_EUNSUPPORTED, "codes must be smaller than 2 GiB");
+  if ((int64_t)W->N * cbq::index_row_bytes(W->K, W->bits, W->layout == CBQ_LAYOUT_BLOCKED) >= (int64_t(1) << 31))
+    return fail(CBQ_EUNSUPPORTED, "the index block must be smaller than 2 GiB");
+  if (!codes || !scales || !x || !lora_a || !lora_b || !adapter_of || !out)
+    return fail(CBQ_EINVAL, "codes, scales, x, lora_a, lora_b, adapter_of and out must be non-null");
+  if (!aligned16(codes) || !aligned16(x) || !aligned16(lora_a) || !aligned16(lora_b) || !aligned16(out))
+    return fail(CBQ_EINVAL, "codes, x, lora_a, lora_b and out must be 16-byte aligned");
+  const size_t need = cbq::adapter_workspace_bytes(T, rank);
+  if (!ws || ws_bytes < need)
+    return fail(CBQ_EWORKSPACE, "workspace of %zu bytes required (got %zu)", need, ws ? ws_bytes : (size_t)0);
+  if (!aligned16(ws)) return fail(CBQ_EINVAL, "ws must be 16-byte aligned");
+  cbq::GemmArgs a{};
+  a.codes = codes; a.scales = scales; a.act_bits = act_bits; a.n_rows = T;
+  a.w[0] = a.w[1] = cbq::GemmW{W->idx, W->codebook};
+  a.n_w = 1; a.E = 1; a.N = W->N; a.K = W->K; a.bits = W->bits;
+  a.blocked = W->layout == CBQ_LAYOUT_BLOCKED;
+  a.out = out; a.ldo = ldo;
+  cbq::AdapterArgs ad{};
+  ad.of = adapter_of; ad.n_adapters = n_adapters; ad.rank = rank; ad.lora_b = lora_b;
+  hipError_t e = cbq::launch_adapter_gemm(a, ad, x, ldx, lora_a, adapter_scale, static_cast<float*>(ws),
+                                          (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "codebook_adapter_gemm launch");
+  return CBQ_OK;
+}
+
 CBQ_EXPORT int cbq_moe_combine(const float* expert_out, const int32_t* slot_of, const float* topk_w,
                                int64_t T, int32_t topk, int32_t H, int32_t n_shared, float* y,
                                void* stream) {

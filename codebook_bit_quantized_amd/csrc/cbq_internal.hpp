@@ -104,6 +104,21 @@ struct MoeFewArgs {
 size_t moe_few_workspace_bytes(int64_t T, int topk, int n_shared, int H, int F, int act_bits);
 hipError_t launch_moe_few(const MoeFewArgs& m, hipStream_t stream);
 
+// Low-rank adapters beside a projection (adapter_gemm.hip): what the projection's epilogue
+// reads.  Token t of adapter a = of[t] (none outside [0, n_adapters)) adds
+// sum_r u[t][r] lora_b[a][n][r] to column n.
+struct AdapterArgs {
+  const int32_t* of;          // [T]
+  int n_adapters, rank;       // rank: a multiple of 8
+  const uint16_t* lora_b;     // bf16 [n_adapters][N][rank]
+  const float* u;             // fp32 [T][rank]
+};
+size_t adapter_workspace_bytes(int64_t T, int rank);
+hipError_t launch_adapter_gemm(const GemmArgs& a, AdapterArgs ad, const uint16_t* x, int64_t ldx,
+                               const uint16_t* lora_a, const float* adapter_scale, float* u, hipStream_t stream);
+// The MFMA path with the adapters in its epilogue: one weight set, dense rows.
+hipError_t launch_mfma_prefill_adapter(const GemmArgs& a, const AdapterArgs& ad, hipStream_t stream);
+
 // Compute units of the current device (cached per device after the first query).
 hipError_t device_cu_count(int* out);
 

@@ -41,6 +41,7 @@ constexpr int XG = 4;       // consecutive M-tiles kept on one XCD
 static_assert(XG == 1 || XG == 2 || XG == 4, "the kernel counts the padding of runs of 2 and 4 only");
 constexpr int BK = 64;      // channels per step
 constexpr int LDW = BK + 8; // fp16 per LDS row (padding staggers the banks)
+struct NoAdapter {};
 
 }  // namespace
 
@@ -67,11 +68,75 @@ struct TileCtx {
   uint32_t poff[2];
 };
 
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// Low-rank adapters beside a dense projection: each tile row's adapter (-1: none), the tile's
+// first row and the projection's columns.  Empty without them.
+template <bool ADP> struct TileAdapters {};
+template <> struct TileAdapters<true> {
+  AdapterArgs ad;
+  const int32_t* s_of;
+  int64_t m0;
+  int N;
+};
+
+// The adapter terms of the 32 rows from tile row `mrow` on, at this lane's column n (valid:
+// n < N): low[v] = sum_r u[row][r] lora_b[a][n][r], in the accumulators' layout.  One pass per
+// distinct adapter among the rows, each taken only by its own rows.  u is split into three
+// bf16 parts (8 bits each, so their sum is u's 24 bits), whose products with lora_b are exact
+// and accumulate in fp32: 3 MFMAs per 16 ranks against K / 16 of the projection.
+__device__ __forceinline__ f32x16 adapter_terms(const AdapterArgs& ad, const int32_t* s_of, int64_t m0, int mrow,
+                                                int nl, int g, int n, bool valid, int N) {
+  f32x16 low;
+#pragma unroll
+  for (int v = 0; v < 16; ++v) low[v] = 0.0f;
+  const int of = s_of[mrow + nl];
+  uint32_t todo = (uint32_t)__ballot(of >= 0);
+  const float* u = ad.u + (m0 + mrow + nl) * ad.rank + 8 * g;
+  while (todo != 0) {
+    const int a = __builtin_amdgcn_readlane(of, __builtin_ctz(todo));
+    const bool row = of == a;
+    const uint32_t mine = (uint32_t)__ballot(row);
+    todo &= ~mine;
+    const uint16_t* lb = ad.lora_b + ((int64_t)a * N + (valid ? n : 0)) * ad.rank + 8 * g;
+    f32x16 d;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) d[v] = 0.0f;
+    for (int r = 0; r < ad.rank; r += 16) {
+      const bool in = r + 8 * g < ad.rank;
+      f32x4 u0 = {0.0f, 0.0f, 0.0f, 0.0f}, u1 = u0;
+      if (in && row) {
+        u0 = *reinterpret_cast<const f32x4*>(u + r);
+        u1 = *reinterpret_cast<const f32x4*>(u + r + 4);
+      }
+      u32x4 bv = {0, 0, 0, 0};
+      if (in && valid) bv = *reinterpret_cast<const u32x4*>(lb + r);
+      const bf16x8 b = __builtin_bit_cast(bf16x8, bv);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        bf16x8 p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[i] = (__bf16)u0[i];
+          p[i + 4] = (__bf16)u1[i];
+          u0[i] -= (float)p[i];
+          u1[i] -= (float)p[i + 4];
+        }
+        d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(p, b, d, 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < 16; ++v) low[v] = ((mine >> (8 * (v / 4) + 4 * g + v % 4)) & 1u) ? d[v] : low[v];
+  }
+  return low;
+}
+
 // NS: 32-column weight slots per wave (2; 1 for a single matrix in 128-column tiles).
-template <int BITS, int ABITS, int NW, int NMS, bool LT, bool BLK, int BM, int NS>
+// ADP: the adapters' terms are added to the scaled sums before they are stored (N: columns).
+template <int BITS, int ABITS, int NW, int NMS, bool LT, bool BLK, int BM, int NS, bool ADP>
 __device__ __forceinline__ void tile_run(const TileCtx<BITS, ABITS, LT>& c, uint16_t (*As)[BM * LDW],
                                          const float* s_scale, const uint32_t* s_rowoff,
-                                         __amdgpu_buffer_rsrc_t ores) {
+                                         __amdgpu_buffer_rsrc_t ores, const TileAdapters<ADP>& ta) {
   const int K = c.K, g = c.g, nl = c.nl, tid = c.tid;
   constexpr int TPR = 256 / BM;            // threads per tile row (1 or 2)
   constexpr int NPA = 8 / TPR;             // activation pieces per thread and step
@@ -231,6 +296,15 @@ __device__ __forceinline__ void tile_run(const TileCtx<BITS, ABITS, LT>& c, uint
   for (int s = 0; s < NS; ++s) coff[s] = c.nvalid[s] ? (uint32_t)c.nrow[s] * ESZ : kOffCol;
 #pragma unroll
   for (int ms = 0; ms < NMS; ++ms) {
+    if constexpr (ADP) {                                 // the rows' outputs, before the stores below
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const f32x16 low = adapter_terms(ta.ad, ta.s_of, ta.m0, ms * 32, nl, g, c.nrow[s], c.nvalid[s], ta.N);
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          acc[ms][s][v] = __builtin_fmaf(acc[ms][s][v], s_scale[ms * 32 + 8 * (v / 4) + 4 * g + v % 4], low[v]);
+      }
+    }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int m0 = ms * 32 + 8 * q + 4 * g;            // rows m0 .. m0+3 of this lane
@@ -268,7 +342,10 @@ __device__ __forceinline__ void tile_run(const TileCtx<BITS, ABITS, LT>& c, uint
         for (int j = 0; j < 4; ++j) {
           const int v = 4 * q + j;
 #pragma unroll
-          for (int s = 0; s < NS; ++s) buf_store_f32(ores, ro[j] + coff[s], acc[ms][s][v] * sc[j]);
+          for (int s = 0; s < NS; ++s) {
+            if constexpr (ADP) buf_store_f32(ores, ro[j] + coff[s], acc[ms][s][v]);
+            else buf_store_f32(ores, ro[j] + coff[s], acc[ms][s][v] * sc[j]);
+          }
         }
       }
     }
@@ -278,13 +355,14 @@ __device__ __forceinline__ void tile_run(const TileCtx<BITS, ABITS, LT>& c, uint
 // BLK: 3-bit indices in the blocked layout's re-encoded units (cbq_prepack_weights).
 // NS: 32-column weight slots per wave (1: a single matrix in 128-column tiles, twice the
 // workgroups and half the accumulators, so two workgroups share each CU at BM = 256 too).
-template <int BITS, int ABITS, int NW, bool LT, bool BLK, int NS, int BM = tile_rows<BITS>()>
+// ADP: with low-rank adapters (one weight set, dense rows).
+template <int BITS, int ABITS, int NW, bool LT, bool BLK, int NS, bool ADP = false, int BM = tile_rows<BITS>()>
 __global__ void __launch_bounds__(256, (BM == 128 || NS == 1) ? 2 : 1)
 mfma_prefill_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales,
                     const int32_t* __restrict__ offsets, const int32_t* __restrict__ row_token,
                     GemmW w0, GemmW w1, int64_t n_rows, int E, int N, int K, int min_rows,
                     int blocked, void* __restrict__ out, int64_t ldo, float* __restrict__ ws,
-                    int tc0) {
+                    int tc0, std::conditional_t<ADP, AdapterArgs, NoAdapter> adp) {
   // K split z of gridDim.z (single matrix): z = 0 writes out, z >= 1 writes its partial
   // sums to ws + (z - 1) * n_rows * N (pitch N); a reduction adds them after.  The gate/up
   // pair with 256-row tiles, tc0 >= 0: column tiles tcol >= tc0 split in two, in calls of at
@@ -302,6 +380,7 @@ mfma_prefill_kernel(const uint8_t* __restrict__ codes, const float* __restrict__
   __shared__ uint32_t s_pad;
   __shared__ uint64_t s_nruns;
   __shared__ int s_e;
+  __shared__ int32_t s_of[ADP ? BM : 1];
 
   const int tid = threadIdx.x;
   // ---- workgroup -> (M-tile, column tile tcol) ----
@@ -474,7 +553,13 @@ mfma_prefill_kernel(const uint8_t* __restrict__ codes, const float* __restrict__
     }
     s_rowoff[tid] = ro;
     s_scale[tid] = sv;
+    if constexpr (ADP) {
+      const int of = tid < rows ? adp.of[m0 + tid] : -1;
+      s_of[tid] = (uint32_t)of < (uint32_t)adp.n_adapters ? of : -1;
+    }
   }
+  TileAdapters<ADP> ta;
+  if constexpr (ADP) ta = TileAdapters<true>{adp, s_of, m0, N};
   if (c.avalid) {
     const int64_t r = r0 + m0 + arow;
     atok = row_token ? (int64_t)row_token[r] : r;
@@ -539,17 +624,17 @@ mfma_prefill_kernel(const uint8_t* __restrict__ codes, const float* __restrict__
     ores = make_rsrc(ws + (int64_t)(split - 1) * n_rows * N, (uint32_t)(n_rows * N * 4));
   }
   switch (nms) {
-    case 1: tile_run<BITS, ABITS, NW, 1, LT, BLK, BM, NS>(c, As, s_scale, s_rowoff, ores); break;
-    case 2: tile_run<BITS, ABITS, NW, 2, LT, BLK, BM, NS>(c, As, s_scale, s_rowoff, ores); break;
-    case 3: tile_run<BITS, ABITS, NW, 3, LT, BLK, BM, NS>(c, As, s_scale, s_rowoff, ores); break;
-    case 4: tile_run<BITS, ABITS, NW, 4, LT, BLK, BM, NS>(c, As, s_scale, s_rowoff, ores); break;
+    case 1: tile_run<BITS, ABITS, NW, 1, LT, BLK, BM, NS, ADP>(c, As, s_scale, s_rowoff, ores, ta); break;
+    case 2: tile_run<BITS, ABITS, NW, 2, LT, BLK, BM, NS, ADP>(c, As, s_scale, s_rowoff, ores, ta); break;
+    case 3: tile_run<BITS, ABITS, NW, 3, LT, BLK, BM, NS, ADP>(c, As, s_scale, s_rowoff, ores, ta); break;
+    case 4: tile_run<BITS, ABITS, NW, 4, LT, BLK, BM, NS, ADP>(c, As, s_scale, s_rowoff, ores, ta); break;
     default:
       if constexpr (BM == 256) {
         switch (nms) {
-          case 5: tile_run<BITS, ABITS, NW, 5, LT, BLK, BM, NS>(c, As, s_scale, s_rowoff, ores); break;
-          case 6: tile_run<BITS, ABITS, NW, 6, LT, BLK, BM, NS>(c, As, s_scale, s_rowoff, ores); break;
-          case 7: tile_run<BITS, ABITS, NW, 7, LT, BLK, BM, NS>(c, As, s_scale, s_rowoff, ores); break;
-          default: tile_run<BITS, ABITS, NW, 8, LT, BLK, BM, NS>(c, As, s_scale, s_rowoff, ores); break;
+          case 5: tile_run<BITS, ABITS, NW, 5, LT, BLK, BM, NS, ADP>(c, As, s_scale, s_rowoff, ores, ta); break;
+          case 6: tile_run<BITS, ABITS, NW, 6, LT, BLK, BM, NS, ADP>(c, As, s_scale, s_rowoff, ores, ta); break;
+          case 7: tile_run<BITS, ABITS, NW, 7, LT, BLK, BM, NS, ADP>(c, As, s_scale, s_rowoff, ores, ta); break;
+          default: tile_run<BITS, ABITS, NW, 8, LT, BLK, BM, NS, ADP>(c, As, s_scale, s_rowoff, ores, ta); break;
         }
       }
       break;
@@ -694,7 +779,7 @@ static hipError_t launch_p2(const GemmArgs& a, int min_rows, hipStream_t stream)
     grid.x += (unsigned)extra;                       // the split column tiles' second halves
     hipLaunchKernelGGL((mfma_prefill_kernel<BITS, ABITS, 2, LT, BLK, 2>), grid, dim3(256), 0, stream,
                        a.codes, a.scales, a.offsets, a.row_token, a.w[0], a.w[1], a.n_rows, E, a.N, a.K,
-                       min_rows, a.blocked, a.out, a.ldo, static_cast<float*>(a.ws), tc0);
+                       min_rows, a.blocked, a.out, a.ldo, static_cast<float*>(a.ws), tc0, NoAdapter{});
     if (extra > 0) {
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
@@ -718,7 +803,7 @@ static hipError_t launch_p2(const GemmArgs& a, int min_rows, hipStream_t stream)
       grid.z = (unsigned)nsplit;
       hipLaunchKernelGGL((mfma_prefill_kernel<BITS, ABITS, 1, LT, BLK, 1>), grid, dim3(256), 0, stream,
                          a.codes, a.scales, a.offsets, a.row_token, a.w[0], a.w[1], a.n_rows, E, a.N, a.K,
-                         min_rows, a.blocked, a.out, a.ldo, static_cast<float*>(a.ws), -1);
+                         min_rows, a.blocked, a.out, a.ldo, static_cast<float*>(a.ws), -1, NoAdapter{});
       if (nsplit > 1) {
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -732,7 +817,7 @@ static hipError_t launch_p2(const GemmArgs& a, int min_rows, hipStream_t stream)
   }
   hipLaunchKernelGGL((mfma_prefill_kernel<BITS, ABITS, 1, LT, BLK, 2>), grid_for(256), dim3(256), 0, stream,
                      a.codes, a.scales, a.offsets, a.row_token, a.w[0], a.w[1], a.n_rows, E, a.N, a.K,
-                     min_rows, a.blocked, a.out, a.ldo, nullptr, -1);
+                     min_rows, a.blocked, a.out, a.ldo, nullptr, -1, NoAdapter{});
   return hipGetLastError();
 }
 
@@ -759,6 +844,41 @@ hipError_t launch_mfma_prefill(const GemmArgs& a, int min_rows, hipStream_t stre
     case 28: return lt ? launch_p<2, 8, true>(a, min_rows, stream) : launch_p<2, 8, false>(a, min_rows, stream);
   }
   return hipErrorInvalidValue;
+}
+
+// The single-matrix kernels with adapters: the tile choice of launch_p2 without its K split.
+template <int BITS, int ABITS, bool BLK>
+static hipError_t launch_adp(const GemmArgs& a, const AdapterArgs& ad, hipStream_t stream) {
+  constexpr int BM = tile_rows<BITS>();
+  const int64_t mt = (a.n_rows + BM - 1) / BM;
+  int64_t G = 1;
+  while (2 * G <= XG && 8 * 2 * G <= mt) G *= 2;
+  const int64_t mtiles = (mt + 8 * G - 1) / (8 * G) * (8 * G);
+  auto grid_for = [&](int ncol) { return dim3((unsigned)((a.N + ncol - 1) / ncol), (unsigned)mtiles); };
+  if constexpr (BM == 256) {
+    if ((int64_t)((a.N + 255) / 256) * mt < 2 * 256) {
+      hipLaunchKernelGGL((mfma_prefill_kernel<BITS, ABITS, 1, false, BLK, 1, true>), grid_for(128), dim3(256), 0, stream,
+                         a.codes, a.scales, nullptr, nullptr, a.w[0], a.w[0], a.n_rows, 1, a.N, a.K, 0, a.blocked,
+                         a.out, a.ldo, nullptr, -1, ad);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((mfma_prefill_kernel<BITS, ABITS, 1, false, BLK, 2, true>), grid_for(256), dim3(256), 0, stream,
+                     a.codes, a.scales, nullptr, nullptr, a.w[0], a.w[0], a.n_rows, 1, a.N, a.K, 0, a.blocked,
+                     a.out, a.ldo, nullptr, -1, ad);
+  return hipGetLastError();
+}
+
+hipError_t launch_mfma_prefill_adapter(const GemmArgs& a, const AdapterArgs& ad, hipStream_t stream) {
+  const bool blk = a.blocked != 0;
+  if (a.act_bits == 4) {
+    if (a.bits == 4) return launch_adp<4, 4, false>(a, ad, stream);
+    if (a.bits == 2) return launch_adp<2, 4, false>(a, ad, stream);
+    return blk ? launch_adp<3, 4, true>(a, ad, stream) : launch_adp<3, 4, false>(a, ad, stream);
+  }
+  if (a.bits == 4) return launch_adp<4, 8, false>(a, ad, stream);
+  if (a.bits == 2) return launch_adp<2, 8, false>(a, ad, stream);
+  return blk ? launch_adp<3, 8, true>(a, ad, stream) : launch_adp<3, 8, false>(a, ad, stream);
 }
 
 }  // namespace cbq

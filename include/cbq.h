@@ -448,6 +448,40 @@ int cbq_moe_ffn_few(const uint8_t* codes, const float* scales, int32_t act_bits,
                     size_t ws_bytes, void* stream);
 
 /*
+ * cbq_codebook_adapter_gemm - a dense codebook projection (cbq_codebook_lut_gemm with E = 1,
+ * CBQ_EPI_F32) with a low-rank adapter per token beside it: many requests, each with its own
+ * adapter or none, share one frozen quantised projection.  Passage: CodeQuant2, Figure 3
+ * (the codebook weights; the adapters stay in full precision beside them).
+ *
+ *  codes, scales : as for cbq_codebook_lut_gemm, row t = token t (T of them).
+ *  W          : one weight set with E = 1.
+ *  x, ldx     : bf16 [T][ldx] (ldx >= K, ldx % 8 == 0, 16-byte aligned): the unquantised,
+ *               unrotated activations, which the adapters read.
+ *  lora_a     : bf16 [n_adapters][rank][K] (16-byte aligned).
+ *  lora_b     : bf16 [n_adapters][N][rank] (16-byte aligned).
+ *  adapter_scale : optional fp32 [n_adapters] (NULL: 1).
+ *  n_adapters : >= 1.  rank: a multiple of 8, 8 <= rank <= 128 (smaller ranks: zero rows).
+ *  adapter_of : int32 [T]: token t's adapter; an entry outside [0, n_adapters) (say -1) means
+ *               none.  Tokens may come in any order.
+ *  out        : fp32 [T][ldo] (ldo >= N, ldo % 4 == 0, 16-byte aligned):
+ *               out[t][n] = scales[t] * sum_k q[t][k] W[n][k]
+ *                           + adapter_scale[a] * sum_r lora_b[a][n][r] * (sum_k lora_a[a][r][k] x[t][k]),
+ *               a = adapter_of[t]; every product exact, sums and the middle vector in fp32.
+ *  ws, ws_bytes : device workspace of cbq_adapter_workspace(T, rank) bytes, 16-byte aligned
+ *               (the middle vectors; rewritten by every call; calls that overlap in time
+ *               need one each).
+ *  A token's result does not depend on other tokens' adapters, non-finite ones included.
+ *  Limits: those of cbq_codebook_lut_gemm, K <= 16384.
+ */
+size_t cbq_adapter_workspace(int64_t T, int32_t rank);
+int cbq_codebook_adapter_gemm(const uint8_t* codes, const float* scales, int32_t act_bits,
+                              int64_t T, const cbq_weights* W, const uint16_t* x, int64_t ldx,
+                              const uint16_t* lora_a, const uint16_t* lora_b,
+                              const float* adapter_scale, int32_t n_adapters, int32_t rank,
+                              const int32_t* adapter_of, float* out, int64_t ldo, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/*
  * cbq_kmeans_codebooks - offline codebook construction, one 1-D K-means per weight row.
  * Passage: CodeQuant2, Figure 3 (right: K-means initialises the centroid matrix and the
  * per-row assignment matrices); CodeQuant abstract (weight outliers absorbed into

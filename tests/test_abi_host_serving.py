@@ -92,3 +92,25 @@ def test_moe_few_workspace_sizes(lib):
     f = lib.cbq_moe_few_workspace
     assert f(0, 2, 0, 128, 96, 4) == 0 and f(33, 2, 0, 128, 96, 4) == 0 and f(1, 9, 0, 128, 96, 4) == 0
     assert f(32, 8, 8, 16384, 16384, 8) >= 32 * 16 * (4 + 1 + 4) * 16384
+
+
+def test_codebook_adapter_gemm_refusals(lib):
+    need = lib.cbq_adapter_workspace(4, 16)
+    assert need >= 4 * 16 * 4 and lib.cbq_adapter_workspace(4, 12) == 0 and lib.cbq_adapter_workspace(0, 16) == 0
+
+    def f(codes=P, scales=P, act_bits=4, T=4, W=_w(E=1), x=P, ldx=128, a=P, b=P, sc=None, n_ad=3, rank=16, of=P, out=P,
+          ldo=96, ws=P, n=need):
+        return lib.cbq_codebook_adapter_gemm(codes, scales, act_bits, T, W, x, ldx, a, b, sc, n_ad, rank, of, out, ldo,
+                                             ws, n, None)
+
+    for bad in (dict(W=None), dict(W=_w(E=2)), dict(W=_w(E=1, K=100)), dict(act_bits=5), dict(T=-1), dict(ldx=120),
+                dict(ldx=130), dict(ldo=92), dict(ldo=98), dict(n_ad=0), dict(rank=0), dict(rank=12), dict(rank=136),
+                dict(codes=None), dict(scales=None), dict(x=None), dict(a=None), dict(b=None), dict(of=None),
+                dict(out=None), dict(codes=U), dict(x=U), dict(a=U), dict(b=U), dict(out=U), dict(ws=U)):
+        assert f(**bad) == cbq.CBQ_EINVAL, bad
+        assert lib.cbq_last_error()
+    assert f(T=1 << 31) == cbq.CBQ_EUNSUPPORTED
+    assert f(T=3 << 20) == cbq.CBQ_EUNSUPPORTED                       # out of 1 GiB or more
+    assert f(W=_w(E=1, K=16416), ldx=16416) == cbq.CBQ_EUNSUPPORTED
+    assert f(ws=None) == cbq.CBQ_EWORKSPACE and f(n=need - 1) == cbq.CBQ_EWORKSPACE
+    assert f(T=0, codes=None, x=None, out=None, ws=None) == cbq.CBQ_OK
