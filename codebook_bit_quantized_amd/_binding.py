@@ -116,6 +116,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     return lib
 
 
+def _opt_ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
 def _check(status: int):
     if status != CBQ_OK:
         lib = load_library()
@@ -139,11 +143,17 @@ def _require_gpu(*ts: Optional[torch.Tensor]):
             raise ValueError("cbq operates on device tensors only")
 
 
+# handle of a device's current stream: torch's own accessor where it has one (the public
+# torch.cuda.current_stream() builds an object, 3 us of a call that takes 15)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _on_stream(dev: torch.device, stream, call):
     """call(stream handle) with `dev` current and what it allocates belonging to the stream it
     launches on: the given one, or dev's current one."""
     if stream is None and dev.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
+        return call(_raw_stream(dev.index))
     st = stream if stream is not None else torch.cuda.current_stream(dev)
     if not hasattr(st, "cuda_stream"):
         st = torch.cuda.ExternalStream(int(st), device=dev)
@@ -155,10 +165,12 @@ def _on_stream(dev: torch.device, stream, call):
 
 def _tensor(name: str, t: Optional[torch.Tensor], dev: torch.device, dtype, shape=None,
             rows: bool = False, contiguous: bool = False):
-    """Checks an argument tensor's place, type, shape and layout; None passes."""
-    if t is None:
+    """Checks an argument tensor's place, type, shape and layout; None passes.  rows: unit
+    stride along the last dimension."""
+    if t is None or (t.dtype is dtype and t.device == dev and (shape is None or t.shape == shape)
+                     and t.is_contiguous()):
         return
-    if t.device != dev or dev.type != "cuda":
+    if t.device != dev:
         raise ValueError(f"{name} must be on the same GPU as the other tensors (got {t.device}, {dev})")
     if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
         raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
@@ -195,14 +207,18 @@ class CodebookWeights:
     def N(self) -> int:
         return self.idx.shape[1]
 
-    def _check(self, dev: torch.device, name: str):
-        """The tensors as the C struct describes them: on dev, packed, of these sizes."""
-        kp = self.K if self.layout == LAYOUT_ROWS else (self.K + 127) // 128 * 128
-        _tensor(name + ".idx", self.idx, dev, torch.uint8, (self.E, self.N, kp * self.bits // 8), contiguous=True)
-        if self.codebook.element_size() != 2:
-            raise ValueError(f"{name}.codebook must hold 16-bit fp16 patterns (got {self.codebook.dtype})")
-        _tensor(name + ".codebook", self.codebook, dev, self.codebook.dtype, (self.E, self.N, 1 << self.bits),
-                contiguous=True)
+    def _c_checked(self, dev: torch.device, name: str) -> cbq_weights:
+        """c_struct() of tensors that are as it describes them: on dev, packed, of these sizes."""
+        idx, cb, K, bits = self.idx, self.codebook, self.K, self.bits
+        kp = K if self.layout == LAYOUT_ROWS else (K + 127) // 128 * 128
+        if idx.dim() != 3:
+            raise ValueError(f"{name}.idx must have three dimensions (got shape {tuple(idx.shape)})")
+        E, N, _ = idx.shape
+        _tensor(name + ".idx", idx, dev, torch.uint8, (E, N, kp * bits // 8), contiguous=True)
+        if cb.element_size() != 2:
+            raise ValueError(f"{name}.codebook must hold 16-bit fp16 patterns (got {cb.dtype})")
+        _tensor(name + ".codebook", cb, dev, cb.dtype, (E, N, 1 << bits), contiguous=True)
+        return cbq_weights(idx.data_ptr(), cb.data_ptr(), E, N, K, bits, self.layout)
 
     def c_struct(self) -> cbq_weights:
         return cbq_weights(self.idx.data_ptr(), self.codebook.data_ptr(), self.E, self.N, self.K,
@@ -393,19 +409,26 @@ def moe_combine(expert_out: torch.Tensor, slot_of: torch.Tensor, topk_w: torch.T
     return y
 
 
-def _norm_outputs(T: int, K: int, dev, act_bits: int, normed, codes, scales, want_normed: bool = True):
+def _like_rows(x: torch.Tensor) -> torch.Tensor:
+    """A contiguous bf16 tensor of x's shape."""
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
+def _norm_outputs(x: torch.Tensor, act_bits: int, normed, codes, scales, want_normed: bool = True):
     if normed is None and want_normed:
-        normed = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
+        normed = _like_rows(x)
+    T, K = x.shape
+    dev = x.device
     if act_bits:
         if codes is None:
             codes = torch.empty((T, K * act_bits // 8), dtype=torch.uint8, device=dev)
         if scales is None:
-            scales = torch.empty((T,), dtype=torch.float32, device=dev)
+            scales = torch.empty(T, dtype=torch.float32, device=dev)
     return normed, codes, scales
 
 
 def _norm_struct(weight, eps, had_block, act_bits, normed, codes, scales) -> cbq_norm:
-    return cbq_norm(weight.data_ptr(), eps, had_block, act_bits, None if normed is None else normed.data_ptr(),
+    return cbq_norm(weight.data_ptr(), eps, had_block, act_bits, _opt_ptr(normed),
                     0 if normed is None else _row_stride(normed), codes.data_ptr() if act_bits else None,
                     scales.data_ptr() if act_bits else None)
 
@@ -432,7 +455,7 @@ def norm_rotate_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-
     _check_norm_args(T, K, dev, weight, act_bits, normed, codes, scales)
 
     def call(st):
-        n, c, s = _norm_outputs(T, K, dev, act_bits, normed, codes, scales, want_normed)
+        n, c, s = _norm_outputs(x, act_bits, normed, codes, scales, want_normed)
         nrm = _norm_struct(weight, eps, had_block, act_bits, n, c, s)
         _check(lib.cbq_norm_rotate_quantize(x.data_ptr(), T, K, _row_stride(x), ctypes.byref(nrm), st))
         return (n, c, s) if act_bits else (n, None, None)
@@ -479,14 +502,14 @@ def combine_norm_residual(rows: torch.Tensor, residual: torch.Tensor, slot_of: O
         _check_norm_args(T, H, dev, next_weight, act_bits, normed, codes, scales)
 
     def call(st):
-        o = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if out is None else out
+        o = _like_rows(residual) if out is None else out
         nrm = None
         if next_weight is not None:
-            n, c, s = _norm_outputs(T, H, dev, act_bits, normed, codes, scales)
+            n, c, s = _norm_outputs(residual, act_bits, normed, codes, scales)
             nrm = ctypes.byref(_norm_struct(next_weight, eps, had_block, act_bits, n, c, s))
         _check(lib.cbq_combine_norm_residual(
-            rows.data_ptr(), TYPE_F32 if rows.dtype == torch.float32 else TYPE_BF16, _row_stride(rows), _ptr(slot_of),
-            _ptr(topk_w), T, topk, n_shared, H, _ptr(post_weight), eps, _ptr(gate), ldg, scale, residual.data_ptr(),
+            rows.data_ptr(), TYPE_F32 if rows.dtype == torch.float32 else TYPE_BF16, _row_stride(rows), _opt_ptr(slot_of),
+            _opt_ptr(topk_w), T, topk, n_shared, H, _opt_ptr(post_weight), eps, _opt_ptr(gate), ldg, scale, residual.data_ptr(),
             _row_stride(residual), o.data_ptr(), _row_stride(o), nrm, st))
         if next_weight is None:
             return o
@@ -518,8 +541,7 @@ def moe_ffn_few(codes: torch.Tensor, scales: torch.Tensor, logits: torch.Tensor,
     _tensor("codes", codes, dev, torch.uint8, (T, H * act_bits // 8), contiguous=True)
     _tensor("scales", scales, dev, torch.float32, (T,), contiguous=True)
     _tensor("logits", logits, dev, torch.float32, contiguous=True)
-    for name, w in (("gate", gate), ("up", up), ("down", down)):
-        w._check(dev, name)
+    g, u, d = gate._c_checked(dev, "gate"), up._c_checked(dev, "up"), down._c_checked(dev, "down")
     if y is not None:
         y_dtype = y.dtype
     if y_dtype not in (torch.float32, torch.bfloat16):
@@ -532,8 +554,8 @@ def moe_ffn_few(codes: torch.Tensor, scales: torch.Tensor, logits: torch.Tensor,
         w = ws if ws is not None else torch.empty((moe_few_workspace(T, topk, n_shared, H, F, act_bits),),
                                                   dtype=torch.uint8, device=dev)
         _check(lib.cbq_moe_ffn_few(codes.data_ptr(), scales.data_ptr(), act_bits, logits.data_ptr(), T, E, topk,
-                                   int(bool(renormalize)), n_shared, ctypes.byref(gate.c_struct()),
-                                   ctypes.byref(up.c_struct()), ctypes.byref(down.c_struct()), o.data_ptr(),
+                                   int(bool(renormalize)), n_shared, ctypes.byref(g), ctypes.byref(u),
+                                   ctypes.byref(d), o.data_ptr(),
                                    TYPE_F32 if y_dtype == torch.float32 else TYPE_BF16, _row_stride(o), w.data_ptr(),
                                    w.numel(), st))
         return o
@@ -564,7 +586,7 @@ def codebook_adapter_gemm(codes: torch.Tensor, scales: torch.Tensor, act_bits: i
     n_ad, rank = lora_a.shape[0], lora_a.shape[1]
     _tensor("codes", codes, dev, torch.uint8, (T, K * act_bits // 8), contiguous=True)
     _tensor("scales", scales, dev, torch.float32, (T,), contiguous=True)
-    weights._check(dev, "weights")
+    W = weights._c_checked(dev, "weights")
     _tensor("x", x, dev, torch.bfloat16, (T, K), rows=True)
     _tensor("lora_a", lora_a, dev, torch.bfloat16, (n_ad, rank, K), contiguous=True)
     _tensor("lora_b", lora_b, dev, torch.bfloat16, (n_ad, N, rank), contiguous=True)
@@ -577,8 +599,8 @@ def codebook_adapter_gemm(codes: torch.Tensor, scales: torch.Tensor, act_bits: i
         o = torch.empty((T, N), dtype=torch.float32, device=dev) if out is None else out
         w = ws if ws is not None else torch.empty((adapter_workspace(T, rank),), dtype=torch.uint8, device=dev)
         _check(lib.cbq_codebook_adapter_gemm(
-            codes.data_ptr(), scales.data_ptr(), act_bits, T, ctypes.byref(weights.c_struct()), x.data_ptr(),
-            _row_stride(x), lora_a.data_ptr(), lora_b.data_ptr(), _ptr(adapter_scale), n_ad, rank,
+            codes.data_ptr(), scales.data_ptr(), act_bits, T, ctypes.byref(W), x.data_ptr(),
+            _row_stride(x), lora_a.data_ptr(), lora_b.data_ptr(), _opt_ptr(adapter_scale), n_ad, rank,
             adapter_of.data_ptr(), o.data_ptr(), _row_stride(o), w.data_ptr(), w.numel(), st))
         return o
 

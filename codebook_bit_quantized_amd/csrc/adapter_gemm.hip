@@ -105,15 +105,15 @@ few_adapter_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ 
   const int cpw = (nchunks + SK - 1) / SK;
   const int c0 = sk * cpw, c1 = min(nchunks, c0 + cpw);
   FewWeights<BITS, 1> W;
-  W.init(&w, 0, n0, N, K, blocked, lane);
+  W.init(&w, false, 0, n0, N, K, blocked, lane);
   uint32_t ring[DEPTH][1][BITS];
 #pragma unroll
   for (int i = 0; i < DEPTH; ++i) W.load(c0 + i, c1, ring[i]);
-  f32x4 acc[1][2], low[1][2];
+  f32x4 acc[1][2], low[2];
   uint32_t aoff[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    acc[0][s] = low[0][s] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    acc[0][s] = low[s] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     aoff[s] = s * 16 + m < T ? (uint32_t)((s * 16 + m) * ((int64_t)K * ABITS / 8)) + (uint32_t)(g * 4 * ABITS) : kOffNone;
   }
   const __amdgpu_buffer_rsrc_t cres = make_rsrc(codes, 0x7FFFFFFFu);
@@ -133,28 +133,27 @@ few_adapter_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ 
         for (int r = sk * 8; r < a.rank; r += SK * 8) {
           const u32x4 bv = *reinterpret_cast<const u32x4*>(b + r);
           const f32x4 u0 = *reinterpret_cast<const f32x4*>(u + r), u1 = *reinterpret_cast<const f32x4*>(u + r + 4);
-          float d = low[0][s][i];
+          float d = low[s][i];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float lo = __builtin_bit_cast(float, bv[j] << 16), hi = __builtin_bit_cast(float, bv[j] & 0xFFFF0000u);
             d = __builtin_fmaf(j < 2 ? u0[2 * j] : u1[2 * j - 4], lo, d);
             d = __builtin_fmaf(j < 2 ? u0[2 * j + 1] : u1[2 * j - 3], hi, d);
           }
-          low[0][s][i] = d;
+          low[s][i] = d;
         }
       }
     }
   }
-  const int nsub = T > 16 ? 2 : 1;
-  few_reduce<1>(red, cw, sk, SK, nsub, lane, acc);
-  few_reduce<1>(red + (size_t)(SK - 1) * CW * 2 * 64, cw, sk, SK, nsub, lane, low);
+  f32x4 sums[4] = {acc[0][0], low[0], acc[0][1], low[1]};
+  few_reduce<4>(red, cw, sk, SK, lane, sums);
   if (sk != 0 || n0 >= N) return;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = s * 16 + 4 * g + i;
-      if (t < T) out[t * ldo + n0 + m] = __builtin_fmaf(scales[t], acc[0][s][i], low[0][s][i]);
+      if (t < T) out[t * ldo + n0 + m] = __builtin_fmaf(scales[t], sums[2 * s][i], sums[2 * s + 1][i]);
     }
   }
 }

@@ -449,7 +449,7 @@ CBQ_EXPORT size_t cbq_moe_few_workspace(int64_t T, int32_t topk, int32_t n_share
   if (T <= 0 || T > CBQ_FEW_MAX_TOKENS || topk < 1 || topk > 8 || n_shared < 0 || n_shared > 8 || H < 32 ||
       H > 16384 || F < 32 || F > 16384 || (act_bits != 4 && act_bits != 8))
     return 0;
-  return cbq::moe_few_workspace_bytes(T, topk, n_shared, H, F, act_bits);
+  return cbq::moe_few_workspace_bytes(T, topk, n_shared, H, F);
 }
 
 CBQ_EXPORT int cbq_moe_ffn_few(const uint8_t* codes, const float* scales, int32_t act_bits,
@@ -485,7 +485,7 @@ CBQ_EXPORT int cbq_moe_ffn_few(const uint8_t* codes, const float* scales, int32_
   if (T == 0) return CBQ_OK;
   if (!codes || !scales || !logits || !y) return fail(CBQ_EINVAL, "codes, scales, logits and y must be non-null");
   if (!aligned16(codes) || !aligned16(y)) return fail(CBQ_EINVAL, "codes and y must be 16-byte aligned");
-  const size_t need = cbq::moe_few_workspace_bytes(T, topk, n_shared, H, F, act_bits);
+  const size_t need = cbq::moe_few_workspace_bytes(T, topk, n_shared, H, F);
   if (!ws || ws_bytes < need)
     return fail(CBQ_EWORKSPACE, "workspace of %zu bytes required (got %zu)", need, ws ? ws_bytes : (size_t)0);
   if (!aligned16(ws)) return fail(CBQ_EINVAL, "ws must be 16-byte aligned");

@@ -46,7 +46,7 @@ hipError_t launch_rotate_quantize(const uint16_t* x, int64_t T, int K, int64_t l
 
 // Norms around a block (norm_quantize.hip).  Pointers may be null where the comment says so.
 // What is normed: x, or combined rows of that type; or fp32 rows rotated and quantised as they
-// are (no norm).
+// are (no norm; codes then gets the few-row GEMM's fp16 codes, few_device.hpp).
 enum { kNormX = 0, kNormF32 = 1, kNormBF16 = 2, kRotateF32 = 3 };
 struct NormArgs {
   const uint16_t* x;          // bf16 [T][ldx]: the row, or the residual stream beside rows
@@ -81,13 +81,24 @@ hipError_t launch_norm_quantize(NormArgs a, int src, int b, hipStream_t stream);
 // The few-token MoE layer (moe_few.hip).  FewArgs: one of its grouped GEMMs.
 struct FewArgs {
   const float* logits;        // [T][E]
-  int32_t* ids;               // [T][topk]: written by the gate/up kernel, read by the down kernel
+  int32_t* ids;               // [T][topk]
   int T, E, topk, n_shared;
   const uint8_t* codes;       // code rows: tokens (gate/up) or choices (down)
   const float* scales;
   GemmW w[2];
   int N, K, blocked;
   float* out;                 // fp32 [T*topk + n_shared*T][N]
+};
+struct FewDownArgs {
+  const float* h;             // fp32 [topk + n_shared][F]
+  const int32_t* ids;         // [topk]
+  const float* logits;        // [E]
+  int E, topk, n_shared, renormalize, act_bits, H, F;
+  GemmW w;
+  int blocked;
+  float c_b;                  // 1 / sqrt(rotation block)
+  void* y;                    // [H]
+  int y_bf16;
 };
 struct MoeFewArgs {
   const uint8_t* codes;
@@ -101,7 +112,7 @@ struct MoeFewArgs {
   int y_bf16;
   void* ws;
 };
-size_t moe_few_workspace_bytes(int64_t T, int topk, int n_shared, int H, int F, int act_bits);
+size_t moe_few_workspace_bytes(int64_t T, int topk, int n_shared, int H, int F);
 hipError_t launch_moe_few(const MoeFewArgs& m, hipStream_t stream);
 
 // Low-rank adapters beside a projection (adapter_gemm.hip): what the projection's epilogue

@@ -4,22 +4,36 @@
 // CodeQuant2, Figures 3 and 4 (codebook weights looked up in on-chip tables); the AI Radio
 // episode, introduction (a router in front of the experts).
 //
-// At one to 32 tokens the layer is a few launches that each read weights once, and what it
-// costs beyond those bytes is launches and dependent loads.  So there is no routing kernel and
-// there are no row lists in memory: every workgroup of the gate/up kernel finds the rows of its
-// expert from the logits (the rank of expert e in a token's logits is the number of experts
-// ahead of it), and rows are numbered by choice (row t * topk + j is token t's j-th choice,
-// row T * topk + s * T + t shared expert s), which needs no counting.  Kernels:
-//   1. gate/up: h = silu(g) * u in fp32, and the chosen ids;
-//   2. rotation and quantisation of h's rows (norm_quantize.hip, without the norm);
-//   3. down: the rows of its expert found from the ids;
-//   4. the weighted sum of each token's rows, with the softmax weights from the logits.
+// What the layer costs beyond the bytes of its weights is launches, dependent loads and, at
+// 4 bits, the vector instructions of the table lookups.  Rows are numbered by choice (row
+// t * topk + j is token t's j-th choice, row T * topk + s * T + t shared expert s), which
+// needs no counting and no row lists in memory: a workgroup finds its expert's rows by
+// scanning the chosen ids.  Two forms:
+//
+// A batch:
+//   1. per token: the chosen ids and weights, and the input codes converted to fp16 once (per
+//      wave and chunk the conversion is 44 of about 230 vector instructions of a gate/up pair,
+//      and of 140 of a single matrix);
+//   2. gate/up: h = silu(g) * u in fp32;
+//   3. rotation and quantisation of h's rows, codes left in fp16 (norm_quantize.hip);
+//   4. down: the expert rows;
+//   5. the weighted sum of each token's rows.
+// One token with F <= 2048, where launches and dependent loads are most of it:
+//   1. gate/up whose waves find their choice's expert from the logits themselves;
+//   2. one kernel for the rest: every workgroup rotates and quantises all rows of h (a few
+//      thousand values), a wave a row, multiplies its 16 columns of down and combines them.
+// These two run every instruction a few times only, so instruction fetches count: their loops
+// stay rolled where the unrolled code would run once.
 // h is kept in fp32 up to the quantiser: the codes are those of the unrounded h up to fp32
 // sums (a bf16 h would move a code wherever its rounding crosses a border).
 #include "cbq_internal.hpp"
 #include "few_device.hpp"
+#include "rotate_device.hpp"
 #include "route_device.hpp"
 
+#ifndef FEW_OCC
+#define FEW_OCC 5
+#endif
 namespace cbq {
 
 namespace {
@@ -38,18 +52,96 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   return max(max(a, b), max(c, d));
 }
 
-// the expert of rank j in a token's logits (ties to the lower id); whole waves only
+// the expert of rank j in a token's logits (ties to the lower id): j + 1 rounds of a wave
+// maximum; whole waves only.  NI: 64-expert groups (E <= 64 * NI)
+template <int NI>
 __device__ __forceinline__ int expert_of_rank(const float* row, int E, int j, int lane) {
-  uint32_t key[4];
+  uint32_t key[NI];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < NI; ++i) {
     const int e = lane + 64 * i;
     key[i] = e < E ? order_bits(row[e]) : 0u;
   }
   int e = 0;
+#pragma unroll 1
   for (int r = 0; r <= j; ++r) {
-    const uint32_t m = wave_max_u32(max(max(key[0], key[1]), max(key[2], key[3])));
+    uint32_t m = key[0];
+#pragma unroll
+    for (int i = 1; i < NI; ++i) m = max(m, key[i]);
+    m = wave_max_u32(m);
     e = 0;
+#pragma unroll
+    for (int i = NI - 1; i >= 0; --i) {
+      const uint64_t at = __ballot(key[i] == m);
+      if (at) e = 64 * i + __builtin_ctzll(at);
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      if (lane + 64 * i == e) key[i] = 0u;
+  }
+  return e;
+}
+
+// the softmax weight of a choice: lane j < topk holds the j-th chosen logit; lg: the token's
+// logits.  Whole waves only.
+__device__ __forceinline__ float choice_weight(float l, const float* lg, int E, int topk, int renormalize, int lane) {
+  const float top = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, l), 0));
+  const float ex = lane < topk ? expf(l - top) : 0.0f;
+  float den = ex;
+  if (!renormalize) {
+    den = 0.0f;
+    for (int i = 0; i < 4; ++i)
+      if (lane + 64 * i < E) den += expf(lg[lane + 64 * i] - top);
+  }
+  den += xor_lane_f32<1>(den);
+  den += xor_lane_f32<2>(den);
+  den += xor_lane_f32<4>(den);
+  den += xor_lane_f32<8>(den);
+  den += xor_lane_f32<16>(den);
+  den += xor_lane_f32<32>(den);
+  return ex / den;
+}
+
+}  // namespace
+
+// One workgroup per token: wave 0 ranks the logits by topk rounds of a wave maximum (ties to
+// the lower id) and forms the weights; the workgroup converts the token's codes.
+template <int ABITS>
+__global__ void __launch_bounds__(256)
+few_prepare_kernel(const float* __restrict__ logits, int T, int E, int topk, int renormalize,
+                   const uint8_t* __restrict__ codes, int K, int32_t* __restrict__ ids, float* __restrict__ wts,
+                   uint8_t* __restrict__ codes16) {
+  const int t = blockIdx.x, lane = threadIdx.x & 63;
+  const int64_t pitch = few_row16_bytes(K);
+  for (int p = threadIdx.x; p < (int)(pitch / 64); p += 256) {   // 32 channels each
+    uint32_t raw[ABITS] = {}, d[16];
+    if (32 * p < K) {
+      const u32x4* src = reinterpret_cast<const u32x4*>(codes + (int64_t)t * (K * ABITS / 8) + p * 4 * ABITS);
+#pragma unroll
+      for (int h = 0; h < ABITS / 4; ++h) {
+        const u32x4 v = src[h];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw[4 * h + i] = v[i];
+      }
+    }
+    codes32_to_f16<ABITS>(raw, d);           // zero codes past K
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<u32x4*>(codes16 + t * pitch + few_pos16(32 * p + 8 * j)) =
+          u32x4{d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]};
+  }
+  if (threadIdx.x >= 64) return;
+  const float* lg = logits + (int64_t)t * E;
+  uint32_t key[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = lane + 64 * i;
+    key[i] = e < E ? order_bits(lg[e]) : 0u;
+  }
+  int mine = 0;
+  for (int r = 0; r < topk; ++r) {
+    const uint32_t m = wave_max_u32(max(max(key[0], key[1]), max(key[2], key[3])));
+    int e = 0;
 #pragma unroll
     for (int i = 3; i >= 0; --i) {
       const uint64_t at = __ballot(key[i] == m);
@@ -58,76 +150,44 @@ __device__ __forceinline__ int expert_of_rank(const float* row, int E, int j, in
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (lane + 64 * i == e) key[i] = 0u;
+    if (lane == r) mine = e;
   }
-  return e;
-}
-
-// the rank of expert e in a token's logits; whole waves only
-__device__ __forceinline__ int rank_of_expert(const float* row, int E, int e, int lane) {
-  const uint32_t ke = order_bits(row[e]);
-  int n = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int o = lane + 64 * i;
-    bool ahead = false;
-    if (o < E) {
-      const uint32_t k = order_bits(row[o]);
-      ahead = k > ke || (k == ke && o < e);
-    }
-    n += __popcll(__ballot(ahead));
+  const float w = choice_weight(lg[mine], lg, E, topk, renormalize, lane);
+  if (lane < topk) {
+    ids[t * topk + lane] = mine;
+    wts[t * topk + lane] = w;
   }
-  return n;
 }
-
-}  // namespace
 
 // Rows of this workgroup's expert, in LDS: code row and output row of each.
 struct FewRows {
-  int n, e;
+  int n;
   int16_t code[kFewRows], out[kFewRows];
-  int16_t rank[kFewRows];
 };
 
-// PAIR: the gate/up kernel (rows from the logits; writes h and ids), else the down kernel
-// (rows from the ids; writes the expert rows).  Workgroups of CW * SK waves: CW column tiles
-// of 16 weight rows, each with K split over SK waves.
-template <int BITS, int ABITS, bool PAIR, bool BLK, int DEPTH>
-__global__ void __launch_bounds__(PAIR ? 512 : 1024)
+// h = silu(g) * u with the accurate exponential and division: its error moves codes of h
+__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// A batch's grouped GEMM on fp16 codes.  PAIR: gate/up (code rows are tokens, 16 columns of
+// both matrices a wave); else down (code rows are choices, 32 columns a wave, so a wave always
+// dequantises two sets of 16 weight rows for each piece of codes it loads).  Workgroups of
+// CW * SK waves: CW column tiles, each with K split over SK waves.  blockIdx.y: an expert, or,
+// when there are fewer choices than experts, a choice (the first one of its expert does the
+// work).  An expert of more than 16 rows sweeps its weights twice.
+template <int BITS, bool PAIR, bool BLK, int DEPTH>
+__global__ void __launch_bounds__(512, FEW_OCC)
 few_gemm_kernel(FewArgs a, int CW, int SK) {
-  constexpr int NW = PAIR ? 2 : 1;
   extern __shared__ f32x4 red[];
   __shared__ FewRows s_rows;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nwaves = CW * SK;
   const int cw = wave / SK, sk = wave - cw * SK;
   const int T = a.T, E = a.E, topk = a.topk;
   // shared experts, which every token visits, come last in y and are started first
   const int y = (int)(gridDim.y - 1 - blockIdx.y);
   const int routed = (int)gridDim.y - a.n_shared;
-  const bool by_choice = routed < E;         // one y per choice (t, j) instead of one per expert
-  const bool shared = y >= routed;
-
-  int e = shared ? E + y - routed : y;
-  if (by_choice && !shared) {
-    if constexpr (PAIR) {
-      e = expert_of_rank(a.logits + (int64_t)(y / topk) * E, E, y % topk, lane);
-    } else {
-      e = a.ids[y];
-      if ((uint32_t)e >= (uint32_t)E) return;       // only where logits were not numbers
-    }
-  }
-  const int n0 = (blockIdx.x * CW + cw) * 16;
-  const int nchunks = (a.K + 127) >> 7;
-  const int cpw = (nchunks + SK - 1) / SK;
-  const int c0 = sk * cpw, c1 = min(nchunks, c0 + cpw);
-  FewWeights<BITS, NW> W;
-  W.init(a.w, e, n0, a.N, a.K, a.blocked, lane);
-  uint32_t ring[DEPTH][NW][BITS];
-#pragma unroll
-  for (int i = 0; i < DEPTH; ++i) W.load(c0 + i, c1, ring[i]);
-
-  // ---- the expert's rows ----
+  const bool by_choice = routed < E, shared = y >= routed;
+  const int e = shared ? E + y - routed : by_choice ? a.ids[y] : y;
   if (shared) {
     if (threadIdx.x < T) {
       const int row = T * topk + (y - routed) * T + threadIdx.x;
@@ -135,107 +195,269 @@ few_gemm_kernel(FewArgs a, int CW, int SK) {
       s_rows.out[threadIdx.x] = (int16_t)row;
     }
     if (threadIdx.x == 0) s_rows.n = T;
-  } else if constexpr (PAIR) {
-    for (int t = wave; t < T; t += nwaves) {
-      const int r = T == 1 && by_choice ? y : rank_of_expert(a.logits + (int64_t)t * E, E, e, lane);
-      if (lane == 0) s_rows.rank[t] = (int16_t)(r < topk ? r : -1);
-    }
-    lds_barrier();
-    if (wave == 0) {
-      const int r = lane < T ? s_rows.rank[lane] : -1;
-      const uint64_t mine = __ballot(r >= 0);
-      if (r >= 0) {
-        const int p = __popcll(mine & ((1ull << lane) - 1));
-        s_rows.code[p] = (int16_t)lane;
-        s_rows.out[p] = (int16_t)(lane * topk + r);
-        if (blockIdx.x == 0) a.ids[lane * topk + r] = e;
+  } else if (wave == 0) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {            // T * topk <= 256
+      const int p = 64 * i + lane;
+      const bool is = p < T * topk && a.ids[p] == e;
+      const uint64_t at = __ballot(is);
+      const int pos = n + __popcll(at & ((1ull << lane) - 1));
+      if (is && pos < kFewRows) {
+        s_rows.code[pos] = (int16_t)(PAIR ? p / topk : p);
+        s_rows.out[pos] = (int16_t)p;
       }
-      // by choice, the first token that chose the expert works for all of them
-      if (lane == 0) s_rows.n = by_choice && mine && __builtin_ctzll(mine) != y / topk ? 0 : __popcll(mine);
+      n += __popcll(at);
     }
-  } else {
-    if (wave == 0) {
-      int n = 0;
-      for (int base = 0; base < T * topk; base += 64) {
-        const int p = base + lane;
-        const bool is = p < T * topk && a.ids[p] == e;
-        const uint64_t mine = __ballot(is);
-        const int at = n + __popcll(mine & ((1ull << lane) - 1));
-        if (is && at < kFewRows) {
-          s_rows.code[at] = (int16_t)p;
-          s_rows.out[at] = (int16_t)p;
-        }
-        n += __popcll(mine);
-      }
-      if (lane == 0) s_rows.n = min(n, kFewRows);
-    }
-    lds_barrier();
-    if (by_choice && s_rows.n > 0 && s_rows.out[0] != y) return;   // an earlier choice works for it
+    if (lane == 0) s_rows.n = min(n, kFewRows);
   }
+  const int n0 = (blockIdx.x * CW + cw) * (PAIR ? 16 : 32);
+  const int nchunks = (a.K + 127) >> 7;
+  const int cpw = (nchunks + SK - 1) / SK;
+  const int c0 = sk * cpw, c1 = min(nchunks, c0 + cpw);
+  FewWeights<BITS, 2> W;
+  W.init(a.w, !PAIR, (uint32_t)e < (uint32_t)(E + a.n_shared) ? e : 0, n0, a.N, a.K, a.blocked, lane);
+  uint32_t ring[DEPTH][2][BITS];
+#pragma unroll
+  for (int i = 0; i < DEPTH; ++i) W.load(c0 + i, c1, ring[i]);
   lds_barrier();
   const int me = s_rows.n;
-  if (me == 0) return;
+  if (me == 0 || (by_choice && !shared && s_rows.out[0] != y)) return;
 
-  // ---- the products ----
-  f32x4 acc[NW][2];
-#pragma unroll
-  for (int i = 0; i < NW; ++i) acc[i][0] = acc[i][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int64_t code_bytes = (int64_t)a.K * ABITS / 8;
-  uint32_t aoff[2];
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int m = s * 16 + (lane & 15);
-    aoff[s] = m < me ? (uint32_t)(s_rows.code[m] * code_bytes) + (uint32_t)((lane >> 4) * 4 * ABITS) : kOffNone;
-  }
+  const int64_t pitch = few_row16_bytes(a.K);
   const __amdgpu_buffer_rsrc_t cres = make_rsrc(a.codes, 0x7FFFFFFFu);
-  if (me > 16) few_sweep<BITS, ABITS, NW, BLK, 2, DEPTH>(W, ring, cres, aoff, c0, c1, acc);
-  else few_sweep<BITS, ABITS, NW, BLK, 1, DEPTH>(W, ring, cres, aoff, c0, c1, acc);
-  few_reduce<NW>(red, cw, sk, SK, me > 16 ? 2 : 1, lane, acc);
-
-  // lane holds D[m = 4 * (lane >> 4) + i][n = lane & 15]
-  if (sk != 0 || n0 >= a.N) return;
+  for (int m0 = 0; m0 < me; m0 += 16) {
+    if (m0 > 0) {
+      if (SK > 1) lds_barrier();             // red is free again
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
+      for (int i = 0; i < DEPTH; ++i) W.load(c0 + i, c1, ring[i]);
+    }
+    f32x4 acc[2];
+    acc[0] = acc[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int ma = m0 + (lane & 15);
+    const uint32_t aoff = ma < me ? (uint32_t)(s_rows.code[ma] * pitch) + (uint32_t)((lane >> 4) * 16) : kOffNone;
+    few_sweep16<BITS, 2, BLK, DEPTH>(W, ring, cres, aoff, c0, c1, acc);
+    few_reduce<2>(red, cw, sk, SK, lane, acc);
+    if (sk != 0) continue;
+    // lane holds D[m = 4 * (lane >> 4) + i][n = lane & 15]
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int m = s * 16 + 4 * (lane >> 4) + i;
+      const int m = m0 + 4 * (lane >> 4) + i;
       if (m >= me) continue;
       const float sc = a.scales[s_rows.code[m]];
-      float v = acc[0][s][i] * sc;
+      float* out = a.out + (int64_t)s_rows.out[m] * a.N + n0 + (lane & 15);
       if constexpr (PAIR) {
-        // silu(g) * u with the accurate exponential and division: its error moves codes of h
-        const float u = acc[NW - 1][s][i] * sc;
-        v = v / (1.0f + expf(-v)) * u;
+        if (n0 < a.N) out[0] = swiglu(acc[0][i] * sc, acc[1][i] * sc);
+      } else {
+        if (n0 < a.N) out[0] = acc[0][i] * sc;
+        if (n0 + 16 < a.N) out[16] = acc[1][i] * sc;
       }
-      a.out[(int64_t)s_rows.out[m] * a.N + n0 + (lane & 15)] = v;
     }
   }
 }
 
-// y[t] = sum_j w_j out[t * topk + j] + the shared rows, w the softmax over the chosen logits
-// (or over all).  One workgroup per token and 1024 columns.
-__global__ void __launch_bounds__(256)
-few_combine_kernel(const float* __restrict__ rows, const float* __restrict__ logits, const int32_t* __restrict__ ids,
-                   int T, int E, int topk, int n_shared, int renormalize, int H, void* __restrict__ y, int64_t ldy,
-                   int bf16) {
-  __shared__ float s_w[8];
-  const int t = blockIdx.x, lane = threadIdx.x & 63;
-  if (threadIdx.x < 64) {
-    const float* lg = logits + (int64_t)t * E;
-    int id = lane < topk ? ids[t * topk + lane] : 0;
-    id = (uint32_t)id < (uint32_t)E ? id : 0;       // only where logits were not numbers
-    const float l = lane < topk ? lg[id] : -INFINITY;
-    const float top = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, l), 0));
-    const float ex = lane < topk ? expf(l - top) : 0.0f;
-    float den = ex;
-    if (!renormalize) {
-      den = 0.0f;
-      for (int e = lane; e < E; e += 64) den += expf(lg[e] - top);
-    }
-    for (int m = 32; m >= 1; m >>= 1) den += __shfl_xor(den, m);
-    if (lane < topk) s_w[lane] = ex / den;
+// Gate/up of one token, on its packed codes.  blockIdx.y: a choice, then the shared experts;
+// row y of h.  The SK waves split K.
+template <int BITS, int ABITS, bool BLK, int DEPTH>
+__global__ void __launch_bounds__(512, 4)
+few_gate_one_kernel(FewArgs a, int SK) {
+  __shared__ float s_part[8][32];
+  const int lane = threadIdx.x & 63;
+  const int sk = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int y = (int)blockIdx.y;
+  int e = a.E + y - a.topk;
+  if (y < a.topk) {
+    e = a.E <= 64    ? expert_of_rank<1>(a.logits, a.E, y, lane)
+        : a.E <= 128 ? expert_of_rank<2>(a.logits, a.E, y, lane)
+                     : expert_of_rank<4>(a.logits, a.E, y, lane);
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.ids[y] = e;
   }
-  __syncthreads();
+  const int n0 = blockIdx.x * 16;
+  const int nchunks = (a.K + 127) >> 7;
+  const int cpw = (nchunks + SK - 1) / SK;
+  const int c0 = sk * cpw, c1 = min(nchunks, c0 + cpw);
+  FewWeights<BITS, 2> W;
+  W.init(a.w, false, e, n0, a.N, a.K, a.blocked, lane);
+  uint32_t ring[DEPTH][2][BITS];
+#pragma unroll
+  for (int i = 0; i < DEPTH; ++i) W.load(c0 + i, c1, ring[i]);
+  f32x4 acc[2][2];
+  acc[0][0] = acc[1][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  // row 0 of A is the token, the others are zero
+  const uint32_t aoff[2] = {(lane & 15) == 0 ? (uint32_t)((lane >> 4) * 4 * ABITS) : kOffNone, kOffNone};
+  const __amdgpu_buffer_rsrc_t cres = make_rsrc(a.codes, 0x7FFFFFFFu);
+  few_sweep<BITS, ABITS, 2, BLK, 1, DEPTH>(W, ring, cres, aoff, c0, c1, acc);
+  const float sc = a.scales[0];
+  if (lane < 16) {
+    s_part[sk][lane] = acc[0][0][0];
+    s_part[sk][16 + lane] = acc[1][0][0];
+  }
+  lds_barrier();
+  if (threadIdx.x < 32) {
+    float v = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < SK; ++k) v += s_part[k][lane];
+    v *= sc;
+    const float u = xor_lane_f32<16>(v);
+    if (lane < 16) a.out[(int64_t)y * a.N + n0 + lane] = swiglu(v, u);
+  }
+}
+
+constexpr int kOneF = 2048;                  // h rows of the one-token form: at most this long
+
+// The rest of the one-token form.  Workgroup: 16 columns of y; wave = row << ksh | split of K.
+template <int BITS, bool BLK, int DEPTH>
+__global__ void __launch_bounds__(1024)
+few_down_one_kernel(FewDownArgs a, int ksh) {
+  extern __shared__ uint8_t s_codes[];       // fp16 codes of every row, [R][pitch]
+  __shared__ float s_part[16][16];           // by wave
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nw = (int)blockDim.x >> 6, F = a.F, topk = a.topk;
+  const int row = wave >> ksh, split = wave & ((1 << ksh) - 1);
+  const float* h = a.h + (int64_t)row * F;
+  const int id = lane < topk ? a.ids[lane] : 0;
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  // the row's first 256 channels are requested with the ids
+  f32x4 next = split == 0 && 4 * lane < F ? *reinterpret_cast<const f32x4*>(h + 4 * lane) : zero;
+  const int e = row < topk ? __builtin_amdgcn_readlane(id, row) : a.E + row - topk;
+  const int n0 = blockIdx.x * 16;
+  const int nchunks = (F + 127) >> 7, cpw = (nchunks + (1 << ksh) - 1) >> ksh;
+  const int c0 = split * cpw, c1 = min(nchunks, c0 + cpw);
+  const int pitch = (int)few_row16_bytes(F);
+  // the weights' first chunks are on their way while h is transformed
+  FewWeights<BITS, 1> W;
+  W.init(&a.w, false, e, n0, a.H, F, a.blocked, lane);
+  uint32_t ring[DEPTH][1][BITS];
+#pragma unroll
+  for (int i = 0; i < DEPTH; ++i) W.load(c0 + i, c1, ring[i]);
+  const float lg = a.logits[id];
+
+  // Rotation of row `row` by its first wave, 256 channels a pass (4 consecutive ones a lane):
+  // butterflies in the lane and between lanes, the transformed values kept as fp32 in the
+  // row's LDS; blocks beyond 256 channels finish with passes over LDS.  fp32: the transform
+  // rounds by about as much as h's own sums.
+  float* u = reinterpret_cast<float*>(s_codes + (size_t)(nw >> ksh) * pitch) + row * ((F + 255) & ~255);
+  if (split == 0) {
+    const int b = F & -F;                    // >= 32
+    float amax = 0.0f;
+    f32x4 v = next;
+#pragma unroll 1
+    for (int c = 4 * lane; c < ((F + 255) & ~255); c += 256) {
+      v = next;
+      next = c + 256 < F ? *reinterpret_cast<const f32x4*>(h + c + 256) : zero;
+      const f32x4 p = {v[0] + v[1], v[0] - v[1], v[2] + v[3], v[2] - v[3]};
+      v = f32x4{p[0] + p[2], p[1] + p[3], p[0] - p[2], p[1] - p[3]};
+      auto stage = [&](auto m) {
+        constexpr int M = decltype(m)::value;
+        const float sg = (lane & M) ? -1.0f : 1.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = __builtin_fmaf(v[k], sg, xor_lane_f32<M>(v[k]));
+      };
+      stage(std::integral_constant<int, 1>{});
+      stage(std::integral_constant<int, 2>{});
+      stage(std::integral_constant<int, 4>{});
+      if (b > 32) stage(std::integral_constant<int, 8>{});
+      if (b > 64) stage(std::integral_constant<int, 16>{});
+      if (b > 128) stage(std::integral_constant<int, 32>{});
+      *reinterpret_cast<f32x4*>(u + c) = v;  // zeros past F
+      if (b <= 256) amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
+    }
+    // a lane only ever touches its own channels (mod 256), so these passes need no barrier
+#pragma unroll 1
+    for (int m = 256; m < b; m *= 2) {
+#pragma unroll 1
+      for (int c = 4 * lane; c < F; c += 256) {
+        if (c & m) continue;
+        const f32x4 p = *reinterpret_cast<f32x4*>(u + c), q = *reinterpret_cast<f32x4*>(u + c + m);
+        const f32x4 x = p + q, z = p - q;
+        *reinterpret_cast<f32x4*>(u + c) = x;
+        *reinterpret_cast<f32x4*>(u + c + m) = z;
+        if (2 * m == b)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fmaxf(fabsf(x[k]), fabsf(z[k])));
+      }
+    }
+    amax = fmaxf(amax, xor_lane_f32<1>(amax));
+    amax = fmaxf(amax, xor_lane_f32<2>(amax));
+    amax = fmaxf(amax, xor_lane_f32<4>(amax));
+    amax = fmaxf(amax, xor_lane_f32<8>(amax));
+    amax = fmaxf(amax, xor_lane_f32<16>(amax));
+    amax = fmaxf(amax, xor_lane_f32<32>(amax));
+    // the quantiser of rotate_quantize
+    const float Q = a.act_bits == 4 ? 7.0f : 127.0f, lo = a.act_bits == 4 ? -8.0f : -127.0f;
+    constexpr float kMagic = 12582912.0f;
+    const float s = amax / Q;
+    const double rs = amax > 0.0f ? 1.0 / (double)s : 0.0;
+#pragma unroll 1
+    for (int c = 4 * lane; c < pitch / 2; c += 256) {   // zeros past F
+      v = *reinterpret_cast<f32x4*>(u + c);
+      f16x2 q[2];                            // (k0, k2), (k1, k3) of this half group
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float r = (float)((double)v[k] * rs);
+        q[k & 1][k >> 1] = (_Float16)(__builtin_amdgcn_fmed3f(r + kMagic, kMagic + lo, kMagic + Q) - kMagic);
+      }
+      uint8_t* d = s_codes + row * pitch + few_pos16(c & ~7) + (c & 4);
+      *reinterpret_cast<uint32_t*>(d) = __builtin_bit_cast(uint32_t, q[0]);
+      *reinterpret_cast<uint32_t*>(d + 8) = __builtin_bit_cast(uint32_t, q[1]);
+    }
+    // the row's factor: its scale and its choice's weight (1 for a shared expert)
+    float f = amax > 0.0f ? s * a.c_b : 0.0f;
+    if (row < topk) {
+      const float w = choice_weight(lg, a.logits, a.E, topk, a.renormalize, lane);
+      f *= __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), row));
+    }
+    if (lane == 0) s_part[wave][0] = f;
+  }
+  lds_barrier();
+  const float f = s_part[row << ksh][0];
+
+  // D row 0 is the wave's row; the other rows of A are zero
+  f32x4 acc = zero;
+  const uint8_t* arow = s_codes + row * pitch + (lane >> 4) * 16;
+#pragma unroll 1
+  for (int c = c0; c < c1; c += DEPTH) {
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) {
+      if (c + i < c1) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          u32x4 av = {0, 0, 0, 0};
+          if ((lane & 15) == 0) av = *reinterpret_cast<const u32x4*>(arow + (c + i) * 256 + j * 64);
+          uint32_t d[4];
+          dequant8<BITS, BLK>(W.tab[0], ring[i][0], j, d);
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, av), as_f16x8(d[0], d[1], d[2], d[3]), acc,
+                                                       0, 0, 0);
+        }
+      }
+      W.load(c + DEPTH + i, c1, ring[i]);
+    }
+  }
+  lds_barrier();                             // every wave has read its row's factor
+  if (lane < 16) s_part[wave][lane] = acc[0] * f;
+  lds_barrier();
+  if (threadIdx.x < 64) {                    // quarters of the waves, then their sums
+    const int n = lane & 15, w0 = (lane >> 4) * 4;
+    float y = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (w0 + i < nw) y += s_part[w0 + i][n];
+    y += xor_lane_f32<16>(y);
+    y += xor_lane_f32<32>(y);
+    if (lane < 16) {
+      if (a.y_bf16) static_cast<uint16_t*>(a.y)[n0 + n] = f32_to_bf16_rne(y);
+      else static_cast<float*>(a.y)[n0 + n] = y;
+    }
+  }
+}
+
+// y[t] = sum_j w_j out[t * topk + j] + the shared rows.  One workgroup per token and 1024
+// columns.
+__global__ void __launch_bounds__(256)
+few_combine_kernel(const float* __restrict__ rows, const float* __restrict__ wts, int T, int topk, int n_shared, int H,
+                   void* __restrict__ y, int64_t ldy, int bf16) {
+  const int t = blockIdx.x;
   const int c = (blockIdx.y * 256 + threadIdx.x) * 4;
   if (c >= H) return;
   f32x4 r[8];
@@ -245,7 +467,8 @@ few_combine_kernel(const float* __restrict__ rows, const float* __restrict__ log
   f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    if (j < topk) acc += s_w[j] * r[j];
+    if (j < topk) acc += wts[t * topk + j] * r[j];
+#pragma unroll 1
   for (int s = 0; s < n_shared; ++s)
     acc += *reinterpret_cast<const f32x4*>(rows + (int64_t)(T * topk + s * T + t) * H + c);
   if (bf16) {
@@ -259,76 +482,144 @@ few_combine_kernel(const float* __restrict__ rows, const float* __restrict__ log
   }
 }
 
-template <int BITS, int ABITS, bool PAIR, bool BLK>
+#ifndef FEW_DEPTH
+#define FEW_DEPTH 2
+#endif
+#ifndef FEW_WAVES
+#define FEW_WAVES 4096
+#endif
+#ifndef FEW_MINCH
+#define FEW_MINCH 4
+#endif
+#ifndef FEW_WGW
+#define FEW_WGW 4
+#endif
+template <int BITS, bool PAIR, bool BLK>
 static hipError_t launch_few_gemm(const FewArgs& a, hipStream_t stream) {
-  constexpr int NW = PAIR ? 2 : 1;
   const int ys = (a.T * a.topk < a.E ? a.T * a.topk : a.E) + a.n_shared;
-  const int tiles = a.N / 16;
+  const int tiles = PAIR ? a.N / 16 : (a.N + 31) / 32;
   const int nchunks = (a.K + 127) / 128;
   int SK = 1;
-  while (SK < (PAIR ? 8 : 16) && (int64_t)tiles * ys * SK < 2048 && SK * 8 <= nchunks) SK *= 2;
-  int CW = 4 / SK;
-  if (CW < 1) CW = 1;
+  while (SK < 8 && (int64_t)tiles * ys * SK < FEW_WAVES && SK * FEW_MINCH <= nchunks) SK *= 2;
+  const int CW = SK < FEW_WGW ? FEW_WGW / SK : 1;
   const dim3 grid((unsigned)((tiles + CW - 1) / CW), (unsigned)ys), block((unsigned)(64 * CW * SK));
-  const size_t lds = (size_t)(SK - 1) * CW * NW * 2 * 64 * sizeof(f32x4);
-  hipLaunchKernelGGL((few_gemm_kernel<BITS, ABITS, PAIR, BLK, 4>), grid, block, lds, stream, a, CW, SK);
+  const size_t lds = (size_t)(SK - 1) * CW * 2 * 64 * sizeof(f32x4);
+  hipLaunchKernelGGL((few_gemm_kernel<BITS, PAIR, BLK, FEW_DEPTH>), grid, block, lds, stream, a, CW, SK);
   return hipGetLastError();
 }
 
 template <bool PAIR>
-static hipError_t launch_few_bits(const FewArgs& a, int bits, int act_bits, hipStream_t s) {
-  const bool blk = a.blocked != 0;
-  if (act_bits == 4) {
-    if (bits == 4) return launch_few_gemm<4, 4, PAIR, false>(a, s);
-    if (bits == 2) return launch_few_gemm<2, 4, PAIR, false>(a, s);
-    return blk ? launch_few_gemm<3, 4, PAIR, true>(a, s) : launch_few_gemm<3, 4, PAIR, false>(a, s);
-  }
-  if (bits == 4) return launch_few_gemm<4, 8, PAIR, false>(a, s);
-  if (bits == 2) return launch_few_gemm<2, 8, PAIR, false>(a, s);
-  return blk ? launch_few_gemm<3, 8, PAIR, true>(a, s) : launch_few_gemm<3, 8, PAIR, false>(a, s);
+static hipError_t launch_few_bits(const FewArgs& a, int bits, hipStream_t s) {
+  if (bits == 4) return launch_few_gemm<4, PAIR, false>(a, s);
+  if (bits == 2) return launch_few_gemm<2, PAIR, false>(a, s);
+  return a.blocked ? launch_few_gemm<3, PAIR, true>(a, s) : launch_few_gemm<3, PAIR, false>(a, s);
 }
 
-// Workspace: ids, then h, its codes and scales, then the expert rows, each 256-byte aligned.
+#ifndef SMALL_SK
+#define SMALL_SK 2
+#endif
+template <int BITS, int ABITS, bool BLK>
+static hipError_t launch_gate_one(const FewArgs& a, hipStream_t stream) {
+  const int nchunks = (a.K + 127) / 128;
+  int SK = 1;
+  while (SK < 8 && SK * 2 * SMALL_SK <= nchunks) SK *= 2;
+  const dim3 grid((unsigned)(a.N / 16), (unsigned)(a.topk + a.n_shared));
+  hipLaunchKernelGGL((few_gate_one_kernel<BITS, ABITS, BLK, 2>), grid, dim3(64 * SK), 0, stream, a, SK);
+  return hipGetLastError();
+}
+
+template <int ABITS>
+static hipError_t launch_gate_one_bits(const FewArgs& a, int bits, hipStream_t s) {
+  if (bits == 4) return launch_gate_one<4, ABITS, false>(a, s);
+  if (bits == 2) return launch_gate_one<2, ABITS, false>(a, s);
+  return a.blocked ? launch_gate_one<3, ABITS, true>(a, s) : launch_gate_one<3, ABITS, false>(a, s);
+}
+
+template <int BITS, bool BLK>
+static hipError_t launch_down_one(const FewDownArgs& a, hipStream_t stream) {
+  const int R = a.topk + a.n_shared, nchunks = (a.F + 127) / 128;
+  int ksh = 0;
+  while (R << (ksh + 1) <= 16 && (2 << ksh) <= nchunks) ++ksh;
+  // fp16 codes and the transform's fp32 values of every row
+  const size_t lds = (size_t)R * (few_row16_bytes(a.F) + (a.F + 255) / 256 * 1024);
+  hipLaunchKernelGGL((few_down_one_kernel<BITS, BLK, 4>), dim3((unsigned)(a.H / 16)), dim3((unsigned)(64 * R << ksh)), lds,
+                     stream, a, ksh);
+  return hipGetLastError();
+}
+
+// The one-token form: its rows fit a workgroup's waves, and their codes and values its LDS.
+static bool one_token_form(int64_t T, int topk, int n_shared, int F) {
+  const int R = topk + n_shared;
+  return T == 1 && R <= 16 && F <= kOneF && (size_t)R * (few_row16_bytes(F) + (F + 255) / 256 * 1024) <= 150 * 1024;
+}
+
+// Workspace: ids and weights, the input's fp16 codes, then h, its fp16 codes and scales, then
+// the expert rows, each 256-byte aligned.
 static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 struct FewLayout {
-  size_t h, codes, scales, rows, bytes;
-  FewLayout(int64_t T, int topk, int n_shared, int H, int F, int act_bits) {
+  size_t wts, x16, h, h16, scales, rows, bytes;
+  FewLayout(int64_t T, int topk, int n_shared, int H, int F) {
     const size_t R = (size_t)T * (topk + n_shared);
-    h = up256((size_t)T * topk * 4);
-    codes = h + up256(R * F * 4);
-    scales = codes + up256(R * (size_t)F * act_bits / 8);
+    wts = up256((size_t)T * topk * 4);
+    x16 = wts + up256((size_t)T * topk * 4);
+    h = x16 + up256((size_t)T * few_row16_bytes(H));
+    h16 = h + up256(R * F * 4);
+    scales = h16 + up256(R * few_row16_bytes(F));
     rows = scales + up256(R * 4);
     bytes = rows + up256(R * H * 4);
   }
 };
 
-size_t moe_few_workspace_bytes(int64_t T, int topk, int n_shared, int H, int F, int act_bits) {
-  return FewLayout(T, topk, n_shared, H, F, act_bits).bytes;
+size_t moe_few_workspace_bytes(int64_t T, int topk, int n_shared, int H, int F) {
+  return FewLayout(T, topk, n_shared, H, F).bytes;
 }
 
 hipError_t launch_moe_few(const MoeFewArgs& m, hipStream_t stream) {
-  const FewLayout L(m.T, m.topk, m.n_shared, m.H, m.F, m.act_bits);
+  const FewLayout L(m.T, m.topk, m.n_shared, m.H, m.F);
   uint8_t* ws = static_cast<uint8_t*>(m.ws);
   int32_t* ids = reinterpret_cast<int32_t*>(ws);
+  float* wts = reinterpret_cast<float*>(ws + L.wts);
   const int R = m.T * (m.topk + m.n_shared);
   FewArgs a{};
   a.logits = m.logits; a.ids = ids; a.T = m.T; a.E = m.E; a.topk = m.topk; a.n_shared = m.n_shared;
-  a.codes = m.codes; a.scales = m.scales; a.w[0] = m.gate; a.w[1] = m.up; a.N = m.F; a.K = m.H;
+  a.scales = m.scales; a.w[0] = m.gate; a.w[1] = m.up; a.N = m.F; a.K = m.H;
   a.blocked = m.blocked_gu; a.out = reinterpret_cast<float*>(ws + L.h);
-  hipError_t e = launch_few_bits<true>(a, m.bits_gu, m.act_bits, stream);
+  const float c_b = (float)(1.0 / std::sqrt((double)(m.F & -m.F)));
+  hipError_t e;
+  if (one_token_form(m.T, m.topk, m.n_shared, m.F)) {
+    a.codes = m.codes;
+    e = m.act_bits == 4 ? launch_gate_one_bits<4>(a, m.bits_gu, stream) : launch_gate_one_bits<8>(a, m.bits_gu, stream);
+    if (e != hipSuccess) return e;
+    FewDownArgs d{};
+    d.h = a.out; d.ids = ids; d.logits = m.logits; d.E = m.E; d.topk = m.topk; d.n_shared = m.n_shared;
+    d.renormalize = m.renormalize; d.act_bits = m.act_bits; d.H = m.H; d.F = m.F; d.w = m.down; d.blocked = m.blocked_d;
+    d.c_b = c_b; d.y = m.y; d.y_bf16 = m.y_bf16;
+    if (m.bits_d == 4) return launch_down_one<4, false>(d, stream);
+    if (m.bits_d == 2) return launch_down_one<2, false>(d, stream);
+    return m.blocked_d ? launch_down_one<3, true>(d, stream) : launch_down_one<3, false>(d, stream);
+  }
+  if (m.act_bits == 4)
+    hipLaunchKernelGGL(few_prepare_kernel<4>, dim3((unsigned)m.T), dim3(256), 0, stream, m.logits, m.T, m.E, m.topk,
+                       m.renormalize, m.codes, m.H, ids, wts, ws + L.x16);
+  else
+    hipLaunchKernelGGL(few_prepare_kernel<8>, dim3((unsigned)m.T), dim3(256), 0, stream, m.logits, m.T, m.E, m.topk,
+                       m.renormalize, m.codes, m.H, ids, wts, ws + L.x16);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  a.codes = ws + L.x16;
+  e = launch_few_bits<true>(a, m.bits_gu, stream);
   if (e != hipSuccess) return e;
   NormArgs n{};
-  n.rows = ws + L.h; n.ldr = m.F; n.codes = ws + L.codes; n.scales = reinterpret_cast<float*>(ws + L.scales);
+  n.rows = ws + L.h; n.ldr = m.F; n.codes = ws + L.h16; n.scales = reinterpret_cast<float*>(ws + L.scales);
   n.act_bits = m.act_bits; n.T = R; n.K = m.F;
   e = launch_norm_quantize(n, kRotateF32, m.F & -m.F, stream);
   if (e != hipSuccess) return e;
-  a.codes = ws + L.codes; a.scales = reinterpret_cast<float*>(ws + L.scales); a.w[0] = a.w[1] = m.down;
+  a.codes = ws + L.h16; a.scales = reinterpret_cast<float*>(ws + L.scales); a.w[0] = a.w[1] = m.down;
   a.N = m.H; a.K = m.F; a.blocked = m.blocked_d; a.out = reinterpret_cast<float*>(ws + L.rows);
-  e = launch_few_bits<false>(a, m.bits_d, m.act_bits, stream);
+  e = launch_few_bits<false>(a, m.bits_d, stream);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(few_combine_kernel, dim3((unsigned)m.T, (unsigned)((m.H + 1023) / 1024)), dim3(256), 0, stream,
-                     reinterpret_cast<const float*>(ws + L.rows), m.logits, ids, m.T, m.E, m.topk, m.n_shared,
-                     m.renormalize, m.H, m.y, m.ldy, m.y_bf16);
+                     reinterpret_cast<const float*>(ws + L.rows), wts, m.T, m.topk, m.n_shared, m.H, m.y, m.ldy, m.y_bf16);
   return hipGetLastError();
 }
 

@@ -19,6 +19,7 @@
 // between lanes, and the ones across waves in one LDS pass whatever their number (each
 // thread reads its partners in the block's other waves and adds them with their signs).
 #include "cbq_internal.hpp"
+#include "few_device.hpp"
 #include "rotate_device.hpp"
 
 namespace cbq {
@@ -282,7 +283,11 @@ norm_quantize_kernel(NormArgs a) {
   // ---- quantise: the fp32 sequence of rotate_quantize (s = M / Q, q = clamp(rint(v / s)),
   // the quotient as fp64(v) * fp64(1 / s) rounded to fp32, rint by the magic-number add);
   // the lane stages' sign, the parity of the lane's bits inside the block, is folded in ----
-  if (!act) return;
+  if constexpr (SRC == kRotateF32) {
+    if (c0 >= (a.K + 127) / 128 * 128) return;   // the fp16 rows hold zeros up to there
+  } else {
+    if (!act) return;
+  }
   const float Q = a.act_bits == 4 ? 7.0f : 127.0f;
   const float lo = a.act_bits == 4 ? -8.0f : -127.0f;
   constexpr float kMagic = 12582912.0f;
@@ -290,6 +295,25 @@ norm_quantize_kernel(NormArgs a) {
   const int lpb = b / CPT < 64 ? b / CPT : 64;   // lanes per block within a wave
   const bool neg = lpb > 1 && (__builtin_popcount((unsigned)lane & (unsigned)(lpb - 1)) & 1);
   const double rs = amax > 0.0f ? (neg ? -1.0 : 1.0) / (double)s : 0.0;
+  if constexpr (SRC == kRotateF32) {
+    // the codes as fp16, in the order the few-row GEMM dequantises weights to
+    uint8_t* dst = a.codes + t * few_row16_bytes(a.K);
+#pragma unroll
+    for (int k = 0; k < CPT / 8; ++k) {
+      f16x2 d[4];                            // (k0, k2) (k4, k6) (k1, k3) (k5, k7)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float r = (float)((double)u[8 * k + i] * rs);
+        d[(i & 1) * 2 + (i >> 2)][(i >> 1) & 1] =
+            (_Float16)(__builtin_amdgcn_fmed3f(r + kMagic, kMagic + lo, kMagic + Q) - kMagic);
+      }
+      *reinterpret_cast<u32x4*>(dst + few_pos16(c0 + 8 * k)) =
+          u32x4{__builtin_bit_cast(uint32_t, d[0]), __builtin_bit_cast(uint32_t, d[1]),
+                __builtin_bit_cast(uint32_t, d[2]), __builtin_bit_cast(uint32_t, d[3])};
+    }
+    if (tid == 0) a.scales[t] = amax > 0.0f ? s * a.c_b : 0.0f;
+    return;
+  }
   uint32_t q[CPT];
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {

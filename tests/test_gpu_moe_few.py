@@ -91,6 +91,16 @@ def test_sizes(H, F):
     _check_layer(4, H, F, 6, 2, 1, 4, 3, 4)
 
 
+@pytest.mark.parametrize("H,F,E,topk,n_shared", [(32, 32, 8, 2, 0), (96, 64, 8, 8, 8), (2048, 768, 16, 8, 0), (64, 1408, 9, 6, 2),
+                                                 (48 * 32, 160, 70, 3, 1), (64, 512, 130, 8, 0), (96, 1024, 8, 4, 1),
+                                                 (128, 2048, 12, 8, 3), (128, 2048, 9, 8, 8), (64, 2016, 20, 5, 0),
+                                                 (64, 2080, 6, 2, 1), (64, 4096, 4, 2, 0)])
+@pytest.mark.parametrize("act_bits", [4, 8])
+def test_one_token(H, F, E, topk, n_shared, act_bits):
+    _check_layer(1, H, F, E, topk, n_shared, 4, 3, act_bits)
+    _check_layer(1, H, F, E, topk, n_shared, 2, 4, act_bits, renorm=False, blocked=False, y_dtype=torch.bfloat16)
+
+
 @pytest.mark.parametrize("renorm", [False, True])
 @pytest.mark.parametrize("y_dtype", [torch.float32, torch.bfloat16])
 def test_weights_and_output_types(renorm, y_dtype):
