@@ -17,22 +17,25 @@ namespace cbq {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-// u = s_a A_a x for 16 tokens and RT * 16 rank rows.  Workgroup (tile, y, z): the distinct
-// adapters y, y + gridDim.y, ... of the tile; rank rows from 16 RT z on; the waves split K and
-// their sums meet in LDS in wave order.  Bound by the latency of one pass over the adapter's
-// rows in a decode batch, by reading x in a prefill batch.
+// u = s_a A_a x for 16 tokens and RT * 16 rank rows, part z of K.  Workgroup (tile, y, z): the
+// distinct adapters y, y + ny, ... of the tile, rank rows from 16 RT (z / parts) on, channels
+// of part z % parts; the waves split those and their sums meet in LDS in wave order.  The
+// parts are summed by the projection.  Bound by load latency in a decode batch (so K is cut
+// into enough parts to have all of an adapter's rows in flight at once), by reading x in a
+// prefill batch.
 template <int RT>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(256)
 adapter_shrink_kernel(AdapterArgs a, const uint16_t* __restrict__ x, int64_t ldx, const uint16_t* __restrict__ lora_a,
                       const float* __restrict__ adapter_scale, int64_t T, int K, float* __restrict__ u) {
-  __shared__ f32x4 red[7][RT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+  __shared__ f32x4 red[3][RT][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, g = lane >> 4;
   const int64_t t0 = (int64_t)blockIdx.x * 16;
   const int of = t0 + m < T ? a.of[t0 + m] : -1;
-  const int r0 = (int)blockIdx.z * 16 * RT;
-  const int nc = K >> 5, cpw = (nc + nw - 1) / nw;
-  const int k0 = wave * cpw, k1 = min(nc, k0 + cpw);
+  const int part = (int)blockIdx.z % a.parts, r0 = (int)blockIdx.z / a.parts * 16 * RT;
+  // 32-channel steps [k0, k1) of this wave
+  const int nc = K >> 5, cpp = (nc + a.parts - 1) / a.parts, p1 = min(nc, (part + 1) * cpp), cpw = (cpp + 3) >> 2;
+  const int k0 = part * cpp + wave * cpw, k1 = min(p1, k0 + cpw);
 
   uint32_t todo = (uint32_t)__ballot((uint32_t)of < (uint32_t)a.n_adapters) & 0xFFFFu;
   for (int i = 0; todo != 0; ++i) {
@@ -46,7 +49,7 @@ adapter_shrink_kernel(AdapterArgs a, const uint16_t* __restrict__ x, int64_t ldx
     f32x4 acc[RT];
 #pragma unroll
     for (int q = 0; q < RT; ++q) acc[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int UN = RT >= 4 ? 2 : 4;      // 32-channel steps in flight
+    constexpr int UN = RT >= 4 ? 3 : RT == 2 ? 5 : 6;   // steps in flight
     for (int k = k0; k < k1; k += UN) {
       u32x4 xv[UN], av[UN][RT];
 #pragma unroll
@@ -74,13 +77,15 @@ adapter_shrink_kernel(AdapterArgs a, const uint16_t* __restrict__ x, int64_t ldx
     lds_barrier();
     if (wave == 0) {
       const float s = adapter_scale != nullptr ? adapter_scale[ad] : 1.0f;
+      float* up = u + part * a.part_stride;
 #pragma unroll
       for (int q = 0; q < RT; ++q) {
-        for (int w = 0; w < nw - 1; ++w) acc[q] += red[w][q][lane];
+#pragma unroll
+        for (int w = 0; w < 3; ++w) acc[q] += red[w][q][lane];
         const int r = r0 + q * 16 + m;       // lane holds D[4 g + i][m]
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (((mine >> (4 * g + i)) & 1u) && r < a.rank) u[(t0 + 4 * g + i) * a.rank + r] = s * acc[q][i];
+          if (((mine >> (4 * g + i)) & 1u) && r < a.rank) up[(t0 + 4 * g + i) * a.rank + r] = s * acc[q][i];
       }
     }
     lds_barrier();                           // red is free for the next adapter
@@ -96,6 +101,7 @@ __global__ void __launch_bounds__(1024)
 few_adapter_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales, GemmW w, int T, int N, int K,
                    int blocked, AdapterArgs a, float* __restrict__ out, int64_t ldo, int CW, int SK) {
   extern __shared__ f32x4 red[];
+  float* s_u = reinterpret_cast<float*>(red + (size_t)(SK - 1) * CW * 4 * 64);   // [T][rank]
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cw = wave / SK, sk = wave - cw * SK;
@@ -109,6 +115,14 @@ few_adapter_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ 
   uint32_t ring[DEPTH][1][BITS];
 #pragma unroll
   for (int i = 0; i < DEPTH; ++i) W.load(c0 + i, c1, ring[i]);
+  // the tokens' middle vectors, their parts summed in order (rows without an adapter: whatever
+  // the workspace held, never used)
+  for (int i = threadIdx.x; i < T * a.rank / 4; i += blockDim.x) {
+    f32x4 v = reinterpret_cast<const f32x4*>(a.u)[i];
+#pragma unroll 4
+    for (int p = 1; p < a.parts; ++p) v += reinterpret_cast<const f32x4*>(a.u + p * a.part_stride)[i];
+    reinterpret_cast<f32x4*>(s_u)[i] = v;
+  }
   f32x4 acc[1][2], low[2];
   uint32_t aoff[2];
 #pragma unroll
@@ -119,6 +133,7 @@ few_adapter_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ 
   const __amdgpu_buffer_rsrc_t cres = make_rsrc(codes, 0x7FFFFFFFu);
   if (T > 16) few_sweep<BITS, ABITS, 1, BLK, 2, DEPTH>(W, ring, cres, aoff, c0, c1, acc);
   else few_sweep<BITS, ABITS, 1, BLK, 1, DEPTH>(W, ring, cres, aoff, c0, c1, acc);
+  lds_barrier();
   if (n0 < N) {
     const int n = n0 + m;
 #pragma unroll
@@ -129,7 +144,7 @@ few_adapter_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ 
         const int ad = t < T ? a.of[t] : -1;
         if ((uint32_t)ad >= (uint32_t)a.n_adapters) continue;
         const uint16_t* b = a.lora_b + ((int64_t)ad * N + n) * a.rank;
-        const float* u = a.u + (int64_t)t * a.rank;
+        const float* u = s_u + t * a.rank;
         for (int r = sk * 8; r < a.rank; r += SK * 8) {
           const u32x4 bv = *reinterpret_cast<const u32x4*>(b + r);
           const f32x4 u0 = *reinterpret_cast<const f32x4*>(u + r), u1 = *reinterpret_cast<const f32x4*>(u + r + 4);
@@ -165,26 +180,38 @@ static hipError_t launch_few_adapter(const GemmArgs& a, const AdapterArgs& ad, h
   while (SK < 16 && (int64_t)tiles * SK < 2048 && SK * 8 <= nchunks) SK *= 2;
   const int CW = SK < 4 ? 4 / SK : 1;
   const dim3 grid((unsigned)((tiles + CW - 1) / CW)), block((unsigned)(64 * CW * SK));
-  const size_t lds = (size_t)(SK - 1) * CW * 2 * 2 * 64 * sizeof(f32x4);
-  hipLaunchKernelGGL((few_adapter_kernel<BITS, ABITS, BLK, 4>), grid, block, lds, stream, a.codes, a.scales, a.w[0],
+  const size_t lds = (size_t)(SK - 1) * CW * 4 * 64 * sizeof(f32x4) + (size_t)a.n_rows * ad.rank * sizeof(float);
+  hipLaunchKernelGGL((few_adapter_kernel<BITS, ABITS, BLK, 2>), grid, block, lds, stream, a.codes, a.scales, a.w[0],
                      (int)a.n_rows, a.N, a.K, a.blocked, ad, static_cast<float*>(a.out), a.ldo, CW, SK);
   return hipGetLastError();
 }
 
-size_t adapter_workspace_bytes(int64_t T, int rank) { return ((size_t)T * rank * sizeof(float) + 255) / 256 * 256; }
+// Parts of K in the first launch, at most: enough workgroups for a decode batch or a short
+// prefill; one part beyond, where the token tiles fill the GPU.
+static int adapter_max_parts(int64_t T) { return T <= kFewRows ? 16 : T <= 1024 ? 4 : T <= 8192 ? 2 : 1; }
+
+size_t adapter_workspace_bytes(int64_t T, int rank) {
+  return ((size_t)T * rank * adapter_max_parts(T) * sizeof(float) + 255) / 256 * 256;
+}
 
 hipError_t launch_adapter_gemm(const GemmArgs& a, AdapterArgs ad, const uint16_t* x, int64_t ldx,
                                const uint16_t* lora_a, const float* adapter_scale, float* u, hipStream_t stream) {
   ad.u = u;
   const int64_t T = a.n_rows;
   const int rt = (ad.rank + 15) / 16;
-  const int RT = rt >= 4 ? 4 : rt >= 2 ? 2 : 1;
+  const int RT = rt >= 4 ? 4 : rt >= 2 ? 2 : 1, zr = (rt + RT - 1) / RT;
   // a decode batch's tile may hold 16 adapters, one a workgroup; in larger batches, where
   // requests span tiles, a tile's workgroups take turns
-  const dim3 grid((unsigned)((T + 15) / 16), T <= 256 ? (unsigned)(T < 16 ? T : 16) : 2u, (unsigned)((rt + RT - 1) / RT));
-  if (RT == 4) hipLaunchKernelGGL(adapter_shrink_kernel<4>, grid, dim3(512), 0, stream, ad, x, ldx, lora_a, adapter_scale, T, a.K, u);
-  else if (RT == 2) hipLaunchKernelGGL(adapter_shrink_kernel<2>, grid, dim3(512), 0, stream, ad, x, ldx, lora_a, adapter_scale, T, a.K, u);
-  else hipLaunchKernelGGL(adapter_shrink_kernel<1>, grid, dim3(512), 0, stream, ad, x, ldx, lora_a, adapter_scale, T, a.K, u);
+  const int ny = T <= 256 ? (int)(T < 16 ? T : 16) : 2;
+  const int64_t tiles = (T + 15) / 16;
+  // parts of at least 8 steps of 32 channels (two a wave)
+  ad.parts = 1;
+  while (ad.parts * 2 <= adapter_max_parts(T) && ad.parts * 2 * 8 <= a.K / 32 && tiles * ny * zr * ad.parts < 1024) ad.parts *= 2;
+  ad.part_stride = T * ad.rank;
+  const dim3 grid((unsigned)tiles, (unsigned)ny, (unsigned)(zr * ad.parts));
+  if (RT == 4) hipLaunchKernelGGL(adapter_shrink_kernel<4>, grid, dim3(256), 0, stream, ad, x, ldx, lora_a, adapter_scale, T, a.K, u);
+  else if (RT == 2) hipLaunchKernelGGL(adapter_shrink_kernel<2>, grid, dim3(256), 0, stream, ad, x, ldx, lora_a, adapter_scale, T, a.K, u);
+  else hipLaunchKernelGGL(adapter_shrink_kernel<1>, grid, dim3(256), 0, stream, ad, x, ldx, lora_a, adapter_scale, T, a.K, u);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (T > kFewRows) return launch_mfma_prefill_adapter(a, ad, stream);

@@ -122,7 +122,9 @@ struct AdapterArgs {
   const int32_t* of;          // [T]
   int n_adapters, rank;       // rank: a multiple of 8
   const uint16_t* lora_b;     // bf16 [n_adapters][N][rank]
-  const float* u;             // fp32 [T][rank]
+  const float* u;             // fp32 [parts][T][rank], to be summed in order
+  int parts;
+  int64_t part_stride;        // T * rank
 };
 size_t adapter_workspace_bytes(int64_t T, int rank);
 hipError_t launch_adapter_gemm(const GemmArgs& a, AdapterArgs ad, const uint16_t* x, int64_t ldx,

@@ -80,55 +80,119 @@ template <> struct TileAdapters<true> {
   int N;
 };
 
-// The adapter terms of the 32 rows from tile row `mrow` on, at this lane's column n (valid:
-// n < N): low[v] = sum_r u[row][r] lora_b[a][n][r], in the accumulators' layout.  One pass per
-// distinct adapter among the rows, each taken only by its own rows.  u is split into three
-// bf16 parts (8 bits each, so their sum is u's 24 bits), whose products with lora_b are exact
-// and accumulate in fp32: 3 MFMAs per 16 ranks against K / 16 of the projection.
-__device__ __forceinline__ f32x16 adapter_terms(const AdapterArgs& ad, const int32_t* s_of, int64_t m0, int mrow,
-                                                int nl, int g, int n, bool valid, int N) {
-  f32x16 low;
+// Adds the adapters' terms to a tile's scaled sums: column n of row m gains
+// sum_r u[m][r] lora_b[a][n][r], a the row's adapter.  u (its parts summed in order) is split
+// into three bf16 parts (8 bits each, so their sum is u's 24 bits), whose products with lora_b
+// are exact and accumulate in fp32: 3 MFMAs per 16 ranks against K / 16 of the projection.
+// The split vectors are staged in the activation tiles' LDS, 32 ranks at a time, with a row of
+// zeros behind them.  Each 32-row sub-tile makes one pass per distinct adapter among its rows,
+// in which the other rows read the zeros; lora_b's fragments stay in registers while
+// consecutive sub-tiles use one adapter.  Where a fragment holds an infinity or NaN, zeros
+// would not keep it from the other rows, so that pass is summed apart and taken by its own
+// rows only.  This code runs once per tile, so its size in instructions is its time (a version
+// unrolled over ranks and split in registers took 60 us a tile).
+constexpr int kStageRanks = 32, kStagePitch = 2 * kStageRanks + 16;   // bytes; the padding staggers the banks
+template <int BM, int NMS, int NS>
+__device__ __forceinline__ void add_adapter_terms(f32x16 (&acc)[NMS][NS], const TileAdapters<true>& ta, uint8_t* stage,
+                                                  int rows, int tid, int nl, int g, const int* nrow, const bool* nvalid) {
+  constexpr uint32_t kPlane = (BM + 1) * kStagePitch;
+  const AdapterArgs& ad = ta.ad;
+  for (int rc = 0; rc < ad.rank; rc += kStageRanks) {
+    lds_barrier();                           // the main loop's (or the last pass's) reads are done
+    // four rows' loads in flight a thread: they come from another launch's results, far away
+    constexpr int kQuads = kStageRanks / 4;
+#pragma unroll 1
+    for (int i0 = tid; i0 < (BM + 1) * kQuads; i0 += 4 * 256) {
+      f32x4 vs[4];
 #pragma unroll
-  for (int v = 0; v < 16; ++v) low[v] = 0.0f;
-  const int of = s_of[mrow + nl];
-  uint32_t todo = (uint32_t)__ballot(of >= 0);
-  const float* u = ad.u + (m0 + mrow + nl) * ad.rank + 8 * g;
-  while (todo != 0) {
-    const int a = __builtin_amdgcn_readlane(of, __builtin_ctz(todo));
-    const bool row = of == a;
-    const uint32_t mine = (uint32_t)__ballot(row);
-    todo &= ~mine;
-    const uint16_t* lb = ad.lora_b + ((int64_t)a * N + (valid ? n : 0)) * ad.rank + 8 * g;
-    f32x16 d;
+      for (int j = 0; j < 4; ++j) vs[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+      for (int p = 0; p < ad.parts; ++p) {
+        f32x4 w[4];
 #pragma unroll
-    for (int v = 0; v < 16; ++v) d[v] = 0.0f;
-    for (int r = 0; r < ad.rank; r += 16) {
-      const bool in = r + 8 * g < ad.rank;
-      f32x4 u0 = {0.0f, 0.0f, 0.0f, 0.0f}, u1 = u0;
-      if (in && row) {
-        u0 = *reinterpret_cast<const f32x4*>(u + r);
-        u1 = *reinterpret_cast<const f32x4*>(u + r + 4);
-      }
-      u32x4 bv = {0, 0, 0, 0};
-      if (in && valid) bv = *reinterpret_cast<const u32x4*>(lb + r);
-      const bf16x8 b = __builtin_bit_cast(bf16x8, bv);
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        bf16x8 p;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p[i] = (__bf16)u0[i];
-          p[i + 4] = (__bf16)u1[i];
-          u0[i] -= (float)p[i];
-          u1[i] -= (float)p[i + 4];
+        for (int j = 0; j < 4; ++j) {
+          const int i = i0 + 256 * j, m = i / kQuads, r = 4 * (i % kQuads);
+          w[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          if (m < rows && rc + r < ad.rank)
+            w[j] = *reinterpret_cast<const f32x4*>(ad.u + p * ad.part_stride + (ta.m0 + m) * ad.rank + rc + r);
         }
-        d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(p, b, d, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) vs[j] += w[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + 256 * j, m = i / kQuads, r = 4 * (i % kQuads);
+        if (m > BM) continue;
+        f32x4 v = vs[j];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          uint32_t w[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t lo = f32_to_bf16_rne(v[2 * h]), hi = f32_to_bf16_rne(v[2 * h + 1]);
+            w[h] = lo | (hi << 16);
+            v[2 * h] -= __builtin_bit_cast(float, lo << 16);
+            v[2 * h + 1] -= __builtin_bit_cast(float, hi << 16);
+          }
+          *reinterpret_cast<u32x2*>(stage + k * kPlane + m * kStagePitch + 2 * r) = u32x2{w[0], w[1]};
+        }
       }
     }
+    lds_barrier();
+    // one 32-column slot at a time: the accumulators leave few registers
 #pragma unroll
-    for (int v = 0; v < 16; ++v) low[v] = ((mine >> (8 * (v / 4) + 4 * g + v % 4)) & 1u) ? d[v] : low[v];
+    for (int s = 0; s < NS; ++s) {
+      int held = -1;                         // the adapter whose fragments are in bf
+      bool finite = true;                    // of those, over the wave
+      bf16x8 bf[2];
+#pragma unroll
+      for (int ms = 0; ms < NMS; ++ms) {
+        const int of = ta.s_of[ms * 32 + nl];
+        uint32_t todo = (uint32_t)__ballot(of >= 0);
+        while (todo != 0) {
+          const int a = __builtin_amdgcn_readlane(of, __builtin_ctz(todo));
+          const uint32_t mine = (uint32_t)__ballot(of == a);
+          todo &= ~mine;
+          if (a != held) {
+            held = a;
+            const uint16_t* lb = ad.lora_b + ((int64_t)a * ta.N + (nvalid[s] ? nrow[s] : 0)) * ad.rank + rc + 8 * g;
+            bool bad = false;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const u32x4 w = rc + 16 * q + 8 * g < ad.rank ? *reinterpret_cast<const u32x4*>(lb + 16 * q) : u32x4{0, 0, 0, 0};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                bad = bad || (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u;
+              bf[q] = __builtin_bit_cast(bf16x8, w);
+            }
+            finite = __ballot(bad) == 0;
+          }
+          const uint8_t* u = stage + (of == a ? ms * 32 + nl : BM) * kStagePitch + 16 * g;
+          if (finite) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int k = 0; k < 3; ++k)
+                acc[ms][s] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    *reinterpret_cast<const bf16x8*>(u + k * kPlane + 32 * q), bf[q], acc[ms][s], 0, 0, 0);
+          } else {
+            f32x16 d;
+#pragma unroll
+            for (int v = 0; v < 16; ++v) d[v] = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int k = 0; k < 3; ++k)
+                d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(u + k * kPlane + 32 * q),
+                                                            bf[q], d, 0, 0, 0);
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+              if ((mine >> (8 * (v / 4) + 4 * g + v % 4)) & 1u) acc[ms][s][v] += d[v];
+          }
+        }
+      }
+    }
   }
-  return low;
 }
 
 // NS: 32-column weight slots per wave (2; 1 for a single matrix in 128-column tiles).
@@ -294,17 +358,18 @@ __device__ __forceinline__ void tile_run(const TileCtx<BITS, ABITS, LT>& c, uint
   uint32_t coff[NS];
 #pragma unroll
   for (int s = 0; s < NS; ++s) coff[s] = c.nvalid[s] ? (uint32_t)c.nrow[s] * ESZ : kOffCol;
+  if constexpr (ADP) {                                   // the stores below take the sums as they are
+    static_assert(2 * BM * LDW * 2 >= 3 * (BM + 1) * kStagePitch, "the adapters' vectors are staged in the activation tiles");
+#pragma unroll
+    for (int ms = 0; ms < NMS; ++ms)
+#pragma unroll
+      for (int v = 0; v < 16; ++v)
+#pragma unroll
+        for (int s = 0; s < NS; ++s) acc[ms][s][v] *= s_scale[ms * 32 + 8 * (v / 4) + 4 * g + v % 4];
+    add_adapter_terms<BM, NMS, NS>(acc, ta, reinterpret_cast<uint8_t*>(&As[0][0]), c.rows, tid, nl, g, c.nrow, c.nvalid);
+  }
 #pragma unroll
   for (int ms = 0; ms < NMS; ++ms) {
-    if constexpr (ADP) {                                 // the rows' outputs, before the stores below
-#pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        const f32x16 low = adapter_terms(ta.ad, ta.s_of, ta.m0, ms * 32, nl, g, c.nrow[s], c.nvalid[s], ta.N);
-#pragma unroll
-        for (int v = 0; v < 16; ++v)
-          acc[ms][s][v] = __builtin_fmaf(acc[ms][s][v], s_scale[ms * 32 + 8 * (v / 4) + 4 * g + v % 4], low[v]);
-      }
-    }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int m0 = ms * 32 + 8 * q + 4 * g;            // rows m0 .. m0+3 of this lane
@@ -472,11 +537,18 @@ mfma_prefill_kernel(const uint8_t* __restrict__ codes, const float* __restrict__
       }
     }
   }
+  // a dense call of fewer M-tiles than XCDs would leave XCDs idle: there (ADP only) the column
+  // tiles go round the XCDs instead
+  bool plain = false;
+  if constexpr (ADP) {
+    plain = ttot < 8;
+    if (plain) tcol = (int)blockIdx.x;
+  }
   // ---- (run, tile of the run) -> (expert, first row): wave 0 scans the experts' run counts ----
   if (tid < 64) {
     if (!offsets) {
       if (tid == 0) {                                // one matrix of n_rows rows: runs are contiguous
-        const int64_t ty = run * G + rr;
+        const int64_t ty = plain ? (int64_t)blockIdx.y : run * G + rr;
         const bool ok = ty * BM < n_rows;
         s_e = ok ? 0 : -1; s_r0 = 0; s_me = n_rows; s_m0 = ty * BM;
       }
@@ -846,27 +918,35 @@ hipError_t launch_mfma_prefill(const GemmArgs& a, int min_rows, hipStream_t stre
   return hipErrorInvalidValue;
 }
 
-// The single-matrix kernels with adapters: the tile choice of launch_p2 without its K split.
+// The single-matrix kernels with adapters, without a K split.  2- and 3-bit codebooks: tiles of
+// 128 rows x 256 columns where they make at least two workgroups a CU, else 128 columns.
+// 4-bit: 256 rows x 128 columns (two workgroups a CU; with 256 columns the accumulators fill
+// the registers and the epilogue spills: 4096 tokens, 2560 -> 9728, rank 16: 309 us a call
+// against 229), and 128 rows where 256 would leave CUs without a tile (333 tokens: 152 tiles
+// of 256 rows or 228 of 128).
+template <int BITS, int ABITS, bool BLK, int NS, int BM>
+static hipError_t launch_adp_tiles(const GemmArgs& a, const AdapterArgs& ad, hipStream_t stream) {
+  const int64_t mt = (a.n_rows + BM - 1) / BM;
+  int64_t G = 1;
+  while (2 * G <= XG && 8 * 2 * G <= mt) G *= 2;
+  const int64_t mtiles = mt < 8 ? mt : (mt + 8 * G - 1) / (8 * G) * (8 * G);
+  const int ncol = 128 * NS;
+  hipLaunchKernelGGL((mfma_prefill_kernel<BITS, ABITS, 1, false, BLK, NS, true, BM>),
+                     dim3((unsigned)((a.N + ncol - 1) / ncol), (unsigned)mtiles), dim3(256), 0, stream, a.codes, a.scales,
+                     nullptr, nullptr, a.w[0], a.w[0], a.n_rows, 1, a.N, a.K, 0, a.blocked, a.out, a.ldo, nullptr, -1, ad);
+  return hipGetLastError();
+}
+
 template <int BITS, int ABITS, bool BLK>
 static hipError_t launch_adp(const GemmArgs& a, const AdapterArgs& ad, hipStream_t stream) {
   constexpr int BM = tile_rows<BITS>();
   const int64_t mt = (a.n_rows + BM - 1) / BM;
-  int64_t G = 1;
-  while (2 * G <= XG && 8 * 2 * G <= mt) G *= 2;
-  const int64_t mtiles = (mt + 8 * G - 1) / (8 * G) * (8 * G);
-  auto grid_for = [&](int ncol) { return dim3((unsigned)((a.N + ncol - 1) / ncol), (unsigned)mtiles); };
   if constexpr (BM == 256) {
-    if ((int64_t)((a.N + 255) / 256) * mt < 2 * 256) {
-      hipLaunchKernelGGL((mfma_prefill_kernel<BITS, ABITS, 1, false, BLK, 1, true>), grid_for(128), dim3(256), 0, stream,
-                         a.codes, a.scales, nullptr, nullptr, a.w[0], a.w[0], a.n_rows, 1, a.N, a.K, 0, a.blocked,
-                         a.out, a.ldo, nullptr, -1, ad);
-      return hipGetLastError();
-    }
+    if ((int64_t)((a.N + 127) / 128) * mt >= 256) return launch_adp_tiles<BITS, ABITS, BLK, 1, 256>(a, ad, stream);
+  } else {
+    if ((int64_t)((a.N + 255) / 256) * mt >= 2 * 256) return launch_adp_tiles<BITS, ABITS, BLK, 2, BM>(a, ad, stream);
   }
-  hipLaunchKernelGGL((mfma_prefill_kernel<BITS, ABITS, 1, false, BLK, 2, true>), grid_for(256), dim3(256), 0, stream,
-                     a.codes, a.scales, nullptr, nullptr, a.w[0], a.w[0], a.n_rows, 1, a.N, a.K, 0, a.blocked,
-                     a.out, a.ldo, nullptr, -1, ad);
-  return hipGetLastError();
+  return launch_adp_tiles<BITS, ABITS, BLK, 1, 128>(a, ad, stream);
 }
 
 hipError_t launch_mfma_prefill_adapter(const GemmArgs& a, const AdapterArgs& ad, hipStream_t stream) {

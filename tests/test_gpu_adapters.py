@@ -91,6 +91,16 @@ def test_many_tiles_of_rows_and_columns():
     _case(T, 128, 784, 3, 8, 32, 6, of=of, check_rows=np.arange(290, 330))
 
 
+@pytest.mark.parametrize("T,K,N", [(900, 64, 2576), (2100, 64, 16384), (2304, 96, 9728), (4200, 32, 4112)])
+@pytest.mark.parametrize("bits", [3, 4])
+def test_tile_choices(T, K, N, bits):
+    """Every tile shape of the larger path, ranks beyond one staging pass, ragged columns."""
+    rng = np.random.default_rng(T)
+    rows = np.unique(np.concatenate([[0, T - 1], rng.integers(0, T, 40)]))
+    _case(T, K, N, bits, 8, 48, 5, of=np.sort(rng.integers(-1, 5, T)), check_rows=rows)
+    _case(T, K, N, bits, 4, 72, 9, check_rows=rows)
+
+
 @pytest.mark.parametrize("T", [7, 70])
 def test_orders_and_none(T):
     _case(T, 128, 64, 4, 8, 8, 4, of=np.full(T, 2))
