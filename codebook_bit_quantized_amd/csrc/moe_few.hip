@@ -31,9 +31,6 @@
 #include "rotate_device.hpp"
 #include "route_device.hpp"
 
-#ifndef FEW_OCC
-#define FEW_OCC 5
-#endif
 namespace cbq {
 
 namespace {
@@ -105,7 +102,8 @@ __device__ __forceinline__ float choice_weight(float l, const float* lg, int E, 
 }  // namespace
 
 // One workgroup per token: wave 0 ranks the logits by topk rounds of a wave maximum (ties to
-// the lower id) and forms the weights; the workgroup converts the token's codes.
+// the lower id) and forms the weights, the others convert the token's codes.  Latency-bound
+// (about 4.5 us): a chain of loads and rounds.
 template <int ABITS>
 __global__ void __launch_bounds__(256)
 few_prepare_kernel(const float* __restrict__ logits, int T, int E, int topk, int renormalize,
@@ -113,7 +111,7 @@ few_prepare_kernel(const float* __restrict__ logits, int T, int E, int topk, int
                    uint8_t* __restrict__ codes16) {
   const int t = blockIdx.x, lane = threadIdx.x & 63;
   const int64_t pitch = few_row16_bytes(K);
-  for (int p = threadIdx.x; p < (int)(pitch / 64); p += 256) {   // 32 channels each
+  for (int p = threadIdx.x - 64; p >= 0 && p < (int)(pitch / 64); p += 192) {   // 32 channels each
     uint32_t raw[ABITS] = {}, d[16];
     if (32 * p < K) {
       const u32x4* src = reinterpret_cast<const u32x4*>(codes + (int64_t)t * (K * ABITS / 8) + p * 4 * ABITS);
@@ -175,7 +173,7 @@ __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + e
 // when there are fewer choices than experts, a choice (the first one of its expert does the
 // work).  An expert of more than 16 rows sweeps its weights twice.
 template <int BITS, bool PAIR, bool BLK, int DEPTH>
-__global__ void __launch_bounds__(512, FEW_OCC)
+__global__ void __launch_bounds__(512, 5)
 few_gemm_kernel(FewArgs a, int CW, int SK) {
   extern __shared__ f32x4 red[];
   __shared__ FewRows s_rows;
@@ -482,29 +480,17 @@ few_combine_kernel(const float* __restrict__ rows, const float* __restrict__ wts
   }
 }
 
-#ifndef FEW_DEPTH
-#define FEW_DEPTH 2
-#endif
-#ifndef FEW_WAVES
-#define FEW_WAVES 4096
-#endif
-#ifndef FEW_MINCH
-#define FEW_MINCH 4
-#endif
-#ifndef FEW_WGW
-#define FEW_WGW 4
-#endif
 template <int BITS, bool PAIR, bool BLK>
 static hipError_t launch_few_gemm(const FewArgs& a, hipStream_t stream) {
   const int ys = (a.T * a.topk < a.E ? a.T * a.topk : a.E) + a.n_shared;
   const int tiles = PAIR ? a.N / 16 : (a.N + 31) / 32;
   const int nchunks = (a.K + 127) / 128;
   int SK = 1;
-  while (SK < 8 && (int64_t)tiles * ys * SK < FEW_WAVES && SK * FEW_MINCH <= nchunks) SK *= 2;
-  const int CW = SK < FEW_WGW ? FEW_WGW / SK : 1;
+  while (SK < 8 && (int64_t)tiles * ys * SK < 4096 && SK * 4 <= nchunks) SK *= 2;
+  const int CW = SK < 4 ? 4 / SK : 1;
   const dim3 grid((unsigned)((tiles + CW - 1) / CW), (unsigned)ys), block((unsigned)(64 * CW * SK));
   const size_t lds = (size_t)(SK - 1) * CW * 2 * 64 * sizeof(f32x4);
-  hipLaunchKernelGGL((few_gemm_kernel<BITS, PAIR, BLK, FEW_DEPTH>), grid, block, lds, stream, a, CW, SK);
+  hipLaunchKernelGGL((few_gemm_kernel<BITS, PAIR, BLK, 2>), grid, block, lds, stream, a, CW, SK);
   return hipGetLastError();
 }
 
@@ -515,14 +501,11 @@ static hipError_t launch_few_bits(const FewArgs& a, int bits, hipStream_t s) {
   return a.blocked ? launch_few_gemm<3, PAIR, true>(a, s) : launch_few_gemm<3, PAIR, false>(a, s);
 }
 
-#ifndef SMALL_SK
-#define SMALL_SK 2
-#endif
 template <int BITS, int ABITS, bool BLK>
 static hipError_t launch_gate_one(const FewArgs& a, hipStream_t stream) {
   const int nchunks = (a.K + 127) / 128;
   int SK = 1;
-  while (SK < 8 && SK * 2 * SMALL_SK <= nchunks) SK *= 2;
+  while (SK < 8 && SK * 4 <= nchunks) SK *= 2;
   const dim3 grid((unsigned)(a.N / 16), (unsigned)(a.topk + a.n_shared));
   hipLaunchKernelGGL((few_gate_one_kernel<BITS, ABITS, BLK, 2>), grid, dim3(64 * SK), 0, stream, a, SK);
   return hipGetLastError();

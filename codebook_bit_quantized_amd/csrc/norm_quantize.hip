@@ -12,10 +12,12 @@
 // wider one elsewhere.  fp64 sums make them (and so the codes) independent of the order
 // of summation, except where a value lies within about 2^-50 of a rounding border.
 //
-// One workgroup per token, CPT = 8 consecutive channels a thread (16 beyond K = 8192), so
-// one token's work is spread over K / 512 waves: a single token's latency is what decode
-// sees, and a token's loads, sums and transform then take a quarter of what 32 channels a
-// thread take.  The transform's first stages run in the thread, the next ones
+// One workgroup per token, CPT consecutive channels a thread: 8 (16 beyond K = 8192), so one
+// token's work is spread over K / 512 waves (a single token's latency is what decode sees),
+// or 32 for the norm before a block of many tokens (norm_width).  With expert rows it is bound
+// by reading them (4096 x 2048, 8 rows each, gates, norms and codes: 344 MB in 76 us, 4.5 TB/s
+// of the 5.1 a large copy reaches); the norm alone by its vector instructions, mostly the
+// transform's exchanges in fp64 (4096 x 2048: 42 MB in 20 us).  The transform's first stages run in the thread, the next ones
 // between lanes, and the ones across waves in one LDS pass whatever their number (each
 // thread reads its partners in the block's other waves and adds them with their signs).
 #include "cbq_internal.hpp"
@@ -135,37 +137,44 @@ norm_quantize_kernel(NormArgs a) {
   } else {
     using Row = std::conditional_t<SRC == kNormF32, float, uint16_t>;
     const Row* rows = reinterpret_cast<const Row*>(a.rows) + c0;
-    float g[CPT], res[CPT];
+    const int n = a.topk + a.n_shared;
+    float res[CPT], gate[CPT], pw[CPT];
     double y[CPT];
 #pragma unroll
     for (int i = 0; i < CPT; ++i) y[i] = 0.0;
     if (act) {
-      // RB rows' loads are requested before the first is used: a token's rows lie apart
+      // everything is requested up front, RB of the rows before the first is used: a token's
+      // rows lie apart, and each load that waits for another costs its whole latency
       constexpr int RB = CPT == 8 && NT <= 512 ? 8 : CPT == 8 ? 4 : 2;   // what the registers hold
       float r[RB][CPT];
-      auto load_row = [&](int64_t row, float* d) {
-        if constexpr (SRC == kNormF32) load_f32<CPT>(rows + row * a.ldr, d);
-        else load_bf16<CPT>(rows + row * a.ldr, d);
+      auto row_of = [&](int j) {
+        return j < a.topk ? (int64_t)a.slot_of[t * a.topk + j] : a.T * a.topk + (j - a.topk) * a.T + t;
       };
+      auto load_row = [&](int j, float* d) {
+        if constexpr (SRC == kNormF32) load_f32<CPT>(rows + row_of(j) * a.ldr, d);
+        else load_bf16<CPT>(rows + row_of(j) * a.ldr, d);
+      };
+#pragma unroll
+      for (int j = 0; j < RB; ++j)
+        if (j < n) load_row(j, r[j]);
       load_bf16<CPT>(a.x + t * a.ldx + c0, res);
+      if (CPT == 8 && a.gate != nullptr) load_bf16<CPT>(a.gate + t * a.ldg + c0, gate);
+      if (CPT == 8 && a.post_weight != nullptr) load_f32<CPT>(a.post_weight + c0, pw);
+#pragma unroll 1
+      for (int j0 = 0; j0 < n; j0 += RB) {
+        if (j0 > 0) {
 #pragma unroll
-      for (int j0 = 0; j0 < 8; j0 += RB) {
-#pragma unroll
-        for (int j = 0; j < RB; ++j)
-          if (j0 + j < a.topk) load_row(a.slot_of[t * a.topk + j0 + j], r[j]);
+          for (int j = 0; j < RB; ++j)
+            if (j0 + j < n) load_row(j0 + j, r[j]);
+        }
 #pragma unroll
         for (int j = 0; j < RB; ++j) {
-          if (j0 + j < a.topk) {
-            const double w = a.topk_w[t * a.topk + j0 + j];
+          if (j0 + j < n) {
+            const double w = j0 + j < a.topk ? (double)a.topk_w[t * a.topk + j0 + j] : 1.0;
 #pragma unroll
             for (int i = 0; i < CPT; ++i) y[i] = __builtin_fma(w, (double)r[j][i], y[i]);
           }
         }
-      }
-      for (int s = 0; s < a.n_shared; ++s) {
-        load_row(a.T * a.topk + s * a.T + t, r[0]);
-#pragma unroll
-        for (int i = 0; i < CPT; ++i) y[i] += (double)r[0][i];
       }
     }
     if (a.post_weight != nullptr) {
@@ -173,22 +182,20 @@ norm_quantize_kernel(NormArgs a) {
 #pragma unroll
       for (int i = 0; i < CPT; ++i) ss = __builtin_fma(y[i], y[i], ss);
       ss = wave_sum_f64(ss);
+      if (CPT > 8 && act) load_f32<CPT>(a.post_weight + c0, pw);   // 16 channels leave no registers for it above
       if (lane == 0) s_sum[0][wave] = ss;
-      __syncthreads();
+      lds_barrier();
       double tot = 0.0;
       for (int w = 0; w < nw; ++w) tot += s_sum[0][w];
       const double rn = rsqrt_f64(tot * a.inv_K + (double)a.post_eps);
-      if (act) {
-        load_f32<CPT>(a.post_weight + c0, g);
 #pragma unroll
-        for (int i = 0; i < CPT; ++i) y[i] = y[i] * rn * (double)g[i];
-      }
+      for (int i = 0; i < CPT; ++i) y[i] = act ? y[i] * rn * (double)pw[i] : 0.0;
     }
     if (act) {
       if (a.gate != nullptr) {
-        load_bf16<CPT>(a.gate + t * a.ldg + c0, g);
+        if (CPT > 8) load_bf16<CPT>(a.gate + t * a.ldg + c0, gate);
 #pragma unroll
-        for (int i = 0; i < CPT; ++i) y[i] *= (double)g[i];
+        for (int i = 0; i < CPT; ++i) y[i] *= (double)gate[i];
       }
 #pragma unroll
       for (int i = 0; i < CPT; ++i) y[i] = __builtin_fma((double)a.scale, y[i], (double)res[i]);
@@ -209,7 +216,7 @@ norm_quantize_kernel(NormArgs a) {
     for (int i = 0; i < CPT; ++i) ss = __builtin_fma((double)f[i], (double)f[i], ss);
     ss = wave_sum_f64(ss);
     if (lane == 0) s_sum[1][wave] = ss;
-    __syncthreads();
+    lds_barrier();
     double tot = 0.0;
     for (int w = 0; w < nw; ++w) tot += s_sum[1][w];
     const double rn = rsqrt_f64(tot * a.inv_K + (double)a.eps);
@@ -252,10 +259,10 @@ norm_quantize_kernel(NormArgs a) {
     const int pitch = (int)blockDim.x;
 #pragma unroll
     for (int c = 0; c < CPT; c += 8) {
-      if (c > 0) __syncthreads();
+      if (c > 0) lds_barrier();
 #pragma unroll
       for (int i = 0; i < 8; ++i) xchg[i * pitch + tid] = v[c + i];
-      __syncthreads();
+      lds_barrier();
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[c + i] = (__builtin_popcount(wb) & 1) ? -v[c + i] : v[c + i];
       for (int w = 0; w < wpb; ++w) {
@@ -276,7 +283,7 @@ norm_quantize_kernel(NormArgs a) {
   }
   amax = wave_max_f32(amax);
   if (lane == 0) s_max[wave] = amax;
-  __syncthreads();
+  lds_barrier();
   amax = s_max[0];
   for (int w = 1; w < nw; ++w) amax = fmaxf(amax, s_max[w]);
 
@@ -354,16 +361,29 @@ static void launch_nt(const NormArgs& a, int src, unsigned threads, size_t lds, 
   else hipLaunchKernelGGL((norm_quantize_kernel<CPT, NT, kRotateF32>), grid, block, lds, stream, a);
 }
 
+// Channels a thread of the norm before a block: 8 is the shortest chain, and the faster one up
+// to about 8 million values; beyond, 32 where they fill the waves, as a wave's reductions and
+// exchanges then serve four times the channels (us, 8 against 32: 4096 x 2048 20.2 / 19.7,
+// 4096 x 4096 40.0 / 34.2, 2048 x 8192 51.0 / 37.5, 1024 x 4096 13.9 / 14.8).  Beyond 8192
+// channels a workgroup's 1024 threads need 16 (or 32).
+static int norm_width(int64_t T, int K) {
+  const int threads = K / 32, full = (threads + 63) / 64 * 64;
+  if (T * K >= (1 << 23) && 10 * threads >= 9 * full) return 32;
+  return K <= 8192 ? 8 : 16;
+}
+
 hipError_t launch_norm_quantize(NormArgs a, int src, int b, hipStream_t stream) {
   a.logb = 0;
   while ((1 << a.logb) < b) ++a.logb;
   a.c_b = (float)(1.0 / std::sqrt((double)b));
   a.inv_K = 1.0 / (double)a.K;
-  const int cpt = a.K <= 8192 ? 8 : 16;
+  const int cpt = src == kNormX ? norm_width(a.T, a.K) : a.K <= 8192 ? 8 : 16;
   const unsigned threads = (unsigned)((a.K / cpt + 63) / 64 * 64);
   // cross-wave transform stages only where a block spans waves
   const size_t lds = a.codes != nullptr && b > 64 * cpt ? (size_t)8 * threads * sizeof(double) : 0;
-  if (cpt == 16) launch_nt<16, 1024>(a, src, threads, lds, stream);
+  const dim3 grid((unsigned)a.T);
+  if (cpt == 32) hipLaunchKernelGGL((norm_quantize_kernel<32, 512, kNormX>), grid, dim3(threads), lds, stream, a);
+  else if (cpt == 16) launch_nt<16, 1024>(a, src, threads, lds, stream);
   else if (threads <= 256) launch_nt<8, 256>(a, src, threads, lds, stream);
   else if (threads <= 512) launch_nt<8, 512>(a, src, threads, lds, stream);
   else launch_nt<8, 1024>(a, src, threads, lds, stream);
