@@ -201,8 +201,8 @@ hipError_t launch_adapter_gemm(const GemmArgs& a, AdapterArgs ad, const uint16_t
   const int rt = (ad.rank + 15) / 16;
   const int RT = rt >= 4 ? 4 : rt >= 2 ? 2 : 1, zr = (rt + RT - 1) / RT;
   // a decode batch's tile may hold 16 adapters, one a workgroup; in larger batches, where
-  // requests span tiles, a tile's workgroups take turns
-  const int ny = T <= 256 ? (int)(T < 16 ? T : 16) : 2;
+  // requests mostly span tiles, a tile's four workgroups take turns
+  const int most = (int)(T < 16 ? T : T <= 256 ? 16 : 4), ny = ad.n_adapters < most ? ad.n_adapters : most;
   const int64_t tiles = (T + 15) / 16;
   // parts of at least 8 steps of 32 channels (two a wave)
   ad.parts = 1;

@@ -85,9 +85,9 @@ template <> struct TileAdapters<true> {
 // into three bf16 parts (8 bits each, so their sum is u's 24 bits), whose products with lora_b
 // are exact and accumulate in fp32: 3 MFMAs per 16 ranks against K / 16 of the projection.
 // The split vectors are staged in the activation tiles' LDS, 32 ranks at a time, with a row of
-// zeros behind them.  Each 32-row sub-tile makes one pass per distinct adapter among its rows,
-// in which the other rows read the zeros; lora_b's fragments stay in registers while
-// consecutive sub-tiles use one adapter.  Where a fragment holds an infinity or NaN, zeros
+// zeros behind them.  One pass per distinct adapter among the tile's rows (one to three where
+// requests are contiguous), in which the other rows read the zeros, over the 32-row sub-tiles
+// that hold any of its rows; the next adapter's fragments of lora_b load meanwhile.  Where a fragment holds an infinity or NaN, zeros
 // would not keep it from the other rows, so that pass is summed apart and taken by its own
 // rows only.  This code runs once per tile, so its size in instructions is its time (a version
 // unrolled over ranks and split in registers took 60 us a tile).
@@ -142,32 +142,54 @@ __device__ __forceinline__ void add_adapter_terms(f32x16 (&acc)[NMS][NS], const 
     // one 32-column slot at a time: the accumulators leave few registers
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      int held = -1;                         // the adapter whose fragments are in bf
-      bool finite = true;                    // of those, over the wave
-      bf16x8 bf[2];
+      const int64_t n = nvalid[s] ? nrow[s] : 0;
+      auto fragments = [&](int a, u32x4 (&w)[2]) {
+        const uint16_t* lb = ad.lora_b + ((int64_t)a * ta.N + n) * ad.rank + rc + 8 * g;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          w[q] = rc + 16 * q + 8 * g < ad.rank ? *reinterpret_cast<const u32x4*>(lb + 16 * q) : u32x4{0, 0, 0, 0};
+      };
+      int of[NMS];
+      uint32_t todo[NMS];                    // the sub-tiles' rows whose adapter is still to come
 #pragma unroll
       for (int ms = 0; ms < NMS; ++ms) {
-        const int of = ta.s_of[ms * 32 + nl];
-        uint32_t todo = (uint32_t)__ballot(of >= 0);
-        while (todo != 0) {
-          const int a = __builtin_amdgcn_readlane(of, __builtin_ctz(todo));
-          const uint32_t mine = (uint32_t)__ballot(of == a);
-          todo &= ~mine;
-          if (a != held) {
-            held = a;
-            const uint16_t* lb = ad.lora_b + ((int64_t)a * ta.N + (nvalid[s] ? nrow[s] : 0)) * ad.rank + rc + 8 * g;
-            bool bad = false;
+        of[ms] = ta.s_of[ms * 32 + nl];
+        todo[ms] = (uint32_t)__ballot(of[ms] >= 0);
+      }
+      auto first_left = [&]() {              // the adapter of the first row left, -1: none
+        int a = -1;
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const u32x4 w = rc + 16 * q + 8 * g < ad.rank ? *reinterpret_cast<const u32x4*>(lb + 16 * q) : u32x4{0, 0, 0, 0};
+        for (int ms = NMS - 1; ms >= 0; --ms)
+          if (todo[ms] != 0) a = __builtin_amdgcn_readlane(of[ms], __builtin_ctz(todo[ms]));
+        return a;
+      };
+      int a = first_left();
+      u32x4 next[2];
+      if (a >= 0) fragments(a, next);
+#pragma unroll 1
+      while (a >= 0) {
+        bf16x8 bf[2];
+        bool bad = false;
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                bad = bad || (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u;
-              bf[q] = __builtin_bit_cast(bf16x8, w);
-            }
-            finite = __ballot(bad) == 0;
-          }
-          const uint8_t* u = stage + (of == a ? ms * 32 + nl : BM) * kStagePitch + 16 * g;
+        for (int q = 0; q < 2; ++q) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            bad = bad || (next[q][i] & 0x7F80u) == 0x7F80u || (next[q][i] & 0x7F800000u) == 0x7F800000u;
+          bf[q] = __builtin_bit_cast(bf16x8, next[q]);
+        }
+        const bool finite = __ballot(bad) == 0;
+        uint32_t mine[NMS];
+#pragma unroll
+        for (int ms = 0; ms < NMS; ++ms) {
+          mine[ms] = (uint32_t)__ballot(of[ms] == a);
+          todo[ms] &= ~mine[ms];
+        }
+        const int a1 = first_left();
+        if (a1 >= 0) fragments(a1, next);    // on their way during this adapter's products
+#pragma unroll
+        for (int ms = 0; ms < NMS; ++ms) {
+          if (mine[ms] == 0) continue;
+          const uint8_t* u = stage + (of[ms] == a ? ms * 32 + nl : BM) * kStagePitch + 16 * g;
           if (finite) {
 #pragma unroll
             for (int q = 0; q < 2; ++q)
@@ -187,9 +209,10 @@ __device__ __forceinline__ void add_adapter_terms(f32x16 (&acc)[NMS][NS], const 
                                                             bf[q], d, 0, 0, 0);
 #pragma unroll
             for (int v = 0; v < 16; ++v)
-              if ((mine >> (8 * (v / 4) + 4 * g + v % 4)) & 1u) acc[ms][s][v] += d[v];
+              if ((mine[ms] >> (8 * (v / 4) + 4 * g + v % 4)) & 1u) acc[ms][s][v] += d[v];
           }
         }
+        a = a1;
       }
     }
   }
