@@ -72,9 +72,10 @@ struct NormArgs {
   int act_bits;
   int64_t T;
   int K;
-  int logb;                   // set by the launcher, as the next two
+  int logb;                   // set by the launcher, as the next three
   float c_b;
   double inv_K;
+  int64_t t0;                 // first token of the launch
 };
 hipError_t launch_norm_quantize(NormArgs a, int src, int b, hipStream_t stream);
 

@@ -338,7 +338,8 @@ few_down_one_kernel(FewDownArgs a, int ksh) {
   float* u = reinterpret_cast<float*>(s_codes + (size_t)(nw >> ksh) * pitch) + row * ((F + 255) & ~255);
   if (split == 0) {
     const int b = F & -F;                    // >= 32
-    float amax = 0.0f;
+    uint32_t top = 0;                        // of |v|'s bits, which put NaN above infinity
+    auto take = [&](float x) { top = max(top, __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu); };
     f32x4 v = next;
 #pragma unroll 1
     for (int c = 4 * lane; c < ((F + 255) & ~255); c += 256) {
@@ -359,7 +360,9 @@ few_down_one_kernel(FewDownArgs a, int ksh) {
       if (b > 64) stage(std::integral_constant<int, 16>{});
       if (b > 128) stage(std::integral_constant<int, 32>{});
       *reinterpret_cast<f32x4*>(u + c) = v;  // zeros past F
-      if (b <= 256) amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))));
+      if (b <= 256)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) take(v[k]);
     }
     // a lane only ever touches its own channels (mod 256), so these passes need no barrier
 #pragma unroll 1
@@ -373,20 +376,18 @@ few_down_one_kernel(FewDownArgs a, int ksh) {
         *reinterpret_cast<f32x4*>(u + c + m) = z;
         if (2 * m == b)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fmaxf(fabsf(x[k]), fabsf(z[k])));
+          for (int k = 0; k < 4; ++k) {
+            take(x[k]);
+            take(z[k]);
+          }
       }
     }
-    amax = fmaxf(amax, xor_lane_f32<1>(amax));
-    amax = fmaxf(amax, xor_lane_f32<2>(amax));
-    amax = fmaxf(amax, xor_lane_f32<4>(amax));
-    amax = fmaxf(amax, xor_lane_f32<8>(amax));
-    amax = fmaxf(amax, xor_lane_f32<16>(amax));
-    amax = fmaxf(amax, xor_lane_f32<32>(amax));
+    const float amax = __builtin_bit_cast(float, wave_max_u32(top));
     // the quantiser of rotate_quantize
     const float Q = a.act_bits == 4 ? 7.0f : 127.0f, lo = a.act_bits == 4 ? -8.0f : -127.0f;
     constexpr float kMagic = 12582912.0f;
     const float s = amax / Q;
-    const double rs = amax > 0.0f ? 1.0 / (double)s : 0.0;
+    const double rs = amax != 0.0f ? 1.0 / (double)s : 0.0;
 #pragma unroll 1
     for (int c = 4 * lane; c < pitch / 2; c += 256) {   // zeros past F
       v = *reinterpret_cast<f32x4*>(u + c);
@@ -401,7 +402,7 @@ few_down_one_kernel(FewDownArgs a, int ksh) {
       *reinterpret_cast<uint32_t*>(d + 8) = __builtin_bit_cast(uint32_t, q[1]);
     }
     // the row's factor: its scale and its choice's weight (1 for a shared expert)
-    float f = amax > 0.0f ? s * a.c_b : 0.0f;
+    float f = amax != 0.0f ? s * a.c_b : 0.0f;
     if (row < topk) {
       const float w = choice_weight(lg, a.logits, a.E, topk, a.renormalize, lane);
       f *= __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), row));

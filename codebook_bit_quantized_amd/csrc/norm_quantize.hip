@@ -51,13 +51,17 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
   return v;
 }
 
-__device__ __forceinline__ float wave_max_f32(float v) {
-  v = fmaxf(v, xor_lane_f32<1>(v));
-  v = fmaxf(v, xor_lane_f32<2>(v));
-  v = fmaxf(v, xor_lane_f32<4>(v));
-  v = fmaxf(v, xor_lane_f32<8>(v));
-  v = fmaxf(v, xor_lane_f32<16>(v));
-  v = fmaxf(v, xor_lane_f32<32>(v));
+// Absolute maxima are taken over the bit patterns of |v|, which order as the values do and put
+// NaN above infinity, so a row that is not finite gets a scale that is not finite.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
+
+__device__ __forceinline__ uint32_t wave_max_bits(uint32_t v) {
+  v = max(v, (uint32_t)xor_lane<1>((int)v));
+  v = max(v, (uint32_t)xor_lane<2>((int)v));
+  v = max(v, (uint32_t)xor_lane<4>((int)v));
+  v = max(v, (uint32_t)xor_lane<8>((int)v));
+  v = max(v, (uint32_t)xor_lane<16>((int)v));
+  v = max(v, (uint32_t)xor_lane<32>((int)v));
   return v;
 }
 
@@ -121,11 +125,11 @@ __global__ void __launch_bounds__(NT)
 norm_quantize_kernel(NormArgs a) {
   extern __shared__ double xchg[];           // cross-wave transform stages: [8][blockDim]
   __shared__ double s_sum[2][16];            // per-wave sums of squares: post norm, norm
-  __shared__ float s_max[16];
+  __shared__ uint32_t s_max[16];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int nw = (int)blockDim.x >> 6;
-  const int64_t t = blockIdx.x;
+  const int64_t t = a.t0 + blockIdx.x;
   const int c0 = tid * CPT;
   const bool act = c0 < a.K;                 // K is a multiple of 32, so whole threads
   float f[CPT];                              // the row that is normed and quantised
@@ -275,17 +279,19 @@ norm_quantize_kernel(NormArgs a) {
   }
 
   // ---- per-token absmax ----
-  float u[CPT], amax = 0.0f;
+  float u[CPT];
+  uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
     u[i] = (float)v[i];
-    amax = fmaxf(amax, fabsf(u[i]));
+    top = max(top, abs_bits(u[i]));
   }
-  amax = wave_max_f32(amax);
-  if (lane == 0) s_max[wave] = amax;
+  top = wave_max_bits(top);
+  if (lane == 0) s_max[wave] = top;
   lds_barrier();
-  amax = s_max[0];
-  for (int w = 1; w < nw; ++w) amax = fmaxf(amax, s_max[w]);
+  top = s_max[0];
+  for (int w = 1; w < nw; ++w) top = max(top, s_max[w]);
+  const float amax = __builtin_bit_cast(float, top);
 
   // ---- quantise: the fp32 sequence of rotate_quantize (s = M / Q, q = clamp(rint(v / s)),
   // the quotient as fp64(v) * fp64(1 / s) rounded to fp32, rint by the magic-number add);
@@ -301,7 +307,7 @@ norm_quantize_kernel(NormArgs a) {
   const float s = amax / Q;
   const int lpb = b / CPT < 64 ? b / CPT : 64;   // lanes per block within a wave
   const bool neg = lpb > 1 && (__builtin_popcount((unsigned)lane & (unsigned)(lpb - 1)) & 1);
-  const double rs = amax > 0.0f ? (neg ? -1.0 : 1.0) / (double)s : 0.0;
+  const double rs = amax != 0.0f ? (neg ? -1.0 : 1.0) / (double)s : 0.0;
   if constexpr (SRC == kRotateF32) {
     // the codes as fp16, in the order the few-row GEMM dequantises weights to
     uint8_t* dst = a.codes + t * few_row16_bytes(a.K);
@@ -318,7 +324,7 @@ norm_quantize_kernel(NormArgs a) {
           u32x4{__builtin_bit_cast(uint32_t, d[0]), __builtin_bit_cast(uint32_t, d[1]),
                 __builtin_bit_cast(uint32_t, d[2]), __builtin_bit_cast(uint32_t, d[3])};
     }
-    if (tid == 0) a.scales[t] = amax > 0.0f ? s * a.c_b : 0.0f;
+    if (tid == 0) a.scales[t] = amax != 0.0f ? s * a.c_b : 0.0f;
     return;
   }
   uint32_t q[CPT];
@@ -349,12 +355,12 @@ norm_quantize_kernel(NormArgs a) {
 #pragma unroll
     for (int k = 0; k < CPT / 8; ++k) dst[k] = u32x2{w[2 * k], w[2 * k + 1]};
   }
-  if (tid == 0) a.scales[t] = amax > 0.0f ? s * a.c_b : 0.0f;
+  if (tid == 0) a.scales[t] = amax != 0.0f ? s * a.c_b : 0.0f;
 }
 
 template <int CPT, int NT>
-static void launch_nt(const NormArgs& a, int src, unsigned threads, size_t lds, hipStream_t stream) {
-  const dim3 grid((unsigned)a.T), block(threads);
+static void launch_nt(const NormArgs& a, int src, unsigned tokens, unsigned threads, size_t lds, hipStream_t stream) {
+  const dim3 grid(tokens), block(threads);
   if (src == kNormX) hipLaunchKernelGGL((norm_quantize_kernel<CPT, NT, kNormX>), grid, block, lds, stream, a);
   else if (src == kNormF32) hipLaunchKernelGGL((norm_quantize_kernel<CPT, NT, kNormF32>), grid, block, lds, stream, a);
   else if (src == kNormBF16) hipLaunchKernelGGL((norm_quantize_kernel<CPT, NT, kNormBF16>), grid, block, lds, stream, a);
@@ -381,13 +387,19 @@ hipError_t launch_norm_quantize(NormArgs a, int src, int b, hipStream_t stream) 
   const unsigned threads = (unsigned)((a.K / cpt + 63) / 64 * 64);
   // cross-wave transform stages only where a block spans waves
   const size_t lds = a.codes != nullptr && b > 64 * cpt ? (size_t)8 * threads * sizeof(double) : 0;
-  const dim3 grid((unsigned)a.T);
-  if (cpt == 32) hipLaunchKernelGGL((norm_quantize_kernel<32, 512, kNormX>), grid, dim3(threads), lds, stream, a);
-  else if (cpt == 16) launch_nt<16, 1024>(a, src, threads, lds, stream);
-  else if (threads <= 256) launch_nt<8, 256>(a, src, threads, lds, stream);
-  else if (threads <= 512) launch_nt<8, 512>(a, src, threads, lds, stream);
-  else launch_nt<8, 1024>(a, src, threads, lds, stream);
-  return hipGetLastError();
+  // a launch holds fewer than 2^32 threads
+  constexpr int64_t kMaxGrid = 1 << 21;
+  for (a.t0 = 0; a.t0 < a.T; a.t0 += kMaxGrid) {
+    const unsigned n = (unsigned)(a.T - a.t0 < kMaxGrid ? a.T - a.t0 : kMaxGrid);
+    if (cpt == 32) hipLaunchKernelGGL((norm_quantize_kernel<32, 512, kNormX>), dim3(n), dim3(threads), lds, stream, a);
+    else if (cpt == 16) launch_nt<16, 1024>(a, src, n, threads, lds, stream);
+    else if (threads <= 256) launch_nt<8, 256>(a, src, n, threads, lds, stream);
+    else if (threads <= 512) launch_nt<8, 512>(a, src, n, threads, lds, stream);
+    else launch_nt<8, 1024>(a, src, n, threads, lds, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace cbq

@@ -20,7 +20,7 @@
  *  - Empty work (zero tokens or rows) is a successful no-op.  Results for non-finite
  *    inputs are unspecified.
  *  - The library keeps no mutable global state; calls on different streams may run
- *    concurrently.
+ *    concurrently.  It computes no gradients.
  *  - bf16 / fp16 tensors are passed as uint16_t bit patterns.
  */
 #ifndef CBQ_H
@@ -359,7 +359,7 @@ enum {
  *  scales     : fp32 [T], its scales.  Without codes, scales, had_block and act_bits are
  *               not read.
  *  At least one of normed and codes is given.  A row of zeros gives n = 0, codes 0 and
- *  scale 0.
+ *  scale 0; a row that is not finite a scale that is not finite.
  */
 typedef struct {
   const float* weight;
@@ -404,6 +404,7 @@ int cbq_norm_rotate_quantize(const uint16_t* x, int64_t T, int32_t K, int64_t ld
  *               out = bf16(fp32(residual + scale * gate * y)), evaluated in fp64 and
  *               rounded to fp32, then to bf16.
  *  next       : NULL, or the norm taken of out (as cbq_norm_rotate_quantize of it).
+ *  Outputs must not overlap rows, gate or each other.
  *  0 <= topk <= 8, 0 <= n_shared <= 8, topk + n_shared >= 1; H as K above.
  */
 int cbq_combine_norm_residual(const void* rows, int32_t rows_type, int64_t ldr,
@@ -426,7 +427,7 @@ int cbq_combine_norm_residual(const void* rows, int32_t rows_type, int64_t ldr,
  *  down       : E + n_shared experts, N = H, K = F; its own bits and layout.
  *  y, y_type  : fp32 or bf16 (CBQ_TYPE_*) [T][ldy] (ldy >= H, ldy % 4 == 0, 16-byte
  *               aligned): y[t] = sum_j w_j out_j + the shared experts' outputs, summed in
- *               fp32 (j ascending, then the shared experts).
+ *               fp32 in a fixed order.
  *  ws, ws_bytes : device workspace of cbq_moe_few_workspace(...) bytes, 16-byte aligned;
  *               rewritten by every call, so it needs no clearing; calls that overlap in
  *               time need one each.
@@ -435,6 +436,8 @@ int cbq_combine_norm_residual(const void* rows, int32_t rows_type, int64_t ldr,
  *  transform and quantiser of cbq_rotate_quantize with F's own block (F & -F), and down's
  *  product of those codes.  (The sequence of single calls rounds h to bf16 first, so its
  *  codes of h differ now and then.)  Deterministic: no result depends on the order of atomics.
+ *  A token's non-finite scale or logits reach its own y only (logits that are all -inf have no
+ *  softmax: that token's y is NaN, as its routing weights are).
  *  Limits: 0 <= T <= CBQ_FEW_MAX_TOKENS (CBQ_EUNSUPPORTED above: use the single calls),
  *  H % 32 == 0, F % 32 == 0, H, F <= 16384, one expert's index block below 2 GiB.
  */

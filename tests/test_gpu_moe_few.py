@@ -216,3 +216,28 @@ def test_argument_checks():
     with pytest.raises(cbq.CbqError) as e:
         cbq.moe_ffn_few(codes[:1].repeat(many, 1), scales[:1].repeat(many), L[:1].repeat(many, 1), *dev, 2)
     assert e.value.status == cbq.CBQ_EUNSUPPORTED
+
+
+@pytest.mark.parametrize("T", [2, 9])
+def test_another_tokens_infinities_stay_with_it(T):
+    """A masked-out token (all logits -inf) and one with an infinite scale leave the other
+    tokens' outputs as they are, bit for bit."""
+    gate, up, down, x, lg = _inputs(T, 256, 128, 16, 4, 1, 3, 2, 4)
+    dev = [cbq.prepack_weights(upload_weights(w)) for w in (gate, up, down)]
+    codes, scales = cbq.rotate_quantize(bf16_dev(x), 4)
+    L = to_dev(lg)
+    run = lambda s, l: cbq.moe_ffn_few(codes, s, l, *dev, 4, 1, 4, y_dtype=torch.float32)  # noqa: E731
+    want = run(scales, L)
+    masked = L.clone()
+    masked[1] = float("-inf")
+    got = run(scales, masked)
+    keep = torch.arange(T, device=DEV) != 1
+    assert torch.equal(got[keep], want[keep]) and torch.isnan(got[1]).all()
+    huge = scales.clone()
+    huge[1] = float("inf")
+    got = run(huge, L)
+    assert torch.equal(got[keep], want[keep]) and not torch.isfinite(got[1]).all()
+    nan = L.clone()
+    nan[1, 3:9] = float("nan")
+    got = run(scales, nan)
+    assert torch.equal(got[keep], want[keep])

@@ -107,6 +107,27 @@ def test_norm_extreme_values():
     _check_codes(nb[[0, 2]], codes[[0, 2]], scales[[0, 2]], 0, 8)
 
 
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("K", [256, 16384])
+def test_a_row_that_is_not_finite_says_so_and_stays_alone(bad, K):
+    x = bf16_dev(datagen.random_tokens(8, 3, K))
+    w = to_dev(_weight(1, K))
+    want = cbq.norm_rotate_quantize(x, w, 1e-6, 8)
+    x[1, 5] = bad
+    got = cbq.norm_rotate_quantize(x, w, 1e-6, 8)
+    for a, b in zip(want, got):
+        assert torch.equal(a[[0, 2]], b[[0, 2]])
+    assert not torch.isfinite(got[2][1])
+    rows = torch.randn((3, K), device=DEV)
+    res = bf16_dev(datagen.random_tokens(9, 3, K))
+    want = cbq.combine_norm_residual(rows, res, post_weight=w, next_weight=w, act_bits=8)
+    rows[1, 7] = bad
+    got = cbq.combine_norm_residual(rows, res, post_weight=w, next_weight=w, act_bits=8)
+    for a, b in zip(want, got):
+        assert torch.equal(a[[0, 2]], b[[0, 2]])
+    assert not torch.isfinite(got[0][1].float()).all() and not torch.isfinite(got[3][1])
+
+
 def _block_case(T, H, topk, n_shared, bf16_rows, post, gate, nxt, act_bits=8, pad=0, in_place=False, scale=0.75):
     rng = np.random.default_rng(T * 7 + H + topk)
     n = T * topk + n_shared * T
