@@ -84,40 +84,80 @@ template <> struct TileAdapters<true> {
 // sum_r u[m][r] lora_b[a][n][r], a the row's adapter.  u (its parts summed in order) is split
 // into three bf16 parts (8 bits each, so their sum is u's 24 bits), whose products with lora_b
 // are exact and accumulate in fp32: 3 MFMAs per 16 ranks against K / 16 of the projection.
-// The split vectors are staged in the activation tiles' LDS, 32 ranks at a time, with a row of
+// The split vectors are staged in the activation tiles' LDS, 32 or 64 ranks at a time, with a row of
 // zeros behind them.  One pass per distinct adapter among the tile's rows (one to three where
 // requests are contiguous), in which the other rows read the zeros, over the 32-row sub-tiles
 // that hold any of its rows; the next adapter's fragments of lora_b load meanwhile.  Where a fragment holds an infinity or NaN, zeros
 // would not keep it from the other rows, so that pass is summed apart and taken by its own
 // rows only.  This code runs once per tile, so its size in instructions is its time (a version
 // unrolled over ranks and split in registers took 60 us a tile).
-constexpr int kStageRanks = 32, kStagePitch = 2 * kStageRanks + 16;   // bytes; the padding staggers the banks
+// ranks staged at a time; the small tiles have the registers to stage 64 with all loads in flight
+template <int BM, int NS> constexpr int stage_ranks() { return BM == 128 && NS == 1 ? 64 : 32; }
+template <int BM, int NS> constexpr int stage_pitch() { return 2 * stage_ranks<BM, NS>() + 16; }   // bytes; padded for the banks
+// fp16 that an activation tile holds beyond its rows to make room for the stage
+template <int BM, int NS, bool ADP> constexpr int stage_pad() {
+  const int need = (3 * (BM + 1) * stage_pitch<BM, NS>() + 3) / 4, have = BM * LDW;
+  return ADP && need > have ? (need - have + 7) / 8 * 8 : 0;
+}
 template <int BM, int NMS, int NS>
 __device__ __forceinline__ void add_adapter_terms(f32x16 (&acc)[NMS][NS], const TileAdapters<true>& ta, uint8_t* stage,
                                                   int rows, int tid, int nl, int g, const int* nrow, const bool* nvalid) {
+  constexpr int SR = stage_ranks<BM, NS>(), kStagePitch = stage_pitch<BM, NS>(), Q = SR / 16;
   constexpr uint32_t kPlane = (BM + 1) * kStagePitch;
   const AdapterArgs& ad = ta.ad;
-  for (int rc = 0; rc < ad.rank; rc += kStageRanks) {
+  int of[NMS];
+#pragma unroll
+  for (int ms = 0; ms < NMS; ++ms) of[ms] = ta.s_of[ms * 32 + nl];
+  uint32_t todo[NMS];                        // the sub-tiles' rows whose adapter is still to come
+  auto all_left = [&]() {
+#pragma unroll
+    for (int ms = 0; ms < NMS; ++ms) todo[ms] = (uint32_t)__ballot(of[ms] >= 0);
+  };
+  auto first_left = [&]() {                  // the adapter of the first row left, -1: none
+    int a = -1;
+#pragma unroll
+    for (int ms = NMS - 1; ms >= 0; --ms)
+      if (todo[ms] != 0) a = __builtin_amdgcn_readlane(of[ms], __builtin_ctz(todo[ms]));
+    return a;
+  };
+  u32x4 next[Q];
+  auto fragments = [&](int a, int rc, int s) {
+    const int64_t n = nvalid[s] ? nrow[s] : 0;
+    const uint16_t* lb = ad.lora_b + ((int64_t)a * ta.N + n) * ad.rank + rc + 8 * g;
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      next[q] = rc + 16 * q + 8 * g < ad.rank ? *reinterpret_cast<const u32x4*>(lb + 16 * q) : u32x4{0, 0, 0, 0};
+  };
+  for (int rc = 0; rc < ad.rank; rc += SR) {
+    all_left();
+    int a = first_left();
+    if (a >= 0) fragments(a, rc, 0);         // on their way during the staging
     lds_barrier();                           // the main loop's (or the last pass's) reads are done
-    // four rows' loads in flight a thread: they come from another launch's results, far away
-    constexpr int kQuads = kStageRanks / 4;
+    // four pieces of PF parts in flight a thread: they come from another launch's results, far
+    // away
+    constexpr int kQuads = SR / 4, PF = SR == 64 ? 4 : 1;
 #pragma unroll 1
     for (int i0 = tid; i0 < (BM + 1) * kQuads; i0 += 4 * 256) {
       f32x4 vs[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) vs[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-      for (int p = 0; p < ad.parts; ++p) {
-        f32x4 w[4];
+      for (int p0 = 0; p0 < ad.parts; p0 += PF) {
+        f32x4 w[4][PF];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int i = i0 + 256 * j, m = i / kQuads, r = 4 * (i % kQuads);
-          w[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-          if (m < rows && rc + r < ad.rank)
-            w[j] = *reinterpret_cast<const f32x4*>(ad.u + p * ad.part_stride + (ta.m0 + m) * ad.rank + rc + r);
+          const bool in = m < rows && rc + r < ad.rank;
+          const float* u = ad.u + p0 * ad.part_stride + (in ? (ta.m0 + m) * ad.rank + rc + r : 0);
+#pragma unroll
+          for (int p = 0; p < PF; ++p)
+            w[j][p] = in && p0 + p < ad.parts ? *reinterpret_cast<const f32x4*>(u + p * ad.part_stride)
+                                              : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) vs[j] += w[j];
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int p = 0; p < PF; ++p) vs[j] += w[j][p];
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -142,36 +182,17 @@ __device__ __forceinline__ void add_adapter_terms(f32x16 (&acc)[NMS][NS], const 
     // one 32-column slot at a time: the accumulators leave few registers
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      const int64_t n = nvalid[s] ? nrow[s] : 0;
-      auto fragments = [&](int a, u32x4 (&w)[2]) {
-        const uint16_t* lb = ad.lora_b + ((int64_t)a * ta.N + n) * ad.rank + rc + 8 * g;
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          w[q] = rc + 16 * q + 8 * g < ad.rank ? *reinterpret_cast<const u32x4*>(lb + 16 * q) : u32x4{0, 0, 0, 0};
-      };
-      int of[NMS];
-      uint32_t todo[NMS];                    // the sub-tiles' rows whose adapter is still to come
-#pragma unroll
-      for (int ms = 0; ms < NMS; ++ms) {
-        of[ms] = ta.s_of[ms * 32 + nl];
-        todo[ms] = (uint32_t)__ballot(of[ms] >= 0);
+      if (s > 0) {
+        all_left();
+        a = first_left();
+        if (a >= 0) fragments(a, rc, s);
       }
-      auto first_left = [&]() {              // the adapter of the first row left, -1: none
-        int a = -1;
-#pragma unroll
-        for (int ms = NMS - 1; ms >= 0; --ms)
-          if (todo[ms] != 0) a = __builtin_amdgcn_readlane(of[ms], __builtin_ctz(todo[ms]));
-        return a;
-      };
-      int a = first_left();
-      u32x4 next[2];
-      if (a >= 0) fragments(a, next);
 #pragma unroll 1
       while (a >= 0) {
-        bf16x8 bf[2];
+        bf16x8 bf[Q];
         bool bad = false;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < Q; ++q) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             bad = bad || (next[q][i] & 0x7F80u) == 0x7F80u || (next[q][i] & 0x7F800000u) == 0x7F800000u;
@@ -185,24 +206,26 @@ __device__ __forceinline__ void add_adapter_terms(f32x16 (&acc)[NMS][NS], const 
           todo[ms] &= ~mine[ms];
         }
         const int a1 = first_left();
-        if (a1 >= 0) fragments(a1, next);    // on their way during this adapter's products
+        if (a1 >= 0) fragments(a1, rc, s);   // on their way during this adapter's products
 #pragma unroll
         for (int ms = 0; ms < NMS; ++ms) {
           if (mine[ms] == 0) continue;
           const uint8_t* u = stage + (of[ms] == a ? ms * 32 + nl : BM) * kStagePitch + 16 * g;
           if (finite) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+            for (int q = 0; q < Q; ++q) {
+              if (rc + 16 * q >= ad.rank) continue;
 #pragma unroll
               for (int k = 0; k < 3; ++k)
                 acc[ms][s] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
                     *reinterpret_cast<const bf16x8*>(u + k * kPlane + 32 * q), bf[q], acc[ms][s], 0, 0, 0);
+            }
           } else {
             f32x16 d;
 #pragma unroll
             for (int v = 0; v < 16; ++v) d[v] = 0.0f;
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+            for (int q = 0; q < Q; ++q)
 #pragma unroll
               for (int k = 0; k < 3; ++k)
                 d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(u + k * kPlane + 32 * q),
@@ -221,7 +244,7 @@ __device__ __forceinline__ void add_adapter_terms(f32x16 (&acc)[NMS][NS], const 
 // NS: 32-column weight slots per wave (2; 1 for a single matrix in 128-column tiles).
 // ADP: the adapters' terms are added to the scaled sums before they are stored (N: columns).
 template <int BITS, int ABITS, int NW, int NMS, bool LT, bool BLK, int BM, int NS, bool ADP>
-__device__ __forceinline__ void tile_run(const TileCtx<BITS, ABITS, LT>& c, uint16_t (*As)[BM * LDW],
+__device__ __forceinline__ void tile_run(const TileCtx<BITS, ABITS, LT>& c, uint16_t (*As)[BM * LDW + stage_pad<BM, NS, ADP>()],
                                          const float* s_scale, const uint32_t* s_rowoff,
                                          __amdgpu_buffer_rsrc_t ores, const TileAdapters<ADP>& ta) {
   const int K = c.K, g = c.g, nl = c.nl, tid = c.tid;
@@ -382,7 +405,6 @@ __device__ __forceinline__ void tile_run(const TileCtx<BITS, ABITS, LT>& c, uint
 #pragma unroll
   for (int s = 0; s < NS; ++s) coff[s] = c.nvalid[s] ? (uint32_t)c.nrow[s] * ESZ : kOffCol;
   if constexpr (ADP) {                                   // the stores below take the sums as they are
-    static_assert(2 * BM * LDW * 2 >= 3 * (BM + 1) * kStagePitch, "the adapters' vectors are staged in the activation tiles");
 #pragma unroll
     for (int ms = 0; ms < NMS; ++ms)
 #pragma unroll
@@ -461,7 +483,7 @@ mfma_prefill_kernel(const uint8_t* __restrict__ codes, const float* __restrict__
   // LDS pair tables: per wave, two matrix slots of 32 rows, NE entries each
   constexpr int NE = LT ? PairTab<BITS>::NE : 1;
   __shared__ __attribute__((aligned(16))) uint32_t Tab[LT ? 4 * 2 * NE * 32 : 1];
-  __shared__ __attribute__((aligned(16))) uint16_t As[2][BM * LDW];
+  __shared__ __attribute__((aligned(16))) uint16_t As[2][BM * LDW + stage_pad<BM, NS, ADP>()];
   __shared__ __attribute__((aligned(16))) float s_scale[BM];
   __shared__ __attribute__((aligned(16))) uint32_t s_rowoff[BM];   // byte offset of each row in out
   __shared__ int64_t s_r0, s_me, s_m0, s_ttot;
