@@ -18,12 +18,17 @@
 //   3. rotation and quantisation of h's rows, codes left in fp16 (norm_quantize.hip);
 //   4. down: the expert rows;
 //   5. the weighted sum of each token's rows.
-// One token with F <= 2048, where launches and dependent loads are most of it:
+// One token with a short h (one_token_form), where launches and dependent loads are most of it:
 //   1. gate/up whose waves find their choice's expert from the logits themselves;
 //   2. one kernel for the rest: every workgroup rotates and quantises all rows of h (a few
 //      thousand values), a wave a row, multiplies its 16 columns of down and combines them.
 // These two run every instruction a few times only, so instruction fetches count: their loops
 // stay rolled where the unrolled code would run once.
+//
+// Measured (us; weights of three layers in turn): 128 experts, top 8, 2048 x 768, 4 bits: one
+// token 9.4 + 8.5 (the batch form takes 26 a call, this one 17); 32 tokens 4.8 + 50 + 4.8 + 31
+// + 5.1.  64 + 2 experts, 2048 x 1408, 3 and 2 bits, 8 tokens 3.9 + 26 + 4.8 + 14 + 4.8.  8
+// experts, top 2, 4096 x 14336, 4 bits, 16 tokens 4.8 + 109 + 9 + 61 + 4.8.
 // h is kept in fp32 up to the quantiser: the codes are those of the unrounded h up to fp32
 // sums (a bf16 h would move a code wherever its rounding crosses a border).
 #include "cbq_internal.hpp"
@@ -172,6 +177,12 @@ __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + e
 // CW * SK waves: CW column tiles, each with K split over SK waves.  blockIdx.y: an expert, or,
 // when there are fewer choices than experts, a choice (the first one of its expert does the
 // work).  An expert of more than 16 rows sweeps its weights twice.
+// Bound by reading the weights and, at 4 bits, by looking them up (23 vector instructions for 8
+// weights: about 26 us of the 50 for 362 million weights), which overlap in part: 128 experts
+// at 32 tokens 181 MB in 50 us (3.6 TB/s) and 95 MB in 31 us; 8 wide experts 477 MB in 109 us
+// (4.4 TB/s) and 236 MB in 61 us, where a large copy reaches 5.1.  Five waves a SIMD and two
+// chunks in flight: four waves measured the same to 2 % slower, four chunks 5 to 17 % slower
+// (their registers cost waves).
 template <int BITS, bool PAIR, bool BLK, int DEPTH>
 __global__ void __launch_bounds__(512, 5)
 few_gemm_kernel(FewArgs a, int CW, int SK) {
@@ -255,7 +266,9 @@ few_gemm_kernel(FewArgs a, int CW, int SK) {
 }
 
 // Gate/up of one token, on its packed codes.  blockIdx.y: a choice, then the shared experts;
-// row y of h.  The SK waves split K.
+// row y of h.  The SK waves split K.  Bound by its chain of loads: the logits, then the
+// codebooks and first indices of the expert they name, about 1 us each, behind the launch and
+// the instruction fetches (8 experts of 2048 x 768, 13 MB: 9.4 us).
 template <int BITS, int ABITS, bool BLK, int DEPTH>
 __global__ void __launch_bounds__(512, 4)
 few_gate_one_kernel(FewArgs a, int SK) {
@@ -301,9 +314,10 @@ few_gate_one_kernel(FewArgs a, int SK) {
   }
 }
 
-constexpr int kOneF = 2048;                  // h rows of the one-token form: at most this long
-
 // The rest of the one-token form.  Workgroup: 16 columns of y; wave = row << ksh | split of K.
+// Every workgroup repeats the rotation of all rows (6144 values at 8 rows of 768), which costs
+// less than the launches it saves while the rows are few and short (one_token_form): 8.5 us for
+// the 6.8 MB of down.
 template <int BITS, bool BLK, int DEPTH>
 __global__ void __launch_bounds__(1024)
 few_down_one_kernel(FewDownArgs a, int ksh) {
@@ -481,6 +495,9 @@ few_combine_kernel(const float* __restrict__ rows, const float* __restrict__ wts
   }
 }
 
+// K is split until about 4096 waves share the sweep, while each keeps at least four chunks:
+// half as many waves leave the down sweeps 3 to 17 % slower, twice as many the others up to
+// 8 % (two or eight chunks at least: the same within 2 %).
 template <int BITS, bool PAIR, bool BLK>
 static hipError_t launch_few_gemm(const FewArgs& a, hipStream_t stream) {
   const int ys = (a.T * a.topk < a.E ? a.T * a.topk : a.E) + a.n_shared;
@@ -531,10 +548,14 @@ static hipError_t launch_down_one(const FewDownArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// The one-token form: its rows fit a workgroup's waves, and their codes and values its LDS.
+// The one-token form: its rows have a wave each, which transforms F values, and all of them
+// together their codes and values in LDS (at most 87 KB at these limits).  Beyond the limits
+// that repeated work costs more than the batch form's three launches (4 bits, us a call, this
+// form / batch): 8 rows of 768 17.4 / 24.1, 8 of 1408 23.2 / 27.9, 8 of 2048 33.1 / 31.0, 2 of
+// 2048 17.3 / 24.3, 2 of 4096 32.5 / 29.1, 2 of 8192 60 / 44.
 static bool one_token_form(int64_t T, int topk, int n_shared, int F) {
   const int R = topk + n_shared;
-  return T == 1 && R <= 16 && F <= kOneF && (size_t)R * (few_row16_bytes(F) + (F + 255) / 256 * 1024) <= 150 * 1024;
+  return T == 1 && R <= 16 && F <= 2048 && R * F <= 12288;
 }
 
 // Workspace: ids and weights, the input's fp16 codes, then h, its fp16 codes and scales, then

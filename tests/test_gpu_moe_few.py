@@ -101,6 +101,12 @@ def test_one_token(H, F, E, topk, n_shared, act_bits):
     _check_layer(1, H, F, E, topk, n_shared, 2, 4, act_bits, renorm=False, blocked=False, y_dtype=torch.bfloat16)
 
 
+@pytest.mark.parametrize("F,topk,n_shared", [(2048, 4, 2), (768, 8, 8), (800, 8, 8), (1536, 8, 0), (1568, 8, 0), (2048, 6, 1)])
+def test_one_token_at_the_limits_of_its_form(F, topk, n_shared):
+    """12288 values of h and 2048 a row are the one-token form's largest; beyond, the batch form runs."""
+    _check_layer(1, 64, F, 9, topk, n_shared, 4, 3, 8)
+
+
 @pytest.mark.parametrize("renorm", [False, True])
 @pytest.mark.parametrize("y_dtype", [torch.float32, torch.bfloat16])
 def test_weights_and_output_types(renorm, y_dtype):
