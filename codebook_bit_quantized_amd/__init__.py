@@ -11,6 +11,12 @@ and ``moe_ffn``, which sequences them into one MoE FFN layer, and
 ``refit_codebooks``, the output-aware centroid refit on calibration activations), and
 ``cpu_lut_gemm``, the LUT GEMM on host cores, and ``rotate_quantize_dense`` (with
 ``rotate_dense_workspace``), a dense K x K rotation in place of the Hadamard blocks.
+
+Around the layer in a decoder block: ``norm_rotate_quantize`` (the norm before a block and its
+codes), ``combine_norm_residual`` (after it: combine, norm, gate, residual, the next norm),
+``moe_ffn_few`` (the whole layer for at most ``FEW_MAX_TOKENS`` tokens, with
+``moe_few_workspace``) and ``codebook_adapter_gemm`` (a projection with the low-rank adapters of
+many requests, with ``adapter_workspace``).
 """
 from ._binding import (AUTO_MAX_LUT_ROWS, CBQ_EHIP, CBQ_EINVAL, CBQ_EUNSUPPORTED, CBQ_EWORKSPACE,
                        CBQ_OK, EPI_F32, EPI_SWIGLU_BF16, EXPORTED, LIB_PATH, PATH_AUTO, PATH_LUT,
