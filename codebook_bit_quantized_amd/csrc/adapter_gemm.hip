@@ -6,36 +6,61 @@
 //
 // Two launches.  The first forms u[t] = s_a A_a x[t] (fp32, [T][rank]) for every token that
 // has an adapter; the second is the projection, whose epilogue adds B_a u[t] before the only
-// store of out, so the adapters cost no pass over out.  Nothing is sorted: a tile of 16 or 32
-// tokens works through the distinct adapters among its own tokens (one or two where requests
-// are contiguous, up to one a token in a decode batch), with results taken only for the
-// tokens of that adapter, so another adapter's infinities never reach a token.
+// store of out, so the adapters cost no pass over out.  A tile works through the distinct
+// adapters among its own tokens (one or two where requests are contiguous, up to one a token in
+// a decode batch), with results taken only for the tokens of that adapter, so another adapter's
+// infinities never reach a token.  Beyond a decode batch, tiles of both launches take their
+// group's tokens by adapter (order_by_adapter), which no result depends on: 4096 tokens in
+// random order over 32 adapters of rank 64 176 + 608 us without, 68 + 455 with.
 #include "cbq_internal.hpp"
+#include "adapter_device.hpp"
 #include "few_device.hpp"
 
 namespace cbq {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-// u = s_a A_a x for 16 tokens and RT * 16 rank rows, part z of K.  Workgroup (tile, y, z): the
-// distinct adapters y, y + ny, ... of the tile, rank rows from 16 RT (z / parts) on, channels
-// of part z % parts; the waves split those and their sums meet in LDS in wave order.  The
-// parts are summed by the projection.  Bound by load latency in a decode batch (so K is cut
-// into enough parts to have all of an adapter's rows in flight at once: 16 tokens, K = 9728,
-// rank 32, 16 adapters, 10 MB: 12 us in one part, 5.0 in 8), by its short sweeps in a prefill
-// batch (4096 x 2560, rank 16: 21 MB of x in 12.6 us).
-template <int RT>
+// u = s_a A_a x for 16 tokens (ORDER: of a group of 256 in their order by adapter) and RT * 16
+// rank rows, part z of K.  Workgroup (tile, y, z): the distinct adapters y, y + ny, ... of the
+// tile, rank rows from 16 RT (z / parts) on, channels of part z % parts; the waves split those
+// and their sums meet in LDS in wave order.  The parts are summed by the projection.  Bound by
+// load latency in a decode batch (so K is cut into enough parts to have all of an adapter's
+// rows in flight at once: 16 tokens, K = 9728, rank 32, 16 adapters, 10 MB: 12 us in one part,
+// 5.4 in 8), by its short sweeps in a prefill batch (4096 x 2560, rank 16: 21 MB of x in 12 us).
+template <int RT, bool ORDER>
 __global__ void __launch_bounds__(256)
 adapter_shrink_kernel(AdapterArgs a, const uint16_t* __restrict__ x, int64_t ldx, const uint16_t* __restrict__ lora_a,
                       const float* __restrict__ adapter_scale, int64_t T, int K, float* __restrict__ u) {
   __shared__ f32x4 red[3][RT][64];
+  __shared__ __attribute__((aligned(16))) uint32_t s_key[ORDER ? 256 : 1];
+  __shared__ int s_tok[16], s_of[16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, g = lane >> 4;
-  const int64_t t0 = (int64_t)blockIdx.x * 16;
-  const int of = t0 + m < T ? a.of[t0 + m] : -1;
+  // neighbouring tiles, which mostly share adapters, on one XCD
+  const int nt = (int)gridDim.x, xcd = (int)blockIdx.x & 7;
+  const int tile = xcd * (nt >> 3) + min(xcd, nt & 7) + ((int)blockIdx.x >> 3);
+  int of;
+  int64_t t0 = (int64_t)tile * 16;           // the first token, or the first of the group
+  if constexpr (!ORDER) {
+    of = t0 + m < T ? a.of[t0 + m] : -1;
+    if (threadIdx.x < 16) s_tok[threadIdx.x] = threadIdx.x;
+    lds_barrier();
+  } else {
+    t0 &= ~(int64_t)255;
+    const int first = (tile & 15) * 16, n = (int)min(T - t0, (int64_t)256);
+    if (threadIdx.x < 16) s_of[threadIdx.x] = -1;
+    order_by_adapter<256>(a.of + t0, n, a.n_adapters, threadIdx.x, s_key, [&](int place, int t, int ad) {
+      if ((place & ~15) == first) {
+        s_tok[place & 15] = t;
+        s_of[place & 15] = ad;
+      }
+    });
+    lds_barrier();
+    of = s_of[m];
+  }
   const int part = (int)blockIdx.z % a.parts, r0 = (int)blockIdx.z / a.parts * 16 * RT;
-  // 32-channel steps [k0, k1) of this wave
-  const int nc = K >> 5, cpp = (nc + a.parts - 1) / a.parts, p1 = min(nc, (part + 1) * cpp), cpw = (cpp + 3) >> 2;
+  // 64-channel steps [k0, k1) of this wave
+  const int nc = (K + 63) >> 6, cpp = (nc + a.parts - 1) / a.parts, p1 = min(nc, (part + 1) * cpp), cpw = (cpp + 3) >> 2;
   const int k0 = part * cpp + wave * cpw, k1 = min(p1, k0 + cpw);
 
   uint32_t todo = (uint32_t)__ballot((uint32_t)of < (uint32_t)a.n_adapters) & 0xFFFFu;
@@ -44,32 +69,51 @@ adapter_shrink_kernel(AdapterArgs a, const uint16_t* __restrict__ x, int64_t ldx
     const uint32_t mine = (uint32_t)__ballot(of == ad) & 0xFFFFu;
     todo &= ~mine;
     if (i % (int)gridDim.y != (int)blockIdx.y) continue;
-    const bool row = (mine >> m) & 1u;
-    const uint16_t* px = x + (row ? (t0 + m) * ldx : 0) + 8 * g;
-    const uint16_t* pa = lora_a + ((int64_t)ad * a.rank + r0) * K + 8 * g;
+    // Every load has a valid address, so none needs a lane's branch: other adapters' rows of x
+    // and ranks past the last only feed results that are not stored.  A step is 64 channels, a
+    // whole 128-byte line of each row: lane group g takes 16 g .. 16 g + 15, in two loads on end
+    // (with steps of half a line L1 had lost the line before its other half was read).
+    const uint16_t* px = x + (t0 + s_tok[(mine >> m) & 1u ? m : __builtin_ctz(mine)]) * ldx;
+    const char* pa = reinterpret_cast<const char*>(lora_a + ((int64_t)ad * a.rank + r0) * K);
+    uint32_t ra[RT];
+#pragma unroll
+    for (int q = 0; q < RT; ++q) ra[q] = (uint32_t)(min(q * 16 + m, a.rank - 1 - r0) * K) * 2;
     f32x4 acc[RT];
 #pragma unroll
     for (int q = 0; q < RT; ++q) acc[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int UN = RT >= 4 ? 3 : RT == 2 ? 5 : 6;   // steps in flight
+    constexpr int UN = 3;                    // steps in flight (4: registers cost waves)
     for (int k = k0; k < k1; k += UN) {
-      u32x4 xv[UN], av[UN][RT];
+      u32x4 xv[UN][2], av[UN][2][RT];
 #pragma unroll
       for (int j = 0; j < UN; ++j) {
-        const bool in = k + j < k1;
-        xv[j] = in && row ? *reinterpret_cast<const u32x4*>(px + (k + j) * 32) : u32x4{0, 0, 0, 0};
+        if (k + j >= k1) continue;
+        // the last step's channels past K: any valid ones, cleared below
+        const int c = min((k + j) * 64 + 16 * g, K - 16);
 #pragma unroll
-        for (int q = 0; q < RT; ++q) {
-          const int r = q * 16 + m;
-          av[j][q] = in && r0 + r < a.rank ? *reinterpret_cast<const u32x4*>(pa + (int64_t)r * K + (k + j) * 32)
-                                           : u32x4{0, 0, 0, 0};
+        for (int h = 0; h < 2; ++h) {
+          xv[j][h] = *reinterpret_cast<const u32x4*>(px + c + 8 * h);
+#pragma unroll
+          for (int q = 0; q < RT; ++q) av[j][h][q] = *reinterpret_cast<const u32x4*>(pa + ra[q] + (uint32_t)(2 * c + 16 * h));
         }
       }
 #pragma unroll
-      for (int j = 0; j < UN; ++j)
+      for (int j = 0; j < UN; ++j) {
+        if (k + j >= k1) continue;
+        if ((k + j) * 64 + 64 > K && g >= 2) {
 #pragma unroll
-        for (int q = 0; q < RT; ++q)
-          acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv[j]),
-                                                           __builtin_bit_cast(bf16x8, av[j][q]), acc[q], 0, 0, 0);
+          for (int h = 0; h < 2; ++h) {
+            xv[j][h] = u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int q = 0; q < RT; ++q) av[j][h][q] = u32x4{0, 0, 0, 0};
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int q = 0; q < RT; ++q)
+            acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv[j][h]),
+                                                             __builtin_bit_cast(bf16x8, av[j][h][q]), acc[q], 0, 0, 0);
+      }
     }
     if (wave > 0) {
 #pragma unroll
@@ -86,7 +130,7 @@ adapter_shrink_kernel(AdapterArgs a, const uint16_t* __restrict__ x, int64_t ldx
         const int r = r0 + q * 16 + m;       // lane holds D[4 g + i][m]
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (((mine >> (4 * g + i)) & 1u) && r < a.rank) up[(t0 + 4 * g + i) * a.rank + r] = s * acc[q][i];
+          if (((mine >> (4 * g + i)) & 1u) && r < a.rank) up[(t0 + s_tok[4 * g + i]) * a.rank + r] = s * acc[q][i];
       }
     }
     lds_barrier();                           // red is free for the next adapter
@@ -214,14 +258,18 @@ hipError_t launch_adapter_gemm(const GemmArgs& a, AdapterArgs ad, const uint16_t
   // 5.0 us with 16 workgroups, 9.1 with four, 21 with one; 333 tokens 9.0, 9.0, 14.2)
   const int most = (int)(T < 16 ? T : T <= 256 ? 16 : 4), ny = ad.n_adapters < most ? ad.n_adapters : most;
   const int64_t tiles = (T + 15) / 16;
-  // parts of at least 8 steps of 32 channels (two a wave)
+  // parts of at least 4 steps of 64 channels (one a wave)
   ad.parts = 1;
-  while (ad.parts * 2 <= adapter_max_parts(T) && ad.parts * 2 * 8 <= a.K / 32 && tiles * ny * zr * ad.parts < 1024) ad.parts *= 2;
+  while (ad.parts * 2 <= adapter_max_parts(T) && ad.parts * 2 * 4 <= (a.K + 63) / 64 && tiles * ny * zr * ad.parts < 1024) ad.parts *= 2;
   ad.part_stride = T * ad.rank;
   const dim3 grid((unsigned)tiles, (unsigned)ny, (unsigned)(zr * ad.parts));
-  if (RT == 4) hipLaunchKernelGGL(adapter_shrink_kernel<4>, grid, dim3(256), 0, stream, ad, x, ldx, lora_a, adapter_scale, T, a.K, u);
-  else if (RT == 2) hipLaunchKernelGGL(adapter_shrink_kernel<2>, grid, dim3(256), 0, stream, ad, x, ldx, lora_a, adapter_scale, T, a.K, u);
-  else hipLaunchKernelGGL(adapter_shrink_kernel<1>, grid, dim3(256), 0, stream, ad, x, ldx, lora_a, adapter_scale, T, a.K, u);
+  const auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, ad, x, ldx, lora_a, adapter_scale, T, a.K, u);
+  };
+  const bool order = T > kFewRows;
+  if (RT == 4) order ? launch(adapter_shrink_kernel<4, true>) : launch(adapter_shrink_kernel<4, false>);
+  else if (RT == 2) order ? launch(adapter_shrink_kernel<2, true>) : launch(adapter_shrink_kernel<2, false>);
+  else order ? launch(adapter_shrink_kernel<1, true>) : launch(adapter_shrink_kernel<1, false>);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (T > kFewRows) return launch_mfma_prefill_adapter(a, ad, stream);

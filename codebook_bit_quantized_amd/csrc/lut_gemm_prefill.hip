@@ -27,6 +27,7 @@
 // runs that share its weights in one L2.
 #include <algorithm>
 
+#include "adapter_device.hpp"
 #include "cbq_internal.hpp"
 
 namespace cbq {
@@ -76,6 +77,7 @@ template <bool ADP> struct TileAdapters {};
 template <> struct TileAdapters<true> {
   AdapterArgs ad;
   const int32_t* s_of;
+  const uint8_t* s_tok;                      // the tile's token of each row
   int64_t m0;
   int N;
 };
@@ -93,8 +95,8 @@ template <> struct TileAdapters<true> {
 // instructions is its time (a version unrolled over ranks and split in registers took 60 us a
 // tile).  2560 -> 9728, 4-bit codebooks: 4096 tokens in 8 requests, rank 16, 240 us (0.85
 // PFLOP/s; 256 us without adapters in the tiles of 256 columns), 333 tokens of rank 64 47 us;
-// 4096 tokens in random order over 32 adapters of rank 64 take 690 us, a pass per adapter and
-// tile.
+// 4096 tokens in random order over 32 adapters of rank 64 take 455 us, a pass per adapter and
+// tile whose fragments of lora_b (637 MB over the tiles) come one pass ahead.
 // ranks staged at a time; the small tiles have the registers to stage 64 with all loads in flight
 template <int BM, int NS> constexpr int stage_ranks() { return BM == 128 && NS == 1 ? 64 : 32; }
 template <int BM, int NS> constexpr int stage_pitch() { return 2 * stage_ranks<BM, NS>() + 16; }   // bytes; padded for the banks
@@ -152,7 +154,7 @@ __device__ __forceinline__ void add_adapter_terms(f32x16 (&acc)[NMS][NS], const 
         for (int j = 0; j < 4; ++j) {
           const int i = i0 + 256 * j, m = i / kQuads, r = 4 * (i % kQuads);
           const bool in = m < rows && rc + r < ad.rank;
-          const float* u = ad.u + p0 * ad.part_stride + (in ? (ta.m0 + m) * ad.rank + rc + r : 0);
+          const float* u = ad.u + p0 * ad.part_stride + (in ? (ta.m0 + ta.s_tok[m]) * ad.rank + rc + r : 0);
 #pragma unroll
           for (int p = 0; p < PF; ++p)
             w[j][p] = in && p0 + p < ad.parts ? *reinterpret_cast<const f32x4*>(u + p * ad.part_stride)
@@ -495,6 +497,8 @@ mfma_prefill_kernel(const uint8_t* __restrict__ codes, const float* __restrict__
   __shared__ uint64_t s_nruns;
   __shared__ int s_e;
   __shared__ int32_t s_of[ADP ? BM : 1];
+  __shared__ __attribute__((aligned(16))) uint32_t s_key[ADP ? BM : 1];
+  __shared__ uint8_t s_tok[ADP ? BM : 1];
 
   const int tid = threadIdx.x;
   // ---- workgroup -> (M-tile, column tile tcol) ----
@@ -663,26 +667,30 @@ mfma_prefill_kernel(const uint8_t* __restrict__ codes, const float* __restrict__
   int64_t atok = 0;
   constexpr uint32_t ESZ = NW == 2 ? 2 : 4;
   const int64_t rowb = tsplit ? (int64_t)(N - tc0 * 128) * 4 : pitch * ESZ;   // bytes between rows
+  if constexpr (ADP) {                               // rows take the tile's tokens by adapter
+    if (tid < BM) s_of[tid] = -1;
+    order_by_adapter<BM>(adp.of + m0, rows, adp.n_adapters, tid, s_key, [&](int place, int t, int a) {
+      s_tok[place] = (uint8_t)t;
+      s_of[place] = a;
+    });
+    lds_barrier();
+  }
   if (tid < BM) {                                    // thread t < BM: row t's scale and output offset
     uint32_t ro = kOffNone;
     float sv = 0.0f;
     if (tid < rows) {
-      const int64_t r = r0 + m0 + tid;
+      const int64_t r = r0 + m0 + (ADP ? s_tok[tid] : tid);
       const int64_t tk = row_token ? (int64_t)row_token[r] : r;
       sv = scales[tk];
       ro = (uint32_t)(r * rowb);
     }
     s_rowoff[tid] = ro;
     s_scale[tid] = sv;
-    if constexpr (ADP) {
-      const int of = tid < rows ? adp.of[m0 + tid] : -1;
-      s_of[tid] = (uint32_t)of < (uint32_t)adp.n_adapters ? of : -1;
-    }
   }
   TileAdapters<ADP> ta;
-  if constexpr (ADP) ta = TileAdapters<true>{adp, s_of, m0, N};
+  if constexpr (ADP) ta = TileAdapters<true>{adp, s_of, s_tok, m0, N};
   if (c.avalid) {
-    const int64_t r = r0 + m0 + arow;
+    const int64_t r = r0 + m0 + (ADP ? s_tok[arow] : arow);
     atok = row_token ? (int64_t)row_token[r] : r;
   }
   c.cres = make_rsrc(codes, 0x7FFFFFFFu);

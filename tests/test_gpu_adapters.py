@@ -110,6 +110,34 @@ def test_orders_and_none(T):
     _case(T, 128, 64, 4, 8, 8, 4, scale=False, pad=24)
 
 
+@pytest.mark.parametrize("T,n_ad", [(33, 40), (255, 20), (257, 300), (513, 33), (900, 1000)])
+def test_many_adapters_in_random_order(T, n_ad):
+    """Tiles order their tokens by adapter: ragged groups, ids up to the last, tokens with none."""
+    rng = np.random.default_rng(T)
+    of = rng.integers(-1, n_ad, T)
+    of[[0, T - 1]] = n_ad - 1, -5
+    of[T // 2] = 0x7FFFFFFF
+    _case(T, 96, 48, 4, 8, 24, n_ad, of=of, pad=32)
+    _case(T, 160, 144, 3, 4, 8, n_ad, of=np.sort(of))
+
+
+@pytest.mark.parametrize("T,N,bits", [(300, 160, 4), (300, 160, 3), (2100, 4112, 4)])
+def test_a_tokens_result_does_not_depend_on_the_order(T, N, bits):
+    K, n_ad, rank = 160, 24, 40
+    rng = np.random.default_rng(T + bits)
+    W = cbq.prepack_weights(upload_weights(datagen.random_weights(3, 1, N, K, bits)))
+    x = bf16_dev(datagen.random_tokens(4, T, K))
+    codes, scales = cbq.rotate_quantize(x, 8)
+    la = torch.randn(n_ad, rank, K, device=DEV).to(torch.bfloat16)
+    lb = torch.randn(n_ad, N, rank, device=DEV).to(torch.bfloat16)
+    of = torch.sort(to_dev(rng.integers(-1, n_ad, T).astype(np.int32))).values
+    sorted_out = cbq.codebook_adapter_gemm(codes, scales, 8, W, x, la, lb, of)
+    p = to_dev(rng.permutation(T))
+    got = cbq.codebook_adapter_gemm(codes[p].contiguous(), scales[p].contiguous(), 8, W, x[p].contiguous(), la, lb,
+                                    of[p].contiguous())
+    assert torch.equal(got, sorted_out[p])
+
+
 @pytest.mark.parametrize("T", [5, 80])
 def test_no_adapter_is_the_plain_projection(T):
     K, N = 512, 256
