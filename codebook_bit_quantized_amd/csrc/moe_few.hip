@@ -54,6 +54,9 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   return max(max(a, b), max(c, d));
 }
 
+// a logit's key; 0 stands for an expert that is taken (or none), which one NaN would map to
+__device__ __forceinline__ uint32_t expert_key(float l) { return max(order_bits(l), 1u); }
+
 // the expert of rank j in a token's logits (ties to the lower id): j + 1 rounds of a wave
 // maximum; whole waves only.  NI: 64-expert groups (E <= 64 * NI)
 template <int NI>
@@ -62,7 +65,7 @@ __device__ __forceinline__ int expert_of_rank(const float* row, int E, int j, in
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int e = lane + 64 * i;
-    key[i] = e < E ? order_bits(row[e]) : 0u;
+    key[i] = e < E ? expert_key(row[e]) : 0u;
   }
   int e = 0;
 #pragma unroll 1
@@ -139,7 +142,7 @@ few_prepare_kernel(const float* __restrict__ logits, int T, int E, int topk, int
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int e = lane + 64 * i;
-    key[i] = e < E ? order_bits(lg[e]) : 0u;
+    key[i] = e < E ? expert_key(lg[e]) : 0u;
   }
   int mine = 0;
   for (int r = 0; r < topk; ++r) {

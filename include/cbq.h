@@ -378,7 +378,8 @@ typedef struct {
  *
  *  x    : bf16 [T][ldx] (ldx >= K, ldx % 8 == 0, 16-byte aligned), the residual stream.
  *  norm : the norm and its outputs (host pointer, read during the call only); normed may
- *         be x itself (with ldn == ldx).
+ *         be x itself (with ldn == ldx); otherwise the outputs overlap neither it nor each
+ *         other.
  *  Requires K % 32 == 0, 32 <= K <= 16384, T < 2^31.
  */
 int cbq_norm_rotate_quantize(const uint16_t* x, int64_t T, int32_t K, int64_t ldx,
@@ -437,7 +438,7 @@ int cbq_combine_norm_residual(const void* rows, int32_t rows_type, int64_t ldr,
  *  product of those codes.  (The sequence of single calls rounds h to bf16 first, so its
  *  codes of h differ now and then.)  Deterministic: no result depends on the order of atomics.
  *  A token's non-finite scale or logits reach its own y only (logits that are all -inf have no
- *  softmax: that token's y is NaN, as its routing weights are).
+ *  softmax: that token's y is NaN, as its routing weights are).  y overlaps no input, nor ws.
  *  Limits: 0 <= T <= CBQ_FEW_MAX_TOKENS (CBQ_EUNSUPPORTED above: use the single calls),
  *  H % 32 == 0, F % 32 == 0, H, F <= 16384, one expert's index block below 2 GiB.
  */
@@ -473,7 +474,8 @@ int cbq_moe_ffn_few(const uint8_t* codes, const float* scales, int32_t act_bits,
  *  ws, ws_bytes : device workspace of cbq_adapter_workspace(T, rank) bytes, 16-byte aligned
  *               (the middle vectors; rewritten by every call; calls that overlap in time
  *               need one each).
- *  A token's result does not depend on other tokens' adapters, non-finite ones included.
+ *  A token's result does not depend on other tokens' adapters, non-finite ones included, nor
+ *  on the order of the tokens.  out overlaps no input, nor ws.
  *  Limits: those of cbq_codebook_lut_gemm, K <= 16384.
  */
 size_t cbq_adapter_workspace(int64_t T, int32_t rank);

@@ -247,3 +247,20 @@ def test_another_tokens_infinities_stay_with_it(T):
     nan[1, 3:9] = float("nan")
     got = run(scales, nan)
     assert torch.equal(got[keep], want[keep])
+
+
+@pytest.mark.parametrize("T,E", [(32, 8), (32, 70), (1, 8)])
+def test_logits_of_any_nan(T, E):
+    """Whatever bits a NaN has, its token still takes distinct experts, so no other token's rows go missing."""
+    gate, up, down, x, lg = _inputs(T, 64, 96, E, 8, 0, 3, 2, 4)
+    dev = [cbq.prepack_weights(upload_weights(w)) for w in (gate, up, down)]
+    codes, scales = cbq.rotate_quantize(bf16_dev(x), 4)
+    L = to_dev(lg)
+    L[:, 8:] -= 100.0                                        # every token visits the first eight
+    run = lambda l: cbq.moe_ffn_few(codes, scales, l, *dev, 8, 0, 4, y_dtype=torch.float32)  # noqa: E731
+    want = run(L)
+    for bits in (-1, -2, 0x7FFFFFFF, 0x7FC00000, -0x400000):
+        bad = L.clone()
+        bad.view(torch.int32)[::2] = bits
+        got = run(bad)
+        assert torch.isnan(got[::2]).all() and torch.equal(got[1::2], want[1::2])
