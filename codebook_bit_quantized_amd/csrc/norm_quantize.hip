@@ -17,9 +17,10 @@
 // or 32 for the norm before a block of many tokens (norm_width).  With expert rows it is bound
 // by reading them (4096 x 2048, 8 rows each, gates, norms and codes: 344 MB in 76 us, 4.5 TB/s
 // of the 5.1 a large copy reaches); the norm alone by its vector instructions, mostly the
-// transform's exchanges in fp64 (4096 x 2048: 42 MB in 20 us).  The transform's first stages run in the thread, the next ones
-// between lanes, and the ones across waves in one LDS pass whatever their number (each
-// thread reads its partners in the block's other waves and adds them with their signs).
+// transform's exchanges in fp64 (4096 x 2048: 42 MB in 20 to 22 us).  The transform's first
+// stages run in the thread, the next ones between lanes, and the ones across waves in one LDS
+// pass whatever their number (each thread reads its partners in the block's other waves and
+// adds them with their signs).
 #include "cbq_internal.hpp"
 #include "few_device.hpp"
 #include "rotate_device.hpp"
