@@ -232,3 +232,14 @@ def test_stream_and_graph_replay():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(eager, cap)), k
+
+
+def test_more_tokens_than_one_launch_takes():
+    """2^21 tokens go in one launch; the tokens of the second give what a call of their own gives."""
+    T, K = (1 << 21) + 3, 32
+    x = torch.randn(T, K, device=DEV).to(torch.bfloat16)
+    w = 1 + 0.1 * torch.randn(K, device=DEV)
+    n, c, s = cbq.norm_rotate_quantize(x, w, 1e-6, 4)
+    for a, b in ((0, 5), (T - 7, T)):
+        n1, c1, s1 = cbq.norm_rotate_quantize(x[a:b], w, 1e-6, 4)
+        assert torch.equal(n[a:b], n1) and torch.equal(c[a:b], c1) and torch.equal(s[a:b], s1)
