@@ -12,15 +12,17 @@
 // wider one elsewhere.  fp64 sums make them (and so the codes) independent of the order
 // of summation, except where a value lies within about 2^-50 of a rounding border.
 //
-// One workgroup per token, CPT consecutive channels a thread: 8 (16 beyond K = 8192), so one
-// token's work is spread over K / 512 waves (a single token's latency is what decode sees),
-// or 32 for the norm before a block of many tokens (norm_width).  With expert rows it is bound
-// by reading them (4096 x 2048, 8 rows each, gates, norms and codes: 344 MB in 76 us, 4.5 TB/s
-// of the 5.1 a large copy reaches); the norm alone by its vector instructions, mostly the
-// transform's exchanges in fp64 (4096 x 2048: 42 MB in 20 to 22 us).  The transform's first
-// stages run in the thread, the next ones between lanes, and the ones across waves in one LDS
-// pass whatever their number (each thread reads its partners in the block's other waves and
-// adds them with their signs).
+// One workgroup per token, CPT channels a thread: 8 (16 beyond K = 8192), so one token's work
+// is spread over K / 512 waves (a single token's latency is what decode sees), or 32 for the
+// norm before a block of many tokens (norm_width).  A thread's channels are runs of 8, kRun
+// apart, so that a wave's loads and stores are contiguous whatever CPT is (with 32 consecutive
+// ones the norm alone, without codes, took 13.8 us at 4096 x 2048 instead of 9.8).  With expert
+// rows it is bound by reading them (4096 x 2048, 8 rows each, gates, norms and codes: 344 MB in
+// 76 us, 4.5 TB/s of the 5.1 a large copy reaches); the norm alone by its vector instructions,
+// mostly the transform's exchanges in fp64 (4096 x 2048: 42 MB in 18 to 20 us).  The transform's
+// first stages run in the thread, the next ones between lanes, then between a thread's runs,
+// and the ones across waves in one LDS pass whatever their number (each thread reads its
+// partners in the block's other waves and adds them with their signs).
 #include "cbq_internal.hpp"
 #include "few_device.hpp"
 #include "rotate_device.hpp"
@@ -66,11 +68,16 @@ __device__ __forceinline__ uint32_t wave_max_bits(uint32_t v) {
   return v;
 }
 
+// A thread's N channels are runs of 8, kRun apart, so a wave's loads and stores are contiguous;
+// n: channels from the first run's start to the row's end (whole runs).
+constexpr int kRun = 512;
+
 template <int N>
-__device__ __forceinline__ void load_bf16(const uint16_t* p, float* f) {
+__device__ __forceinline__ void load_bf16(const uint16_t* p, int n, float* f) {
 #pragma unroll
   for (int h = 0; h < N / 8; ++h) {
-    const u32x4 q = reinterpret_cast<const u32x4*>(p)[h];
+    if (kRun * h >= n) continue;
+    const u32x4 q = *reinterpret_cast<const u32x4*>(p + kRun * h);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       f[8 * h + 2 * i] = __builtin_bit_cast(float, q[i] << 16);
@@ -80,10 +87,11 @@ __device__ __forceinline__ void load_bf16(const uint16_t* p, float* f) {
 }
 
 template <int N>
-__device__ __forceinline__ void load_f32(const float* p, float* f) {
+__device__ __forceinline__ void load_f32(const float* p, int n, float* f) {
 #pragma unroll
   for (int h = 0; h < N / 4; ++h) {
-    const f32x4 q = reinterpret_cast<const f32x4*>(p)[h];
+    if (kRun * (h / 2) >= n) continue;
+    const f32x4 q = *reinterpret_cast<const f32x4*>(p + kRun * (h / 2) + 4 * (h % 2));
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[4 * h + i] = q[i];
   }
@@ -100,7 +108,7 @@ __device__ __forceinline__ uint32_t f64_to_bf16(double d) {
 
 // rounds fp64 to fp32 and that to bf16, stores the bf16 and returns their values
 template <int N>
-__device__ __forceinline__ void store_bf16(uint16_t* p, bool store, const double* d, float* f) {
+__device__ __forceinline__ void store_bf16(uint16_t* p, int n, bool store, const double* d, float* f) {
 #pragma unroll
   for (int h = 0; h < N / 8; ++h) {
     u32x4 q;
@@ -112,7 +120,7 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, bool store, const double
       f[8 * h + 2 * i] = __builtin_bit_cast(float, lo << 16);
       f[8 * h + 2 * i + 1] = __builtin_bit_cast(float, hi << 16);
     }
-    if (store) reinterpret_cast<u32x4*>(p)[h] = q;
+    if (store && kRun * h < n) *reinterpret_cast<u32x4*>(p + kRun * h) = q;
   }
 }
 
@@ -131,14 +139,15 @@ norm_quantize_kernel(NormArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int nw = (int)blockDim.x >> 6;
   const int64_t t = a.t0 + blockIdx.x;
-  const int c0 = tid * CPT;
-  const bool act = c0 < a.K;                 // K is a multiple of 32, so whole threads
+  const int c0 = wave * 64 * CPT + lane * 8;
+  const int left = a.K - c0;                 // K is a multiple of 32, so whole runs
+  const bool act = left > 0;
   float f[CPT];                              // the row that is normed and quantised
 
   if constexpr (SRC == kRotateF32) {
-    if (act) load_f32<CPT>(static_cast<const float*>(a.rows) + t * a.ldr + c0, f);
+    if (act) load_f32<CPT>(static_cast<const float*>(a.rows) + t * a.ldr + c0, left, f);
   } else if constexpr (SRC == kNormX) {
-    if (act) load_bf16<CPT>(a.x + t * a.ldx + c0, f);
+    if (act) load_bf16<CPT>(a.x + t * a.ldx + c0, left, f);
   } else {
     using Row = std::conditional_t<SRC == kNormF32, float, uint16_t>;
     const Row* rows = reinterpret_cast<const Row*>(a.rows) + c0;
@@ -156,15 +165,15 @@ norm_quantize_kernel(NormArgs a) {
         return j < a.topk ? (int64_t)a.slot_of[t * a.topk + j] : a.T * a.topk + (j - a.topk) * a.T + t;
       };
       auto load_row = [&](int j, float* d) {
-        if constexpr (SRC == kNormF32) load_f32<CPT>(rows + row_of(j) * a.ldr, d);
-        else load_bf16<CPT>(rows + row_of(j) * a.ldr, d);
+        if constexpr (SRC == kNormF32) load_f32<CPT>(rows + row_of(j) * a.ldr, left, d);
+        else load_bf16<CPT>(rows + row_of(j) * a.ldr, left, d);
       };
 #pragma unroll
       for (int j = 0; j < RB; ++j)
         if (j < n) load_row(j, r[j]);
-      load_bf16<CPT>(a.x + t * a.ldx + c0, res);
-      if (CPT == 8 && a.gate != nullptr) load_bf16<CPT>(a.gate + t * a.ldg + c0, gate);
-      if (CPT == 8 && a.post_weight != nullptr) load_f32<CPT>(a.post_weight + c0, pw);
+      load_bf16<CPT>(a.x + t * a.ldx + c0, left, res);
+      if (CPT == 8 && a.gate != nullptr) load_bf16<CPT>(a.gate + t * a.ldg + c0, left, gate);
+      if (CPT == 8 && a.post_weight != nullptr) load_f32<CPT>(a.post_weight + c0, left, pw);
 #pragma unroll 1
       for (int j0 = 0; j0 < n; j0 += RB) {
         if (j0 > 0) {
@@ -177,7 +186,8 @@ norm_quantize_kernel(NormArgs a) {
           if (j0 + j < n) {
             const double w = j0 + j < a.topk ? (double)a.topk_w[t * a.topk + j0 + j] : 1.0;
 #pragma unroll
-            for (int i = 0; i < CPT; ++i) y[i] = __builtin_fma(w, (double)r[j][i], y[i]);
+            for (int i = 0; i < CPT; ++i)
+              if (kRun * (i / 8) < left) y[i] = __builtin_fma(w, (double)r[j][i], y[i]);
           }
         }
       }
@@ -187,31 +197,30 @@ norm_quantize_kernel(NormArgs a) {
 #pragma unroll
       for (int i = 0; i < CPT; ++i) ss = __builtin_fma(y[i], y[i], ss);
       ss = wave_sum_f64(ss);
-      if (CPT > 8 && act) load_f32<CPT>(a.post_weight + c0, pw);   // 16 channels leave no registers for it above
+      if (CPT > 8 && act) load_f32<CPT>(a.post_weight + c0, left, pw);   // 16 channels leave no registers for it above
       if (lane == 0) s_sum[0][wave] = ss;
       lds_barrier();
       double tot = 0.0;
       for (int w = 0; w < nw; ++w) tot += s_sum[0][w];
       const double rn = rsqrt_f64(tot * a.inv_K + (double)a.post_eps);
 #pragma unroll
-      for (int i = 0; i < CPT; ++i) y[i] = act ? y[i] * rn * (double)pw[i] : 0.0;
+      for (int i = 0; i < CPT; ++i) y[i] = kRun * (i / 8) < left ? y[i] * rn * (double)pw[i] : 0.0;
     }
     if (act) {
       if (a.gate != nullptr) {
-        if (CPT > 8) load_bf16<CPT>(a.gate + t * a.ldg + c0, gate);
+        if (CPT > 8) load_bf16<CPT>(a.gate + t * a.ldg + c0, left, gate);
 #pragma unroll
         for (int i = 0; i < CPT; ++i) y[i] *= (double)gate[i];
       }
 #pragma unroll
       for (int i = 0; i < CPT; ++i) y[i] = __builtin_fma((double)a.scale, y[i], (double)res[i]);
-      store_bf16<CPT>(a.out + t * a.ldo + c0, true, y, f);
+      store_bf16<CPT>(a.out + t * a.ldo + c0, left, true, y, f);
     }
     if (a.weight == nullptr) return;         // uniform over the launch
   }
-  if (!act) {
 #pragma unroll
-    for (int i = 0; i < CPT; ++i) f[i] = 0.0f;
-  }
+  for (int i = 0; i < CPT; ++i)
+    if (kRun * (i / 8) >= left) f[i] = 0.0f;
 
   // ---- RMS norm ----
   double v[CPT];
@@ -226,10 +235,10 @@ norm_quantize_kernel(NormArgs a) {
     for (int w = 0; w < nw; ++w) tot += s_sum[1][w];
     const double rn = rsqrt_f64(tot * a.inv_K + (double)a.eps);
     float wt[CPT];
-    if (act) load_f32<CPT>(a.weight + c0, wt);
+    load_f32<CPT>(a.weight + c0, left, wt);
 #pragma unroll
-    for (int i = 0; i < CPT; ++i) v[i] = act ? (double)f[i] * rn * (double)wt[i] : 0.0;
-    store_bf16<CPT>(a.normed + t * a.ldn + c0, act && a.normed != nullptr, v, f);
+    for (int i = 0; i < CPT; ++i) v[i] = kRun * (i / 8) < left ? (double)f[i] * rn * (double)wt[i] : 0.0;
+    store_bf16<CPT>(a.normed + t * a.ldn + c0, left, a.normed != nullptr, v, f);
   }
   if (a.codes == nullptr) return;            // uniform over the launch
 #pragma unroll
@@ -238,25 +247,30 @@ norm_quantize_kernel(NormArgs a) {
   // ---- block Walsh-Hadamard transform (fp64, exact for bf16 rows within the bound that
   // rotate_quantize states) ----
   const int b = 1 << a.logb;
+  auto in_thread = [&](auto distance) {
+    constexpr int h = decltype(distance)::value;
 #pragma unroll
-  for (int h = 1; h < CPT; h <<= 1) {
-    if (h < b) {
-#pragma unroll
-      for (int i = 0; i < CPT; ++i) {
-        if (!(i & h)) {
-          const double p = v[i], q = v[i + h];
-          v[i] = p + q;
-          v[i + h] = p - q;
-        }
+    for (int i = 0; i < CPT; ++i) {
+      if (!(i & h)) {
+        const double p = v[i], q = v[i + h];
+        v[i] = p + q;
+        v[i + h] = p - q;
       }
     }
-  }
-  if (b > CPT) lane_stage<1, CPT>(v, (lane & 1) != 0);
-  if (b > 2 * CPT) lane_stage<2, CPT>(v, (lane & 2) != 0);
-  if (b > 4 * CPT) lane_stage<4, CPT>(v, (lane & 4) != 0);
-  if (b > 8 * CPT) lane_stage<8, CPT>(v, (lane & 8) != 0);
-  if (b > 16 * CPT) lane_stage<16, CPT>(v, (lane & 16) != 0);
-  if (b > 32 * CPT) lane_stage<32, CPT>(v, (lane & 32) != 0);
+  };
+  if (b > 1) in_thread(std::integral_constant<int, 1>{});
+  if (b > 2) in_thread(std::integral_constant<int, 2>{});
+  if (b > 4) in_thread(std::integral_constant<int, 4>{});
+  if (b > 8) lane_stage<1, CPT>(v, (lane & 1) != 0);
+  if (b > 16) lane_stage<2, CPT>(v, (lane & 2) != 0);
+  if (b > 32) lane_stage<4, CPT>(v, (lane & 4) != 0);
+  if (b > 64) lane_stage<8, CPT>(v, (lane & 8) != 0);
+  if (b > 128) lane_stage<16, CPT>(v, (lane & 16) != 0);
+  if (b > 256) lane_stage<32, CPT>(v, (lane & 32) != 0);
+  if constexpr (CPT >= 16)
+    if (b > kRun) in_thread(std::integral_constant<int, 8>{});
+  if constexpr (CPT >= 32)
+    if (b > 2 * kRun) in_thread(std::integral_constant<int, 16>{});
   const int wpb = b / (64 * CPT);            // waves per block
   if (wpb > 1) {
     // v of wave w is the sum over the block's waves w' of (-1)^popcount(w & w') v of w'
@@ -297,16 +311,11 @@ norm_quantize_kernel(NormArgs a) {
   // ---- quantise: the fp32 sequence of rotate_quantize (s = M / Q, q = clamp(rint(v / s)),
   // the quotient as fp64(v) * fp64(1 / s) rounded to fp32, rint by the magic-number add);
   // the lane stages' sign, the parity of the lane's bits inside the block, is folded in ----
-  if constexpr (SRC == kRotateF32) {
-    if (c0 >= (a.K + 127) / 128 * 128) return;   // the fp16 rows hold zeros up to there
-  } else {
-    if (!act) return;
-  }
   const float Q = a.act_bits == 4 ? 7.0f : 127.0f;
   const float lo = a.act_bits == 4 ? -8.0f : -127.0f;
   constexpr float kMagic = 12582912.0f;
   const float s = amax / Q;
-  const int lpb = b / CPT < 64 ? b / CPT : 64;   // lanes per block within a wave
+  const int lpb = b / 8 < 64 ? b / 8 : 64;   // lanes per block within a wave
   const bool neg = lpb > 1 && (__builtin_popcount((unsigned)lane & (unsigned)(lpb - 1)) & 1);
   const double rs = amax != 0.0f ? (neg ? -1.0 : 1.0) / (double)s : 0.0;
   if constexpr (SRC == kRotateF32) {
@@ -314,6 +323,7 @@ norm_quantize_kernel(NormArgs a) {
     uint8_t* dst = a.codes + t * few_row16_bytes(a.K);
 #pragma unroll
     for (int k = 0; k < CPT / 8; ++k) {
+      if (c0 + kRun * k >= (a.K + 127) / 128 * 128) continue;   // the fp16 rows hold zeros up to there
       f16x2 d[4];                            // (k0, k2) (k4, k6) (k1, k3) (k5, k7)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -321,7 +331,7 @@ norm_quantize_kernel(NormArgs a) {
         d[(i & 1) * 2 + (i >> 2)][(i >> 1) & 1] =
             (_Float16)(__builtin_amdgcn_fmed3f(r + kMagic, kMagic + lo, kMagic + Q) - kMagic);
       }
-      *reinterpret_cast<u32x4*>(dst + few_pos16(c0 + 8 * k)) =
+      *reinterpret_cast<u32x4*>(dst + few_pos16(c0 + kRun * k)) =
           u32x4{__builtin_bit_cast(uint32_t, d[0]), __builtin_bit_cast(uint32_t, d[1]),
                 __builtin_bit_cast(uint32_t, d[2]), __builtin_bit_cast(uint32_t, d[3])};
     }
@@ -346,15 +356,17 @@ norm_quantize_kernel(NormArgs a) {
       const uint32_t od = low_bytes(8 * k + 1, 8 * k + 3, 8 * k + 5, 8 * k + 7);
       w[k] = (ev & 0x0F0F0F0Fu) | ((od << 4) & 0xF0F0F0F0u);
     }
-    uint32_t* dst = reinterpret_cast<uint32_t*>(a.codes + t * (a.K / 2) + c0 / 2);
+    uint8_t* dst = a.codes + t * (a.K / 2) + c0 / 2;
 #pragma unroll
-    for (int k = 0; k < CPT / 8; ++k) dst[k] = w[k];
+    for (int k = 0; k < CPT / 8; ++k)
+      if (kRun * k < left) *reinterpret_cast<uint32_t*>(dst + kRun / 2 * k) = w[k];
   } else {
 #pragma unroll
     for (int k = 0; k < CPT / 4; ++k) w[k] = low_bytes(4 * k, 4 * k + 1, 4 * k + 2, 4 * k + 3);
-    u32x2* dst = reinterpret_cast<u32x2*>(a.codes + t * a.K + c0);
+    uint8_t* dst = a.codes + t * a.K + c0;
 #pragma unroll
-    for (int k = 0; k < CPT / 8; ++k) dst[k] = u32x2{w[2 * k], w[2 * k + 1]};
+    for (int k = 0; k < CPT / 8; ++k)
+      if (kRun * k < left) *reinterpret_cast<u32x2*>(dst + kRun * k) = u32x2{w[2 * k], w[2 * k + 1]};
   }
   if (tid == 0) a.scales[t] = amax != 0.0f ? s * a.c_b : 0.0f;
 }
@@ -369,13 +381,14 @@ static void launch_nt(const NormArgs& a, int src, unsigned tokens, unsigned thre
 }
 
 // Channels a thread of the norm before a block: 8 is the shortest chain, and the faster one up
-// to about 8 million values; beyond, 32 where they fill the waves, as a wave's reductions and
-// exchanges then serve four times the channels (us, 8 against 32: 4096 x 2048 20.2 / 19.7,
-// 4096 x 4096 40.0 / 34.2, 2048 x 8192 51.0 / 37.5, 1024 x 4096 13.9 / 14.8).  Beyond 8192
-// channels a workgroup's 1024 threads need 16 (or 32).
+// to about 4 million values; beyond, 32 where they fill the waves, as a wave's reductions and
+// exchanges then serve four times the channels (us, 8 against 32: 512 x 4096 9.4 / 11.6, 2048 x
+// 2048 12.8 / 11.4, 4096 x 2048 21.3 / 18.2, 4096 x 4096 41.8 / 33.1, 2048 x 8192 55 / 36; waves
+// filled to 62 %: 4096 x 2560 20.8 / 26.4).  Beyond 8192 channels a workgroup's 1024 threads
+// need 16 (or 32).
 static int norm_width(int64_t T, int K) {
   const int threads = K / 32, full = (threads + 63) / 64 * 64;
-  if (T * K >= (1 << 23) && 10 * threads >= 9 * full) return 32;
+  if (T * K >= (1 << 22) && 10 * threads >= 9 * full) return 32;
   return K <= 8192 ? 8 : 16;
 }
 

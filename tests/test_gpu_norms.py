@@ -243,3 +243,17 @@ def test_more_tokens_than_one_launch_takes():
     for a, b in ((0, 5), (T - 7, T)):
         n1, c1, s1 = cbq.norm_rotate_quantize(x[a:b], w, 1e-6, 4)
         assert torch.equal(n[a:b], n1) and torch.equal(c[a:b], c1) and torch.equal(s[a:b], s1)
+
+
+@pytest.mark.parametrize("T,K", [(2200, 1920), (2100, 2048), (1100, 4064), (1300, 3712), (520, 8192), (300, 14336), (280, 16160)])
+@pytest.mark.parametrize("act_bits", [4, 8])
+def test_large_batches_match_single_tokens(T, K, act_bits):
+    """The form of large batches (runs of channels, the last ones partly behind the row) against that of few tokens."""
+    x = torch.randn(T, K + 32, device=DEV).to(torch.bfloat16)[:, :K]
+    w = 1 + 0.1 * torch.randn(K, device=DEV)
+    n, c, s = cbq.norm_rotate_quantize(x, w, 1e-6, act_bits)
+    for t in (0, T // 2, T - 1):
+        n1, c1, s1 = cbq.norm_rotate_quantize(x[t:t + 1], w, 1e-6, act_bits)
+        assert torch.equal(n[t:t + 1], n1) and torch.equal(c[t:t + 1], c1) and torch.equal(s[t:t + 1], s1)
+    cr, sr = cbq.rotate_quantize(n, act_bits)
+    assert torch.equal(c, cr) and torch.equal(s, sr)
