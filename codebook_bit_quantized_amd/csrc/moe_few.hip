@@ -21,12 +21,12 @@
 // One token with a short h (one_token_form), where launches and dependent loads are most of it:
 //   1. gate/up whose waves find their choice's expert from the logits themselves;
 //   2. one kernel for the rest: every workgroup rotates and quantises all rows of h (a few
-//      thousand values), a wave a row, multiplies its 16 columns of down and combines them.
+//      thousand values) as the batch form does, a wave a row, multiplies its 16 columns of down and combines them.
 // These two run every instruction a few times only, so instruction fetches count: their loops
 // stay rolled where the unrolled code would run once.
 //
 // Measured (us; weights of three layers in turn): 128 experts, top 8, 2048 x 768, 4 bits: one
-// token 9.4 + 8.5 (the batch form takes 26 a call, this one 17); 32 tokens 4.8 + 50 + 4.8 + 31
+// token 9.3 + 9.6 (the batch form takes 24 a call, this one 17.6); 32 tokens 4.8 + 50 + 4.8 + 31
 // + 5.1.  64 + 2 experts, 2048 x 1408, 3 and 2 bits, 8 tokens 3.9 + 26 + 4.8 + 14 + 4.8.  8
 // experts, top 2, 4096 x 14336, 4 bits, 16 tokens 4.8 + 109 + 9 + 61 + 4.8.
 // h is kept in fp32 up to the quantiser: the codes are those of the unrounded h up to fp32
@@ -39,6 +39,8 @@
 namespace cbq {
 
 namespace {
+
+typedef double f64x2 __attribute__((ext_vector_type(2)));
 
 // maximum of v over the wave (DPP row rotations, then four scalar reads)
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
@@ -317,10 +319,15 @@ few_gate_one_kernel(FewArgs a, int SK) {
   }
 }
 
+// Bytes of LDS a value of h takes while few_down_one_kernel transforms it: fp64 where blocks of
+// more than 256 channels pass through LDS between their stages, else the fp32 result.
+__host__ __device__ constexpr int one_token_value_bytes(int F) { return (F & -F) > 256 ? 8 : 4; }
+
 // The rest of the one-token form.  Workgroup: 16 columns of y; wave = row << ksh | split of K.
 // Every workgroup repeats the rotation of all rows (6144 values at 8 rows of 768), which costs
-// less than the launches it saves while the rows are few and short (one_token_form): 8.5 us for
-// the 6.8 MB of down.
+// less than the launches it saves while the rows are few and short (one_token_form): 9.6 us for
+// the 6.8 MB of down, of which the transform in fp64 instead of fp32 is 1.0 (with fp32 a code or
+// the scale differed between a token alone and in a batch).
 template <int BITS, bool BLK, int DEPTH>
 __global__ void __launch_bounds__(1024)
 few_down_one_kernel(FewDownArgs a, int ksh) {
@@ -348,27 +355,37 @@ few_down_one_kernel(FewDownArgs a, int ksh) {
   for (int i = 0; i < DEPTH; ++i) W.load(c0 + i, c1, ring[i]);
   const float lg = a.logits[id];
 
-  // Rotation of row `row` by its first wave, 256 channels a pass (4 consecutive ones a lane):
-  // butterflies in the lane and between lanes, the transformed values kept as fp32 in the
-  // row's LDS; blocks beyond 256 channels finish with passes over LDS.  fp32: the transform
-  // rounds by about as much as h's own sums.
-  float* u = reinterpret_cast<float*>(s_codes + (size_t)(nw >> ksh) * pitch) + row * ((F + 255) & ~255);
+  // Rotation of row `row` by its first wave, 256 channels a pass (4 consecutive ones a lane), in
+  // fp64 and rounded once to fp32 as rotate_quantize does: butterflies in the lane and between
+  // lanes, then, for blocks beyond 256 channels, passes over the row's LDS.  u holds four
+  // channels' fp32 results in 16 bytes, or, where such passes need the fp64 values, in the first
+  // 16 of their 32.
+  const int b = F & -F;                      // >= 32
+  const int usz = one_token_value_bytes(F);
+  uint8_t* u = s_codes + (size_t)(nw >> ksh) * pitch + (size_t)row * ((F + 255) & ~255) * usz;
   if (split == 0) {
-    const int b = F & -F;                    // >= 32
     uint32_t top = 0;                        // of |v|'s bits, which put NaN above infinity
-    auto take = [&](float x) { top = max(top, __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu); };
-    f32x4 v = next;
+    auto take = [&](const double* d, uint8_t* to) {   // d rounded to fp32, stored and in the maximum
+      float f[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        f[k] = (float)d[k];
+        top = max(top, __builtin_bit_cast(uint32_t, f[k]) & 0x7FFFFFFFu);
+      }
+      *reinterpret_cast<f32x4*>(to) = f32x4{f[0], f[1], f[2], f[3]};
+    };
 #pragma unroll 1
     for (int c = 4 * lane; c < ((F + 255) & ~255); c += 256) {
-      v = next;
+      const f32x4 x = next;
       next = c + 256 < F ? *reinterpret_cast<const f32x4*>(h + c + 256) : zero;
-      const f32x4 p = {v[0] + v[1], v[0] - v[1], v[2] + v[3], v[2] - v[3]};
-      v = f32x4{p[0] + p[2], p[1] + p[3], p[0] - p[2], p[1] - p[3]};
+      const double p[4] = {(double)x[0] + (double)x[1], (double)x[0] - (double)x[1], (double)x[2] + (double)x[3],
+                           (double)x[2] - (double)x[3]};
+      double v[4] = {p[0] + p[2], p[1] + p[3], p[0] - p[2], p[1] - p[3]};
       auto stage = [&](auto m) {
         constexpr int M = decltype(m)::value;
-        const float sg = (lane & M) ? -1.0f : 1.0f;
+        const double sg = (lane & M) ? -1.0 : 1.0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = __builtin_fmaf(v[k], sg, xor_lane_f32<M>(v[k]));
+        for (int k = 0; k < 4; ++k) v[k] = __builtin_fma(v[k], sg, xor_lane_f64<M>(v[k]));
       };
       stage(std::integral_constant<int, 1>{});
       stage(std::integral_constant<int, 2>{});
@@ -376,10 +393,12 @@ few_down_one_kernel(FewDownArgs a, int ksh) {
       if (b > 32) stage(std::integral_constant<int, 8>{});
       if (b > 64) stage(std::integral_constant<int, 16>{});
       if (b > 128) stage(std::integral_constant<int, 32>{});
-      *reinterpret_cast<f32x4*>(u + c) = v;  // zeros past F
-      if (b <= 256)
+      if (b <= 256) {
+        take(v, u + c * 4);                  // zeros past F
+      } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) take(v[k]);
+        for (int k = 0; k < 4; k += 2) *reinterpret_cast<f64x2*>(u + c * 8 + 8 * k) = f64x2{v[k], v[k + 1]};
+      }
     }
     // a lane only ever touches its own channels (mod 256), so these passes need no barrier
 #pragma unroll 1
@@ -387,16 +406,27 @@ few_down_one_kernel(FewDownArgs a, int ksh) {
 #pragma unroll 1
       for (int c = 4 * lane; c < F; c += 256) {
         if (c & m) continue;
-        const f32x4 p = *reinterpret_cast<f32x4*>(u + c), q = *reinterpret_cast<f32x4*>(u + c + m);
-        const f32x4 x = p + q, z = p - q;
-        *reinterpret_cast<f32x4*>(u + c) = x;
-        *reinterpret_cast<f32x4*>(u + c + m) = z;
-        if (2 * m == b)
+        double x[4], z[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            take(x[k]);
-            take(z[k]);
+        for (int k = 0; k < 4; k += 2) {
+          const f64x2 p = *reinterpret_cast<const f64x2*>(u + c * 8 + 8 * k);
+          const f64x2 q = *reinterpret_cast<const f64x2*>(u + (c + m) * 8 + 8 * k);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            x[k + i] = p[i] + q[i];
+            z[k + i] = p[i] - q[i];
           }
+        }
+        if (2 * m == b) {
+          take(x, u + c * 8);
+          take(z, u + (c + m) * 8);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) {
+            *reinterpret_cast<f64x2*>(u + c * 8 + 8 * k) = f64x2{x[k], x[k + 1]};
+            *reinterpret_cast<f64x2*>(u + (c + m) * 8 + 8 * k) = f64x2{z[k], z[k + 1]};
+          }
+        }
       }
     }
     const float amax = __builtin_bit_cast(float, wave_max_u32(top));
@@ -407,7 +437,7 @@ few_down_one_kernel(FewDownArgs a, int ksh) {
     const double rs = amax != 0.0f ? 1.0 / (double)s : 0.0;
 #pragma unroll 1
     for (int c = 4 * lane; c < pitch / 2; c += 256) {   // zeros past F
-      v = *reinterpret_cast<f32x4*>(u + c);
+      const f32x4 v = *reinterpret_cast<const f32x4*>(u + c * usz);
       f16x2 q[2];                            // (k0, k2), (k1, k3) of this half group
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -544,18 +574,18 @@ static hipError_t launch_down_one(const FewDownArgs& a, hipStream_t stream) {
   const int R = a.topk + a.n_shared, nchunks = (a.F + 127) / 128;
   int ksh = 0;
   while (R << (ksh + 1) <= 16 && (2 << ksh) <= nchunks) ++ksh;
-  // fp16 codes and the transform's fp32 values of every row
-  const size_t lds = (size_t)R * (few_row16_bytes(a.F) + (a.F + 255) / 256 * 1024);
+  // fp16 codes and the transform's values of every row
+  const size_t lds = (size_t)R * (few_row16_bytes(a.F) + (a.F + 255) / 256 * 256 * one_token_value_bytes(a.F));
   hipLaunchKernelGGL((few_down_one_kernel<BITS, BLK, 4>), dim3((unsigned)(a.H / 16)), dim3((unsigned)(64 * R << ksh)), lds,
                      stream, a, ksh);
   return hipGetLastError();
 }
 
 // The one-token form: its rows have a wave each, which transforms F values, and all of them
-// together their codes and values in LDS (at most 87 KB at these limits).  Beyond the limits
-// that repeated work costs more than the batch form's three launches (4 bits, us a call, this
-// form / batch): 8 rows of 768 17.4 / 24.1, 8 of 1408 23.2 / 27.9, 8 of 2048 33.1 / 31.0, 2 of
-// 2048 17.3 / 24.3, 2 of 4096 32.5 / 29.1, 2 of 8192 60 / 44.
+// together their codes and values in LDS (at most 120 KB at these limits).  Beyond the limits
+// that repeated work costs more than the batch form's three launches (4 bits, us a call in a
+// graph, this form / batch): 8 rows of 768 17.6 / 24.1, 8 of 1408 24.9 / 28.4, 8 of 1536 27.0 /
+// 28.8, 6 of 2048 30.2 / 30.0, 2 of 2048 18.6 / 19.8, 2 of 4096 31.3 / 25.4.
 static bool one_token_form(int64_t T, int topk, int n_shared, int F) {
   const int R = topk + n_shared;
   return T == 1 && R <= 16 && F <= 2048 && R * F <= 12288;

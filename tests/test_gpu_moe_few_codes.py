@@ -1,9 +1,11 @@
 """moe_ffn_few on inputs whose matrix products are exact in fp32 (few_layer.py), so that what
-its output may be off by is known element by element."""
+its output may be off by is known element by element, and the codes of h that its two forms
+take can be compared bit for bit."""
 import numpy as np
 import pytest
 import torch
 
+import datagen
 import oracle
 
 pytestmark = pytest.mark.gpu
@@ -57,3 +59,20 @@ def test_one_token(H, F, E, topk, n_shared, act_bits):
 @pytest.mark.parametrize("act_bits", [4, 8])
 def test_batches(T, H, F, E, topk, n_shared, bits_gu, bits_d, act_bits):
     _check(T, H, F, E, topk, n_shared, bits_gu, bits_d, act_bits)
+
+
+@pytest.mark.parametrize("F", [96, 128, 256, 768, 1408, 512, 1024, 1536, 2048])
+@pytest.mark.parametrize("act_bits", [4, 8])
+def test_a_token_alone_has_the_codes_of_h_that_it_has_in_a_batch(F, act_bits):
+    """With one expert a token and one chunk of 128 channels in each row of down, y is an exact
+    sum of that chunk's codes of h, times their scale: one rounding, and equal bit for bit
+    where the codes and the scale are."""
+    T, H, E = 32, 64, 8
+    for seed in range(2):
+        q, scales, lg, gate, up, down = exact_layer(T, H, F, E, 1, 0, 4, 4, act_bits, seed)
+        idx = np.random.default_rng(seed).integers(1, 16, (E, H, F))
+        idx[:, np.arange(F) // 128 != (np.arange(H) % ((F + 127) // 128))[:, None]] = 0
+        down.idx, down.codebook[..., 0] = datagen.pack_lsb_first(idx, 4), 0
+        codes, sc, L, dev = _device(q, scales, lg, (gate, up, down), act_bits)
+        run = lambda a, b: cbq.moe_ffn_few(codes[a:b], sc[a:b], L[a:b], *dev, 1, 0, act_bits, y_dtype=torch.float32)  # noqa: E731
+        assert torch.equal(torch.cat([run(t, t + 1) for t in range(T)]), run(0, T))
