@@ -257,3 +257,28 @@ def test_large_batches_match_single_tokens(T, K, act_bits):
         assert torch.equal(n[t:t + 1], n1) and torch.equal(c[t:t + 1], c1) and torch.equal(s[t:t + 1], s1)
     cr, sr = cbq.rotate_quantize(n, act_bits)
     assert torch.equal(c, cr) and torch.equal(s, sr)
+
+
+@pytest.mark.parametrize("act_bits", [4, 8])
+def test_norm_extreme_values_row_by_row(act_bits):
+    """Rows near the ends of bf16's range, subnormal values among them, rows of one value and a
+    single value beside zeros: each row against the oracle, and each alone as in the batch."""
+    K = 256
+    rng = np.random.default_rng(3)
+    mag = np.array([[1e37], [1e-36], [1e-38], [3e-40], [1.0]])
+    v = (rng.standard_normal((5, K)) * mag).astype(np.float32)
+    one = np.zeros((2, K), dtype=np.float32)
+    one[0], one[1, 77] = 3.0e38, 1e-40
+    xb = datagen.f32_to_bf16_bits(np.concatenate([v, one]))
+    assert ((xb[2:4] & 0x7F80) == 0).any() and (xb[6] & 0x7FFF).any()    # subnormal inputs
+    for eps in (1e-30, 1e-6):
+        w = _weight(2, K)
+        normed, codes, scales = cbq.norm_rotate_quantize(bf16_dev(xb), to_dev(w), eps, act_bits)
+        nb = bf16_to_bits(normed)
+        _check_normed(nb, _f64(xb), w, eps)
+        ref = oracle.rotate_quantize(nb, 0, act_bits)
+        assert np.array_equal(codes.cpu().numpy()[ref["ok"].all(axis=1)], ref["codes"][ref["ok"].all(axis=1)])
+        assert ref["ok"].all(axis=1)[[0, 1, 4, 5]].all()
+        for t in range(len(xb)):
+            n1, c1, s1 = cbq.norm_rotate_quantize(bf16_dev(xb[t:t + 1]), to_dev(w), eps, act_bits)
+            assert torch.equal(n1, normed[t:t + 1]) and torch.equal(c1, codes[t:t + 1]) and torch.equal(s1, scales[t:t + 1])
