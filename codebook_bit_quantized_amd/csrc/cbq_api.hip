@@ -30,6 +30,12 @@ int hip_fail(hipError_t e, const char* where) {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
 
+// whether rows (< 2^31) of stride ld elements of esz bytes take 1 GiB or more; no product here passes 64 bits
+bool reaches_1gib(int64_t rows, int64_t ld, int64_t esz) {
+  constexpr int64_t lim = int64_t(1) << 30;
+  return ld > lim / esz || rows * (ld * esz) >= lim;
+}
+
 int check_weights(const cbq_weights* W, int i) {
   if (!W->idx || !W->codebook) return fail(CBQ_EINVAL, "W[%d]: idx and codebook must be non-null", i);
   if (!aligned16(W->idx) || !aligned16(W->codebook))
@@ -526,7 +532,7 @@ CBQ_EXPORT int cbq_codebook_adapter_gemm(const uint8_t* codes, const float* scal
   if (n_adapters < 1) return fail(CBQ_EINVAL, "n_adapters must be >= 1 (got %d)", n_adapters);
   if (rank < 8 || rank > 128 || rank % 8) return fail(CBQ_EINVAL, "rank must be a multiple of 8 in [8, 128] (got %d)", rank);
   if (T == 0) return CBQ_OK;
-  if (T > (int64_t(1) << 30) / (ldo * 4) || T * ldo * 4 >= (int64_t(1) << 30))
+  if (reaches_1gib(T, ldo, 4))
     return fail(CBQ_EUNSUPPORTED, "output must be smaller than 1 GiB per call (T * ldo * 4 bytes)");
   if (T * ((int64_t)W->K * act_bits / 8) >= (int64_t(1) << 31)) return fail(CBQ_EUNSUPPORTED, "codes must be smaller than 2 GiB");
   if ((int64_t)W->N * cbq::index_row_bytes(W->K, W->bits, W->layout == CBQ_LAYOUT_BLOCKED) >= (int64_t(1) << 31))
