@@ -288,7 +288,7 @@ CBQ_EXPORT int cbq_codebook_lut_gemm(const uint8_t* codes, const float* scales, 
   if (n_rows == 0) return CBQ_OK;
   {
     const int64_t esz = epilogue == CBQ_EPI_SWIGLU_BF16 ? 2 : 4;
-    if (n_rows * ldo * esz >= (int64_t(1) << 30))
+    if (reaches_1gib(n_rows, ldo, esz))
       return fail(CBQ_EUNSUPPORTED, "output must be smaller than 1 GiB per call (n_rows * ldo * %lld bytes)", (long long)esz);
     if ((int64_t)W[0].N * cbq::index_row_bytes(W[0].K, W[0].bits, W[0].layout == CBQ_LAYOUT_BLOCKED) >=
         (int64_t(1) << 31))

@@ -37,3 +37,10 @@ def _child(call):
 
 def test_codebook_adapter_gemm_strides():
     _child(ADAPTER)
+
+
+def test_codebook_lut_gemm_strides():
+    _child("rc = lib.cbq_codebook_lut_gemm(P, P, 4, T, None, None, W, 1, 0, 0, P, ldo, None, 0, None)")
+    # bf16 rows: one of 2^28 elements is half a GiB, and not to be refused
+    _child("if T * ldo < 1 << 29: continue\n"
+           "        rc = lib.cbq_codebook_lut_gemm(P, P, 4, T, None, None, G, 2, 1, 2, P, ldo, None, 0, None)")
