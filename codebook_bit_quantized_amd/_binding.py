@@ -439,6 +439,8 @@ def _check_norm_args(T, K, dev, weight, act_bits, normed, codes, scales):
     if act_bits:
         _tensor("codes", codes, dev, torch.uint8, (T, K * act_bits // 8), contiguous=True)
         _tensor("scales", scales, dev, torch.float32, (T,), contiguous=True)
+    elif codes is not None or scales is not None:
+        raise ValueError("codes and scales are written with act_bits 4 or 8 only (got 0)")
 
 
 def norm_rotate_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, act_bits: int = 4,
@@ -500,6 +502,8 @@ def combine_norm_residual(rows: torch.Tensor, residual: torch.Tensor, slot_of: O
         ldg = 0 if shared_gate else _row_stride(gate)
     if next_weight is not None:
         _check_norm_args(T, H, dev, next_weight, act_bits, normed, codes, scales)
+    elif normed is not None or codes is not None or scales is not None:
+        raise ValueError("normed, codes and scales are written with next_weight only")
 
     def call(st):
         o = _like_rows(residual) if out is None else out
