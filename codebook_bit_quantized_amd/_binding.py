@@ -188,6 +188,9 @@ def _row_stride(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 8 * ((t.shape[1] + 7) // 8))
 
 
+_CODEBOOK_TYPES = (torch.int16, torch.float16, torch.uint16)
+
+
 @dataclass
 class CodebookWeights:
     """One weight matrix type for E experts: packed indices and fp16 codebooks (device).
@@ -215,8 +218,8 @@ class CodebookWeights:
             raise ValueError(f"{name}.idx must have three dimensions (got shape {tuple(idx.shape)})")
         E, N, _ = idx.shape
         _tensor(name + ".idx", idx, dev, torch.uint8, (E, N, kp * bits // 8), contiguous=True)
-        if cb.element_size() != 2:
-            raise ValueError(f"{name}.codebook must hold 16-bit fp16 patterns (got {cb.dtype})")
+        if cb.dtype not in _CODEBOOK_TYPES:
+            raise ValueError(f"{name}.codebook must hold fp16 patterns as float16, int16 or uint16 (got {cb.dtype})")
         _tensor(name + ".codebook", cb, dev, cb.dtype, (E, N, 1 << bits), contiguous=True)
         return cbq_weights(idx.data_ptr(), cb.data_ptr(), E, N, K, bits, self.layout)
 

@@ -2,10 +2,12 @@
 import pytest
 import torch
 
+import datagen
+
 pytestmark = pytest.mark.gpu
 
 cbq = pytest.importorskip("codebook_bit_quantized_amd")
-from gpu_util import DEV  # noqa: E402
+from gpu_util import DEV, upload_weights  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -35,3 +37,25 @@ def test_output_tensors_that_would_stay_unwritten():
     out = cbq.combine_norm_residual(x, x, next_weight=w, act_bits=4, normed=normed, codes=codes, scales=scales)
     assert out[1] is normed and out[2] is codes and out[3] is scales
     assert cbq.combine_norm_residual(x, x, act_bits=4).shape == x.shape
+
+
+def test_codebooks_of_another_16_bit_type():
+    """fp16 patterns come as float16, int16 or uint16; bfloat16 values are not fp16 patterns."""
+    T, K, N = 2, 64, 32
+    w = upload_weights(datagen.random_weights(3, 1, N, K, 4))
+    x = torch.randn((T, K), device=DEV).to(torch.bfloat16)
+    codes, scales = cbq.rotate_quantize(x, 4)
+    a = torch.zeros((1, 8, K), dtype=torch.bfloat16, device=DEV)
+    b = torch.zeros((1, N, 8), dtype=torch.bfloat16, device=DEV)
+    of = torch.zeros(T, dtype=torch.int32, device=DEV)
+    run = lambda v: cbq.codebook_adapter_gemm(  # noqa: E731
+        codes, scales, 4, cbq.CodebookWeights(w.idx, w.codebook.view(v), K, 4), x, a, b, of)
+    want = run(torch.int16)
+    assert torch.equal(run(torch.float16), want) and torch.equal(run(torch.uint16), want)
+    with pytest.raises(ValueError, match="codebook"):
+        run(torch.bfloat16)
+    # the same tensors as a layer of one expert
+    down = upload_weights(datagen.random_weights(4, 1, K, N, 4))
+    bad = cbq.CodebookWeights(w.idx, w.codebook.view(torch.bfloat16), K, 4)
+    with pytest.raises(ValueError, match="codebook"):
+        cbq.moe_ffn_few(codes, scales, torch.zeros((T, 1), device=DEV), w, bad, down, 1)
