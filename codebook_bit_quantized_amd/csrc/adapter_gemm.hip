@@ -11,7 +11,7 @@
 // a decode batch), with results taken only for the tokens of that adapter, so another adapter's
 // infinities never reach a token.  Beyond a decode batch, tiles of both launches take their
 // group's tokens by adapter (order_by_adapter), which no result depends on: 4096 tokens in
-// random order over 32 adapters of rank 64 176 + 608 us without, 68 + 455 with.
+// random order over 32 adapters of rank 64 168 + 549 us without, 66 + 418 with.
 #include "cbq_internal.hpp"
 #include "adapter_device.hpp"
 #include "few_device.hpp"
@@ -25,8 +25,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 // tile, rank rows from 16 RT (z / parts) on, channels of part z % parts; the waves split those
 // and their sums meet in LDS in wave order.  The parts are summed by the projection.  Bound by
 // load latency in a decode batch (so K is cut into enough parts to have all of an adapter's
-// rows in flight at once: 16 tokens, K = 9728, rank 32, 16 adapters, 10 MB: 12 us in one part,
-// 5.4 in 8), by its short sweeps in a prefill batch (4096 x 2560, rank 16: 21 MB of x in 12 us).
+// rows in flight at once: 16 tokens, K = 9728, rank 32, 16 adapters, 10 MB: 23.5 us in one part,
+// 5.5 in 16), by its short sweeps in a prefill batch (4096 x 2560, rank 16: 21 MB of x in 13 us).
 template <int RT, bool ORDER>
 __global__ void __launch_bounds__(256)
 adapter_shrink_kernel(AdapterArgs a, const uint16_t* __restrict__ x, int64_t ldx, const uint16_t* __restrict__ lora_a,
@@ -142,7 +142,8 @@ adapter_shrink_kernel(AdapterArgs a, const uint16_t* __restrict__ x, int64_t ldx
 // 8, dealt to the splits), both reduced in split order.  Every lane forms its own outputs'
 // adapter terms, so tokens with different adapters cost no more than tokens with one.
 // Latency-bound: 2560 -> 9728 at one token 9.0 us for 12.8 MB (cbq_codebook_lut_gemm without
-// adapters: 8.2), 9728 -> 2560 at 16 tokens with 16 adapters 12.9 us for 15 MB (10.5).
+// adapters: 8.2), 9728 -> 2560 at 16 tokens with 16 adapters 12.8 us for 15 MB (10.7), where its
+// 160 workgroups leave 96 CUs without one.
 template <int BITS, int ABITS, bool BLK, int DEPTH>
 __global__ void __launch_bounds__(1024)
 few_adapter_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales, GemmW w, int T, int N, int K,
@@ -222,8 +223,9 @@ few_adapter_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ 
 
 // K is split until about 2048 waves share the sweep, while each keeps at least eight chunks (the
 // splits' sums and the adapters' ranks cost a pass over LDS each): half as many waves, or
-// sixteen chunks at least, take 10.3 us instead of 9.0 for 2560 -> 9728 at one token, and
-// 12.5 instead of 12.9 for 9728 -> 2560 at 16; twice as many waves, or four chunks, the same.
+// sixteen chunks at least, take 10.4 and 10.2 us instead of 9.0 for 2560 -> 9728 at one token,
+// and 12.6 instead of 12.9 for 9728 -> 2560 at 16; twice as many waves the same, four chunks at
+// least the same, or 7.3 instead of 7.9 for 2560 -> 2560 at 16.
 template <int BITS, int ABITS, bool BLK>
 static hipError_t launch_few_adapter(const GemmArgs& a, const AdapterArgs& ad, hipStream_t stream) {
   const int tiles = a.N / 16, nchunks = (a.K + 127) / 128;
@@ -238,9 +240,9 @@ static hipError_t launch_few_adapter(const GemmArgs& a, const AdapterArgs& ad, h
 }
 
 // Parts of K in the first launch, at most: enough workgroups for a decode batch or a short
-// prefill (one part: 16 tokens of K = 9728 12.0 us instead of 5.0, 333 tokens of rank 64 14.8
-// instead of 9.0; more than four save the latter 1.5 us and cost the projection 2.3); one part
-// beyond, where the token tiles fill the GPU.
+// prefill (one part: 16 tokens of K = 9728 23.5 us instead of 5.5, 333 tokens of rank 64 15.8
+// instead of 9.6; sixteen save the latter 2.2 us and cost the projection 2.7); fewer beyond,
+// where the token tiles fill the GPU (2048 tokens of K = 2560 in one part 8.8 instead of 8.5).
 static int adapter_max_parts(int64_t T) { return T <= kFewRows ? 16 : T <= 1024 ? 4 : T <= 8192 ? 2 : 1; }
 
 size_t adapter_workspace_bytes(int64_t T, int rank) {
@@ -255,7 +257,7 @@ hipError_t launch_adapter_gemm(const GemmArgs& a, AdapterArgs ad, const uint16_t
   const int RT = rt >= 4 ? 4 : rt >= 2 ? 2 : 1, zr = (rt + RT - 1) / RT;
   // a decode batch's tile may hold 16 adapters, one a workgroup; in larger batches, where
   // requests mostly span tiles, a tile's four workgroups take turns (16 tokens with 16 adapters:
-  // 5.0 us with 16 workgroups, 9.1 with four, 21 with one; 333 tokens 9.0, 9.0, 14.2)
+  // 5.5 us with 16 workgroups, 10.1 with four, 23.8 with one; 333 tokens 9.5, 9.6, 15.2)
   const int most = (int)(T < 16 ? T : T <= 256 ? 16 : 4), ny = ad.n_adapters < most ? ad.n_adapters : most;
   const int64_t tiles = (T + 15) / 16;
   // parts of at least 4 steps of 64 channels (one a wave)

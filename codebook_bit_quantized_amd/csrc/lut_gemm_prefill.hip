@@ -93,9 +93,9 @@ template <> struct TileAdapters<true> {
 // fragment holds an infinity or NaN, zeros would not keep it from the other rows, so that pass
 // is summed apart and taken by its own rows only.  This code runs once per tile, so its size in
 // instructions is its time (a version unrolled over ranks and split in registers took 60 us a
-// tile).  2560 -> 9728, 4-bit codebooks: 4096 tokens in 8 requests, rank 16, 240 us (0.85
-// PFLOP/s; 256 us without adapters in the tiles of 256 columns), 333 tokens of rank 64 47 us;
-// 4096 tokens in random order over 32 adapters of rank 64 take 455 us, a pass per adapter and
+// tile).  2560 -> 9728, 4-bit codebooks: 4096 tokens in 8 requests, rank 16, 247 us (0.83
+// PFLOP/s; 264 us without adapters in the tiles of 256 columns), 333 tokens of rank 64 48 us;
+// 4096 tokens in random order over 32 adapters of rank 64 take 418 us, a pass per adapter and
 // tile whose fragments of lora_b (637 MB over the tiles) come one pass ahead.
 // ranks staged at a time; the small tiles have the registers to stage 64 with all loads in flight
 template <int BM, int NS> constexpr int stage_ranks() { return BM == 128 && NS == 1 ? 64 : 32; }
@@ -975,12 +975,16 @@ hipError_t launch_mfma_prefill(const GemmArgs& a, int min_rows, hipStream_t stre
   return hipErrorInvalidValue;
 }
 
-// The single-matrix kernels with adapters, without a K split.  2- and 3-bit codebooks: tiles of
-// 128 rows x 256 columns where they make at least two workgroups a CU, else 128 columns.
-// 4-bit: 256 rows x 128 columns (two workgroups a CU; with 256 columns the accumulators fill
-// the registers and the epilogue spills: 4096 tokens, 2560 -> 9728, rank 16: 309 us a call
-// against 229), and 128 rows where 256 would leave CUs without a tile (333 tokens: 152 tiles
-// of 256 rows or 228 of 128).
+// The single-matrix kernels with adapters, without a K split: from 33 tokens on a narrow
+// projection runs few workgroups over all of K (33 tokens of 9728 -> 2560: 20 of them, 97 us,
+// where 32 tokens take 17 in few_adapter_kernel; of 2560 -> 9728 76 and 39 us, against 16).
+// 2- and 3-bit codebooks: tiles of 128 rows x 256 columns where they make at least two
+// workgroups a CU (4096 tokens, 2560 -> 9728, rank 16, 3 bits: 213 us, 247 in 128 columns), else
+// 128 columns (1024 tokens, 304 tiles of 256 columns: 80 us, 76 in those).  4-bit: 256 rows x
+// 128 columns (two workgroups a CU; 4096 tokens 247 us; with 256 columns, where the
+// accumulators fill the registers and the epilogue spills, 305; with 128 rows 295), and 128
+// rows where 256 would leave CUs without a tile (333 tokens: 152 tiles of 256 rows 77 us, 228
+// of 128 48).
 template <int BITS, int ABITS, bool BLK, int NS, int BM>
 static hipError_t launch_adp_tiles(const GemmArgs& a, const AdapterArgs& ad, hipStream_t stream) {
   const int64_t mt = (a.n_rows + BM - 1) / BM;

@@ -26,9 +26,9 @@
 // stay rolled where the unrolled code would run once.
 //
 // Measured (us; weights of three layers in turn): 128 experts, top 8, 2048 x 768, 4 bits: one
-// token 9.3 + 9.6 (the batch form takes 24 a call, this one 17.6); 32 tokens 4.8 + 50 + 4.8 + 31
-// + 5.1.  64 + 2 experts, 2048 x 1408, 3 and 2 bits, 8 tokens 3.9 + 26 + 4.8 + 14 + 4.8.  8
-// experts, top 2, 4096 x 14336, 4 bits, 16 tokens 4.8 + 109 + 9 + 61 + 4.8.
+// token 9.4 + 9.6 (the batch form takes 24 a call, this one 17.6); 32 tokens 4.7 + 49 + 4.8 + 31
+// + 5.2.  64 + 2 experts, 2048 x 1408, 3 and 2 bits, 8 tokens 3.7 + 26 + 4.7 + 14 + 4.6.  8
+// experts, top 2, 4096 x 14336, 4 bits, 16 tokens 4.9 + 110 + 9.7 + 62 + 4.8.
 // h is kept in fp32 up to the quantiser: the codes are those of the unrounded h up to fp32
 // sums (a bf16 h would move a code wherever its rounding crosses a border).
 #include "cbq_internal.hpp"
@@ -183,11 +183,11 @@ __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + e
 // when there are fewer choices than experts, a choice (the first one of its expert does the
 // work).  An expert of more than 16 rows sweeps its weights twice.
 // Bound by reading the weights and, at 4 bits, by looking them up (23 vector instructions for 8
-// weights: about 26 us of the 50 for 362 million weights), which overlap in part: 128 experts
-// at 32 tokens 181 MB in 50 us (3.6 TB/s) and 95 MB in 31 us; 8 wide experts 477 MB in 109 us
-// (4.4 TB/s) and 236 MB in 61 us, where a large copy reaches 5.1.  Five waves a SIMD and two
-// chunks in flight: four waves measured the same to 2 % slower, four chunks 5 to 17 % slower
-// (their registers cost waves).
+// weights: about 26 us of the 49 for 362 million weights), which overlap in part: 128 experts
+// at 32 tokens 181 MB in 49 us (3.7 TB/s) and 95 MB in 31 us; 8 wide experts 477 MB in 110 us
+// (4.3 TB/s) and 236 MB in 62 us, where a large copy reaches 5.1.  Five waves a SIMD and two
+// chunks in flight: four waves measured 3 % faster (128 experts) to 4 % slower (8 wide ones),
+// four chunks the same to 15 % slower (their registers cost waves).
 template <int BITS, bool PAIR, bool BLK, int DEPTH>
 __global__ void __launch_bounds__(512, 5)
 few_gemm_kernel(FewArgs a, int CW, int SK) {
@@ -529,8 +529,9 @@ few_combine_kernel(const float* __restrict__ rows, const float* __restrict__ wts
 }
 
 // K is split until about 4096 waves share the sweep, while each keeps at least four chunks:
-// half as many waves leave the down sweeps 3 to 17 % slower, twice as many the others up to
-// 8 % (two or eight chunks at least: the same within 2 %).
+// half as many waves leave the down sweeps the same to 15 % slower (64 + 2 experts at 8 tokens
+// 14.4 -> 16.6 us), twice as many all of them 18 % faster (the same experts' down at 32 tokens
+// 27.5 -> 22.6 us) to 7 % slower (at 8 tokens 15.4 us); two or eight chunks at least: within 4 %.
 template <int BITS, bool PAIR, bool BLK>
 static hipError_t launch_few_gemm(const FewArgs& a, hipStream_t stream) {
   const int ys = (a.T * a.topk < a.E ? a.T * a.topk : a.E) + a.n_shared;

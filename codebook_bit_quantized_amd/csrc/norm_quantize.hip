@@ -15,14 +15,14 @@
 // One workgroup per token, CPT channels a thread: 8 (16 beyond K = 8192), so one token's work
 // is spread over K / 512 waves (a single token's latency is what decode sees), or 32 for the
 // norm before a block of many tokens (norm_width).  A thread's channels are runs of 8, kRun
-// apart, so that a wave's loads and stores are contiguous whatever CPT is (with 32 consecutive
-// ones the norm alone, without codes, took 13.8 us at 4096 x 2048 instead of 9.8).  With expert
-// rows it is bound by reading them (4096 x 2048, 8 rows each, gates, norms and codes: 344 MB in
-// 76 us, 4.5 TB/s of the 5.1 a large copy reaches); the norm alone by its vector instructions,
-// mostly the transform's exchanges in fp64 (4096 x 2048: 42 MB in 18 to 20 us).  The transform's
-// first stages run in the thread, the next ones between lanes, then between a thread's runs,
-// and the ones across waves in one LDS pass whatever their number (each thread reads its
-// partners in the block's other waves and adds them with their signs).
+// apart, so that a wave's loads and stores are contiguous whatever CPT is.  With expert rows it is
+// bound by reading them (4096 x 2048, 8 fp32 rows each, gates, norms and codes: 344 MB in 76 us,
+// 4.5 TB/s of the 5.1 a large copy reaches; 8 bf16 rows 210 MB in 61 us); the norm alone by its
+// vector instructions, mostly the transform's exchanges in fp64 (4096 x 2048: 42 MB in 20 us;
+// without codes 34 MB in 10 us).  The transform's first stages run in the thread, the next ones
+// between lanes, then between a thread's runs, and the ones across waves in one LDS pass whatever
+// their number (each thread reads its partners in the block's other waves and adds them with
+// their signs).
 #include "cbq_internal.hpp"
 #include "few_device.hpp"
 #include "rotate_device.hpp"
@@ -382,10 +382,10 @@ static void launch_nt(const NormArgs& a, int src, unsigned tokens, unsigned thre
 
 // Channels a thread of the norm before a block: 8 is the shortest chain, and the faster one up
 // to about 4 million values; beyond, 32 where they fill the waves, as a wave's reductions and
-// exchanges then serve four times the channels (us, 8 against 32: 512 x 4096 9.4 / 11.6, 2048 x
-// 2048 12.8 / 11.4, 4096 x 2048 21.3 / 18.2, 4096 x 4096 41.8 / 33.1, 2048 x 8192 55 / 36; waves
-// filled to 62 %: 4096 x 2560 20.8 / 26.4).  Beyond 8192 channels a workgroup's 1024 threads
-// need 16 (or 32).
+// exchanges then serve four times the channels (us, 8 against 32: 512 x 4096 10.1 / 12.3, 1024 x
+// 2048 9.4 / 10.6, 2048 x 2048 14.6 / 14.7, 4096 x 2048 21.2 / 20.1, 4096 x 4096 41.8 / 34.3,
+// 2048 x 8192 58 / 38; waves filled to 62 %: 4096 x 2560 21.7 / 26.8).  Beyond 8192 channels a workgroup's
+// 1024 threads need 16 (or 32).
 static int norm_width(int64_t T, int K) {
   const int threads = K / 32, full = (threads + 63) / 64 * 64;
   if (T * K >= (1 << 22) && 10 * threads >= 9 * full) return 32;
