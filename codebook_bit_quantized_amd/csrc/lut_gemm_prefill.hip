@@ -84,8 +84,8 @@ template <> struct TileAdapters<true> {
 
 // Adds the adapters' terms to a tile's scaled sums: column n of row m gains
 // sum_r u[m][r] lora_b[a][n][r], a the row's adapter.  u (its parts summed in order) is split
-// into three bf16 parts (8 bits each, so their sum is u's 24 bits), whose products with lora_b
-// are exact and accumulate in fp32: 3 MFMAs per 16 ranks against K / 16 of the projection.
+// into three bf16 parts (8 bits each, so their sum is u's 24 bits, but for bits below 2^-133, which
+// are those of |u| < 2^-110), whose products with lora_b are exact and accumulate in fp32: 3 MFMAs per 16 ranks against K / 16 of the projection.
 // The split vectors are staged in the activation tiles' LDS, 32 or 64 ranks at a time, with a row of
 // zeros behind them.  One pass per distinct adapter among the tile's rows (one to three where
 // requests are contiguous), in which the other rows read the zeros, over the 32-row sub-tiles

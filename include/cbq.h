@@ -470,7 +470,9 @@ int cbq_moe_ffn_few(const uint8_t* codes, const float* scales, int32_t act_bits,
  *  out        : fp32 [T][ldo] (ldo >= N, ldo % 4 == 0, 16-byte aligned):
  *               out[t][n] = scales[t] * sum_k q[t][k] W[n][k]
  *                           + adapter_scale[a] * sum_r lora_b[a][n][r] * (sum_k lora_a[a][r][k] x[t][k]),
- *               a = adapter_of[t]; every product exact, sums and the middle vector in fp32.
+ *               a = adapter_of[t]; every product exact, sums and the middle vector in fp32
+ *               (beyond 32 tokens, of the middle vector times adapter_scale, what lies below
+ *               2^-133, bf16's smallest step, does not count).
  *  ws, ws_bytes : device workspace of cbq_adapter_workspace(T, rank) bytes, 16-byte aligned
  *               (the middle vectors; rewritten by every call; calls that overlap in time
  *               need one each).

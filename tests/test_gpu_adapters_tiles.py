@@ -112,3 +112,28 @@ def test_rows_of_x_beyond_32_bit_offsets(T):
     of = to_dev((np.arange(T) % 3).astype(np.int32))
     assert torch.equal(cbq.codebook_adapter_gemm(codes, scales, 4, w, x, a, b, of),
                        cbq.codebook_adapter_gemm(codes, scales, 4, w, x.contiguous(), a, b, of))
+
+
+@pytest.mark.parametrize("T,N,rank,bits,act_bits,n_ad", [(32, 64, 128, 4, 4, 5), (32, 48, 128, 3, 8, 40), (17, 16, 8, 2, 8, 3)])
+def test_decode_batches_with_the_most_splits(T, N, rank, bits, act_bits, n_ad):
+    """K = 16384 on a narrow projection: 16 splits of K in a workgroup, the widest middle vectors beside them."""
+    _case(T, 16384, N, bits, act_bits, rank, n_ad)
+
+
+@pytest.mark.parametrize("T", [4, 40])
+@pytest.mark.parametrize("mag", [(1e-39, 1e30, 1.0), (1e30, 1e-39, 1.0), (1e20, 1e-20, 1e-39), (3e-39, 1.0, 1e30), (1e-30, 1e-8, 1e30)])
+def test_subnormal_factors(T, mag):
+    """Subnormal x, lora_a or lora_b, and middle vectors near and below fp32's smallest normal value: the
+    tolerance of the other tests and, beyond a decode batch, 2^-133 of the middle vector (half a step of
+    its last part's, 2^-134, and of the fp32 sum's, 2^-150, are less)."""
+    K, N, rank = 256, 64, 16
+    w = cbq.prepack_weights(upload_weights(datagen.random_weights(3, 1, N, K, 4)))
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(T)
+    rnd = lambda m, *s: (torch.randn(s, generator=gen, device=DEV) * m).to(torch.bfloat16)  # noqa: E731
+    x, a, b = rnd(mag[0], T, K), rnd(mag[1], 1, rank, K), rnd(mag[2], 1, N, rank)
+    codes = torch.zeros((T, K), dtype=torch.uint8, device=DEV)
+    out = cbq.codebook_adapter_gemm(codes, torch.zeros(T, device=DEV), 8, w, x, a, b, torch.zeros(T, dtype=torch.int32, device=DEV))
+    x, a, b = x.double(), a[0].double(), b[0].double()
+    tol = 6.1e-5 * (x.abs() @ a.abs().T) @ b.abs().T + 2.0 ** -133 * b.abs().sum(1) + 2.0 ** -149
+    assert ((out - (x @ a.T) @ b.T).abs() <= tol).all()

@@ -61,6 +61,12 @@ def test_batches(T, H, F, E, topk, n_shared, bits_gu, bits_d, act_bits):
     _check(T, H, F, E, topk, n_shared, bits_gu, bits_d, act_bits)
 
 
+@pytest.mark.parametrize("T,F,act_bits", [(2, 16384, 8), (17, 12288, 8), (3, 10240, 4), (1, 16384, 4)])
+def test_widest_h(T, F, act_bits):
+    """Rotation blocks of 2048 to 16384 channels of h, across all waves of a workgroup."""
+    _check(T, 64, F, 3, 2, 1, 3, 4, act_bits)
+
+
 @pytest.mark.parametrize("F", [96, 128, 256, 768, 1408, 512, 1024, 1536, 2048])
 @pytest.mark.parametrize("act_bits", [4, 8])
 def test_a_token_alone_has_the_codes_of_h_that_it_has_in_a_batch(F, act_bits):
