@@ -16,7 +16,9 @@ Around the layer in a decoder block: ``norm_rotate_quantize`` (the norm before a
 codes), ``combine_norm_residual`` (after it: combine, norm, gate, residual, the next norm),
 ``moe_ffn_few`` (the whole layer for at most ``FEW_MAX_TOKENS`` tokens, with
 ``moe_few_workspace``) and ``codebook_adapter_gemm`` (a projection with the low-rank adapters of
-many requests, with ``adapter_workspace``).
+many requests, with ``adapter_workspace``).  Its attention: ``KVCache``, a key/value cache held in
+4 bits, ``kv_cache_write`` and ``kv_cache_read``, and ``kv_attention`` over it (with
+``kv_attention_workspace``).
 """
 from ._binding import (AUTO_MAX_LUT_ROWS, CBQ_EHIP, CBQ_EINVAL, CBQ_EUNSUPPORTED, CBQ_EWORKSPACE,
                        CBQ_OK, EPI_F32, EPI_SWIGLU_BF16, EXPORTED, LIB_PATH, PATH_AUTO, PATH_LUT,
@@ -27,13 +29,16 @@ from ._binding import (AUTO_MAX_LUT_ROWS, CBQ_EHIP, CBQ_EINVAL, CBQ_EUNSUPPORTED
                        rotate_dense_workspace, rotate_quantize, rotate_quantize_dense,
                        route_workspace, gemm_workspace, norm_rotate_quantize,
                        combine_norm_residual, moe_ffn_few, moe_few_workspace, FEW_MAX_TOKENS,
-                       codebook_adapter_gemm, adapter_workspace, TYPE_F32, TYPE_BF16)
+                       codebook_adapter_gemm, adapter_workspace, TYPE_F32, TYPE_BF16,
+                       KVCache, KV_ROTATE_K, KV_ROTATE_V, kv_cache_write, kv_cache_read, kv_attention,
+                       kv_attention_workspace)
 
 __all__ = [
     "rotate_quantize", "moe_route_gather", "moe_route_gather_noalloc", "prepack_weights", "LAYOUT_ROWS", "LAYOUT_BLOCKED",
     "codebook_lut_gemm", "moe_combine", "moe_ffn",
     "route_workspace", "gemm_workspace", "kmeans_codebooks", "refit_codebooks", "cpu_lut_gemm", "rotate_quantize_dense",
     "rotate_dense_workspace", "norm_rotate_quantize", "combine_norm_residual", "moe_ffn_few", "moe_few_workspace", "FEW_MAX_TOKENS", "codebook_adapter_gemm", "adapter_workspace", "TYPE_F32", "TYPE_BF16",
+    "KVCache", "KV_ROTATE_K", "KV_ROTATE_V", "kv_cache_write", "kv_cache_read", "kv_attention", "kv_attention_workspace",
     "CodebookWeights", "CbqError", "load_library", "LIB_PATH", "EXPORTED", "cbq_weights",
     "EPI_F32", "EPI_SWIGLU_BF16", "PATH_AUTO", "PATH_LUT", "PATH_MFMA", "PATH_PAGES_PRODUCTS", "PATH_PAGES_BUCKETS", "PATH_REG_TABLES", "PATH_LDS_TABLES", "AUTO_MAX_LUT_ROWS",
     "CBQ_OK", "CBQ_EINVAL", "CBQ_EUNSUPPORTED", "CBQ_EWORKSPACE", "CBQ_EHIP",

@@ -33,7 +33,8 @@ EXPORTED = ("cbq_rotate_quantize", "cbq_rotate_quantize_ex", "cbq_rotate_dense_w
             "cbq_gemm_workspace", "cbq_codebook_lut_gemm", "cbq_moe_combine",
             "cbq_kmeans_codebooks", "cbq_refit_codebooks", "cbq_cpu_lut_gemm", "cbq_status_string", "cbq_last_error",
             "cbq_version", "cbq_norm_rotate_quantize", "cbq_combine_norm_residual", "cbq_moe_few_workspace",
-            "cbq_moe_ffn_few", "cbq_adapter_workspace", "cbq_codebook_adapter_gemm")
+            "cbq_moe_ffn_few", "cbq_adapter_workspace", "cbq_codebook_adapter_gemm", "cbq_kv_cache_write",
+            "cbq_kv_cache_read", "cbq_kv_attention_workspace", "cbq_kv_attention")
 
 
 class CbqError(RuntimeError):
@@ -60,6 +61,20 @@ class cbq_norm(ctypes.Structure):
                 ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
+KV_ROTATE_K, KV_ROTATE_V = 1, 2
+
+
+class cbq_kv_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("n_kv", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("D", ctypes.c_int32), ("rotate", ctypes.c_int32)]
+
+
+class cbq_kv_seqs(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64), ("max_pages", ctypes.c_int32),
+                ("lens", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("B", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -75,6 +90,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     W = ctypes.POINTER(cbq_weights)
     f32, Nrm = ctypes.c_float, ctypes.POINTER(cbq_norm)
+    KVC, KVS = ctypes.POINTER(cbq_kv_cache), ctypes.POINTER(cbq_kv_seqs)
     sig = {
         "cbq_rotate_quantize": (ctypes.c_int, [vp, i64, i32, i64, i32, i32, vp, vp, vp, vp]),
         "cbq_rotate_quantize_ex": (ctypes.c_int, [vp, i64, i32, i64, i32, i32, vp, vp, vp, vp, vp,
@@ -104,6 +120,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "cbq_adapter_workspace": (sz, [i64, i32]),
         "cbq_codebook_adapter_gemm": (ctypes.c_int, [vp, vp, i32, i64, W, vp, i64, vp, vp, vp, i32, i32, vp, vp, i64, vp,
                                                      sz, vp]),
+        "cbq_kv_cache_write": (ctypes.c_int, [KVC, KVS, vp, i64, vp, i64, i64, vp]),
+        "cbq_kv_cache_read": (ctypes.c_int, [KVC, KVS, vp, i64, vp, i64, i64, vp]),
+        "cbq_kv_attention_workspace": (sz, [KVC, i64, i32, i32]),
+        "cbq_kv_attention": (ctypes.c_int, [KVC, KVS, vp, i64, i64, i32, f32, i32, i32, vp, i64, vp, sz, vp]),
         "cbq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "cbq_last_error": (ctypes.c_char_p, []),
         "cbq_version": (ctypes.c_int, []),
@@ -609,6 +629,172 @@ def codebook_adapter_gemm(codes: torch.Tensor, scales: torch.Tensor, act_bits: i
             codes.data_ptr(), scales.data_ptr(), act_bits, T, ctypes.byref(W), x.data_ptr(),
             _row_stride(x), lora_a.data_ptr(), lora_b.data_ptr(), _opt_ptr(adapter_scale), n_ad, rank,
             adapter_of.data_ptr(), o.data_ptr(), _row_stride(o), w.data_ptr(), w.numel(), st))
+        return o
+
+    return _on_stream(dev, stream, call)
+
+
+@dataclass
+class KVCache:
+    """A layer's 4-bit key/value cache (device): E2M1 codes and one fp32 scale a token and head,
+    in pages of `page` tokens (a power of two, 16 to 1024); heads of D = 64 or 128 channels.
+    rotate: which of keys and values are held rotated (KV_ROTATE_K | KV_ROTATE_V)."""
+    k_codes: torch.Tensor    # uint8 [n_pages][n_kv][page][D/2]
+    v_codes: torch.Tensor
+    k_scales: torch.Tensor   # fp32 [n_pages][n_kv][page]
+    v_scales: torch.Tensor
+    rotate: int = KV_ROTATE_K | KV_ROTATE_V
+
+    @classmethod
+    def empty(cls, n_pages: int, n_kv: int, page: int, D: int, device="cuda",
+              rotate: int = KV_ROTATE_K | KV_ROTATE_V) -> "KVCache":
+        """A cache of zeros."""
+        codes = [torch.zeros((n_pages, n_kv, page, D // 2), dtype=torch.uint8, device=device) for _ in "kv"]
+        scales = [torch.zeros((n_pages, n_kv, page), dtype=torch.float32, device=device) for _ in "kv"]
+        return cls(codes[0], codes[1], scales[0], scales[1], rotate)
+
+    @property
+    def n_pages(self) -> int:
+        return self.k_codes.shape[0]
+
+    @property
+    def n_kv(self) -> int:
+        return self.k_codes.shape[1]
+
+    @property
+    def page(self) -> int:
+        return self.k_codes.shape[2]
+
+    @property
+    def D(self) -> int:
+        return self.k_codes.shape[3] * 2
+
+    def _c_checked(self, dev: torch.device) -> cbq_kv_cache:
+        """The C struct of tensors that are as it describes them: on dev, packed, of these sizes."""
+        if self.k_codes.dim() != 4:
+            raise ValueError(f"k_codes must have four dimensions (got shape {tuple(self.k_codes.shape)})")
+        n, h, p, half = self.k_codes.shape
+        _tensor("k_codes", self.k_codes, dev, torch.uint8, contiguous=True)
+        _tensor("v_codes", self.v_codes, dev, torch.uint8, (n, h, p, half), contiguous=True)
+        _tensor("k_scales", self.k_scales, dev, torch.float32, (n, h, p), contiguous=True)
+        _tensor("v_scales", self.v_scales, dev, torch.float32, (n, h, p), contiguous=True)
+        return cbq_kv_cache(self.k_codes.data_ptr(), self.v_codes.data_ptr(), self.k_scales.data_ptr(),
+                            self.v_scales.data_ptr(), n, h, p, 2 * half, self.rotate)
+
+
+def _kv_seqs(cache: KVCache, dev, lens, block_table, offsets) -> cbq_kv_seqs:
+    if lens.dim() != 1:
+        raise ValueError(f"lens must have one dimension (got shape {tuple(lens.shape)})")
+    B = lens.shape[0]
+    _tensor("lens", lens, dev, torch.int32, contiguous=True)
+    _tensor("offsets", offsets, dev, torch.int32, (B + 1,), contiguous=True)
+    if block_table is None:
+        return cbq_kv_seqs(None, 0, cache.n_pages // max(B, 1), lens.data_ptr(), _opt_ptr(offsets), B)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must have shape ({B}, pages) (got {tuple(block_table.shape)})")
+    _tensor("block_table", block_table, dev, torch.int32, rows=True)
+    ld = block_table.stride(0) if B > 1 else block_table.shape[1]
+    if ld < block_table.shape[1]:
+        raise ValueError("block_table's rows must not overlap")
+    return cbq_kv_seqs(block_table.data_ptr(), ld, block_table.shape[1], lens.data_ptr(), _opt_ptr(offsets), B)
+
+
+def _kv_heads(name: str, t: torch.Tensor, dev, T: Optional[int], heads: Optional[int], D: int) -> int:
+    """Checks a bf16 [T][heads*D] or [T][heads][D] tensor (rows may be strided) and returns its row stride."""
+    shape = tuple(t.shape)
+    if t.dim() not in (2, 3) or (t.dim() == 3 and shape[2] != D) or (t.dim() == 2 and shape[1] % D):
+        raise ValueError(f"{name} must have shape (T, heads, {D}) or (T, heads * {D}) (got {shape})")
+    n = shape[1] if t.dim() == 3 else shape[1] // D
+    if (T is not None and shape[0] != T) or (heads is not None and n != heads):
+        raise ValueError(f"{name} must hold {T} tokens of {heads} heads (got shape {shape})")
+    _tensor(name, t, dev, torch.bfloat16, rows=True)
+    if t.dim() == 3 and t.numel() > 0 and n > 1 and t.stride(1) != D:
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.stride(0) if shape[0] > 1 else max(n * D, 8)
+
+
+def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, lens: torch.Tensor,
+                   block_table: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None,
+                   stream=None) -> None:
+    """Quantises a step's keys and values (bf16 [T][n_kv][D] or [T][n_kv*D], rows may be strided) into
+    the cache (cbq_kv_cache_write).
+
+    lens: int32 [B], each sequence's cached tokens, the step's included; block_table: int32
+    [B][pages], or None: sequence b owns pages b*P ... of P = n_pages // B; offsets: int32
+    [B + 1], the step's tokens offsets[b] ... are sequence b's last ones, or None: T / B each."""
+    lib = load_library()
+    _require_gpu(k, v)
+    dev = k.device
+    c = cache._c_checked(dev)
+    T = k.shape[0]
+    ldk = _kv_heads("k", k, dev, T, c.n_kv, c.D)
+    ldv = _kv_heads("v", v, dev, T, c.n_kv, c.D)
+    s = _kv_seqs(cache, dev, lens, block_table, offsets)
+    _on_stream(dev, stream, lambda st: _check(lib.cbq_kv_cache_write(
+        ctypes.byref(c), ctypes.byref(s), k.data_ptr(), ldk, v.data_ptr(), ldv, T, st)))
+
+
+def kv_cache_read(cache: KVCache, lens: torch.Tensor, T: int, block_table: Optional[torch.Tensor] = None,
+                  offsets: Optional[torch.Tensor] = None, k: Optional[torch.Tensor] = None,
+                  v: Optional[torch.Tensor] = None, stream=None):
+    """The cached keys and values of a step's T tokens as bf16 [T][n_kv][D], rotated back: what
+    kv_cache_write of the same arguments stored (cbq_kv_cache_read).  Returns (k, v); rows that
+    belong to no sequence are left as they were (unwritten in tensors made here)."""
+    lib = load_library()
+    _require_gpu(cache.k_codes)
+    dev = cache.k_codes.device
+    c = cache._c_checked(dev)
+    ldk = 0 if k is None else _kv_heads("k", k, dev, T, c.n_kv, c.D)
+    ldv = 0 if v is None else _kv_heads("v", v, dev, T, c.n_kv, c.D)
+    s = _kv_seqs(cache, dev, lens, block_table, offsets)
+
+    def call(st):
+        shape = (T, c.n_kv, c.D)
+        ko = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
+        vo = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
+        _check(lib.cbq_kv_cache_read(ctypes.byref(c), ctypes.byref(s), ko.data_ptr(), ldk or c.n_kv * c.D, vo.data_ptr(),
+                                     ldv or c.n_kv * c.D, T, st))
+        return ko, vo
+
+    return _on_stream(dev, stream, call)
+
+
+def kv_attention_workspace(cache: KVCache, T: int, B: int, n_q: int) -> int:
+    """Bytes of device workspace kv_attention needs (cbq_kv_attention_workspace)."""
+    c = cbq_kv_cache(None, None, None, None, cache.n_pages, cache.n_kv, cache.page, cache.D, cache.rotate)
+    return int(load_library().cbq_kv_attention_workspace(ctypes.byref(c), T, B, n_q))
+
+
+def kv_attention(cache: KVCache, q: torch.Tensor, lens: torch.Tensor, block_table: Optional[torch.Tensor] = None,
+                 offsets: Optional[torch.Tensor] = None, scale: Optional[float] = None, causal: bool = True,
+                 window: int = 0, out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """Attention of a step's queries (bf16 [T][n_q][D] or [T][n_q*D], rows may be strided) over the
+    cache that already holds the step's keys and values (cbq_kv_attention): bf16 of q's shape.
+
+    lens, block_table and offsets as for kv_cache_write.  scale: 1/sqrt(D) unless given;
+    window: 0, or how many positions a token attends, its own the last.  A token that attends
+    nothing gets zeros; rows that belong to no sequence are left as they were.  ws: optional
+    uint8 device workspace of kv_attention_workspace(...) bytes; calls that overlap need one each."""
+    lib = load_library()
+    _require_gpu(q)
+    dev = q.device
+    c = cache._c_checked(dev)
+    T, D = q.shape[0], c.D
+    ldq = _kv_heads("q", q, dev, None, None, D)
+    n_q = q.shape[1] if q.dim() == 3 else q.shape[1] // D
+    ldo = n_q * D if out is None else _kv_heads("out", out, dev, T, n_q, D)
+    s = _kv_seqs(cache, dev, lens, block_table, offsets)
+    _tensor("ws", ws, dev, torch.uint8, contiguous=True)
+    if scale is None:
+        scale = D ** -0.5
+
+    def call(st):
+        o = torch.empty(q.shape, dtype=torch.bfloat16, device=dev) if out is None else out
+        w = ws if ws is not None else torch.empty((int(lib.cbq_kv_attention_workspace(ctypes.byref(c), T, s.B, n_q)),),
+                                                  dtype=torch.uint8, device=dev)
+        _check(lib.cbq_kv_attention(ctypes.byref(c), ctypes.byref(s), q.data_ptr(), ldq, T, n_q, scale,
+                                    int(bool(causal)), window, o.data_ptr(), ldo, w.data_ptr(), w.numel(), st))
         return o
 
     return _on_stream(dev, stream, call)

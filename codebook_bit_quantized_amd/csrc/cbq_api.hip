@@ -78,6 +78,51 @@ int check_norm_sizes(int64_t T, int32_t K, const char* name) {
   return CBQ_OK;
 }
 
+// the argument rules that the calls of the key/value cache share; fills *a.  Places are checked where T > 0.
+int check_kv(const cbq_kv_cache* c, const cbq_kv_seqs* q, int64_t T, cbq::KvArgs* a) {
+  if (!c || !q) return fail(CBQ_EINVAL, "cache and seqs must be non-null");
+  if (T < 0) return fail(CBQ_EINVAL, "T must be >= 0 (got %lld)", (long long)T);
+  if (T > 0x7FFFFFFF) return fail(CBQ_EUNSUPPORTED, "T must be < 2^31");
+  if (c->n_pages < 1) return fail(CBQ_EINVAL, "n_pages must be >= 1 (got %d)", c->n_pages);
+  if (c->n_kv < 1) return fail(CBQ_EINVAL, "n_kv must be >= 1 (got %d)", c->n_kv);
+  if (c->n_kv > 1024) return fail(CBQ_EUNSUPPORTED, "n_kv must be <= 1024 (got %d)", c->n_kv);
+  if (!pow2(c->page) || c->page < 16 || c->page > 1024)
+    return fail(CBQ_EINVAL, "page must be a power of two in [16, 1024] (got %d)", c->page);
+  if (c->D != 64 && c->D != 128) return fail(CBQ_EUNSUPPORTED, "D must be 64 or 128 (got %d)", c->D);
+  if (c->rotate & ~(CBQ_KV_ROTATE_K | CBQ_KV_ROTATE_V)) return fail(CBQ_EINVAL, "unknown rotate flags 0x%x", c->rotate);
+  if (q->B < 0) return fail(CBQ_EINVAL, "B must be >= 0 (got %d)", q->B);
+  if (q->B > 65536) return fail(CBQ_EUNSUPPORTED, "B must be <= 65536 (got %d)", q->B);
+  if (q->max_pages < 1) return fail(CBQ_EINVAL, "max_pages must be >= 1 (got %d)", q->max_pages);
+  if ((int64_t)q->max_pages * c->page > 0x40000000)
+    return fail(CBQ_EUNSUPPORTED, "a sequence holds at most 2^30 positions (max_pages %d)", q->max_pages);
+  if (q->block_table && q->ld_table < q->max_pages)
+    return fail(CBQ_EINVAL, "ld_table must be >= max_pages (got %lld)", (long long)q->ld_table);
+  if (!q->block_table && (int64_t)q->B * q->max_pages > c->n_pages)
+    return fail(CBQ_EINVAL, "without a block table, B * max_pages (%lld) must be at most n_pages (%d)",
+                (long long)q->B * q->max_pages, c->n_pages);
+  if (!q->offsets && (q->B == 0 ? T != 0 : T % q->B != 0))
+    return fail(CBQ_EINVAL, "without offsets, T (%lld) must be a multiple of B (%d)", (long long)T, q->B);
+  if (T == 0 || q->B == 0) return CBQ_OK;
+  if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales || !q->lens)
+    return fail(CBQ_EINVAL, "the cache's tensors and lens must be non-null");
+  if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_scales) || !aligned16(c->v_scales))
+    return fail(CBQ_EINVAL, "the cache's tensors must be 16-byte aligned");
+  a->codes[0] = c->k_codes; a->codes[1] = c->v_codes; a->scales[0] = c->k_scales; a->scales[1] = c->v_scales;
+  a->n_pages = c->n_pages; a->n_kv = c->n_kv; a->logp = __builtin_ctz(c->page); a->D = c->D; a->rotate = c->rotate;
+  a->table = q->block_table; a->ld_table = q->ld_table; a->max_pages = q->max_pages; a->lens = q->lens;
+  a->offsets = q->offsets; a->B = q->B; a->per_seq = q->offsets ? 0 : (int)(T / q->B); a->T = T;
+  return CBQ_OK;
+}
+
+// a [T][ld] bf16 tensor of n heads: alignment and stride (p null: not given)
+int check_heads(const char* name, const uint16_t* p, int64_t ld, int64_t n, int32_t D) {
+  if (ld < n * D || ld % 8)
+    return fail(CBQ_EINVAL, "%s: its row stride must be >= %lld and a multiple of 8 (got %lld)", name, (long long)(n * D), (long long)ld);
+  if (ld > (int64_t(1) << 31)) return fail(CBQ_EUNSUPPORTED, "%s: its row stride must be <= 2^31", name);
+  if (!aligned16(p)) return fail(CBQ_EINVAL, "%s must be 16-byte aligned", name);
+  return CBQ_OK;
+}
+
 }  // namespace
 
 CBQ_EXPORT const char* cbq_status_string(int status) {
@@ -556,6 +601,71 @@ CBQ_EXPORT int cbq_codebook_adapter_gemm(const uint8_t* codes, const float* scal
   hipError_t e = cbq::launch_adapter_gemm(a, ad, x, ldx, lora_a, adapter_scale, static_cast<float*>(ws),
                                           (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "codebook_adapter_gemm launch");
+  return CBQ_OK;
+}
+
+CBQ_EXPORT int cbq_kv_cache_write(const cbq_kv_cache* cache, const cbq_kv_seqs* seqs, const uint16_t* k,
+                                  int64_t ldk, const uint16_t* v, int64_t ldv, int64_t T, void* stream) {
+  g_err[0] = 0;
+  cbq::KvArgs a{};
+  if (int rc = check_kv(cache, seqs, T, &a)) return rc;
+  if (int rc = check_heads("k", k, ldk, cache->n_kv, cache->D)) return rc;
+  if (int rc = check_heads("v", v, ldv, cache->n_kv, cache->D)) return rc;
+  if (T == 0 || seqs->B == 0) return CBQ_OK;
+  if (!k || !v) return fail(CBQ_EINVAL, "k and v must be non-null");
+  hipError_t e = cbq::launch_kv_write(a, k, ldk, v, ldv, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "kv_cache_write launch");
+  return CBQ_OK;
+}
+
+CBQ_EXPORT int cbq_kv_cache_read(const cbq_kv_cache* cache, const cbq_kv_seqs* seqs, uint16_t* k, int64_t ldk,
+                                 uint16_t* v, int64_t ldv, int64_t T, void* stream) {
+  g_err[0] = 0;
+  cbq::KvArgs a{};
+  if (int rc = check_kv(cache, seqs, T, &a)) return rc;
+  if (k)
+    if (int rc = check_heads("k", k, ldk, cache->n_kv, cache->D)) return rc;
+  if (v)
+    if (int rc = check_heads("v", v, ldv, cache->n_kv, cache->D)) return rc;
+  if (T == 0 || seqs->B == 0) return CBQ_OK;
+  if (!k && !v) return fail(CBQ_EINVAL, "k or v must be non-null");
+  hipError_t e = cbq::launch_kv_read(a, k, ldk, v, ldv, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "kv_cache_read launch");
+  return CBQ_OK;
+}
+
+CBQ_EXPORT size_t cbq_kv_attention_workspace(const cbq_kv_cache* cache, int64_t T, int32_t B, int32_t n_q) {
+  if (!cache || T <= 0 || T > 0x7FFFFFFF || B < 1 || B > 65536 || cache->n_kv < 1 || n_q < cache->n_kv || n_q > 1024 ||
+      n_q % cache->n_kv || (cache->D != 64 && cache->D != 128))
+    return 0;
+  return cbq::kv_attention_workspace_bytes(T, B, n_q, cache->n_kv, cache->D);
+}
+
+CBQ_EXPORT int cbq_kv_attention(const cbq_kv_cache* cache, const cbq_kv_seqs* seqs, const uint16_t* q, int64_t ldq,
+                                int64_t T, int32_t n_q, float scale, int32_t causal, int32_t window, uint16_t* out,
+                                int64_t ldo, void* ws, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  cbq::KvAttnArgs g{};
+  if (int rc = check_kv(cache, seqs, T, &g.kv)) return rc;
+  if (n_q < 1 || n_q % cache->n_kv)
+    return fail(CBQ_EINVAL, "n_q must be a positive multiple of n_kv = %d (got %d)", cache->n_kv, n_q);
+  if (n_q > 1024) return fail(CBQ_EUNSUPPORTED, "n_q must be <= 1024 (got %d)", n_q);
+  if (!std::isfinite(scale)) return fail(CBQ_EINVAL, "scale must be finite");
+  if (causal != 0 && causal != 1) return fail(CBQ_EINVAL, "causal must be 0 or 1");
+  if (window < 0) return fail(CBQ_EINVAL, "window must be >= 0 (got %d)", window);
+  if (window > 0 && !causal) return fail(CBQ_EINVAL, "a window needs causal = 1");
+  if (int rc = check_heads("q", q, ldq, n_q, cache->D)) return rc;
+  if (int rc = check_heads("out", out, ldo, n_q, cache->D)) return rc;
+  if (T == 0 || seqs->B == 0) return CBQ_OK;
+  if (!q || !out) return fail(CBQ_EINVAL, "q and out must be non-null");
+  const size_t need = cbq::kv_attention_workspace_bytes(T, seqs->B, n_q, cache->n_kv, cache->D);
+  if (!ws || ws_bytes < need)
+    return fail(CBQ_EWORKSPACE, "workspace of %zu bytes required (got %zu)", need, ws ? ws_bytes : (size_t)0);
+  if (!aligned16(ws)) return fail(CBQ_EINVAL, "ws must be 16-byte aligned");
+  g.q = q; g.ldq = ldq; g.n_q = n_q; g.scale = scale; g.causal = causal; g.window = window; g.out = out; g.ldo = ldo;
+  g.ws = ws;
+  hipError_t e = cbq::launch_kv_attention(g, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "kv_attention launch");
   return CBQ_OK;
 }
 

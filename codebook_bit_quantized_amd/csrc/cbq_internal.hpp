@@ -133,6 +133,37 @@ hipError_t launch_adapter_gemm(const GemmArgs& a, AdapterArgs ad, const uint16_t
 // The MFMA path with the adapters in its epilogue: one weight set, dense rows.
 hipError_t launch_mfma_prefill_adapter(const GemmArgs& a, const AdapterArgs& ad, hipStream_t stream);
 
+// The 4-bit key/value cache and the sequences of a step (kv_cache.hip, kv_attention.hip).
+struct KvArgs {
+  uint8_t* codes[2];          // keys, values
+  float* scales[2];
+  int n_pages, n_kv, logp, D; // logp: log2 of the page's tokens
+  int rotate;                 // bit 0 keys, bit 1 values
+  const int32_t* table;       // or null: sequence b's pages are b*max_pages ...
+  int64_t ld_table;
+  int max_pages;
+  const int32_t* lens;
+  const int32_t* offsets;     // or null: per_seq tokens each
+  int B, per_seq;
+  int64_t T;
+};
+hipError_t launch_kv_write(const KvArgs& a, const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                           hipStream_t stream);
+hipError_t launch_kv_read(const KvArgs& a, uint16_t* k, int64_t ldk, uint16_t* v, int64_t ldv, hipStream_t stream);
+struct KvAttnArgs {
+  KvArgs kv;
+  const uint16_t* q;
+  int64_t ldq;
+  int n_q;
+  float scale;
+  int causal, window;
+  uint16_t* out;
+  int64_t ldo;
+  void* ws;
+};
+size_t kv_attention_workspace_bytes(int64_t T, int B, int n_q, int n_kv, int D);
+hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t stream);
+
 // Compute units of the current device (cached per device after the first query).
 hipError_t device_cu_count(int* out);
 

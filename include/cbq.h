@@ -489,6 +489,114 @@ int cbq_codebook_adapter_gemm(const uint8_t* codes, const float* scales, int32_t
                               size_t ws_bytes, void* stream);
 
 /*
+ * The 4-bit key/value cache.  A head's D channels of one token are held as D E2M1 codes
+ * (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives: the 16 values of a fixed codebook that
+ * gfx950 converts in one instruction) and one fp32 scale, after the rotation of
+ * cbq_rotate_quantize over the head's channels, which spreads the keys' outlier channels.
+ * Passage: CodeQuant2, Figure 1 and Table 5 caption (a fixed rotation smooths outliers before
+ * a low-bit quantiser); the cache is this library's own use of it.
+ *
+ *  k_codes, v_codes   : [n_pages][n_kv][page][D/2] bytes, 16-byte aligned; channel 2j in the
+ *                       low nibble of byte j.  Nibble: sign (bit 3), then the value's index above.
+ *  k_scales, v_scales : fp32 [n_pages][n_kv][page].
+ *  n_pages >= 1; 1 <= n_kv <= 1024 key/value heads; page: tokens a page holds, a power of two, 16 to 1024.
+ *  D        : 64 or 128.
+ *  rotate   : CBQ_KV_ROTATE_K | CBQ_KV_ROTATE_V, or fewer: which of the two are rotated (a
+ *             Sylvester Hadamard transform over the D channels, orthonormal with the scale).
+ *             The calls that read a cache name the same flags as the one that wrote it.
+ */
+enum {
+  CBQ_KV_ROTATE_K = 1,
+  CBQ_KV_ROTATE_V = 2
+};
+typedef struct {
+  uint8_t *k_codes, *v_codes;
+  float *k_scales, *v_scales;
+  int32_t n_pages, n_kv, page, D, rotate;
+} cbq_kv_cache;
+
+/*
+ * The sequences of a step: which pages hold them and which of the step's tokens are theirs.
+ *
+ *  block_table : int32 [B][ld_table]: page of positions page*j .. page*j + page - 1 of sequence
+ *                b at [b][j], j < max_pages; or NULL: sequence b owns pages b*max_pages ...
+ *                (b+1)*max_pages - 1.  An entry outside [0, n_pages) (say -1, a page that was
+ *                given back) holds nothing: its positions are not attended, not written, and
+ *                read as zeros.
+ *  lens        : int32 [B]: cached tokens of each sequence, the step's own included.  Positions
+ *                at max_pages*page and beyond are as in no page.
+ *  offsets     : int32 [B + 1], ascending: the step's tokens offsets[b] ... offsets[b+1] - 1 are
+ *                sequence b's last ones, the i-th at position lens[b] - (offsets[b+1] -
+ *                offsets[b]) + i (a negative position is as in no page).  Tokens before offsets[0] and
+ *                from offsets[B] on belong to no sequence: outputs leave their rows as they
+ *                were.  NULL: each sequence has T / B tokens (T a multiple of B).
+ *  0 <= B <= 65536, max_pages * page <= 2^30.  All three are device memory, so a captured graph
+ *  replays with the lengths and pages of the day.
+ */
+typedef struct {
+  const int32_t* block_table;
+  int64_t ld_table;
+  int32_t max_pages;
+  const int32_t* lens;
+  const int32_t* offsets;
+  int32_t B;
+} cbq_kv_seqs;
+
+/*
+ * cbq_kv_cache_write - quantise a step's keys and values into the cache.
+ *
+ *  k, v : bf16 [T][ldk], [T][ldv]: token t's n_kv heads of D channels in a row (ld >= n_kv*D,
+ *         a multiple of 8, 16-byte aligned: slices of a fused projection's output do).
+ *  Per head: u = H x exactly (or x), v = fp32(u), M = max|v|, s = M / 6, r = v / s (fp32); each
+ *  code is the E2M1 value nearest to r, ties to the even index, at most 6, with v's sign bit; scale =
+ *  s * fp32(1/sqrt(D)) (or s).  M / 6 == 0: codes 0 and scale 0.  A row that is not finite gets
+ *  a scale that is not finite.  Exact for exponents that spread at most 45 - log2(D) binades.
+ *  No other place of the cache is written.  Two tokens of a call that name the same place (a page
+ *  that stands twice in the table) leave it unspecified.
+ *  T < 2^31.
+ */
+int cbq_kv_cache_write(const cbq_kv_cache* cache, const cbq_kv_seqs* seqs, const uint16_t* k,
+                       int64_t ldk, const uint16_t* v, int64_t ldv, int64_t T, void* stream);
+
+/*
+ * cbq_kv_cache_read - the cached keys and values of a step's tokens as bf16, rotated back:
+ * what cbq_kv_cache_write of the same arguments stored.  Whole sequences: as many tokens of
+ * each as lens says.
+ *
+ *  k, v : bf16 [T][ldk], [T][ldv] as above; either may be NULL.
+ *         x = bf16(scale * fp32(1/sqrt(D)) * (H c)), c the codes' values (H c is exact).
+ */
+int cbq_kv_cache_read(const cbq_kv_cache* cache, const cbq_kv_seqs* seqs, uint16_t* k, int64_t ldk,
+                      uint16_t* v, int64_t ldv, int64_t T, void* stream);
+
+/*
+ * cbq_kv_attention - attention of a step's queries over the cache: one token a sequence
+ * (decode), a few (drafted tokens), a prompt or its chunk (prefill), mixed as they come.  The
+ * step's own keys and values are in the cache already (cbq_kv_cache_write).
+ *
+ *  q      : bf16 [T][ldq]: token t's n_q heads of D channels (ldq >= n_q*D, % 8, 16-byte aligned).
+ *  n_q    : query heads, a multiple of n_kv; query head h reads key/value head h / (n_q / n_kv).
+ *  scale  : finite; a_j = scale * <q, k_j> over the dequantised keys.
+ *  causal : 1: a token attends positions up to its own; 0: all lens[b].
+ *  window : 0, or (causal only) how many positions a token attends, its own the last of them.
+ *  out    : bf16 [T][ldo] (as q): sum_j softmax(a)_j v_j, rounded once.  A token that attends
+ *           nothing gets zeros.
+ *  The rotated queries and the weights softmax(a)_j * scale_j enter the matrix cores as fp16
+ *  relative to their own largest value; scores, softmax statistics and sums are fp32.  A
+ *  value scale below 2^-64 counts as 2^-64 in the weights.  What a token does not attend (other pages,
+ *  masked positions, rows of other sequences) reaches its result in no way, whatever it holds.
+ *  Deterministic: no result depends on the order of atomics.
+ *  ws, ws_bytes : device workspace of cbq_kv_attention_workspace(...) bytes, 16-byte aligned;
+ *           rewritten by every call; calls that overlap in time need one each.
+ *  out overlaps no input, nor ws.  T < 2^31, n_q <= 1024.
+ */
+size_t cbq_kv_attention_workspace(const cbq_kv_cache* cache, int64_t T, int32_t B, int32_t n_q);
+int cbq_kv_attention(const cbq_kv_cache* cache, const cbq_kv_seqs* seqs, const uint16_t* q,
+                     int64_t ldq, int64_t T, int32_t n_q, float scale, int32_t causal,
+                     int32_t window, uint16_t* out, int64_t ldo, void* ws, size_t ws_bytes,
+                     void* stream);
+
+/*
  * cbq_kmeans_codebooks - offline codebook construction, one 1-D K-means per weight row.
  * Passage: CodeQuant2, Figure 3 (right: K-means initialises the centroid matrix and the
  * per-row assignment matrices); CodeQuant abstract (weight outliers absorbed into

@@ -7,8 +7,8 @@ shares no code, table or helper with that path.
 
 It is a plain, slow, obviously-correct restatement of what the method computes,
 in fp64 unless a step fixes another precision.  See ``reference.py`` for every
-function and the passage of the CodeQuant / CodeQuant2 pages it follows, and ``serving.py``
-for the calls around a block.
+function and the passage of the CodeQuant / CodeQuant2 pages it follows, ``serving.py``
+for the calls around a block, and ``cache.py`` for the 4-bit key/value cache and its attention.
 
 Pins (what ties each function to something other than itself) live in
 ``tests/test_oracle_*.py``; every function here is pinned.  The only quantity the
@@ -21,5 +21,7 @@ from .reference import *  # noqa: F401,F403
 from .reference import __all__ as _reference_all
 from .serving import *  # noqa: F401,F403
 from .serving import __all__ as _serving_all
+from .cache import *  # noqa: F401,F403
+from .cache import __all__ as _cache_all
 
-__all__ = list(_reference_all) + list(_serving_all)
+__all__ = list(_reference_all) + list(_serving_all) + list(_cache_all)

@@ -1,0 +1,209 @@
+"""GPU parity of cbq_kv_cache_write and cbq_kv_cache_read: codes and scales bit for bit, every place
+that no token names left as it was, values read back within half a bf16 step."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+cbq = pytest.importorskip("codebook_bit_quantized_amd")
+from kv_steps import DEV, Step, bf16_values  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    cbq.load_library()
+
+
+def _host(cache):
+    return [t.cpu().numpy() for t in (cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales)]
+
+
+def _check_write(st, x64, before, rotate):
+    """The cache after a write of x64 = (k, v) [T][n_kv][D] against the oracle."""
+    after = _host(st.cache)
+    place = st.places()
+    at = np.flatnonzero(place[:, 2] >= 0)
+    for i in range(2):
+        q, s = oracle.kv_quantise(x64[i], bool(rotate >> i & 1))
+        codes, scales = before[i].copy(), before[2 + i].copy()
+        codes[place[at, 2], :, place[at, 3]] = oracle.kv_pack(q)[at]
+        scales[place[at, 2], :, place[at, 3]] = s[at]
+        assert np.array_equal(after[i], codes)
+        assert np.array_equal(after[2 + i].view(np.uint32), scales.view(np.uint32))
+    return at, place
+
+
+def _check_read(st, got, kept):
+    """What was read against the cache's own codes: x = scale / sqrt(D) * H c, its two fp32 roundings
+    (2^-24 each) and 1 / sqrt(D) in fp32 (2^-24), then half a bf16 step (2^-8)."""
+    place = st.places()
+    for i in range(2):
+        g = got[i].double().cpu().numpy().reshape(st.T, st.n_kv, st.D)
+        for t in range(st.T):
+            b, _, p, j = place[t]
+            if b < 0:
+                assert np.all(g[t] == kept), "a row of no sequence was written"
+                continue
+            if p < 0:
+                assert not g[t].any()
+                continue
+            codes, scales = _host(st.cache)[i][p, :, j], _host(st.cache)[2 + i][p, :, j]
+            x = oracle.kv_dequantise(oracle.kv_unpack(codes), scales, bool(st.rotate >> i & 1))
+            assert np.all(np.abs(g[t] - x) <= (2.0 ** -8 + 2.0 ** -22) * np.abs(x) + 1e-40)
+
+
+CASES = [  # lens, new, n_kv, D, page, rotate, front, back
+    ([1], [1], 1, 128, 16, 3, 0, 0),
+    ([5, 17, 33], [5, 1, 2], 2, 64, 16, 3, 0, 0),
+    ([40, 0, 16, 100], [3, 0, 16, 7], 4, 128, 32, 3, 2, 3),
+    ([64, 65], [64, 65], 5, 128, 64, 0, 0, 1),
+    ([300, 20], [30, 20], 3, 64, 128, 1, 1, 0),
+    ([70], [70], 1, 128, 1024, 2, 0, 0),
+]
+
+
+@pytest.mark.parametrize("lens,new,n_kv,D,page,rotate,front,back", CASES)
+def test_write_and_read(lens, new, n_kv, D, page, rotate, front, back):
+    st = Step(sum(lens), lens, new, n_kv, D, page, rotate, front=front, back=back).device()
+    (k, k64), (v, v64) = bf16_values(st.rng, (st.T, n_kv, D), 2), bf16_values(st.rng, (st.T, n_kv, D), 0.1)
+    before = _host(st.cache)
+    cbq.kv_cache_write(st.cache, k.to(DEV), v.to(DEV), st.d_lens, **st.at)
+    _check_write(st, (k64, v64), before, rotate)
+    out = [torch.full((st.T, n_kv, D), 55.0, dtype=torch.bfloat16, device=DEV) for _ in "kv"]
+    got = cbq.kv_cache_read(st.cache, st.d_lens, st.T, k=out[0], v=out[1], **st.at)
+    assert got[0] is out[0] and got[1] is out[1]
+    _check_read(st, got, 55.0)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_slices_of_a_fused_projection_and_no_table(D):
+    n_kv, B, n = 3, 4, 5
+    st = Step(7, [20, 5, 64, 33], [n] * B, n_kv, D, 16, table=False, max_pages=4).device()
+    w = n_kv * D
+    qkv, x = bf16_values(st.rng, (st.T, 8 + 3 * w + 8))
+    qkv = qkv.to(DEV)
+    before = _host(st.cache)
+    cbq.kv_cache_write(st.cache, qkv[:, 8 + w:8 + 2 * w], qkv[:, 8 + 2 * w:8 + 3 * w].view(st.T, n_kv, D), st.d_lens)
+    _check_write(st, [x[:, 8 + i * w:8 + (i + 1) * w].reshape(-1, n_kv, D) for i in (1, 2)], before, 3)
+    wide = torch.full((st.T, 8 + 3 * w + 8), 9.0, dtype=torch.bfloat16, device=DEV)
+    cbq.kv_cache_read(st.cache, st.d_lens, st.T, k=wide[:, 8:8 + w], v=wide[:, 16 + w:16 + 2 * w])
+    _check_read(st, (wide[:, 8:8 + w], wide[:, 16 + w:16 + 2 * w]), 9.0)
+    assert bool((wide[:, :8] == 9).all()) and bool((wide[:, 8 + w:16 + w] == 9).all()) and bool((wide[:, 16 + 2 * w:] == 9).all())
+
+
+def test_one_of_keys_and_values_read_through_the_c_call():
+    import ctypes
+    st = Step(8, [20, 37], [20, 37], 2, 64, 16).device()
+    both = cbq.kv_cache_read(st.cache, st.d_lens, st.T, **st.at)
+    lib = cbq.load_library()
+    c = st.cache._c_checked(st.d_lens.device)
+    s = cbq._binding._kv_seqs(st.cache, st.d_lens.device, st.d_lens, st.at["block_table"], st.d_offsets)
+    one = torch.zeros_like(both[0])
+    for i in range(2):
+        ptr = [None, None]
+        ptr[i] = one.data_ptr()
+        assert lib.cbq_kv_cache_read(ctypes.byref(c), ctypes.byref(s), ptr[0], 128, ptr[1], 128, st.T,
+                                     torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(one, both[i])
+
+
+def test_pages_that_hold_nothing_and_positions_outside():
+    """Entries outside [0, n_pages), negative positions, positions past the table: not written, read as zeros."""
+    st = Step(9, [50, 3, 200, -4], [50, 5, 10, 2], 2, 64, 16, max_pages=6)
+    st.table[0, 1], st.table[0, 2] = -1, st.n_pages
+    st.device()
+    (k, k64), (v, v64) = bf16_values(st.rng, (st.T, 2, 64)), bf16_values(st.rng, (st.T, 2, 64))
+    before = _host(st.cache)
+    cbq.kv_cache_write(st.cache, k.to(DEV), v.to(DEV), st.d_lens, **st.at)
+    at, place = _check_write(st, (k64, v64), before, 3)
+    assert 0 < len(at) < st.T
+    _check_read(st, cbq.kv_cache_read(st.cache, st.d_lens, st.T, **st.at), None)
+
+
+def test_extreme_rows():
+    """Zeros, negative zeros, subnormal and large values, values on the codes' borders, one value alone; rows that are not
+    finite get a scale that is not finite and leave their neighbours alone."""
+    D, n_kv = 128, 2
+    rows = np.zeros((12, n_kv, D))
+    rng = np.random.default_rng(3)
+    rows[1, 0, 5] = 1
+    rows[2] = -0.0
+    rows[3] = rng.normal(size=(n_kv, D)) * 2.0 ** -130
+    rows[4] = rng.normal(size=(n_kv, D)) * 1e36
+    rows[5, 0] = np.tile([6, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5], D // 8)      # ties once not rotated
+    rows[5, 1] = -rows[5, 0]
+    rows[6] = 2.0 ** -133
+    rows[7, 0, :] = 3.0
+    rows[8:] = rng.normal(size=(4, n_kv, D))
+    for rotate in (0, 3):
+        st = Step(4, [12], [12], n_kv, D, 16, rotate, garbage=False).device()
+        x = torch.from_numpy(rows.astype(np.float32)).to(torch.bfloat16)
+        before = _host(st.cache)
+        cbq.kv_cache_write(st.cache, x.to(DEV), x.flip(0).to(DEV), st.d_lens, **st.at)
+        _check_write(st, (x.double().numpy(), x.flip(0).double().numpy()), before, rotate)
+        y = x.clone()
+        y[8, 0, 3], y[9, 1, 7] = float("nan"), float("inf")
+        cbq.kv_cache_write(st.cache, y.to(DEV), x.flip(0).to(DEV), st.d_lens, **st.at)
+        q, s = oracle.kv_quantise(x.double().numpy(), bool(rotate & 1))
+        place = st.places()
+        got_c, got_s = _host(st.cache)[0][place[:, 2], :, place[:, 3]], _host(st.cache)[2][place[:, 2], :, place[:, 3]]
+        bad = np.zeros((12, n_kv), dtype=bool)
+        bad[8, 0] = bad[9, 1] = True
+        assert not np.isfinite(got_s[bad]).any()
+        assert np.array_equal(got_s[~bad], s[~bad]) and np.array_equal(got_c[~bad], oracle.kv_pack(q)[~bad])
+
+
+def test_codes_are_those_of_the_same_token_in_any_batch():
+    n_kv, D = 4, 128
+    st = Step(11, [500], [500], n_kv, D, 64).device()
+    x = torch.randn((500, n_kv, D), device=DEV).to(torch.bfloat16)
+    cbq.kv_cache_write(st.cache, x, x, st.d_lens, **st.at)
+    whole = _host(st.cache)
+    cache = cbq.KVCache.empty(st.n_pages, n_kv, 64, D)
+    for n in (1, 2, 130, 499, 500):                      # token n - 1 alone, as a decode step writes it
+        cbq.kv_cache_write(cache, x[n - 1:n], x[n - 1:n], torch.tensor([n], dtype=torch.int32, device=DEV),
+                           st.at["block_table"])
+        p, j = st.table[0, (n - 1) // 64], (n - 1) % 64
+        for a, b in zip(_host(cache), whole):
+            assert np.array_equal(a[p, :, j], b[p, :, j])
+
+
+def test_offsets_beyond_32_bits():
+    """A cache of more than 2^32 bytes of codes: its last pages."""
+    n_kv, D, page = 8, 128, 1024
+    n_pages = (1 << 32) // (n_kv * page * D // 2) + 3
+    cache = cbq.KVCache.empty(n_pages, n_kv, page, D)
+    assert cache.k_codes.numel() > 1 << 32
+    x = torch.randn((20, n_kv, D), device=DEV).to(torch.bfloat16)
+    lens = torch.tensor([1030], dtype=torch.int32, device=DEV)
+    table = torch.tensor([[n_pages - 1, n_pages - 2]], dtype=torch.int32, device=DEV)
+    small = cbq.KVCache.empty(2, n_kv, page, D)
+    low = torch.tensor([[0, 1]], dtype=torch.int32, device=DEV)
+    cbq.kv_cache_write(cache, x, -x, lens, table)
+    cbq.kv_cache_write(small, x, -x, lens, low)
+    for i, p in ((0, n_pages - 1), (1, n_pages - 2)):
+        assert torch.equal(cache.k_codes[p], small.k_codes[i]) and torch.equal(cache.v_codes[p], small.v_codes[i])
+        assert torch.equal(cache.k_scales[p], small.k_scales[i]) and torch.equal(cache.v_scales[p], small.v_scales[i])
+    assert bool((small.k_scales != 0).any()) and not bool((cache.k_scales[:n_pages - 2] != 0).any())
+    a, b = cbq.kv_cache_read(cache, lens, 20, table), cbq.kv_cache_read(small, lens, 20, low)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    q = torch.randn((20, 2 * n_kv, D), device=DEV).to(torch.bfloat16)
+    o = cbq.kv_attention(cache, q, lens, table, window=15)
+    assert torch.equal(o, cbq.kv_attention(small, q, lens, low, window=15)) and bool((o != 0).any())
+
+
+def test_no_tokens():
+    cache = cbq.KVCache.empty(2, 2, 16, 64)
+    x = torch.empty((0, 2, 64), dtype=torch.bfloat16, device=DEV)
+    z = torch.empty((0,), dtype=torch.int32, device=DEV)
+    cbq.kv_cache_write(cache, x, x, z)
+    cbq.kv_cache_write(cache, x, x, torch.tensor([5], dtype=torch.int32, device=DEV))
+    k, v = cbq.kv_cache_read(cache, z, 0)
+    assert k.shape == (0, 2, 64) and not cache.k_codes.any()
+    assert cbq.kv_attention(cache, x, z).shape == (0, 2, 64)
