@@ -1,108 +1,605 @@
 // Attention of a step's queries over the 4-bit key/value cache.
 //
-// One workgroup a query row and head, one pass over its keys in blocks of 256 with the running
-// maximum and sum of the softmax: thread i holds key i's score, then channel i's sum.
+// The mathematics.  With a_j = scale <q, k_j> the result is sum_j exp(a_j) v_j / sum_j exp(a_j), in one
+// pass over the keys with a running maximum.  A key is its scale ks_j times E2M1 codes, so
+// a_j = ks_j <q', codes_j> with the rotated query q' in fp16 (its row divided by a power of two); codes are
+// exact in fp16 and the products' sums are fp32.  A value's scale vs_j joins the weight:
+//     b_j = a_j log2 e + log2 vs_j,   w_j = 2^(b_j - M),   M the running maximum of b,
+//     result = sum_j w_j codes_j / sum_j (w_j / vs_j),
+// so w_j in fp16 is always relative to its row's largest contribution, whatever the scales' range.
+//
+// The tiles.  A wave takes 64 keys at a time.  Scores are computed transposed, keys times queries
+// (16x16x32 MFMA: 16 keys, 16 query rows), so that lane (row r = lane % 16, g = lane / 16) ends
+// with the scores of row r and keys 4g .. 4g+3 of each 16: statistics are per lane and two
+// swaps, and the weights are, where they lie, the second operand of values (channels) times weights. That
+// product wants 8 keys of one channel in a lane: the values go to LDS as they are, and
+// ds_read_b64_tr_b4 hands each lane 16 keys' codes of its channel.  Codes become fp16 by
+// v_cvt_scalef32_pk_f16_fp4, two at a time.
 #include "kv_device.hpp"
 
 namespace cbq {
 namespace {
 
-template <int D>
-__device__ __forceinline__ void head_transform_lds(float* x, int tid) {
-  for (int h = 1; h < D; h *= 2) {
-    __syncthreads();
-    float r = 0;
-    if (tid < D) r = (tid & h) ? x[tid ^ h] - x[tid] : x[tid] + x[tid ^ h];
-    __syncthreads();
-    if (tid < D) x[tid] = r;
+constexpr int kTile = 64;          // keys a wave takes at a time
+constexpr int kMaxGroups = 512;    // workgroups of a split call: two a CU
+
+// A sequence's part of the step, all values uniform over the workgroup.
+struct Seq {
+  int64_t t0;                      // its first token
+  int rows;                        // tokens * G
+  int64_t pos0;                    // position of the first token
+  int len;                         // positions that can hold anything
+};
+
+__device__ __forceinline__ Seq kv_seq(const KvArgs& a, int b, int G) {
+  int64_t o0, o1;
+  if (a.offsets) { o0 = a.offsets[b]; o1 = a.offsets[b + 1]; }
+  else { o0 = (int64_t)b * a.per_seq; o1 = o0 + a.per_seq; }
+  const int64_t s = o0 < 0 ? 0 : o0, e = o1 < a.T ? o1 : a.T;
+  const int64_t len = a.lens[b], cap = (int64_t)a.max_pages << a.logp;
+  Seq q;
+  q.t0 = s;
+  const int64_t r = e > s ? (e - s) * G : 0;
+  q.rows = (int)(r < 0x7FFF0000 ? r : 0x7FFF0000);
+  q.pos0 = len - o1 + s;
+  q.len = (int)(len < 0 ? 0 : len < cap ? len : cap);
+  return q;
+}
+
+struct Range { int lo, hi; };      // [lo, hi)
+
+// Positions that token i of the sequence attends.
+__device__ __forceinline__ Range kv_range(const Seq& q, int i, int causal, int window) {
+  const int64_t pos = q.pos0 + i;
+  Range r{0, q.len};
+  if (causal) {
+    r.hi = (int)(pos + 1 < 0 ? 0 : pos + 1 < q.len ? pos + 1 : q.len);
+    if (window && pos - window + 1 > 0) r.lo = (int)(pos - window + 1 < 0x3FFFFFFF ? pos - window + 1 : 0x3FFFFFFF);
   }
-  __syncthreads();
+  return r;
 }
 
-__device__ __forceinline__ float e2m1_value(uint32_t n) {
-  const float m = (n & 6) ? (1.0f + 0.5f * (n & 1)) * (float)(1 << (((n >> 1) & 3) - 1)) : 0.5f * (n & 1);
-  return (n & 8) ? -m : m;
+// Key tiles [lo, hi) of query rows r0 .. r1 (at least one tile: a row that attends nothing is written too).
+__device__ __forceinline__ Range kv_tiles(const Seq& q, int r0, int r1, int G, int causal, int window) {
+  const int lo = kv_range(q, r0 / G, causal, window).lo / kTile;
+  const int hi = (kv_range(q, r1 / G, causal, window).hi + kTile - 1) / kTile;
+  return Range{lo, hi > lo ? hi : lo + 1};
+}
+
+// What the workgroups of a split call leave for the join: a row block that starts in group w and goes on in the next `more`.
+struct Desc { int b, kvh, r0, more; };
+
+struct SplitArgs {
+  int groups;                      // workgroups
+  int split;                       // 1: units are key tiles; 0: whole row blocks
+  int min_units;                   // units a workgroup takes at least
+  float c_q, c_v;                  // 1/sqrt(D) where queries are rotated / values rotated back, else 1
+  Desc* desc;                      // [groups]
+  float2* ml;                      // [2 * groups][ROWS]: M and sum of each part's rows
+  float* o;                        // [2 * groups][ROWS][D]
+};
+
+template <int D, int NB, int WV>
+struct Lds {
+  static constexpr int ROWS = 16 * NB, P = D + 4;    // padded row: 16 rows start in 16 different bank groups
+  union {
+    struct {
+      uint8_t v[WV][kTile * D / 2];                  // values' codes, 16-byte (8-byte) quarters of a row swizzled
+      float ks[WV][kTile], lv[WV][kTile], iv[WV][kTile];
+    } t;
+    float o[WV][ROWS * P];
+  };
+  float m[WV][ROWS], l[WV][ROWS];
+  int64_t scan[WV];
+  int64_t start_off;
+  int start_b;
+};
+
+// x of the lanes 16 (32) apart: a of the even row (lower half), b of the odd row (upper half), in
+// both lanes.  The swap's second operand is hidden from the compiler, which takes the two
+// results of a swap of equal operands for one.
+template <bool SWAP32>
+__device__ __forceinline__ void swap_pair(float x, float& a, float& b) {
+  uint32_t u = __builtin_bit_cast(uint32_t, x), v = u;
+  asm("" : "+v"(v));
+  u32x2 r;
+  if constexpr (SWAP32) { const auto t = __builtin_amdgcn_permlane32_swap(u, v, false, false); r = u32x2{t[0], t[1]}; }
+  else { const auto t = __builtin_amdgcn_permlane16_swap(u, v, false, false); r = u32x2{t[0], t[1]}; }
+  a = __builtin_bit_cast(float, (uint32_t)r[0]);
+  b = __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+
+// over the four lanes that hold a row
+__device__ __forceinline__ float row_max(float x) {
+  float a, b;
+  swap_pair<false>(x, a, b);
+  swap_pair<true>(fmaxf(a, b), a, b);
+  return fmaxf(a, b);
+}
+__device__ __forceinline__ uint32_t row_max_u32(uint32_t x) {
+  float a, b;
+  swap_pair<false>(__builtin_bit_cast(float, x), a, b);
+  x = max(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+  swap_pair<true>(__builtin_bit_cast(float, x), a, b);
+  return max(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+}
+__device__ __forceinline__ float row_add(float x) {
+  float a, b;
+  swap_pair<false>(x, a, b);
+  swap_pair<true>(a + b, a, b);
+  return a + b;
+}
+
+// 16 query rows as the MFMA's second operand: lane (row, g) holds channels g*D/4 ... of its row.
+// Rotated if asked, divided by a power of two near its largest value; *rs gets that power.
+template <int D>
+__device__ __forceinline__ void load_queries(const uint16_t* q, bool rotate, f16x8* out, float* rs) {
+  constexpr int C = D / 4;
+  float x[C];
+#pragma unroll
+  for (int i = 0; i < C / 8; ++i) {
+    u32x4 v = {0, 0, 0, 0};
+    if (q) v = *reinterpret_cast<const u32x4*>(q + 8 * i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[8 * i + 2 * j] = __builtin_bit_cast(float, v[j] << 16);
+      x[8 * i + 2 * j + 1] = __builtin_bit_cast(float, v[j] & 0xFFFF0000u);
+    }
+  }
+  if (rotate) {
+#pragma unroll
+    for (int h = 1; h < C; h *= 2)
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        if (!(i & h)) {
+          const float s = x[i] + x[i + h], d = x[i] - x[i + h];
+          x[i] = s;
+          x[i + h] = d;
+        }
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {                    // channels C apart: lanes 16 apart; 2C: 32 apart
+      float a, b;
+      swap_pair<false>(x[i], a, b);
+      swap_pair<true>((lane & 16) ? a - b : a + b, a, b);
+      x[i] = (lane & 32) ? a - b : a + b;
+    }
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < C; ++i) m = max(m, __builtin_bit_cast(uint32_t, x[i]) & 0x7FFFFFFFu);
+  m = row_max_u32(m);
+  const uint32_t e = min(m >> 23, 253u);              // 2^(e-127) <= largest value, or smaller
+  const float inv = __builtin_bit_cast(float, (254u - e) << 23);
+  *rs = m >= 0x7F800000u ? NAN : e ? __builtin_bit_cast(float, e << 23) : 0x1p-127f;
+#pragma unroll
+  for (int i = 0; i < C / 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) out[i][j] = (_Float16)(x[8 * i + j] * inv);
+}
+
+// 8 codes -> 8 fp16
+__device__ __forceinline__ f16x8 e2m1_f16x8(uint32_t x) {
+  const f16x2 a = e2m1_pair<0>(x), b = e2m1_pair<1>(x), c = e2m1_pair<2>(x), d = e2m1_pair<3>(x);
+  return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// Row of D values held 8 to a lane, normalised and rotated back, to bf16.
+template <int D>
+__device__ __forceinline__ void finish_row(float* v, float l, bool rotate, float c_v, int lane, uint16_t* dst) {
+  if (rotate) kv_transform<D>(v, lane);
+  const float f = l != 0.0f ? c_v / l : 0.0f;
+  u32x4 out;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    out[i] = (uint32_t)f32_to_bf16_rne(v[2 * i] * f) | ((uint32_t)f32_to_bf16_rne(v[2 * i + 1] * f) << 16);
+  if (dst) *reinterpret_cast<u32x4*>(dst) = out;
+}
+
+__device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.0f : m; }
+
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+
+template <int D> struct Chunk;                        // a quarter of a row of codes
+template <> struct Chunk<128> { typedef u32x4 T; };
+template <> struct Chunk<64> { typedef u32x2 T; };
+
+template <int D>
+struct TileRegs {                                     // one tile's codes and scales on their way
+  typename Chunk<D>::T k[4], v[4];
+  float ks, vs;
+  uint32_t held;                                      // bit i: keys 16i .. 16i+15 lie in a page
+};
+
+// Pages of a wave's tiles: lane 4k + i holds the page of keys 16i ... of the k-th tile to come (every WV-th from `tile` on).
+template <int WV>
+__device__ __forceinline__ int tile_pages(const KvArgs& a, int b, int64_t tile) {
+  const int lane = threadIdx.x & 63;
+  return kv_page(a, b, (tile + (int64_t)(lane >> 2) * WV) * kTile + (lane & 3) * 16);
 }
 
 template <int D>
-__global__ __launch_bounds__(256) void kv_attention_kernel(KvAttnArgs g, float c_b) {
+__device__ __forceinline__ void load_tile(const KvArgs& a, int kvh, int tile, int pages, int at, TileRegs<D>& r) {
+  typedef typename Chunk<D>::T C;
+  const int lane = threadIdx.x & 63;
+  const uint32_t mask = (1u << a.logp) - 1;
+  uint32_t held = 0;
+  int pg[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    pg[i] = __builtin_amdgcn_readlane(pages, 4 * at + i);
+    held |= pg[i] >= 0 ? 1u << i : 0;
+    pg[i] = pg[i] >= 0 ? pg[i] : 0;                   // keys in no page: any page is read, and masked
+    const int64_t row = ((((int64_t)pg[i] * a.n_kv + kvh) << a.logp) + ((tile * kTile + 16 * i) & mask)) * (D / 2);
+    r.k[i] = *reinterpret_cast<const C*>(a.codes[0] + row + (lane & 15) * (D / 2) + (lane >> 4) * (D / 8));
+    r.v[i] = *reinterpret_cast<const C*>(a.codes[1] + row + (lane >> 2) * (D / 2) + (lane & 3) * (D / 8));
+  }
+  const int g = lane >> 4;
+  const int p = g & 2 ? (g & 1 ? pg[3] : pg[2]) : (g & 1 ? pg[1] : pg[0]);
+  const int64_t row = (((int64_t)p * a.n_kv + kvh) << a.logp) + ((tile * kTile + lane) & mask);
+  r.ks = a.scales[0][row];
+  r.vs = a.scales[1][row];
+  r.held = held;
+}
+
+template <int D, int NB, int WV>
+__global__ __launch_bounds__(64 * WV) void kv_attention_kernel(KvAttnArgs g, SplitArgs sp) {
+  constexpr int ROWS = 16 * NB, NT = 64 * WV, P = Lds<D, NB, WV>::P;
+  __shared__ Lds<D, NB, WV> s;
   const KvArgs& a = g.kv;
-  __shared__ float q[D], o[D], w[256], red[256];
-  const int tid = threadIdx.x;
-  const int64_t t = blockIdx.x;
-  const int h = blockIdx.y, kvh = h / (g.n_q / a.n_kv);
-  const int b = kv_seq_of(a, t);
-  if (b < 0) return;
-  const int64_t pos = kv_position(a, b, t);
-  if (tid < D) {
-    q[tid] = bf16_to_f32(g.q[t * g.ldq + (int64_t)h * D + tid]);
-    o[tid] = 0;
-  }
-  if (a.rotate & 1) head_transform_lds<D>(q, tid);
-  __syncthreads();
-  const int64_t cap = (int64_t)a.max_pages << a.logp;
-  int64_t hi = a.lens[b] < cap ? a.lens[b] : cap, lo = 0;
-  if (g.causal && pos + 1 < hi) hi = pos + 1;
-  if (g.window && pos - g.window + 1 > 0) lo = pos - g.window + 1;
-  const float sc = g.scale * ((a.rotate & 1) ? c_b : 1.0f);
-  float m = -INFINITY, l = 0;
-  for (int64_t j0 = lo; j0 < hi; j0 += 256) {
-    const int64_t j = j0 + tid;
-    const int page = j < hi ? kv_page(a, b, j) : -1;
-    float s = -INFINITY, vs = 0;
-    if (page >= 0) {
-      const int64_t at = kv_row(a, page, kvh, j);
-      const uint8_t* c = a.codes[0] + at * (D / 2);
-      float d = 0;
-      for (int i = 0; i < D / 2; ++i)
-        d += q[2 * i] * e2m1_value(c[i] & 15) + q[2 * i + 1] * e2m1_value(c[i] >> 4);
-      s = d * a.scales[0][at] * sc;
-      vs = a.scales[1][at];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int G = g.n_q / a.n_kv;
+
+  // ---- this workgroup's units.  A sequence has n_kv * (units of its row blocks) of them, in the order head, row block, key tile.
+  auto head_units = [&](const Seq& q) {
+    int64_t n = 0;
+    for (int r0 = 0; r0 < q.rows; r0 += ROWS) {
+      if (!sp.split) { ++n; continue; }
+      const Range t = kv_tiles(q, r0, min(r0 + ROWS, q.rows) - 1, G, g.causal, g.window);
+      n += t.hi - t.lo;
+    }
+    return n;
+  };
+  auto block_scan = [&](int64_t x, int64_t& total) {   // exclusive prefix over the workgroup
+    int64_t inc = x;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int64_t y = __shfl_up(inc, d);
+      if (lane >= d) inc += y;
     }
     __syncthreads();
-    red[tid] = s;
+    if (lane == 63) s.scan[wave] = inc;
     __syncthreads();
-    float mn = m;
-    for (int i = 0; i < 256; ++i) mn = fmaxf(mn, red[i]);
-    const float ms = mn == -INFINITY ? 0 : mn;
-    const float p = page >= 0 ? expf(s - ms) : 0;
-    __syncthreads();
-    red[tid] = p;
-    w[tid] = page >= 0 ? p * vs : 0;
-    __syncthreads();
-    const float keep = expf(m - ms);
-    l *= keep;
-    for (int i = 0; i < 256; ++i) l += red[i];
-    if (tid < D) {
-      float x = o[tid] * keep;
-      for (int i = 0; i < 256 && j0 + i < hi; ++i) {
-        const int pg = kv_page(a, b, j0 + i);
-        if (pg < 0) continue;
-        const uint8_t c = a.codes[1][kv_row(a, pg, kvh, j0 + i) * (D / 2) + tid / 2];
-        x += w[i] * e2m1_value((tid & 1) ? c >> 4 : c & 15);
+    int64_t before = 0;
+    total = 0;
+    for (int w = 0; w < WV; ++w) {
+      if (w < wave) before += s.scan[w];
+      total += s.scan[w];
+    }
+    return before + inc - x;
+  };
+  int64_t total = 0, mine = 0, prefix = 0;
+  for (int b0 = 0; b0 < a.B; b0 += NT) {
+    const int b = b0 + tid;
+    mine = b < a.B ? head_units(kv_seq(a, b, G)) * a.n_kv : 0;
+    int64_t part;
+    prefix = block_scan(mine, part);
+    total += part;
+  }
+  int64_t per = (total + sp.groups - 1) / sp.groups;
+  per = per > sp.min_units ? per : sp.min_units;
+  const int64_t first = (int64_t)blockIdx.x * per;
+  if (tid == 0 && sp.split) sp.desc[blockIdx.x].more = 0;
+  if (first >= total) return;
+  int64_t left = total - first < per ? total - first : per;
+  int64_t base = 0;
+  for (int b0 = 0;; b0 += NT) {
+    if (a.B > NT) {
+      const int b = b0 + tid;
+      mine = b < a.B ? head_units(kv_seq(a, b, G)) * a.n_kv : 0;
+      int64_t part;
+      prefix = block_scan(mine, part) + base;
+      base += part;
+    }
+    if (prefix <= first && first < prefix + mine) {
+      s.start_b = b0 + tid;
+      s.start_off = first - prefix;
+    }
+    if (a.B <= NT || base > first) break;
+  }
+  __syncthreads();
+  int b = __builtin_amdgcn_readfirstlane(s.start_b);
+  int64_t off = ((int64_t)__builtin_amdgcn_readfirstlane((int)(s.start_off >> 32)) << 32) |
+                (uint32_t)__builtin_amdgcn_readfirstlane((int)s.start_off);
+
+  const float c_scale = g.scale * sp.c_q * 1.44269504088896341f;
+  for (; left > 0 && b < a.B; ++b, off = 0) {
+    const Seq q = kv_seq(a, b, G);
+    if (q.rows == 0) continue;
+    const int64_t hu = head_units(q);
+    int kvh = (int)(off / hu);
+    off -= kvh * hu;
+    for (; left > 0 && kvh < a.n_kv; ++kvh, off = 0) {
+      for (int r0 = 0; left > 0 && r0 < q.rows; r0 += ROWS) {
+        const int n_rows = min(ROWS, q.rows - r0);
+        const Range all = kv_tiles(q, r0, r0 + n_rows - 1, G, g.causal, g.window);
+        const int units = sp.split ? all.hi - all.lo : 1;
+        if (off >= units) { off -= units; continue; }
+        const int u0 = (int)off;
+        const int u1 = (int)(units - u0 < left ? units : u0 + left);
+        left -= u1 - u0;
+        off = 0;
+        const int t_lo = sp.split ? all.lo + u0 : all.lo, t_hi = sp.split ? all.lo + u1 : all.hi;
+
+        // ---- the queries, and what each row attends
+        f16x8 qf[NB][D / 32];
+        float rs[NB], M[NB], l[NB];
+        int lo[NB], hi[NB];
+        f32x4 o[NB][D / 16];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          const int r = r0 + 16 * n + (lane & 15);
+          const bool row = 16 * n + (lane & 15) < n_rows;
+          const int i = row ? r / G : 0, h = row ? r - i * G : 0;
+          const uint16_t* src = g.q + (q.t0 + i) * g.ldq + ((int64_t)kvh * G + h) * D + (lane >> 4) * (D / 4);
+          load_queries<D>(row ? src : nullptr, a.rotate & 1, qf[n], &rs[n]);
+          rs[n] *= c_scale;
+          const Range w = kv_range(q, i, g.causal, g.window);
+          lo[n] = w.lo;
+          hi[n] = row ? w.hi : 0;
+          M[n] = -INFINITY;
+          l[n] = 0;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) o[n][c] = f32x4{0, 0, 0, 0};
+        }
+        const int all_lo = kv_range(q, (r0 + n_rows - 1) / G, g.causal, g.window).lo;   // positions that every row attends
+        const int all_hi = kv_range(q, r0 / G, g.causal, g.window).hi;
+        __syncthreads();                              // the last block's sums have been read
+
+        // ---- the wave's tiles
+        int tile = t_lo + wave, at = 0;
+        TileRegs<D> nx;
+        int pages = 0;
+        if (tile < t_hi) {
+          pages = tile_pages<WV>(a, b, tile);
+          load_tile<D>(a, kvh, tile, pages, 0, nx);
+        }
+        for (; tile < t_hi; tile += WV) {
+          TileRegs<D> cu = nx;
+          uint8_t* vl = s.t.v[wave];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<typename Chunk<D>::T*>(vl + (16 * i + (lane >> 2)) * (D / 2) + ((lane & 3) ^ i) * (D / 8)) = cu.v[i];
+          {
+            const float v = cu.vs < 0x1p-64f ? 0x1p-64f : cu.vs;
+            s.t.ks[wave][lane] = cu.ks;
+            s.t.lv[wave][lane] = __builtin_amdgcn_logf(v);
+            s.t.iv[wave][lane] = 1.0f / v;
+          }
+          if (tile + WV < t_hi) {
+            if (++at == 16) { pages = tile_pages<WV>(a, b, tile + WV); at = 0; }
+            load_tile<D>(a, kvh, tile + WV, pages, at, nx);
+          }
+          // scores of 64 keys
+          f32x4 sc[NB][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int n = 0; n < NB; ++n) sc[n][i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+              const f16x8 kf = e2m1_f16x8(cu.k[i][k]);
+#pragma unroll
+              for (int n = 0; n < NB; ++n)
+                sc[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[n][k], sc[n][i], 0, 0, 0);
+            }
+          }
+          __builtin_amdgcn_wave_barrier();
+          const bool whole = cu.held == 15u && tile * kTile >= all_lo && tile * kTile + kTile <= all_hi;
+          f32x4 iv[4];
+          f16x8 w[NB][2];
+          float mx[NB];
+#pragma unroll
+          for (int n = 0; n < NB; ++n) mx[n] = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f32x4 ks = *reinterpret_cast<const f32x4*>(&s.t.ks[wave][16 * i + 4 * (lane >> 4)]);
+            const f32x4 lv = *reinterpret_cast<const f32x4*>(&s.t.lv[wave][16 * i + 4 * (lane >> 4)]);
+            iv[i] = *reinterpret_cast<const f32x4*>(&s.t.iv[wave][16 * i + 4 * (lane >> 4)]);
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                float x = __builtin_fmaf(sc[n][i][j] * ks[j], rs[n], lv[j]);
+                if (!whole) {
+                  const int t = tile * kTile + 16 * i + 4 * (lane >> 4) + j;
+                  x = t >= lo[n] && t < hi[n] && ((cu.held >> i) & 1) ? x : -INFINITY;
+                }
+                sc[n][i][j] = x;
+                mx[n] = fmaxf(mx[n], x);
+              }
+          }
+#pragma unroll
+          for (int n = 0; n < NB; ++n) {
+            const float m = fmaxf(M[n], row_max(mx[n]));
+            if (__any(m > M[n])) {
+              const float keep = __builtin_amdgcn_exp2f(M[n] - safe_max(m));
+              l[n] *= keep;
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) o[n][c] *= keep;
+              M[n] = m;
+            }
+            const float ref = safe_max(M[n]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float x = sc[n][i][j];
+                const float p = __builtin_amdgcn_exp2f(x - ref);
+                // a masked key's 1 / vs may be NaN
+                l[n] = whole || x != -INFINITY ? __builtin_fmaf(p, iv[i][j], l[n]) : l[n];
+                w[n][i >> 1][4 * (i & 1) + j] = (_Float16)p;
+              }
+          }
+          // values times weights, 16 channels at a time
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            const int r = lane & 15, key = 16 * (r >> 2) + 4 * (lane >> 4) + (r & 3);
+            const int chunk = c * 8 / (D / 8), in = c * 8 % (D / 8);
+            const uint8_t* src = vl + key * (D / 2) + (chunk ^ (r >> 2)) * (D / 8) + in;
+            const i32x2 x = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2*)src);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const f16x8 vf = e2m1_f16x8((uint32_t)x[k]);
+#pragma unroll
+              for (int n = 0; n < NB; ++n) o[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, w[n][k], o[n][c], 0, 0, 0);
+            }
+          }
+          __builtin_amdgcn_wave_barrier();
+        }
+
+        // ---- the waves' sums, joined
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          const int row = 16 * n + (lane & 15);
+          const float lsum = row_add(l[n]);
+          if (lane < 16) {
+            s.m[wave][row] = M[n];
+            s.l[wave][row] = lsum;
+          }
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+            *reinterpret_cast<f32x4*>(&s.o[wave][row * P + 16 * c + 4 * (lane >> 4)]) = o[n][c];
+        }
+        __syncthreads();
+        constexpr int L = D / 8;
+        const bool starts = u0 == 0, ends = u1 == units;
+        const int64_t part = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
+        const int sub = tid % L;
+        for (int row0 = 0; row0 < ROWS; row0 += NT / L) {
+          const int row = row0 + tid / L;
+          if (row >= n_rows) continue;                // whole groups of L lanes
+          float m = -INFINITY, sum = 0, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+          for (int w = 0; w < WV; ++w) m = fmaxf(m, s.m[w][row]);
+          const float ref = safe_max(m);
+          for (int w = 0; w < WV; ++w) {
+            const float f = __builtin_amdgcn_exp2f(s.m[w][row] - ref);
+            sum = __builtin_fmaf(s.l[w][row], f, sum);
+            const f32x4 x0 = *reinterpret_cast<const f32x4*>(&s.o[w][row * P + 8 * sub]);
+            const f32x4 x1 = *reinterpret_cast<const f32x4*>(&s.o[w][row * P + 8 * sub + 4]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[j] = __builtin_fmaf(x0[j], f, v[j]);
+              v[4 + j] = __builtin_fmaf(x1[j], f, v[4 + j]);
+            }
+          }
+          if (starts && ends) {
+            const int r = r0 + row, i = r / G, h = r - i * G;
+            finish_row<D>(v, sum, a.rotate & 2, sp.c_v, sub, g.out + (q.t0 + i) * g.ldo + ((int64_t)kvh * G + h) * D + 8 * sub);
+          } else {
+            float* dst = sp.o + (part * ROWS + row) * D + 8 * sub;
+            *reinterpret_cast<f32x4*>(dst) = f32x4{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<f32x4*>(dst + 4) = f32x4{v[4], v[5], v[6], v[7]};
+            if (sub == 0) sp.ml[part * ROWS + row] = float2{m, sum};
+          }
+        }
+        if (starts && !ends && tid == 0)
+          sp.desc[blockIdx.x] = Desc{b, kvh, r0, (int)((units - u1 + per - 1) / per)};
       }
-      o[tid] = x;
+    }
+  }
+}
+
+// Joins the parts of a row block that starts in group blockIdx.x and goes on in the next ones: row blockIdx.y, the parts dealt
+// out to the D/8-lane groups of a workgroup.
+template <int D, int ROWS>
+__global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs g, SplitArgs sp) {
+  constexpr int L = D / 8, NG = 256 / L;
+  const int w = blockIdx.x, row = blockIdx.y, tid = threadIdx.x, sub = tid % L, grp = tid / L;
+  const Desc d = sp.desc[w];
+  if (d.more == 0) return;
+  const int G = g.n_q / g.kv.n_kv;
+  const Seq q = kv_seq(g.kv, d.b, G);
+  if (d.r0 + row >= q.rows) return;
+  __shared__ float so[NG][D], sm[NG], sl[NG];
+  // part 0 is the block's start (second slot of w), part p the first slot of w + p
+  float m = -INFINITY, sum = 0, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int p = grp; p <= d.more; p += NG) {
+    const int64_t part = (p == 0 ? 2 * (int64_t)w + 1 : 2 * (int64_t)(w + p)) * ROWS + row;
+    const float2 ml = sp.ml[part];
+    const f32x4 x0 = *reinterpret_cast<const f32x4*>(sp.o + part * D + 8 * sub);
+    const f32x4 x1 = *reinterpret_cast<const f32x4*>(sp.o + part * D + 8 * sub + 4);
+    const float mn = fmaxf(m, ml.x), ref = safe_max(mn);
+    const float f0 = __builtin_amdgcn_exp2f(m - ref), f1 = __builtin_amdgcn_exp2f(ml.x - ref);
+    sum = sum * f0 + ml.y * f1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = v[j] * f0 + x0[j] * f1;
+      v[4 + j] = v[4 + j] * f0 + x1[j] * f1;
     }
     m = mn;
   }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) so[grp][8 * sub + j] = v[j];
+  if (sub == 0) { sm[grp] = m; sl[grp] = sum; }
   __syncthreads();
-  if (a.rotate & 2) head_transform_lds<D>(o, tid);
-  __syncthreads();
-  if (tid < D) {
-    const float x = l != 0 ? o[tid] / l * ((a.rotate & 2) ? c_b : 1.0f) : 0;
-    g.out[t * g.ldo + (int64_t)h * D + tid] = f32_to_bf16_rne(x);
+  if (grp != 0) return;
+  const int n = d.more + 1 < NG ? d.more + 1 : NG;
+  m = sm[0];
+  for (int p = 1; p < n; ++p) m = fmaxf(m, sm[p]);
+  const float ref = safe_max(m);
+  sum = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0;
+  for (int p = 0; p < n; ++p) {
+    const float f = __builtin_amdgcn_exp2f(sm[p] - ref);
+    sum = __builtin_fmaf(sl[p], f, sum);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf(so[p][8 * sub + j], f, v[j]);
   }
+  const int r = d.r0 + row, i = r / G, h = r - i * G;
+  finish_row<D>(v, sum, g.kv.rotate & 2, sp.c_v, sub, g.out + (q.t0 + i) * g.ldo + ((int64_t)d.kvh * G + h) * D + 8 * sub);
+}
+
+// Query rows of a row block: those of a sequence on average, up to 32.
+int row_block(int64_t T, int B, int G) { return (T + B - 1) / B * G <= 16 ? 16 : 32; }
+
+template <int D, int NB, int WV>
+hipError_t launch_form(const KvAttnArgs& g, SplitArgs sp, hipStream_t stream) {
+  kv_attention_kernel<D, NB, WV><<<sp.groups, 64 * WV, 0, stream>>>(g, sp);
+  if (hipError_t e = hipGetLastError()) return e;
+  if (!sp.split) return hipSuccess;
+  kv_join_kernel<D, 16 * NB><<<dim3(sp.groups, 16 * NB), 256, 0, stream>>>(g, sp);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-size_t kv_attention_workspace_bytes(int64_t T, int B, int n_q, int n_kv, int D) { return 16; }
+size_t kv_attention_workspace_bytes(int64_t T, int B, int n_q, int n_kv, int D) {
+  const int rows = row_block(T, B, n_q / n_kv);
+  return (size_t)kMaxGroups * (sizeof(Desc) + 2 * rows * (sizeof(float2) + D * sizeof(float)));
+}
 
 hipError_t launch_kv_attention(const KvAttnArgs& g, hipStream_t stream) {
-  const float c_b = (float)(1.0 / std::sqrt((double)g.kv.D));
-  auto f = g.kv.D == 64 ? kv_attention_kernel<64> : kv_attention_kernel<128>;
-  f<<<dim3((uint32_t)g.kv.T, g.n_q), 256, 0, stream>>>(g, c_b);
-  return hipGetLastError();
+  const KvArgs& a = g.kv;
+  const int G = g.n_q / a.n_kv, rows = row_block(a.T, a.B, G);
+  SplitArgs sp{};
+  const float c = (float)(1.0 / std::sqrt((double)a.D));
+  sp.c_q = a.rotate & 1 ? c : 1.0f;
+  sp.c_v = a.rotate & 2 ? c : 1.0f;
+  sp.desc = static_cast<Desc*>(g.ws);
+  sp.ml = reinterpret_cast<float2*>(sp.desc + kMaxGroups);
+  sp.o = reinterpret_cast<float*>(sp.ml + (size_t)2 * kMaxGroups * rows);
+  const int64_t blocks = ((a.T * G + rows - 1) / rows + a.B) * a.n_kv;      // row blocks at most
+  const int64_t cap = ((int64_t)a.max_pages << a.logp) / kTile + 1;         // key tiles of one at most
+  sp.split = cap > 32;
+  sp.min_units = sp.split ? 4 : 1;
+  const int64_t want = sp.split ? blocks * ((cap + 3) / 4) : blocks;
+  sp.groups = (int)(want < kMaxGroups ? want : kMaxGroups);
+  if (a.D == 64) return rows == 16 ? launch_form<64, 1, 4>(g, sp, stream) : launch_form<64, 2, 4>(g, sp, stream);
+  return rows == 16 ? launch_form<128, 1, 4>(g, sp, stream) : launch_form<128, 2, 4>(g, sp, stream);
 }
 
 }  // namespace cbq

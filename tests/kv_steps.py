@@ -76,14 +76,7 @@ class Step:
         return out[0], out[1], held
 
     def attention(self, q, scale, causal=True, window=0):
-        """(out [T][n_q][D] fp64, bound of the same shape, rows that belong to a sequence).
-
-        The bound, with u = 2^-11 of fp16 and everything relative to a row's largest value:
-        a score moves by at most d = scale * |q||k| * (u + 2^-17) (the rotated queries in fp16, fp32
-        sums of 128 products), so a weight by 2 d and u of its own; a weight below fp16's normal
-        range by 2^-25 of the largest one; the exponential, its argument and the normalisation
-        in fp32 by 2^-18 of a score's size at most.  The rotation back keeps lengths.  Then half a step of bf16."""
-        n_q = q.shape[1]
+        """(out [T][n_q][D] fp64, bound of the same shape, rows that belong to a sequence)."""
         out, tol = np.zeros(q.shape), np.zeros(q.shape)
         mine = np.zeros(self.T, dtype=bool)
         for b in range(len(self.lens)):
@@ -93,25 +86,37 @@ class Step:
             mine[t0:t1] = True
             k, v, held = self.sequence(b)
             pos = np.arange(t0, t1) + self.lens[b] - t1
-            with np.errstate(invalid="ignore", over="ignore"):
-                o, p, a = oracle.kv_attention(k, v, held, q[t0:t1], pos, self.lens[b], scale, causal, window)
-            out[t0:t1] = o
-            for i in range(t1 - t0):
-                for h in range(n_q):
-                    w = p[i, h]
-                    at = np.flatnonzero(w)
-                    if len(at) == 0:
-                        continue
-                    g = h // (n_q // self.n_kv)
-                    kn, vv = np.linalg.norm(k[at, g], axis=1), v[at, g]
-                    vn = np.linalg.norm(vv, axis=1)
-                    d = abs(scale) * np.linalg.norm(q[t0 + i, h]) * kn.max() * (2.0 ** -11 + 2.0 ** -17)
-                    d += np.abs(a[i, h, at]).max() * 2.0 ** -18
-                    err = (w[at] * vn).sum() * (np.expm1(2 * d) + 2.0 ** -11 + 2.0 ** -18)
-                    # an E2M1 row's length is at most 6 sqrt(D) scales, its largest weight at most w * vn / 0.5
-                    err += len(at) * 2.0 ** -25 * 12 * np.sqrt(self.D) * (w[at] * vn).max()
-                    tol[t0 + i, h] = err
-        return out, tol + 2.0 ** -8 * np.abs(out) + 1e-37, mine
+            out[t0:t1], tol[t0:t1] = attention_and_bound(k, v, held, q[t0:t1], pos, self.lens[b], scale, causal, window)
+        return out, tol, mine
+
+
+def attention_and_bound(k, v, held, q, pos, length, scale, causal, window):
+    """The oracle's attention of one sequence, and how far a result may be from it.
+
+    The bound, with u = 2^-11 of fp16 and everything relative to a row's largest value:
+    a score moves by at most d = |scale| |q||k| (u + 2^-17) (the rotated queries in fp16, fp32
+    sums of 128 products), so a weight by 2 d and u of its own; a weight below fp16's normal
+    range by 2^-25 of the largest one; the exponential, its argument and the normalisation
+    in fp32 by 2^-18 of a score's size at most.  The rotation back keeps lengths.  Then half a step of bf16."""
+    with np.errstate(invalid="ignore", over="ignore"):
+        out, p, a = oracle.kv_attention(k, v, held, q, pos, length, scale, causal, window)
+    n, n_q, D = q.shape
+    tol = np.zeros(q.shape)
+    for i in range(n):
+        for h in range(n_q):
+            w = p[i, h]
+            at = np.flatnonzero(w)
+            if len(at) == 0:
+                continue
+            g = h // (n_q // k.shape[1])
+            kn, vn = np.linalg.norm(k[at, g], axis=1), np.linalg.norm(v[at, g], axis=1)
+            d = abs(scale) * np.linalg.norm(q[i, h]) * kn.max() * (2.0 ** -11 + 2.0 ** -17)
+            d += np.abs(a[i, h, at]).max() * 2.0 ** -18
+            err = (w[at] * vn).sum() * (np.expm1(2 * d) + 2.0 ** -11 + 2.0 ** -18)
+            # an E2M1 row's error is at most 6 sqrt(D) of its scale, its length at least half of it
+            err += len(at) * 2.0 ** -25 * 12 * np.sqrt(D) * (w[at] * vn).max()
+            tol[i, h] = err
+    return out, tol + 2.0 ** -8 * np.abs(out) + 1e-37
 
 
 def bf16_values(rng, shape, spread=1.0):
