@@ -79,6 +79,89 @@ struct SplitArgs {
   float* o;                        // [2 * groups][ROWS][D]
 };
 
+// Units of one key/value head of a sequence: its row blocks' key tiles, or its row blocks.
+template <int ROWS>
+__device__ __forceinline__ int64_t head_units(const KvAttnArgs& g, const SplitArgs& sp, const Seq& q, int G) {
+  if (!sp.split) return (q.rows + ROWS - 1) / ROWS;
+  int64_t n = 0;
+  for (int r0 = 0; r0 < q.rows; r0 += ROWS) {
+    const Range t = kv_tiles(q, r0, min(r0 + ROWS, q.rows) - 1, G, g.causal, g.window);
+    n += t.hi - t.lo;
+  }
+  return n;
+}
+
+// A workgroup's units: `left` of them from unit `off` of sequence b on.  All sequences' units in a row (a
+// sequence's in the order head, row block, key tile) are dealt out evenly, `per` to a workgroup; each
+// workgroup counts them for itself, from the lengths.
+struct Walk {
+  int b;
+  int64_t off, left, per;
+};
+
+template <int ROWS, int WV>
+__device__ __forceinline__ Walk walk_start(const KvAttnArgs& g, const SplitArgs& sp, int G, int64_t* scan,
+                                           int64_t* start_off, int* start_b) {
+  constexpr int NT = 64 * WV;
+  const KvArgs& a = g.kv;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  auto block_scan = [&](int64_t x, int64_t& total) {   // exclusive prefix over the workgroup
+    int64_t inc = x;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int64_t y = __shfl_up(inc, d);
+      if (lane >= d) inc += y;
+    }
+    __syncthreads();
+    if (lane == 63) scan[wave] = inc;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+    for (int w = 0; w < WV; ++w) {
+      if (w < wave) before += scan[w];
+      total += scan[w];
+    }
+    return before + inc - x;
+  };
+  int64_t total = 0, mine = 0, prefix = 0;
+  for (int b0 = 0; b0 < a.B; b0 += NT) {
+    const int b = b0 + tid;
+    mine = b < a.B ? head_units<ROWS>(g, sp, kv_seq(a, b, G), G) * a.n_kv : 0;
+    int64_t part;
+    prefix = block_scan(mine, part);
+    total += part;
+  }
+  Walk u{0, 0, 0, 0};
+  u.per = (total + sp.groups - 1) / sp.groups;
+  u.per = u.per > sp.min_units ? u.per : sp.min_units;
+  // unsplit calls start with the last units: a sequence's last rows attend the most keys
+  const int64_t at = sp.split ? (int64_t)blockIdx.x : (int64_t)sp.groups - 1 - blockIdx.x;
+  const int64_t first = at * u.per;
+  if (tid == 0 && sp.split) sp.desc[blockIdx.x].more = 0;
+  if (first >= total) return u;
+  u.left = total - first < u.per ? total - first : u.per;
+  int64_t base = 0;
+  for (int b0 = 0;; b0 += NT) {
+    if (a.B > NT) {
+      const int b = b0 + tid;
+      mine = b < a.B ? head_units<ROWS>(g, sp, kv_seq(a, b, G), G) * a.n_kv : 0;
+      int64_t part;
+      prefix = block_scan(mine, part) + base;
+      base += part;
+    }
+    if (prefix <= first && first < prefix + mine) {
+      *start_b = b0 + tid;
+      *start_off = first - prefix;
+    }
+    if (a.B <= NT || base > first) break;
+  }
+  __syncthreads();
+  u.b = __builtin_amdgcn_readfirstlane(*start_b);
+  u.off = ((int64_t)__builtin_amdgcn_readfirstlane((int)(*start_off >> 32)) << 32) |
+          (uint32_t)__builtin_amdgcn_readfirstlane((int)*start_off);
+  return u;
+}
+
 template <int D, int NB, int WV>
 struct Lds {
   static constexpr int ROWS = 16 * NB, P = D + 4;    // padded row: 16 rows start in 16 different bank groups
@@ -251,77 +334,22 @@ __global__ __launch_bounds__(64 * WV) void kv_attention_kernel(KvAttnArgs g, Spl
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int G = g.n_q / a.n_kv;
 
-  // ---- this workgroup's units.  A sequence has n_kv * (units of its row blocks) of them, in the order head, row block, key tile.
-  auto head_units = [&](const Seq& q) {
-    int64_t n = 0;
-    for (int r0 = 0; r0 < q.rows; r0 += ROWS) {
-      if (!sp.split) { ++n; continue; }
-      const Range t = kv_tiles(q, r0, min(r0 + ROWS, q.rows) - 1, G, g.causal, g.window);
-      n += t.hi - t.lo;
-    }
-    return n;
-  };
-  auto block_scan = [&](int64_t x, int64_t& total) {   // exclusive prefix over the workgroup
-    int64_t inc = x;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int64_t y = __shfl_up(inc, d);
-      if (lane >= d) inc += y;
-    }
-    __syncthreads();
-    if (lane == 63) s.scan[wave] = inc;
-    __syncthreads();
-    int64_t before = 0;
-    total = 0;
-    for (int w = 0; w < WV; ++w) {
-      if (w < wave) before += s.scan[w];
-      total += s.scan[w];
-    }
-    return before + inc - x;
-  };
-  int64_t total = 0, mine = 0, prefix = 0;
-  for (int b0 = 0; b0 < a.B; b0 += NT) {
-    const int b = b0 + tid;
-    mine = b < a.B ? head_units(kv_seq(a, b, G)) * a.n_kv : 0;
-    int64_t part;
-    prefix = block_scan(mine, part);
-    total += part;
-  }
-  int64_t per = (total + sp.groups - 1) / sp.groups;
-  per = per > sp.min_units ? per : sp.min_units;
-  const int64_t first = (int64_t)blockIdx.x * per;
-  if (tid == 0 && sp.split) sp.desc[blockIdx.x].more = 0;
-  if (first >= total) return;
-  int64_t left = total - first < per ? total - first : per;
-  int64_t base = 0;
-  for (int b0 = 0;; b0 += NT) {
-    if (a.B > NT) {
-      const int b = b0 + tid;
-      mine = b < a.B ? head_units(kv_seq(a, b, G)) * a.n_kv : 0;
-      int64_t part;
-      prefix = block_scan(mine, part) + base;
-      base += part;
-    }
-    if (prefix <= first && first < prefix + mine) {
-      s.start_b = b0 + tid;
-      s.start_off = first - prefix;
-    }
-    if (a.B <= NT || base > first) break;
-  }
-  __syncthreads();
-  int b = __builtin_amdgcn_readfirstlane(s.start_b);
-  int64_t off = ((int64_t)__builtin_amdgcn_readfirstlane((int)(s.start_off >> 32)) << 32) |
-                (uint32_t)__builtin_amdgcn_readfirstlane((int)s.start_off);
-
+  Walk u = walk_start<ROWS, WV>(g, sp, G, s.scan, &s.start_off, &s.start_b);
+  if (u.left <= 0) return;
+  int b = u.b;
+  int64_t off = u.off, left = u.left;
+  const int64_t per = u.per;
   const float c_scale = g.scale * sp.c_q * 1.44269504088896341f;
   for (; left > 0 && b < a.B; ++b, off = 0) {
     const Seq q = kv_seq(a, b, G);
     if (q.rows == 0) continue;
-    const int64_t hu = head_units(q);
+    const int64_t hu = head_units<ROWS>(g, sp, q, G);
     int kvh = (int)(off / hu);
     off -= kvh * hu;
     for (; left > 0 && kvh < a.n_kv; ++kvh, off = 0) {
-      for (int r0 = 0; left > 0 && r0 < q.rows; r0 += ROWS) {
+      int r0 = 0;
+      if (!sp.split) { r0 = (int)off * ROWS; off = 0; }
+      for (; left > 0 && r0 < q.rows; r0 += ROWS) {
         const int n_rows = min(ROWS, q.rows - r0);
         const Range all = kv_tiles(q, r0, r0 + n_rows - 1, G, g.causal, g.window);
         const int units = sp.split ? all.hi - all.lo : 1;
@@ -512,21 +540,299 @@ __global__ __launch_bounds__(64 * WV) void kv_attention_kernel(KvAttnArgs g, Spl
   }
 }
 
-// Joins the parts of a row block that starts in group blockIdx.x and goes on in the next ones: row blockIdx.y, the parts dealt
-// out to the D/8-lane groups of a workgroup.
-template <int D, int ROWS>
+// ---------------------------------------------------------------------------
+// Many query rows a sequence (prefill): a workgroup takes 4 x 16 NB rows of one key/value head, each wave its own,
+// and all four read the same key tiles.  A tile (64 keys: codes as they are, 8 KB, and the scales)
+// goes through LDS in two buffers with one barrier a tile, the next one's loads in flight meanwhile; each wave
+// converts what it multiplies.  The running maximum moves only when a score passes it by 2^8: weights up
+// to 256 lose nothing in fp16, and most tiles then need neither an exchange between lanes nor a rescaling.
+constexpr float kSlack = 8.0f;
+
+template <int D>
+struct PrefillLds {
+  struct Buf {
+    uint8_t k[kTile * D / 2], v[kTile * D / 2];
+    float ks[kTile], lv[kTile], iv[kTile];
+    int held[4];
+  } buf[2];
+  int64_t scan[4];
+  int64_t start_off;
+  int start_b;
+};
+
+// A row's channels lie at 16c + 4g + j in o[c][j]: rotated over c and j in the lane, over g between lanes.
+template <int D>
+__device__ __forceinline__ void transform_tile(f32x4* o, int lane) {
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {
+    const f32x4 x = o[c];
+    const float a = x[0] + x[1], b = x[0] - x[1], d = x[2] + x[3], e = x[2] - x[3];
+    o[c] = f32x4{a + d, b + e, a - d, b - e};
+  }
+#pragma unroll
+  for (int h = 1; h < D / 16; h *= 2)
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+      if (!(c & h)) {
+        const f32x4 x = o[c], y = o[c + h];
+        o[c] = x + y;
+        o[c + h] = x - y;
+      }
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float a, b;
+      swap_pair<false>(o[c][j], a, b);
+      swap_pair<true>((lane & 16) ? a - b : a + b, a, b);
+      o[c][j] = (lane & 32) ? a - b : a + b;
+    }
+}
+
+template <int D, int NB>
+__global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitArgs sp) {
+  constexpr int ROWS = 64 * NB;
+  typedef typename Chunk<D>::T C;
+  __shared__ PrefillLds<D> s;
+  const KvArgs& a = g.kv;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int G = g.n_q / a.n_kv;
+  const uint32_t mask = (1u << a.logp) - 1;
+  Walk u = walk_start<ROWS, 4>(g, sp, G, s.scan, &s.start_off, &s.start_b);
+  if (u.left <= 0) return;
+  int b = u.b;
+  int64_t off = u.off, left = u.left;
+  const int64_t per = u.per;
+  const float c_scale = g.scale * sp.c_q * 1.44269504088896341f;
+  for (; left > 0 && b < a.B; ++b, off = 0) {
+    const Seq q = kv_seq(a, b, G);
+    if (q.rows == 0) continue;
+    const int64_t hu = head_units<ROWS>(g, sp, q, G);
+    int kvh = (int)(off / hu);
+    off -= kvh * hu;
+    for (; left > 0 && kvh < a.n_kv; ++kvh, off = 0) {
+      int r0 = 0;
+      if (!sp.split) { r0 = (int)off * ROWS; off = 0; }
+      for (; left > 0 && r0 < q.rows; r0 += ROWS) {
+        const int n_rows = min(ROWS, q.rows - r0);
+        const Range all = kv_tiles(q, r0, r0 + n_rows - 1, G, g.causal, g.window);
+        const int units = sp.split ? all.hi - all.lo : 1;
+        if (off >= units) { off -= units; continue; }
+        const int u0 = (int)off;
+        const int u1 = (int)(units - u0 < left ? units : u0 + left);
+        left -= u1 - u0;
+        off = 0;
+        const int t_lo = sp.split ? all.lo + u0 : all.lo, t_hi = sp.split ? all.lo + u1 : all.hi;
+
+        // ---- the wave's queries
+        const int w0 = r0 + 16 * NB * wave;           // its first row
+        const int w_rows = min(16 * NB, q.rows - w0); // may be <= 0
+        f16x8 qf[NB][D / 32];
+        float rs[NB], M[NB], l[NB];
+        int lo[NB], hi[NB];
+        f32x4 o[NB][D / 16];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          const int rr = 16 * n + (lane & 15);
+          const bool row = rr < w_rows;
+          const int r = row ? w0 + rr : r0, i = r / G, h = r - i * G;
+          const uint16_t* src = g.q + (q.t0 + i) * g.ldq + ((int64_t)kvh * G + h) * D + (lane >> 4) * (D / 4);
+          load_queries<D>(row ? src : nullptr, a.rotate & 1, qf[n], &rs[n]);
+          rs[n] *= c_scale;
+          const Range w = kv_range(q, i, g.causal, g.window);
+          lo[n] = w.lo;
+          hi[n] = row ? w.hi : 0;
+          M[n] = -INFINITY;
+          l[n] = 0;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) o[n][c] = f32x4{0, 0, 0, 0};
+        }
+        Range any{0, 0}, every{0, 0};                 // positions that some, that every row of the wave attends
+        if (w_rows > 0) {
+          const Range r_first = kv_range(q, w0 / G, g.causal, g.window), r_last = kv_range(q, (w0 + w_rows - 1) / G, g.causal, g.window);
+          any = Range{r_first.lo, r_last.hi};
+          every = Range{r_last.lo, r_first.hi};
+        }
+
+        // ---- the tiles: each wave brings 16 keys of each
+        C kr, vr;
+        float scale = 0;
+        int held = 0, pages = 0;
+        auto fetch = [&](int tile, int at) {
+          const int p0 = __builtin_amdgcn_readlane(pages, at);
+          held = p0 >= 0;
+          const int p = p0 >= 0 ? p0 : 0;             // keys in no page: any page is read, and masked
+          const int64_t row = (((int64_t)p * a.n_kv + kvh) << a.logp) + ((tile * kTile + 16 * wave) & mask);
+          kr = *reinterpret_cast<const C*>(a.codes[0] + row * (D / 2) + lane * (D / 8));
+          vr = *reinterpret_cast<const C*>(a.codes[1] + row * (D / 2) + lane * (D / 8));
+          scale = a.scales[(lane >> 4) & 1][row + (lane & 15)];
+        };
+        auto page_batch = [&](int tile) { pages = kv_page(a, b, (int64_t)(tile + lane) * kTile + 16 * wave); };
+        page_batch(t_lo);
+        fetch(t_lo, 0);
+        lds_barrier();                                // the last block's tiles have been read
+        int at = 0;
+        for (int tile = t_lo; tile < t_hi; ++tile) {
+          auto& B = s.buf[(tile - t_lo) & 1];
+          {
+            const int key = 16 * wave + (lane >> 2);
+            *reinterpret_cast<C*>(B.k + key * (D / 2) + ((lane & 3) ^ ((lane >> 4) & 3)) * (D / 8)) = kr;
+            *reinterpret_cast<C*>(B.v + key * (D / 2) + ((lane & 3) ^ wave) * (D / 8)) = vr;
+            if (lane < 16) B.ks[16 * wave + lane] = scale;
+            else if (lane < 32) {
+              const float v = scale < 0x1p-64f ? 0x1p-64f : scale;
+              B.lv[16 * wave + lane - 16] = __builtin_amdgcn_logf(v);
+              B.iv[16 * wave + lane - 16] = 1.0f / v;
+            }
+            if (lane == 0) B.held[wave] = held;
+          }
+          lds_barrier();
+          if (tile + 1 < t_hi) {
+            if (++at == 64) { page_batch(tile + 1); at = 0; }
+            fetch(tile + 1, at);
+          }
+          const int t0 = tile * kTile;
+          if (t0 >= any.hi || t0 + kTile <= any.lo) continue;
+          f32x4 sc[NB][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const C kc = *reinterpret_cast<const C*>(B.k + (16 * i + (lane & 15)) * (D / 2) + ((lane >> 4) ^ ((lane >> 2) & 3)) * (D / 8));
+#pragma unroll
+            for (int n = 0; n < NB; ++n) sc[n][i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+              const f16x8 kf = e2m1_f16x8(kc[k]);
+#pragma unroll
+              for (int n = 0; n < NB; ++n)
+                sc[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[n][k], sc[n][i], 0, 0, 0);
+            }
+          }
+          const int held4 = B.held[0] | B.held[1] << 1 | B.held[2] << 2 | B.held[3] << 3;
+          const bool whole = held4 == 15 && t0 >= every.lo && t0 + kTile <= every.hi;
+          f32x4 iv[4];
+          f16x8 w[NB][2];
+          float mx[NB];
+#pragma unroll
+          for (int n = 0; n < NB; ++n) mx[n] = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f32x4 ks = *reinterpret_cast<const f32x4*>(&B.ks[16 * i + 4 * (lane >> 4)]);
+            const f32x4 lv = *reinterpret_cast<const f32x4*>(&B.lv[16 * i + 4 * (lane >> 4)]);
+            iv[i] = *reinterpret_cast<const f32x4*>(&B.iv[16 * i + 4 * (lane >> 4)]);
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float x = __builtin_fmaf(sc[n][i][j] * ks[j], rs[n], lv[j]);
+                sc[n][i][j] = x;
+              }
+          }
+          if (!whole) {
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int t = t0 + 16 * i + 4 * (lane >> 4) + j;
+                  if (!(t >= lo[n] && t < hi[n] && ((held4 >> i) & 1))) sc[n][i][j] = -INFINITY;
+                }
+          }
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) mx[n] = fmaxf(mx[n], sc[n][i][j]);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) {
+            if (__any(mx[n] > M[n] + kSlack)) {
+              const float m = fmaxf(M[n], row_max(mx[n]));
+              const float keep = __builtin_amdgcn_exp2f(M[n] - safe_max(m));
+              l[n] *= keep;
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) o[n][c] *= keep;
+              M[n] = m;
+            }
+            const float ref = safe_max(M[n]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float x = sc[n][i][j];
+                const float p = __builtin_amdgcn_exp2f(x - ref);
+                // a masked key's 1 / vs may be NaN
+                l[n] = whole || x != -INFINITY ? __builtin_fmaf(p, iv[i][j], l[n]) : l[n];
+                w[n][i >> 1][4 * (i & 1) + j] = (_Float16)p;
+              }
+          }
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            const int r = lane & 15, key = 16 * (r >> 2) + 4 * (lane >> 4) + (r & 3);
+            const int chunk = c * 8 / (D / 8), in = c * 8 % (D / 8);
+            const uint8_t* src = B.v + key * (D / 2) + (chunk ^ (r >> 2)) * (D / 8) + in;
+            const i32x2 x = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2*)src);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const f16x8 vf = e2m1_f16x8((uint32_t)x[k]);
+#pragma unroll
+              for (int n = 0; n < NB; ++n) o[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, w[n][k], o[n][c], 0, 0, 0);
+            }
+          }
+        }
+
+        // ---- the rows, each in its wave
+        const bool starts = u0 == 0, ends = u1 == units;
+        const int64_t part = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          const int rr = 16 * n + (lane & 15);
+          const float sum = row_add(l[n]);
+          if (starts && ends) {
+            if (a.rotate & 2) transform_tile<D>(o[n], lane);
+            const float f = sum != 0.0f ? sp.c_v / sum : 0.0f;
+            if (rr < w_rows) {
+              const int r = w0 + rr, i = r / G, h = r - i * G;
+              uint16_t* dst = g.out + (q.t0 + i) * g.ldo + ((int64_t)kvh * G + h) * D + 4 * (lane >> 4);
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) {
+                u32x2 x;
+                x[0] = (uint32_t)f32_to_bf16_rne(o[n][c][0] * f) | ((uint32_t)f32_to_bf16_rne(o[n][c][1] * f) << 16);
+                x[1] = (uint32_t)f32_to_bf16_rne(o[n][c][2] * f) | ((uint32_t)f32_to_bf16_rne(o[n][c][3] * f) << 16);
+                *reinterpret_cast<u32x2*>(dst + 16 * c) = x;
+              }
+            }
+          } else if (rr < w_rows) {
+            const int64_t at_row = part * ROWS + 16 * NB * wave + rr;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) *reinterpret_cast<f32x4*>(sp.o + at_row * D + 16 * c + 4 * (lane >> 4)) = o[n][c];
+            if (lane < 16) sp.ml[at_row] = float2{M[n], sum};
+          }
+        }
+        if (starts && !ends && tid == 0)
+          sp.desc[blockIdx.x] = Desc{b, kvh, r0, (int)((units - u1 + per - 1) / per)};
+      }
+    }
+  }
+}
+
+// Joins the parts of a row block that starts in group blockIdx.x and goes on in the next ones.  RB rows a workgroup, from
+// RB * blockIdx.y on, and a row's parts dealt out to NG groups of D/8 lanes.
+template <int D, int ROWS, int RB>
 __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs g, SplitArgs sp) {
-  constexpr int L = D / 8, NG = 256 / L;
-  const int w = blockIdx.x, row = blockIdx.y, tid = threadIdx.x, sub = tid % L, grp = tid / L;
+  constexpr int L = D / 8, NG = 256 / L / RB;
+  const int tid = threadIdx.x, sub = tid % L, grp = tid / L % NG, rb = tid / L / NG;
+  const int w = blockIdx.x, row = blockIdx.y * RB + rb;
   const Desc d = sp.desc[w];
   if (d.more == 0) return;
   const int G = g.n_q / g.kv.n_kv;
   const Seq q = kv_seq(g.kv, d.b, G);
-  if (d.r0 + row >= q.rows) return;
-  __shared__ float so[NG][D], sm[NG], sl[NG];
+  const bool mine = d.r0 + row < q.rows;
+  if (RB == 1 && !mine) return;
+  __shared__ float so[RB][NG][D], sm[RB][NG], sl[RB][NG];
   // part 0 is the block's start (second slot of w), part p the first slot of w + p
   float m = -INFINITY, sum = 0, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int p = grp; p <= d.more; p += NG) {
+  for (int p = grp; mine && p <= d.more; p += NG) {
     const int64_t part = (p == 0 ? 2 * (int64_t)w + 1 : 2 * (int64_t)(w + p)) * ROWS + row;
     const float2 ml = sp.ml[part];
     const f32x4 x0 = *reinterpret_cast<const f32x4*>(sp.o + part * D + 8 * sub);
@@ -541,37 +847,52 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs g, SplitArgs sp
     }
     m = mn;
   }
+  if constexpr (NG > 1) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) so[grp][8 * sub + j] = v[j];
-  if (sub == 0) { sm[grp] = m; sl[grp] = sum; }
-  __syncthreads();
-  if (grp != 0) return;
-  const int n = d.more + 1 < NG ? d.more + 1 : NG;
-  m = sm[0];
-  for (int p = 1; p < n; ++p) m = fmaxf(m, sm[p]);
-  const float ref = safe_max(m);
-  sum = 0;
+    for (int j = 0; j < 8; ++j) so[rb][grp][8 * sub + j] = v[j];
+    if (sub == 0) { sm[rb][grp] = m; sl[rb][grp] = sum; }
+    __syncthreads();
+    if (grp != 0) return;
+    const int n = d.more + 1 < NG ? d.more + 1 : NG;
+    for (int p = 1; p < n; ++p) m = fmaxf(m, sm[rb][p]);
+    const float ref = safe_max(m);
+    sum = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = 0;
-  for (int p = 0; p < n; ++p) {
-    const float f = __builtin_amdgcn_exp2f(sm[p] - ref);
-    sum = __builtin_fmaf(sl[p], f, sum);
+    for (int j = 0; j < 8; ++j) v[j] = 0;
+    for (int p = 0; p < n; ++p) {
+      const float f = __builtin_amdgcn_exp2f(sm[rb][p] - ref);
+      sum = __builtin_fmaf(sl[rb][p], f, sum);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf(so[p][8 * sub + j], f, v[j]);
+      for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf(so[rb][p][8 * sub + j], f, v[j]);
+    }
   }
+  if (!mine) return;                                  // whole groups of lanes
   const int r = d.r0 + row, i = r / G, h = r - i * G;
   finish_row<D>(v, sum, g.kv.rotate & 2, sp.c_v, sub, g.out + (q.t0 + i) * g.ldo + ((int64_t)d.kvh * G + h) * D + 8 * sub);
 }
 
-// Query rows of a row block: those of a sequence on average, up to 32.
-int row_block(int64_t T, int B, int G) { return (T + B - 1) / B * G <= 16 ? 16 : 32; }
+// Query rows of a row block: 16 or 32, all in every wave, for at most 32 rows a sequence on average;
+// else 128, each wave its own 32.
+int row_block(int64_t T, int B, int G) {
+  const int64_t rows = (T + B - 1) / B * G;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
+}
 
 template <int D, int NB, int WV>
-hipError_t launch_form(const KvAttnArgs& g, SplitArgs sp, hipStream_t stream) {
+hipError_t launch_decode(const KvAttnArgs& g, SplitArgs sp, hipStream_t stream) {
   kv_attention_kernel<D, NB, WV><<<sp.groups, 64 * WV, 0, stream>>>(g, sp);
   if (hipError_t e = hipGetLastError()) return e;
   if (!sp.split) return hipSuccess;
-  kv_join_kernel<D, 16 * NB><<<dim3(sp.groups, 16 * NB), 256, 0, stream>>>(g, sp);
+  kv_join_kernel<D, 16 * NB, 1><<<dim3(sp.groups, 16 * NB), 256, 0, stream>>>(g, sp);
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_prefill(const KvAttnArgs& g, SplitArgs sp, hipStream_t stream) {
+  kv_prefill_kernel<D, 2><<<sp.groups, 256, 0, stream>>>(g, sp);
+  if (hipError_t e = hipGetLastError()) return e;
+  if (!sp.split) return hipSuccess;
+  kv_join_kernel<D, 128, 8><<<dim3(sp.groups, 16), 256, 0, stream>>>(g, sp);
   return hipGetLastError();
 }
 
@@ -594,12 +915,19 @@ hipError_t launch_kv_attention(const KvAttnArgs& g, hipStream_t stream) {
   sp.o = reinterpret_cast<float*>(sp.ml + (size_t)2 * kMaxGroups * rows);
   const int64_t blocks = ((a.T * G + rows - 1) / rows + a.B) * a.n_kv;      // row blocks at most
   const int64_t cap = ((int64_t)a.max_pages << a.logp) / kTile + 1;         // key tiles of one at most
+  if (rows == 128) {
+    sp.split = blocks < 3 * kMaxGroups && cap > 16;
+    sp.min_units = sp.split ? 4 : 1;
+    const int64_t want = sp.split ? blocks * ((cap + 3) / 4) : blocks;
+    sp.groups = (int)(sp.split && want > kMaxGroups ? kMaxGroups : want < (1 << 22) ? want : 1 << 22);
+    return a.D == 64 ? launch_prefill<64>(g, sp, stream) : launch_prefill<128>(g, sp, stream);
+  }
   sp.split = cap > 32;
   sp.min_units = sp.split ? 4 : 1;
   const int64_t want = sp.split ? blocks * ((cap + 3) / 4) : blocks;
   sp.groups = (int)(want < kMaxGroups ? want : kMaxGroups);
-  if (a.D == 64) return rows == 16 ? launch_form<64, 1, 4>(g, sp, stream) : launch_form<64, 2, 4>(g, sp, stream);
-  return rows == 16 ? launch_form<128, 1, 4>(g, sp, stream) : launch_form<128, 2, 4>(g, sp, stream);
+  if (a.D == 64) return rows == 16 ? launch_decode<64, 1, 4>(g, sp, stream) : launch_decode<64, 2, 4>(g, sp, stream);
+  return rows == 16 ? launch_decode<128, 1, 4>(g, sp, stream) : launch_decode<128, 2, 4>(g, sp, stream);
 }
 
 }  // namespace cbq
