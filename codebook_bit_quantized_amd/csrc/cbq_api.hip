@@ -85,6 +85,7 @@ int check_kv(const cbq_kv_cache* c, const cbq_kv_seqs* q, int64_t T, cbq::KvArgs
   if (T > 0x7FFFFFFF) return fail(CBQ_EUNSUPPORTED, "T must be < 2^31");
   if (c->n_pages < 1) return fail(CBQ_EINVAL, "n_pages must be >= 1 (got %d)", c->n_pages);
   if (c->n_kv < 1) return fail(CBQ_EINVAL, "n_kv must be >= 1 (got %d)", c->n_kv);
+  if ((int64_t)c->n_pages * c->n_kv > 0x7FFFFFFF) return fail(CBQ_EUNSUPPORTED, "n_pages * n_kv must be < 2^31");
   if (c->n_kv > 1024) return fail(CBQ_EUNSUPPORTED, "n_kv must be <= 1024 (got %d)", c->n_kv);
   if (!pow2(c->page) || c->page < 16 || c->page > 1024)
     return fail(CBQ_EINVAL, "page must be a power of two in [16, 1024] (got %d)", c->page);
@@ -650,6 +651,7 @@ CBQ_EXPORT int cbq_kv_attention(const cbq_kv_cache* cache, const cbq_kv_seqs* se
   if (n_q < 1 || n_q % cache->n_kv)
     return fail(CBQ_EINVAL, "n_q must be a positive multiple of n_kv = %d (got %d)", cache->n_kv, n_q);
   if (n_q > 1024) return fail(CBQ_EUNSUPPORTED, "n_q must be <= 1024 (got %d)", n_q);
+  if (T * n_q > 0x7FFFFFFF) return fail(CBQ_EUNSUPPORTED, "T * n_q must be < 2^31");
   if (!std::isfinite(scale)) return fail(CBQ_EINVAL, "scale must be finite");
   if (causal != 0 && causal != 1) return fail(CBQ_EINVAL, "causal must be 0 or 1");
   if (window < 0) return fail(CBQ_EINVAL, "window must be >= 0 (got %d)", window);

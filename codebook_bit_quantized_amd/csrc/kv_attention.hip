@@ -25,46 +25,12 @@ constexpr int kMaxGroups = 512;    // workgroups of a split call: two a CU
 
 // A sequence's part of the step, all values uniform over the workgroup.
 struct Seq {
-  int64_t t0;                      // its first token
-  int rows;                        // tokens * G
-  int64_t pos0;                    // position of the first token
+  int t0, rows;                    // its first token; tokens * G
+  int pos0;                        // position of the first token
   int len;                         // positions that can hold anything
 };
 
-__device__ __forceinline__ Seq kv_seq(const KvArgs& a, int b, int G) {
-  int64_t o0, o1;
-  if (a.offsets) { o0 = a.offsets[b]; o1 = a.offsets[b + 1]; }
-  else { o0 = (int64_t)b * a.per_seq; o1 = o0 + a.per_seq; }
-  const int64_t s = o0 < 0 ? 0 : o0, e = o1 < a.T ? o1 : a.T;
-  const int64_t len = a.lens[b], cap = (int64_t)a.max_pages << a.logp;
-  Seq q;
-  q.t0 = s;
-  const int64_t r = e > s ? (e - s) * G : 0;
-  q.rows = (int)(r < 0x7FFF0000 ? r : 0x7FFF0000);
-  q.pos0 = len - o1 + s;
-  q.len = (int)(len < 0 ? 0 : len < cap ? len : cap);
-  return q;
-}
-
 struct Range { int lo, hi; };      // [lo, hi)
-
-// Positions that token i of the sequence attends.
-__device__ __forceinline__ Range kv_range(const Seq& q, int i, int causal, int window) {
-  const int64_t pos = q.pos0 + i;
-  Range r{0, q.len};
-  if (causal) {
-    r.hi = (int)(pos + 1 < 0 ? 0 : pos + 1 < q.len ? pos + 1 : q.len);
-    if (window && pos - window + 1 > 0) r.lo = (int)(pos - window + 1 < 0x3FFFFFFF ? pos - window + 1 : 0x3FFFFFFF);
-  }
-  return r;
-}
-
-// Key tiles [lo, hi) of query rows r0 .. r1 (at least one tile: a row that attends nothing is written too).
-__device__ __forceinline__ Range kv_tiles(const Seq& q, int r0, int r1, int G, int causal, int window) {
-  const int lo = kv_range(q, r0 / G, causal, window).lo / kTile;
-  const int hi = (kv_range(q, r1 / G, causal, window).hi + kTile - 1) / kTile;
-  return Range{lo, hi > lo ? hi : lo + 1};
-}
 
 // What the workgroups of a split call leave for the join: a row block that starts in group w and goes on in the next `more`.
 struct Desc { int b, kvh, r0, more; };
@@ -72,95 +38,165 @@ struct Desc { int b, kvh, r0, more; };
 struct SplitArgs {
   int groups;                      // workgroups
   int split;                       // 1: units are key tiles; 0: whole row blocks
+  int shift;                       // split: a unit is 2^shift key tiles, so that all units fit 31 bits
+  int start_cost;                  // split: units that the start of a row block counts for
   int min_units;                   // units a workgroup takes at least
+  int G;                           // query heads a key/value head
+  uint32_t g_mul, g_shift;         // r / G = r * g_mul >> g_shift for r < 2^31
+  int join_rows;                   // rows of a row block that any has
   float c_q, c_v;                  // 1/sqrt(D) where queries are rotated / values rotated back, else 1
   Desc* desc;                      // [groups]
   float2* ml;                      // [2 * groups][ROWS]: M and sum of each part's rows
   float* o;                        // [2 * groups][ROWS][D]
 };
 
+__device__ __forceinline__ int div_g(const SplitArgs& sp, int r) {
+  return (int)(((uint64_t)(uint32_t)r * sp.g_mul) >> sp.g_shift);
+}
+
+__device__ __forceinline__ Seq kv_seq(const KvArgs& a, int b, int G) {
+  const int T = (int)a.T, cap = a.max_pages << a.logp, len = a.lens[b];
+  int o0, o1;
+  if (a.offsets) { o0 = a.offsets[b]; o1 = a.offsets[b + 1]; }
+  else { o0 = b * a.per_seq; o1 = o0 + a.per_seq; }
+  const int s = max(o0, 0), e = min(o1, T);
+  Seq q;
+  q.t0 = s;
+  q.rows = e > s ? (e - s) * G : 0;                   // T * n_q < 2^31
+  const int64_t pos0 = (int64_t)len - o1 + s;         // pos0 + i < len for its tokens i: no sum below leaves 32 bits
+  q.pos0 = (int)max(pos0, (int64_t)-0x80000000LL);
+  q.len = min(max(len, 0), cap);
+  return q;
+}
+
+// Positions that token i of the sequence attends.
+__device__ __forceinline__ Range kv_range(const Seq& q, int i, int causal, int window) {
+  const int pos = q.pos0 + i;
+  Range r{0, q.len};
+  if (causal) {
+    r.hi = min(max(pos + 1, 0), q.len);
+    if (window && pos >= window) r.lo = pos - window + 1;
+  }
+  return r;
+}
+
+// Key tiles [lo, hi) of query rows r0 .. r1 (at least one tile: a row that attends nothing is written too).
+__device__ __forceinline__ Range kv_tiles(const KvAttnArgs& g, const SplitArgs& sp, const Seq& q, int r0, int r1) {
+  const int lo = kv_range(q, div_g(sp, r0), g.causal, g.window).lo / kTile;
+  const int hi = (int)(((uint32_t)kv_range(q, div_g(sp, r1), g.causal, g.window).hi + kTile - 1) / kTile);
+  return Range{lo, max(hi, lo + 1)};
+}
+
+__device__ __forceinline__ int block_units(const SplitArgs& sp, Range t) {
+  return sp.split ? ((t.hi - t.lo - 1) >> sp.shift) + 1 + sp.start_cost : 1;
+}
+
 // Units of one key/value head of a sequence: its row blocks' key tiles, or its row blocks.
 template <int ROWS>
-__device__ __forceinline__ int64_t head_units(const KvAttnArgs& g, const SplitArgs& sp, const Seq& q, int G) {
-  if (!sp.split) return (q.rows + ROWS - 1) / ROWS;
-  int64_t n = 0;
-  for (int r0 = 0; r0 < q.rows; r0 += ROWS) {
-    const Range t = kv_tiles(q, r0, min(r0 + ROWS, q.rows) - 1, G, g.causal, g.window);
-    n += t.hi - t.lo;
-  }
+__device__ __forceinline__ int head_units(const KvAttnArgs& g, const SplitArgs& sp, const Seq& q) {
+  if (!sp.split) return (int)((uint32_t)(q.rows + ROWS - 1) / ROWS);
+  int n = 0;
+  for (int r0 = 0; r0 < q.rows; r0 += ROWS) n += block_units(sp, kv_tiles(g, sp, q, r0, min(r0 + ROWS, q.rows) - 1));
   return n;
 }
 
-// A workgroup's units: `left` of them from unit `off` of sequence b on.  All sequences' units in a row (a
+// The row blocks, or parts of them, that a workgroup works through.  All sequences' units in a row (a
 // sequence's in the order head, row block, key tile) are dealt out evenly, `per` to a workgroup; each
-// workgroup counts them for itself, from the lengths.
+// wave counts them for itself, from the lengths, so the lengths stay on the device and the work is even
+// whatever they are.
+template <int ROWS>
 struct Walk {
-  int b;
-  int64_t off, left, per;
-};
+  Seq q;
+  int b, kvh, r0, off, left, per;  // r0: the next row block, off: units of it that are not this workgroup's
+  // whether and for how many groups the current part goes on: only the last part of a group does
+  __device__ __forceinline__ int following(const SplitArgs& sp) const {
+    const uint32_t n = ((uint32_t)(units - u1) + per - 1) / (uint32_t)per;
+    return (int)min(n, (uint32_t)sp.groups - 1 - blockIdx.x);
+  }
+  // the current part: units [u0, u1) of `units` of row block `row0` of head `h` of sequence `seq`
+  int seq, h, row0, u0, u1, units;
+  Range tiles;                     // its key tiles
 
-template <int ROWS, int WV>
-__device__ __forceinline__ Walk walk_start(const KvAttnArgs& g, const SplitArgs& sp, int G, int64_t* scan,
-                                           int64_t* start_off, int* start_b) {
-  constexpr int NT = 64 * WV;
-  const KvArgs& a = g.kv;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  auto block_scan = [&](int64_t x, int64_t& total) {   // exclusive prefix over the workgroup
-    int64_t inc = x;
+  __device__ __forceinline__ void start(const KvAttnArgs& g, const SplitArgs& sp) {
+    const KvArgs& a = g.kv;
+    const int lane = threadIdx.x & 63;
+    const int each = (a.B + 63) >> 6;                 // sequences a lane counts
+    int mine = 0;
+    for (int k = 0; k < each; ++k) {
+      const int s = lane * each + k;
+      if (s < a.B) mine += head_units<ROWS>(g, sp, kv_seq(a, s, sp.G)) * a.n_kv;
+    }
+    int inc = mine;
+    if (a.B > 1) {
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int64_t y = __shfl_up(inc, d);
-      if (lane >= d) inc += y;
+      for (int d = 1; d < 64; d *= 2) {
+        const int y = __shfl_up(inc, d);
+        if (lane >= d) inc += y;
+      }
     }
-    __syncthreads();
-    if (lane == 63) scan[wave] = inc;
-    __syncthreads();
-    int64_t before = 0;
-    total = 0;
-    for (int w = 0; w < WV; ++w) {
-      if (w < wave) before += scan[w];
-      total += scan[w];
+    const int total = __builtin_amdgcn_readlane(inc, a.B > 1 ? 63 : 0);
+    per = max((int)(((uint32_t)total + sp.groups - 1) / (uint32_t)sp.groups), sp.min_units);
+    // unsplit calls start with the last units: a sequence's last rows attend the most keys
+    const int64_t at = sp.split ? (int64_t)blockIdx.x : (int64_t)sp.groups - 1 - blockIdx.x;
+    left = 0;
+    b = a.B;
+    if (at * per >= total) return;
+    const int first = (int)at * per;
+    left = min(total - first, per);
+    const uint64_t past = __ballot(first < inc);
+    const int f = past ? (int)__builtin_ctzll(past) : 63;
+    b = f * each;
+    off = first - (__builtin_amdgcn_readlane(inc, f) - __builtin_amdgcn_readlane(mine, f));
+    kvh = 0;
+    r0 = 0;
+    for (;; ++b) {                                    // at most `each` times
+      if (b >= a.B) { left = 0; return; }             // offsets that do not ascend
+      q = kv_seq(a, b, sp.G);
+      const int hu = head_units<ROWS>(g, sp, q);
+      if (off < hu * a.n_kv) {
+        kvh = off / hu;
+        off -= kvh * hu;
+        break;
+      }
+      off -= hu * a.n_kv;
     }
-    return before + inc - x;
-  };
-  int64_t total = 0, mine = 0, prefix = 0;
-  for (int b0 = 0; b0 < a.B; b0 += NT) {
-    const int b = b0 + tid;
-    mine = b < a.B ? head_units<ROWS>(g, sp, kv_seq(a, b, G), G) * a.n_kv : 0;
-    int64_t part;
-    prefix = block_scan(mine, part);
-    total += part;
+    if (!sp.split) { r0 = off * ROWS; off = 0; }
   }
-  Walk u{0, 0, 0, 0};
-  u.per = (total + sp.groups - 1) / sp.groups;
-  u.per = u.per > sp.min_units ? u.per : sp.min_units;
-  // unsplit calls start with the last units: a sequence's last rows attend the most keys
-  const int64_t at = sp.split ? (int64_t)blockIdx.x : (int64_t)sp.groups - 1 - blockIdx.x;
-  const int64_t first = at * u.per;
-  if (tid == 0 && sp.split) sp.desc[blockIdx.x].more = 0;
-  if (first >= total) return u;
-  u.left = total - first < u.per ? total - first : u.per;
-  int64_t base = 0;
-  for (int b0 = 0;; b0 += NT) {
-    if (a.B > NT) {
-      const int b = b0 + tid;
-      mine = b < a.B ? head_units<ROWS>(g, sp, kv_seq(a, b, G), G) * a.n_kv : 0;
-      int64_t part;
-      prefix = block_scan(mine, part) + base;
-      base += part;
+
+  __device__ __forceinline__ bool next(const KvAttnArgs& g, const SplitArgs& sp) {
+    if (left <= 0) return false;
+    for (;;) {
+      if (r0 >= q.rows) {
+        r0 = 0;
+        if (++kvh >= g.kv.n_kv) {
+          kvh = 0;
+          do {
+            if (++b >= g.kv.B) return false;
+            q = kv_seq(g.kv, b, sp.G);
+          } while (q.rows == 0);
+        }
+      }
+      tiles = kv_tiles(g, sp, q, r0, min(r0 + ROWS, q.rows) - 1);
+      units = block_units(sp, tiles);
+      row0 = r0;
+      r0 += ROWS;
+      if (off < units) break;
+      off -= units;
     }
-    if (prefix <= first && first < prefix + mine) {
-      *start_b = b0 + tid;
-      *start_off = first - prefix;
+    seq = b;
+    h = kvh;
+    u0 = off;
+    u1 = min(units, off + left);
+    left -= u1 - u0;
+    off = 0;
+    if (sp.split) {                                   // the units that count for the start hold no keys
+      const int lo = tiles.lo + (max(u0 - sp.start_cost, 0) << sp.shift);
+      tiles.hi = min(tiles.hi, tiles.lo + (max(u1 - sp.start_cost, 0) << sp.shift));
+      tiles.lo = lo;
     }
-    if (a.B <= NT || base > first) break;
+    return true;
   }
-  __syncthreads();
-  u.b = __builtin_amdgcn_readfirstlane(*start_b);
-  u.off = ((int64_t)__builtin_amdgcn_readfirstlane((int)(*start_off >> 32)) << 32) |
-          (uint32_t)__builtin_amdgcn_readfirstlane((int)*start_off);
-  return u;
-}
+};
 
 template <int D, int NB, int WV>
 struct Lds {
@@ -173,9 +209,6 @@ struct Lds {
     float o[WV][ROWS * P];
   };
   float m[WV][ROWS], l[WV][ROWS];
-  int64_t scan[WV];
-  int64_t start_off;
-  int start_b;
 };
 
 // x of the lanes 16 (32) apart: a of the even row (lower half), b of the odd row (upper half), in
@@ -314,13 +347,13 @@ __device__ __forceinline__ void load_tile(const KvArgs& a, int kvh, int tile, in
     pg[i] = __builtin_amdgcn_readlane(pages, 4 * at + i);
     held |= pg[i] >= 0 ? 1u << i : 0;
     pg[i] = pg[i] >= 0 ? pg[i] : 0;                   // keys in no page: any page is read, and masked
-    const int64_t row = ((((int64_t)pg[i] * a.n_kv + kvh) << a.logp) + ((tile * kTile + 16 * i) & mask)) * (D / 2);
+    const int64_t row = (((int64_t)(pg[i] * a.n_kv + kvh) << a.logp) + ((tile * kTile + 16 * i) & mask)) * (D / 2);
     r.k[i] = *reinterpret_cast<const C*>(a.codes[0] + row + (lane & 15) * (D / 2) + (lane >> 4) * (D / 8));
     r.v[i] = *reinterpret_cast<const C*>(a.codes[1] + row + (lane >> 2) * (D / 2) + (lane & 3) * (D / 8));
   }
   const int g = lane >> 4;
   const int p = g & 2 ? (g & 1 ? pg[3] : pg[2]) : (g & 1 ? pg[1] : pg[0]);
-  const int64_t row = (((int64_t)p * a.n_kv + kvh) << a.logp) + ((tile * kTile + lane) & mask);
+  const int64_t row = ((int64_t)(p * a.n_kv + kvh) << a.logp) + ((tile * kTile + lane) & mask);
   r.ks = a.scales[0][row];
   r.vs = a.scales[1][row];
   r.held = held;
@@ -328,214 +361,205 @@ __device__ __forceinline__ void load_tile(const KvArgs& a, int kvh, int tile, in
 
 template <int D, int NB, int WV>
 __global__ __launch_bounds__(64 * WV) void kv_attention_kernel(KvAttnArgs g, SplitArgs sp) {
-  constexpr int ROWS = 16 * NB, NT = 64 * WV, P = Lds<D, NB, WV>::P;
+  constexpr int ROWS = 16 * NB, NT = 64 * WV, P = Lds<D, NB, WV>::P, L = D / 8;
   __shared__ Lds<D, NB, WV> s;
   const KvArgs& a = g.kv;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int G = g.n_q / a.n_kv;
-
-  Walk u = walk_start<ROWS, WV>(g, sp, G, s.scan, &s.start_off, &s.start_b);
-  if (u.left <= 0) return;
-  int b = u.b;
-  int64_t off = u.off, left = u.left;
-  const int64_t per = u.per;
+  if (tid == 0 && sp.split) sp.desc[blockIdx.x].more = 0;
+  Walk<ROWS> u;
+  u.start(g, sp);
   const float c_scale = g.scale * sp.c_q * 1.44269504088896341f;
-  for (; left > 0 && b < a.B; ++b, off = 0) {
-    const Seq q = kv_seq(a, b, G);
-    if (q.rows == 0) continue;
-    const int64_t hu = head_units<ROWS>(g, sp, q, G);
-    int kvh = (int)(off / hu);
-    off -= kvh * hu;
-    for (; left > 0 && kvh < a.n_kv; ++kvh, off = 0) {
-      int r0 = 0;
-      if (!sp.split) { r0 = (int)off * ROWS; off = 0; }
-      for (; left > 0 && r0 < q.rows; r0 += ROWS) {
-        const int n_rows = min(ROWS, q.rows - r0);
-        const Range all = kv_tiles(q, r0, r0 + n_rows - 1, G, g.causal, g.window);
-        const int units = sp.split ? all.hi - all.lo : 1;
-        if (off >= units) { off -= units; continue; }
-        const int u0 = (int)off;
-        const int u1 = (int)(units - u0 < left ? units : u0 + left);
-        left -= u1 - u0;
-        off = 0;
-        const int t_lo = sp.split ? all.lo + u0 : all.lo, t_hi = sp.split ? all.lo + u1 : all.hi;
 
-        // ---- the queries, and what each row attends
-        f16x8 qf[NB][D / 32];
-        float rs[NB], M[NB], l[NB];
-        int lo[NB], hi[NB];
-        f32x4 o[NB][D / 16];
+  Seq q;                                              // the part in hand
+  int row0 = 0, n_rows = 0, kvh = 0;
+  bool have = false, starts = false, ends = false;
+  float M[NB], l[NB];
+  f32x4 o[NB][D / 16];
+  for (;;) {
+    // ---- the next part: its first keys are on their way before the last part's sums are joined
+    const bool more = u.next(g, sp);
+    int tile = u.tiles.lo + wave, at = 0, pages = 0;
+    const bool mine = more && tile < u.tiles.hi;
+    TileRegs<D> nx;
+    if (mine) pages = tile_pages<WV>(a, u.seq, tile);
+    if (have) {
+      __syncthreads();
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          const int r = r0 + 16 * n + (lane & 15);
-          const bool row = 16 * n + (lane & 15) < n_rows;
-          const int i = row ? r / G : 0, h = row ? r - i * G : 0;
-          const uint16_t* src = g.q + (q.t0 + i) * g.ldq + ((int64_t)kvh * G + h) * D + (lane >> 4) * (D / 4);
-          load_queries<D>(row ? src : nullptr, a.rotate & 1, qf[n], &rs[n]);
-          rs[n] *= c_scale;
-          const Range w = kv_range(q, i, g.causal, g.window);
-          lo[n] = w.lo;
-          hi[n] = row ? w.hi : 0;
-          M[n] = -INFINITY;
-          l[n] = 0;
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) o[n][c] = f32x4{0, 0, 0, 0};
+      for (int n = 0; n < NB; ++n) {
+        const int row = 16 * n + (lane & 15);
+        const float lsum = row_add(l[n]);
+        if (lane < 16) {
+          s.m[wave][row] = M[n];
+          s.l[wave][row] = lsum;
         }
-        const int all_lo = kv_range(q, (r0 + n_rows - 1) / G, g.causal, g.window).lo;   // positions that every row attends
-        const int all_hi = kv_range(q, r0 / G, g.causal, g.window).hi;
-        __syncthreads();                              // the last block's sums have been read
-
-        // ---- the wave's tiles
-        int tile = t_lo + wave, at = 0;
-        TileRegs<D> nx;
-        int pages = 0;
-        if (tile < t_hi) {
-          pages = tile_pages<WV>(a, b, tile);
-          load_tile<D>(a, kvh, tile, pages, 0, nx);
-        }
-        for (; tile < t_hi; tile += WV) {
-          TileRegs<D> cu = nx;
-          uint8_t* vl = s.t.v[wave];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<typename Chunk<D>::T*>(vl + (16 * i + (lane >> 2)) * (D / 2) + ((lane & 3) ^ i) * (D / 8)) = cu.v[i];
-          {
-            const float v = cu.vs < 0x1p-64f ? 0x1p-64f : cu.vs;
-            s.t.ks[wave][lane] = cu.ks;
-            s.t.lv[wave][lane] = __builtin_amdgcn_logf(v);
-            s.t.iv[wave][lane] = 1.0f / v;
-          }
-          if (tile + WV < t_hi) {
-            if (++at == 16) { pages = tile_pages<WV>(a, b, tile + WV); at = 0; }
-            load_tile<D>(a, kvh, tile + WV, pages, at, nx);
-          }
-          // scores of 64 keys
-          f32x4 sc[NB][4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int n = 0; n < NB; ++n) sc[n][i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-              const f16x8 kf = e2m1_f16x8(cu.k[i][k]);
-#pragma unroll
-              for (int n = 0; n < NB; ++n)
-                sc[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[n][k], sc[n][i], 0, 0, 0);
-            }
-          }
-          __builtin_amdgcn_wave_barrier();
-          const bool whole = cu.held == 15u && tile * kTile >= all_lo && tile * kTile + kTile <= all_hi;
-          f32x4 iv[4];
-          f16x8 w[NB][2];
-          float mx[NB];
-#pragma unroll
-          for (int n = 0; n < NB; ++n) mx[n] = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const f32x4 ks = *reinterpret_cast<const f32x4*>(&s.t.ks[wave][16 * i + 4 * (lane >> 4)]);
-            const f32x4 lv = *reinterpret_cast<const f32x4*>(&s.t.lv[wave][16 * i + 4 * (lane >> 4)]);
-            iv[i] = *reinterpret_cast<const f32x4*>(&s.t.iv[wave][16 * i + 4 * (lane >> 4)]);
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                float x = __builtin_fmaf(sc[n][i][j] * ks[j], rs[n], lv[j]);
-                if (!whole) {
-                  const int t = tile * kTile + 16 * i + 4 * (lane >> 4) + j;
-                  x = t >= lo[n] && t < hi[n] && ((cu.held >> i) & 1) ? x : -INFINITY;
-                }
-                sc[n][i][j] = x;
-                mx[n] = fmaxf(mx[n], x);
-              }
-          }
-#pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            const float m = fmaxf(M[n], row_max(mx[n]));
-            if (__any(m > M[n])) {
-              const float keep = __builtin_amdgcn_exp2f(M[n] - safe_max(m));
-              l[n] *= keep;
-#pragma unroll
-              for (int c = 0; c < D / 16; ++c) o[n][c] *= keep;
-              M[n] = m;
-            }
-            const float ref = safe_max(M[n]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float x = sc[n][i][j];
-                const float p = __builtin_amdgcn_exp2f(x - ref);
-                // a masked key's 1 / vs may be NaN
-                l[n] = whole || x != -INFINITY ? __builtin_fmaf(p, iv[i][j], l[n]) : l[n];
-                w[n][i >> 1][4 * (i & 1) + j] = (_Float16)p;
-              }
-          }
-          // values times weights, 16 channels at a time
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            const int r = lane & 15, key = 16 * (r >> 2) + 4 * (lane >> 4) + (r & 3);
-            const int chunk = c * 8 / (D / 8), in = c * 8 % (D / 8);
-            const uint8_t* src = vl + key * (D / 2) + (chunk ^ (r >> 2)) * (D / 8) + in;
-            const i32x2 x = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2*)src);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const f16x8 vf = e2m1_f16x8((uint32_t)x[k]);
-#pragma unroll
-              for (int n = 0; n < NB; ++n) o[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, w[n][k], o[n][c], 0, 0, 0);
-            }
-          }
-          __builtin_amdgcn_wave_barrier();
-        }
-
-        // ---- the waves' sums, joined
-        __syncthreads();
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          const int row = 16 * n + (lane & 15);
-          const float lsum = row_add(l[n]);
-          if (lane < 16) {
-            s.m[wave][row] = M[n];
-            s.l[wave][row] = lsum;
-          }
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c)
-            *reinterpret_cast<f32x4*>(&s.o[wave][row * P + 16 * c + 4 * (lane >> 4)]) = o[n][c];
-        }
-        __syncthreads();
-        constexpr int L = D / 8;
-        const bool starts = u0 == 0, ends = u1 == units;
-        const int64_t part = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
-        const int sub = tid % L;
-        for (int row0 = 0; row0 < ROWS; row0 += NT / L) {
-          const int row = row0 + tid / L;
-          if (row >= n_rows) continue;                // whole groups of L lanes
-          float m = -INFINITY, sum = 0, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-          for (int w = 0; w < WV; ++w) m = fmaxf(m, s.m[w][row]);
-          const float ref = safe_max(m);
-          for (int w = 0; w < WV; ++w) {
-            const float f = __builtin_amdgcn_exp2f(s.m[w][row] - ref);
-            sum = __builtin_fmaf(s.l[w][row], f, sum);
-            const f32x4 x0 = *reinterpret_cast<const f32x4*>(&s.o[w][row * P + 8 * sub]);
-            const f32x4 x1 = *reinterpret_cast<const f32x4*>(&s.o[w][row * P + 8 * sub + 4]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              v[j] = __builtin_fmaf(x0[j], f, v[j]);
-              v[4 + j] = __builtin_fmaf(x1[j], f, v[4 + j]);
-            }
-          }
-          if (starts && ends) {
-            const int r = r0 + row, i = r / G, h = r - i * G;
-            finish_row<D>(v, sum, a.rotate & 2, sp.c_v, sub, g.out + (q.t0 + i) * g.ldo + ((int64_t)kvh * G + h) * D + 8 * sub);
-          } else {
-            float* dst = sp.o + (part * ROWS + row) * D + 8 * sub;
-            *reinterpret_cast<f32x4*>(dst) = f32x4{v[0], v[1], v[2], v[3]};
-            *reinterpret_cast<f32x4*>(dst + 4) = f32x4{v[4], v[5], v[6], v[7]};
-            if (sub == 0) sp.ml[part * ROWS + row] = float2{m, sum};
-          }
-        }
-        if (starts && !ends && tid == 0)
-          sp.desc[blockIdx.x] = Desc{b, kvh, r0, (int)((units - u1 + per - 1) / per)};
+        for (int c = 0; c < D / 16; ++c)
+          *reinterpret_cast<f32x4*>(&s.o[wave][row * P + 16 * c + 4 * (lane >> 4)]) = o[n][c];
       }
+      __syncthreads();
+    }
+    if (mine) load_tile<D>(a, u.h, tile, pages, 0, nx);
+    if (have) {
+      const int64_t part = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
+      const int sub = tid % L;
+      for (int b0 = 0; b0 < ROWS; b0 += NT / L) {
+        const int row = b0 + tid / L;
+        if (row >= n_rows) continue;                  // whole groups of L lanes
+        float m = -INFINITY, sum = 0, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < WV; ++w) m = fmaxf(m, s.m[w][row]);
+        const float ref = safe_max(m);
+#pragma unroll
+        for (int w = 0; w < WV; ++w) {
+          const float f = __builtin_amdgcn_exp2f(s.m[w][row] - ref);
+          sum = __builtin_fmaf(s.l[w][row], f, sum);
+          const f32x4 x0 = *reinterpret_cast<const f32x4*>(&s.o[w][row * P + 8 * sub]);
+          const f32x4 x1 = *reinterpret_cast<const f32x4*>(&s.o[w][row * P + 8 * sub + 4]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[j] = __builtin_fmaf(x0[j], f, v[j]);
+            v[4 + j] = __builtin_fmaf(x1[j], f, v[4 + j]);
+          }
+        }
+        if (starts && ends) {
+          const int r = row0 + row, i = div_g(sp, r), h = r - i * sp.G;
+          finish_row<D>(v, sum, a.rotate & 2, sp.c_v, sub, g.out + (int64_t)(q.t0 + i) * g.ldo + (kvh * sp.G + h) * D + 8 * sub);
+        } else {
+          float* dst = sp.o + (part * ROWS + row) * D + 8 * sub;
+          *reinterpret_cast<f32x4*>(dst) = f32x4{v[0], v[1], v[2], v[3]};
+          *reinterpret_cast<f32x4*>(dst + 4) = f32x4{v[4], v[5], v[6], v[7]};
+          if (sub == 0) sp.ml[part * ROWS + row] = float2{m, sum};
+        }
+      }
+    }
+    if (!more) return;
+    q = u.q;
+    row0 = u.row0;
+    kvh = u.h;
+    n_rows = min(ROWS, q.rows - row0);
+    starts = u.u0 == 0;
+    ends = u.u1 == u.units;
+    have = true;
+    if (starts && !ends && tid == 0)
+      sp.desc[blockIdx.x] = Desc{u.seq, kvh, row0, u.following(sp)};
+
+    // ---- the queries, and what each row attends
+    f16x8 qf[NB][D / 32];
+    float rs[NB];
+    int lo[NB], hi[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const bool row = 16 * n + (lane & 15) < n_rows;
+      const int r = row ? row0 + 16 * n + (lane & 15) : row0, i = div_g(sp, r), h = r - i * sp.G;
+      const uint16_t* src = g.q + (int64_t)(q.t0 + i) * g.ldq + (kvh * sp.G + h) * D + (lane >> 4) * (D / 4);
+      load_queries<D>(row ? src : nullptr, a.rotate & 1, qf[n], &rs[n]);
+      rs[n] *= c_scale;
+      const Range w = kv_range(q, i, g.causal, g.window);
+      lo[n] = w.lo;
+      hi[n] = row ? w.hi : 0;
+      M[n] = -INFINITY;
+      l[n] = 0;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) o[n][c] = f32x4{0, 0, 0, 0};
+    }
+    const int all_lo = kv_range(q, div_g(sp, row0 + n_rows - 1), g.causal, g.window).lo;   // positions that every row attends
+    const int all_hi = kv_range(q, div_g(sp, row0), g.causal, g.window).hi;
+    const int t_hi = u.tiles.hi;
+    __syncthreads();                                  // the last part's sums have been read
+
+    // ---- the wave's tiles
+    for (; tile < t_hi; tile += WV) {
+      TileRegs<D> cu = nx;
+      uint8_t* vl = s.t.v[wave];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<typename Chunk<D>::T*>(vl + (16 * i + (lane >> 2)) * (D / 2) + ((lane & 3) ^ i) * (D / 8)) = cu.v[i];
+      {
+        const float v = cu.vs < 0x1p-64f ? 0x1p-64f : cu.vs;
+        s.t.ks[wave][lane] = cu.ks;
+        s.t.lv[wave][lane] = __builtin_amdgcn_logf(v);
+        s.t.iv[wave][lane] = 1.0f / v;
+      }
+      if (tile + WV < t_hi) {
+        if (++at == 16) { pages = tile_pages<WV>(a, u.seq, tile + WV); at = 0; }
+        load_tile<D>(a, kvh, tile + WV, pages, at, nx);
+      }
+      // scores of 64 keys
+      f32x4 sc[NB][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) sc[n][i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          const f16x8 kf = e2m1_f16x8(cu.k[i][k]);
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+            sc[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[n][k], sc[n][i], 0, 0, 0);
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+      const bool whole = cu.held == 15u && tile * kTile >= all_lo && tile * kTile + kTile <= all_hi;
+      f32x4 iv[4];
+      f16x8 w[NB][2];
+      float mx[NB];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) mx[n] = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x4 ks = *reinterpret_cast<const f32x4*>(&s.t.ks[wave][16 * i + 4 * (lane >> 4)]);
+        const f32x4 lv = *reinterpret_cast<const f32x4*>(&s.t.lv[wave][16 * i + 4 * (lane >> 4)]);
+        iv[i] = *reinterpret_cast<const f32x4*>(&s.t.iv[wave][16 * i + 4 * (lane >> 4)]);
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float x = __builtin_fmaf(sc[n][i][j] * ks[j], rs[n], lv[j]);
+            if (!whole) {
+              const int t = tile * kTile + 16 * i + 4 * (lane >> 4) + j;
+              x = t >= lo[n] && t < hi[n] && ((cu.held >> i) & 1) ? x : -INFINITY;
+            }
+            sc[n][i][j] = x;
+            mx[n] = fmaxf(mx[n], x);
+          }
+      }
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const float m = fmaxf(M[n], row_max(mx[n]));
+        if (__any(m > M[n])) {
+          const float keep = __builtin_amdgcn_exp2f(M[n] - safe_max(m));
+          l[n] *= keep;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) o[n][c] *= keep;
+          M[n] = m;
+        }
+        const float ref = safe_max(M[n]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float x = sc[n][i][j];
+            const float p = __builtin_amdgcn_exp2f(x - ref);
+            // a masked key's 1 / vs may be NaN
+            l[n] = whole || x != -INFINITY ? __builtin_fmaf(p, iv[i][j], l[n]) : l[n];
+            w[n][i >> 1][4 * (i & 1) + j] = (_Float16)p;
+          }
+      }
+      // values times weights, 16 channels at a time
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const int r = lane & 15, key = 16 * (r >> 2) + 4 * (lane >> 4) + (r & 3);
+        const int chunk = c * 8 / (D / 8), in = c * 8 % (D / 8);
+        const uint8_t* src = vl + key * (D / 2) + (chunk ^ (r >> 2)) * (D / 8) + in;
+        const i32x2 x = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2*)src);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const f16x8 vf = e2m1_f16x8((uint32_t)x[k]);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) o[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, w[n][k], o[n][c], 0, 0, 0);
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
     }
   }
 }
@@ -555,9 +579,6 @@ struct PrefillLds {
     float ks[kTile], lv[kTile], iv[kTile];
     int held[4];
   } buf[2];
-  int64_t scan[4];
-  int64_t start_off;
-  int start_b;
 };
 
 // A row's channels lie at 16c + 4g + j in o[c][j]: rotated over c and j in the lane, over g between lanes.
@@ -596,223 +617,204 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
   __shared__ PrefillLds<D> s;
   const KvArgs& a = g.kv;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int G = g.n_q / a.n_kv;
   const uint32_t mask = (1u << a.logp) - 1;
-  Walk u = walk_start<ROWS, 4>(g, sp, G, s.scan, &s.start_off, &s.start_b);
-  if (u.left <= 0) return;
-  int b = u.b;
-  int64_t off = u.off, left = u.left;
-  const int64_t per = u.per;
+  if (tid == 0 && sp.split) sp.desc[blockIdx.x].more = 0;
+  Walk<ROWS> u;
+  u.start(g, sp);
   const float c_scale = g.scale * sp.c_q * 1.44269504088896341f;
-  for (; left > 0 && b < a.B; ++b, off = 0) {
-    const Seq q = kv_seq(a, b, G);
-    if (q.rows == 0) continue;
-    const int64_t hu = head_units<ROWS>(g, sp, q, G);
-    int kvh = (int)(off / hu);
-    off -= kvh * hu;
-    for (; left > 0 && kvh < a.n_kv; ++kvh, off = 0) {
-      int r0 = 0;
-      if (!sp.split) { r0 = (int)off * ROWS; off = 0; }
-      for (; left > 0 && r0 < q.rows; r0 += ROWS) {
-        const int n_rows = min(ROWS, q.rows - r0);
-        const Range all = kv_tiles(q, r0, r0 + n_rows - 1, G, g.causal, g.window);
-        const int units = sp.split ? all.hi - all.lo : 1;
-        if (off >= units) { off -= units; continue; }
-        const int u0 = (int)off;
-        const int u1 = (int)(units - u0 < left ? units : u0 + left);
-        left -= u1 - u0;
-        off = 0;
-        const int t_lo = sp.split ? all.lo + u0 : all.lo, t_hi = sp.split ? all.lo + u1 : all.hi;
+  while (u.next(g, sp)) {
+    const Seq q = u.q;
+    const int r0 = u.row0, kvh = u.h, b = u.seq;
+    const int t_lo = u.tiles.lo, t_hi = u.tiles.hi;
 
-        // ---- the wave's queries
-        const int w0 = r0 + 16 * NB * wave;           // its first row
-        const int w_rows = min(16 * NB, q.rows - w0); // may be <= 0
-        f16x8 qf[NB][D / 32];
-        float rs[NB], M[NB], l[NB];
-        int lo[NB], hi[NB];
-        f32x4 o[NB][D / 16];
+    // ---- the wave's queries
+    const int w0 = r0 + 16 * NB * wave;           // its first row
+    const int w_rows = min(16 * NB, q.rows - w0); // may be <= 0
+    f16x8 qf[NB][D / 32];
+    float rs[NB], M[NB], l[NB];
+    int lo[NB], hi[NB];
+    f32x4 o[NB][D / 16];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          const int rr = 16 * n + (lane & 15);
-          const bool row = rr < w_rows;
-          const int r = row ? w0 + rr : r0, i = r / G, h = r - i * G;
-          const uint16_t* src = g.q + (q.t0 + i) * g.ldq + ((int64_t)kvh * G + h) * D + (lane >> 4) * (D / 4);
-          load_queries<D>(row ? src : nullptr, a.rotate & 1, qf[n], &rs[n]);
-          rs[n] *= c_scale;
-          const Range w = kv_range(q, i, g.causal, g.window);
-          lo[n] = w.lo;
-          hi[n] = row ? w.hi : 0;
-          M[n] = -INFINITY;
-          l[n] = 0;
+    for (int n = 0; n < NB; ++n) {
+      const int rr = 16 * n + (lane & 15);
+      const bool row = rr < w_rows;
+      const int r = row ? w0 + rr : r0, i = div_g(sp, r), h = r - i * sp.G;
+      const uint16_t* src = g.q + (int64_t)(q.t0 + i) * g.ldq + (kvh * sp.G + h) * D + (lane >> 4) * (D / 4);
+      load_queries<D>(row ? src : nullptr, a.rotate & 1, qf[n], &rs[n]);
+      rs[n] *= c_scale;
+      const Range w = kv_range(q, i, g.causal, g.window);
+      lo[n] = w.lo;
+      hi[n] = row ? w.hi : 0;
+      M[n] = -INFINITY;
+      l[n] = 0;
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) o[n][c] = f32x4{0, 0, 0, 0};
-        }
-        Range any{0, 0}, every{0, 0};                 // positions that some, that every row of the wave attends
-        if (w_rows > 0) {
-          const Range r_first = kv_range(q, w0 / G, g.causal, g.window), r_last = kv_range(q, (w0 + w_rows - 1) / G, g.causal, g.window);
-          any = Range{r_first.lo, r_last.hi};
-          every = Range{r_last.lo, r_first.hi};
-        }
+      for (int c = 0; c < D / 16; ++c) o[n][c] = f32x4{0, 0, 0, 0};
+    }
+    Range any{0, 0}, every{0, 0};                 // positions that some, that every row of the wave attends
+    if (w_rows > 0) {
+      const Range r_first = kv_range(q, div_g(sp, w0), g.causal, g.window);
+      const Range r_last = kv_range(q, div_g(sp, w0 + w_rows - 1), g.causal, g.window);
+      any = Range{r_first.lo, r_last.hi};
+      every = Range{r_last.lo, r_first.hi};
+    }
 
-        // ---- the tiles: each wave brings 16 keys of each
-        C kr, vr;
-        float scale = 0;
-        int held = 0, pages = 0;
-        auto fetch = [&](int tile, int at) {
-          const int p0 = __builtin_amdgcn_readlane(pages, at);
-          held = p0 >= 0;
-          const int p = p0 >= 0 ? p0 : 0;             // keys in no page: any page is read, and masked
-          const int64_t row = (((int64_t)p * a.n_kv + kvh) << a.logp) + ((tile * kTile + 16 * wave) & mask);
-          kr = *reinterpret_cast<const C*>(a.codes[0] + row * (D / 2) + lane * (D / 8));
-          vr = *reinterpret_cast<const C*>(a.codes[1] + row * (D / 2) + lane * (D / 8));
-          scale = a.scales[(lane >> 4) & 1][row + (lane & 15)];
-        };
-        auto page_batch = [&](int tile) { pages = kv_page(a, b, (int64_t)(tile + lane) * kTile + 16 * wave); };
-        page_batch(t_lo);
-        fetch(t_lo, 0);
-        lds_barrier();                                // the last block's tiles have been read
-        int at = 0;
-        for (int tile = t_lo; tile < t_hi; ++tile) {
-          auto& B = s.buf[(tile - t_lo) & 1];
-          {
-            const int key = 16 * wave + (lane >> 2);
-            *reinterpret_cast<C*>(B.k + key * (D / 2) + ((lane & 3) ^ ((lane >> 4) & 3)) * (D / 8)) = kr;
-            *reinterpret_cast<C*>(B.v + key * (D / 2) + ((lane & 3) ^ wave) * (D / 8)) = vr;
-            if (lane < 16) B.ks[16 * wave + lane] = scale;
-            else if (lane < 32) {
-              const float v = scale < 0x1p-64f ? 0x1p-64f : scale;
-              B.lv[16 * wave + lane - 16] = __builtin_amdgcn_logf(v);
-              B.iv[16 * wave + lane - 16] = 1.0f / v;
-            }
-            if (lane == 0) B.held[wave] = held;
-          }
-          lds_barrier();
-          if (tile + 1 < t_hi) {
-            if (++at == 64) { page_batch(tile + 1); at = 0; }
-            fetch(tile + 1, at);
-          }
-          const int t0 = tile * kTile;
-          if (t0 >= any.hi || t0 + kTile <= any.lo) continue;
-          f32x4 sc[NB][4];
+    // ---- the tiles: each wave brings 16 keys of each
+    C kr, vr;
+    float scale = 0;
+    int held = 0, pages = 0;
+    auto fetch = [&](int tile, int at) {
+      const int p0 = __builtin_amdgcn_readlane(pages, at);
+      held = p0 >= 0;
+      const int p = p0 >= 0 ? p0 : 0;             // keys in no page: any page is read, and masked
+      const int64_t row = ((int64_t)(p * a.n_kv + kvh) << a.logp) + ((tile * kTile + 16 * wave) & mask);
+      kr = *reinterpret_cast<const C*>(a.codes[0] + row * (D / 2) + lane * (D / 8));
+      vr = *reinterpret_cast<const C*>(a.codes[1] + row * (D / 2) + lane * (D / 8));
+      scale = a.scales[(lane >> 4) & 1][row + (lane & 15)];
+    };
+    auto page_batch = [&](int tile) { pages = kv_page(a, b, (int64_t)(tile + lane) * kTile + 16 * wave); };
+    page_batch(t_lo);
+    fetch(t_lo, 0);
+    lds_barrier();                                // the last block's tiles have been read
+    int at = 0;
+    for (int tile = t_lo; tile < t_hi; ++tile) {
+      auto& B = s.buf[(tile - t_lo) & 1];
+      {
+        const int key = 16 * wave + (lane >> 2);
+        *reinterpret_cast<C*>(B.k + key * (D / 2) + ((lane & 3) ^ ((lane >> 4) & 3)) * (D / 8)) = kr;
+        *reinterpret_cast<C*>(B.v + key * (D / 2) + ((lane & 3) ^ wave) * (D / 8)) = vr;
+        if (lane < 16) B.ks[16 * wave + lane] = scale;
+        else if (lane < 32) {
+          const float v = scale < 0x1p-64f ? 0x1p-64f : scale;
+          B.lv[16 * wave + lane - 16] = __builtin_amdgcn_logf(v);
+          B.iv[16 * wave + lane - 16] = 1.0f / v;
+        }
+        if (lane == 0) B.held[wave] = held;
+      }
+      lds_barrier();
+      if (tile + 1 < t_hi) {
+        if (++at == 64) { page_batch(tile + 1); at = 0; }
+        fetch(tile + 1, at);
+      }
+      const int t0 = tile * kTile;
+      if (t0 >= any.hi || t0 + kTile <= any.lo) continue;
+      f32x4 sc[NB][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const C kc = *reinterpret_cast<const C*>(B.k + (16 * i + (lane & 15)) * (D / 2) + ((lane >> 4) ^ ((lane >> 2) & 3)) * (D / 8));
+      for (int i = 0; i < 4; ++i) {
+        const C kc = *reinterpret_cast<const C*>(B.k + (16 * i + (lane & 15)) * (D / 2) + ((lane >> 4) ^ ((lane >> 2) & 3)) * (D / 8));
 #pragma unroll
-            for (int n = 0; n < NB; ++n) sc[n][i] = f32x4{0, 0, 0, 0};
+        for (int n = 0; n < NB; ++n) sc[n][i] = f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-              const f16x8 kf = e2m1_f16x8(kc[k]);
-#pragma unroll
-              for (int n = 0; n < NB; ++n)
-                sc[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[n][k], sc[n][i], 0, 0, 0);
-            }
-          }
-          const int held4 = B.held[0] | B.held[1] << 1 | B.held[2] << 2 | B.held[3] << 3;
-          const bool whole = held4 == 15 && t0 >= every.lo && t0 + kTile <= every.hi;
-          f32x4 iv[4];
-          f16x8 w[NB][2];
-          float mx[NB];
-#pragma unroll
-          for (int n = 0; n < NB; ++n) mx[n] = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const f32x4 ks = *reinterpret_cast<const f32x4*>(&B.ks[16 * i + 4 * (lane >> 4)]);
-            const f32x4 lv = *reinterpret_cast<const f32x4*>(&B.lv[16 * i + 4 * (lane >> 4)]);
-            iv[i] = *reinterpret_cast<const f32x4*>(&B.iv[16 * i + 4 * (lane >> 4)]);
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float x = __builtin_fmaf(sc[n][i][j] * ks[j], rs[n], lv[j]);
-                sc[n][i][j] = x;
-              }
-          }
-          if (!whole) {
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const int t = t0 + 16 * i + 4 * (lane >> 4) + j;
-                  if (!(t >= lo[n] && t < hi[n] && ((held4 >> i) & 1))) sc[n][i][j] = -INFINITY;
-                }
-          }
+        for (int k = 0; k < D / 32; ++k) {
+          const f16x8 kf = e2m1_f16x8(kc[k]);
 #pragma unroll
           for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) mx[n] = fmaxf(mx[n], sc[n][i][j]);
-#pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            if (__any(mx[n] > M[n] + kSlack)) {
-              const float m = fmaxf(M[n], row_max(mx[n]));
-              const float keep = __builtin_amdgcn_exp2f(M[n] - safe_max(m));
-              l[n] *= keep;
-#pragma unroll
-              for (int c = 0; c < D / 16; ++c) o[n][c] *= keep;
-              M[n] = m;
-            }
-            const float ref = safe_max(M[n]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float x = sc[n][i][j];
-                const float p = __builtin_amdgcn_exp2f(x - ref);
-                // a masked key's 1 / vs may be NaN
-                l[n] = whole || x != -INFINITY ? __builtin_fmaf(p, iv[i][j], l[n]) : l[n];
-                w[n][i >> 1][4 * (i & 1) + j] = (_Float16)p;
-              }
-          }
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            const int r = lane & 15, key = 16 * (r >> 2) + 4 * (lane >> 4) + (r & 3);
-            const int chunk = c * 8 / (D / 8), in = c * 8 % (D / 8);
-            const uint8_t* src = B.v + key * (D / 2) + (chunk ^ (r >> 2)) * (D / 8) + in;
-            const i32x2 x = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2*)src);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const f16x8 vf = e2m1_f16x8((uint32_t)x[k]);
-#pragma unroll
-              for (int n = 0; n < NB; ++n) o[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, w[n][k], o[n][c], 0, 0, 0);
-            }
-          }
+            sc[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[n][k], sc[n][i], 0, 0, 0);
         }
-
-        // ---- the rows, each in its wave
-        const bool starts = u0 == 0, ends = u1 == units;
-        const int64_t part = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
+      }
+      const int held4 = B.held[0] | B.held[1] << 1 | B.held[2] << 2 | B.held[3] << 3;
+      const bool whole = held4 == 15 && t0 >= every.lo && t0 + kTile <= every.hi;
+      f32x4 iv[4];
+      f16x8 w[NB][2];
+      float mx[NB];
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          const int rr = 16 * n + (lane & 15);
-          const float sum = row_add(l[n]);
-          if (starts && ends) {
-            if (a.rotate & 2) transform_tile<D>(o[n], lane);
-            const float f = sum != 0.0f ? sp.c_v / sum : 0.0f;
-            if (rr < w_rows) {
-              const int r = w0 + rr, i = r / G, h = r - i * G;
-              uint16_t* dst = g.out + (q.t0 + i) * g.ldo + ((int64_t)kvh * G + h) * D + 4 * (lane >> 4);
+      for (int n = 0; n < NB; ++n) mx[n] = -INFINITY;
 #pragma unroll
-              for (int c = 0; c < D / 16; ++c) {
-                u32x2 x;
-                x[0] = (uint32_t)f32_to_bf16_rne(o[n][c][0] * f) | ((uint32_t)f32_to_bf16_rne(o[n][c][1] * f) << 16);
-                x[1] = (uint32_t)f32_to_bf16_rne(o[n][c][2] * f) | ((uint32_t)f32_to_bf16_rne(o[n][c][3] * f) << 16);
-                *reinterpret_cast<u32x2*>(dst + 16 * c) = x;
-              }
-            }
-          } else if (rr < w_rows) {
-            const int64_t at_row = part * ROWS + 16 * NB * wave + rr;
+      for (int i = 0; i < 4; ++i) {
+        const f32x4 ks = *reinterpret_cast<const f32x4*>(&B.ks[16 * i + 4 * (lane >> 4)]);
+        const f32x4 lv = *reinterpret_cast<const f32x4*>(&B.lv[16 * i + 4 * (lane >> 4)]);
+        iv[i] = *reinterpret_cast<const f32x4*>(&B.iv[16 * i + 4 * (lane >> 4)]);
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) *reinterpret_cast<f32x4*>(sp.o + at_row * D + 16 * c + 4 * (lane >> 4)) = o[n][c];
-            if (lane < 16) sp.ml[at_row] = float2{M[n], sum};
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float x = __builtin_fmaf(sc[n][i][j] * ks[j], rs[n], lv[j]);
+            sc[n][i][j] = x;
           }
+      }
+      if (!whole) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int t = t0 + 16 * i + 4 * (lane >> 4) + j;
+              if (!(t >= lo[n] && t < hi[n] && ((held4 >> i) & 1))) sc[n][i][j] = -INFINITY;
+            }
+      }
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx[n] = fmaxf(mx[n], sc[n][i][j]);
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        if (__any(mx[n] > M[n] + kSlack)) {
+          const float m = fmaxf(M[n], row_max(mx[n]));
+          const float keep = __builtin_amdgcn_exp2f(M[n] - safe_max(m));
+          l[n] *= keep;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) o[n][c] *= keep;
+          M[n] = m;
         }
-        if (starts && !ends && tid == 0)
-          sp.desc[blockIdx.x] = Desc{b, kvh, r0, (int)((units - u1 + per - 1) / per)};
+        const float ref = safe_max(M[n]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float x = sc[n][i][j];
+            const float p = __builtin_amdgcn_exp2f(x - ref);
+            // a masked key's 1 / vs may be NaN
+            l[n] = whole || x != -INFINITY ? __builtin_fmaf(p, iv[i][j], l[n]) : l[n];
+            w[n][i >> 1][4 * (i & 1) + j] = (_Float16)p;
+          }
+      }
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const int r = lane & 15, key = 16 * (r >> 2) + 4 * (lane >> 4) + (r & 3);
+        const int chunk = c * 8 / (D / 8), in = c * 8 % (D / 8);
+        const uint8_t* src = B.v + key * (D / 2) + (chunk ^ (r >> 2)) * (D / 8) + in;
+        const i32x2 x = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2*)src);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const f16x8 vf = e2m1_f16x8((uint32_t)x[k]);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) o[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, w[n][k], o[n][c], 0, 0, 0);
+        }
       }
     }
+
+    // ---- the rows, each in its wave
+    const bool starts = u.u0 == 0, ends = u.u1 == u.units;
+    const int64_t part = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const int rr = 16 * n + (lane & 15);
+      const float sum = row_add(l[n]);
+      if (starts && ends) {
+        if (a.rotate & 2) transform_tile<D>(o[n], lane);
+        const float f = sum != 0.0f ? sp.c_v / sum : 0.0f;
+        if (rr < w_rows) {
+          const int r = w0 + rr, i = div_g(sp, r), h = r - i * sp.G;
+          uint16_t* dst = g.out + (int64_t)(q.t0 + i) * g.ldo + (kvh * sp.G + h) * D + 4 * (lane >> 4);
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            u32x2 x;
+            x[0] = (uint32_t)f32_to_bf16_rne(o[n][c][0] * f) | ((uint32_t)f32_to_bf16_rne(o[n][c][1] * f) << 16);
+            x[1] = (uint32_t)f32_to_bf16_rne(o[n][c][2] * f) | ((uint32_t)f32_to_bf16_rne(o[n][c][3] * f) << 16);
+            *reinterpret_cast<u32x2*>(dst + 16 * c) = x;
+          }
+        }
+      } else if (rr < w_rows) {
+        const int64_t at_row = part * ROWS + 16 * NB * wave + rr;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) *reinterpret_cast<f32x4*>(sp.o + at_row * D + 16 * c + 4 * (lane >> 4)) = o[n][c];
+        if (lane < 16) sp.ml[at_row] = float2{M[n], sum};
+      }
+    }
+    if (starts && !ends && tid == 0)
+      sp.desc[blockIdx.x] = Desc{b, kvh, r0, u.following(sp)};
   }
 }
 
@@ -825,8 +827,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs g, SplitArgs sp
   const int w = blockIdx.x, row = blockIdx.y * RB + rb;
   const Desc d = sp.desc[w];
   if (d.more == 0) return;
-  const int G = g.n_q / g.kv.n_kv;
-  const Seq q = kv_seq(g.kv, d.b, G);
+  const Seq q = kv_seq(g.kv, d.b, sp.G);
   const bool mine = d.r0 + row < q.rows;
   if (RB == 1 && !mine) return;
   __shared__ float so[RB][NG][D], sm[RB][NG], sl[RB][NG];
@@ -867,8 +868,8 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs g, SplitArgs sp
     }
   }
   if (!mine) return;                                  // whole groups of lanes
-  const int r = d.r0 + row, i = r / G, h = r - i * G;
-  finish_row<D>(v, sum, g.kv.rotate & 2, sp.c_v, sub, g.out + (q.t0 + i) * g.ldo + ((int64_t)d.kvh * G + h) * D + 8 * sub);
+  const int r = d.r0 + row, i = div_g(sp, r), h = r - i * sp.G;
+  finish_row<D>(v, sum, g.kv.rotate & 2, sp.c_v, sub, g.out + (int64_t)(q.t0 + i) * g.ldo + (d.kvh * sp.G + h) * D + 8 * sub);
 }
 
 // Query rows of a row block: 16 or 32, all in every wave, for at most 32 rows a sequence on average;
@@ -883,7 +884,7 @@ hipError_t launch_decode(const KvAttnArgs& g, SplitArgs sp, hipStream_t stream) 
   kv_attention_kernel<D, NB, WV><<<sp.groups, 64 * WV, 0, stream>>>(g, sp);
   if (hipError_t e = hipGetLastError()) return e;
   if (!sp.split) return hipSuccess;
-  kv_join_kernel<D, 16 * NB, 1><<<dim3(sp.groups, 16 * NB), 256, 0, stream>>>(g, sp);
+  kv_join_kernel<D, 16 * NB, 1><<<dim3(sp.groups, sp.join_rows), 256, 0, stream>>>(g, sp);
   return hipGetLastError();
 }
 
@@ -892,7 +893,7 @@ hipError_t launch_prefill(const KvAttnArgs& g, SplitArgs sp, hipStream_t stream)
   kv_prefill_kernel<D, 2><<<sp.groups, 256, 0, stream>>>(g, sp);
   if (hipError_t e = hipGetLastError()) return e;
   if (!sp.split) return hipSuccess;
-  kv_join_kernel<D, 128, 8><<<dim3(sp.groups, 16), 256, 0, stream>>>(g, sp);
+  kv_join_kernel<D, 128, 8><<<dim3(sp.groups, (sp.join_rows + 7) / 8), 256, 0, stream>>>(g, sp);
   return hipGetLastError();
 }
 
@@ -913,19 +914,27 @@ hipError_t launch_kv_attention(const KvAttnArgs& g, hipStream_t stream) {
   sp.desc = static_cast<Desc*>(g.ws);
   sp.ml = reinterpret_cast<float2*>(sp.desc + kMaxGroups);
   sp.o = reinterpret_cast<float*>(sp.ml + (size_t)2 * kMaxGroups * rows);
+  sp.G = G;
+  const uint32_t lg = G > 1 ? 32 - __builtin_clz(G - 1) : 0;                // 2^lg >= G
+  sp.g_shift = 31 + lg;
+  sp.g_mul = (uint32_t)(((uint64_t(1) << sp.g_shift) + G - 1) / G);
+  const int64_t own = (int64_t)a.per_seq * G;
+  sp.join_rows = a.offsets || own > rows ? rows : (int)own;
   const int64_t blocks = ((a.T * G + rows - 1) / rows + a.B) * a.n_kv;      // row blocks at most
   const int64_t cap = ((int64_t)a.max_pages << a.logp) / kTile + 1;         // key tiles of one at most
-  if (rows == 128) {
-    sp.split = blocks < 3 * kMaxGroups && cap > 16;
-    sp.min_units = sp.split ? 4 : 1;
-    const int64_t want = sp.split ? blocks * ((cap + 3) / 4) : blocks;
-    sp.groups = (int)(sp.split && want > kMaxGroups ? kMaxGroups : want < (1 << 22) ? want : 1 << 22);
-    return a.D == 64 ? launch_prefill<64>(g, sp, stream) : launch_prefill<128>(g, sp, stream);
+  sp.split = rows == 128 ? blocks < 3 * kMaxGroups && cap > 16 : cap > 32;
+  sp.min_units = 1;
+  int64_t want = blocks;
+  if (sp.split) {
+    sp.min_units = 4;
+    sp.start_cost = rows == 128 ? 1 : 2;
+    while (blocks * ((cap >> sp.shift) + 1 + sp.start_cost) >= 0x7FFFFFFF - kMaxGroups) ++sp.shift;
+    want = blocks * ((cap >> sp.shift) + 1 + sp.start_cost);
+    want = (want + sp.min_units - 1) / sp.min_units;
   }
-  sp.split = cap > 32;
-  sp.min_units = sp.split ? 4 : 1;
-  const int64_t want = sp.split ? blocks * ((cap + 3) / 4) : blocks;
-  sp.groups = (int)(want < kMaxGroups ? want : kMaxGroups);
+  const int64_t most = rows == 128 && !sp.split ? 1 << 22 : kMaxGroups;
+  sp.groups = (int)(want < most ? want : most);
+  if (rows == 128) return a.D == 64 ? launch_prefill<64>(g, sp, stream) : launch_prefill<128>(g, sp, stream);
   if (a.D == 64) return rows == 16 ? launch_decode<64, 1, 4>(g, sp, stream) : launch_decode<64, 2, 4>(g, sp, stream);
   return rows == 16 ? launch_decode<128, 1, 4>(g, sp, stream) : launch_decode<128, 2, 4>(g, sp, stream);
 }

@@ -499,7 +499,7 @@ int cbq_codebook_adapter_gemm(const uint8_t* codes, const float* scales, int32_t
  *  k_codes, v_codes   : [n_pages][n_kv][page][D/2] bytes, 16-byte aligned; channel 2j in the
  *                       low nibble of byte j.  Nibble: sign (bit 3), then the value's index above.
  *  k_scales, v_scales : fp32 [n_pages][n_kv][page].
- *  n_pages >= 1; 1 <= n_kv <= 1024 key/value heads; page: tokens a page holds, a power of two, 16 to 1024.
+ *  n_pages >= 1, n_pages * n_kv < 2^31; 1 <= n_kv <= 1024 key/value heads; page: tokens a page holds, a power of two, 16 to 1024.
  *  D        : 64 or 128.
  *  rotate   : CBQ_KV_ROTATE_K | CBQ_KV_ROTATE_V, or fewer: which of the two are rotated (a
  *             Sylvester Hadamard transform over the D channels, orthonormal with the scale).
@@ -588,7 +588,7 @@ int cbq_kv_cache_read(const cbq_kv_cache* cache, const cbq_kv_seqs* seqs, uint16
  *  Deterministic: no result depends on the order of atomics.
  *  ws, ws_bytes : device workspace of cbq_kv_attention_workspace(...) bytes, 16-byte aligned;
  *           rewritten by every call; calls that overlap in time need one each.
- *  out overlaps no input, nor ws.  T < 2^31, n_q <= 1024.
+ *  out overlaps no input, nor ws.  n_q <= 1024, T * n_q < 2^31.
  */
 size_t cbq_kv_attention_workspace(const cbq_kv_cache* cache, int64_t T, int32_t B, int32_t n_q);
 int cbq_kv_attention(const cbq_kv_cache* cache, const cbq_kv_seqs* seqs, const uint16_t* q,
