@@ -117,6 +117,14 @@ struct Walk {
   int seq, h, row0, u0, u1, units;
   Range tiles;                     // its key tiles
 
+  Seq lane_q;                      // up to 64 sequences: the lane's own, so that no start waits for a length
+
+  __device__ __forceinline__ Seq get(const KvArgs& a, const SplitArgs& sp, int i) const {
+    if (a.B > 64) return kv_seq(a, i, sp.G);
+    return Seq{__builtin_amdgcn_readlane(lane_q.t0, i), __builtin_amdgcn_readlane(lane_q.rows, i),
+               __builtin_amdgcn_readlane(lane_q.pos0, i), __builtin_amdgcn_readlane(lane_q.len, i)};
+  }
+
   __device__ __forceinline__ void start(const KvAttnArgs& g, const SplitArgs& sp) {
     const KvArgs& a = g.kv;
     const int lane = threadIdx.x & 63;
@@ -124,17 +132,19 @@ struct Walk {
     int mine = 0;
     for (int k = 0; k < each; ++k) {
       const int s = lane * each + k;
-      if (s < a.B) mine += head_units<ROWS>(g, sp, kv_seq(a, s, sp.G)) * a.n_kv;
-    }
-    int inc = mine;
-    if (a.B > 1) {
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const int y = __shfl_up(inc, d);
-        if (lane >= d) inc += y;
+      if (s < a.B) {
+        lane_q = kv_seq(a, s, sp.G);
+        mine += head_units<ROWS>(g, sp, lane_q) * a.n_kv;
       }
     }
-    const int total = __builtin_amdgcn_readlane(inc, a.B > 1 ? 63 : 0);
+    int inc = mine;                                   // inclusive sums over the lanes
+    inc += __builtin_amdgcn_update_dpp(0, inc, 0x111, 0xF, 0xF, false);
+    inc += __builtin_amdgcn_update_dpp(0, inc, 0x112, 0xF, 0xF, false);
+    inc += __builtin_amdgcn_update_dpp(0, inc, 0x114, 0xF, 0xF, false);
+    inc += __builtin_amdgcn_update_dpp(0, inc, 0x118, 0xF, 0xF, false);
+    inc += __builtin_amdgcn_update_dpp(0, inc, 0x142, 0xA, 0xF, false);   // lane 15 of a row into the next row
+    inc += __builtin_amdgcn_update_dpp(0, inc, 0x143, 0xC, 0xF, false);   // lane 31 into the upper half
+    const int total = __builtin_amdgcn_readlane(inc, 63);
     per = max((int)(((uint32_t)total + sp.groups - 1) / (uint32_t)sp.groups), sp.min_units);
     // unsplit calls start with the last units: a sequence's last rows attend the most keys
     const int64_t at = sp.split ? (int64_t)blockIdx.x : (int64_t)sp.groups - 1 - blockIdx.x;
@@ -151,7 +161,7 @@ struct Walk {
     r0 = 0;
     for (;; ++b) {                                    // at most `each` times
       if (b >= a.B) { left = 0; return; }             // offsets that do not ascend
-      q = kv_seq(a, b, sp.G);
+      q = get(a, sp, b);
       const int hu = head_units<ROWS>(g, sp, q);
       if (off < hu * a.n_kv) {
         kvh = off / hu;
@@ -172,7 +182,7 @@ struct Walk {
           kvh = 0;
           do {
             if (++b >= g.kv.B) return false;
-            q = kv_seq(g.kv, b, sp.G);
+            q = get(g.kv, sp, b);
           } while (q.rows == 0);
         }
       }
@@ -203,13 +213,17 @@ struct Lds {
   static constexpr int ROWS = 16 * NB, P = D + 4;    // padded row: 16 rows start in 16 different bank groups
   union {
     struct {
-      uint8_t v[WV][kTile * D / 2];                  // values' codes, 16-byte (8-byte) quarters of a row swizzled
-      float ks[WV][kTile], lv[WV][kTile], iv[WV][kTile];
+      alignas(16) uint8_t v[WV][kTile * D / 2];                  // values' codes, 16-byte (8-byte) quarters of a row swizzled
+      alignas(16) float ks[WV][kTile], lv[WV][kTile], iv[WV][kTile];
     } t;
-    float o[WV][ROWS * P];
+    alignas(16) float o[WV][ROWS * P];
   };
   float m[WV][ROWS], l[WV][ROWS];
 };
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.0f : m; }
 
 // x of the lanes 16 (32) apart: a of the even row (lower half), b of the odd row (upper half), in
 // both lanes.  The swap's second operand is hidden from the compiler, which takes the two
@@ -247,51 +261,69 @@ __device__ __forceinline__ float row_add(float x) {
 }
 
 // 16 query rows as the MFMA's second operand: lane (row, g) holds channels g*D/4 ... of its row.
-// Rotated if asked, divided by a power of two near its largest value; *rs gets that power.
 template <int D>
-__device__ __forceinline__ void load_queries(const uint16_t* q, bool rotate, f16x8* out, float* rs) {
-  constexpr int C = D / 4;
-  float x[C];
+struct Queries { u32x4 x[D / 32]; };
+
+template <int D>
+__device__ __forceinline__ Queries<D> fetch_queries(const KvAttnArgs& g, const SplitArgs& sp, const Seq& q, int kvh, int r, bool row) {
+  const int lane = threadIdx.x & 63, i = div_g(sp, r), h = r - i * sp.G;
+  const uint16_t* src = g.q + (int64_t)(q.t0 + i) * g.ldq + (kvh * sp.G + h) * D + (lane >> 4) * (D / 4);
+  Queries<D> f;
 #pragma unroll
-  for (int i = 0; i < C / 8; ++i) {
-    u32x4 v = {0, 0, 0, 0};
-    if (q) v = *reinterpret_cast<const u32x4*>(q + 8 * i);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[8 * i + 2 * j] = __builtin_bit_cast(float, v[j] << 16);
-      x[8 * i + 2 * j + 1] = __builtin_bit_cast(float, v[j] & 0xFFFF0000u);
-    }
-  }
+  for (int k = 0; k < D / 32; ++k) f.x[k] = row ? *reinterpret_cast<const u32x4*>(src + 8 * k) : u32x4{0, 0, 0, 0};
+  return f;
+}
+
+// Rotated if asked, divided by a power of two near the row's largest value; *rs gets that power.  The rotation is a
+// product with the +-1 matrix on the matrix cores (bf16 inputs exact, fp32 sums): its row m of tile c
+// is output channel D/4 (m / 4) + 4c + m % 4, so that lane (row, g) gets the channels it needs.  An entry's sign is
+// the parity of the bits that input and output channel share; with input channel D/4 g + 8k + j
+// it falls into parities of j with (m % 4, c % 2), of k with c / 2, and of g with m / 4.
+template <int D>
+__device__ __forceinline__ void convert_queries(const Queries<D>& f, bool rotate, f16x8* out, float* rs) {
+  const int lane = threadIdx.x & 63;
+  f32x4 x[D / 16];
   if (rotate) {
+    const uint32_t m4 = lane & 3, gm = (lane >> 4) & ((lane >> 2) & 3);
+    const uint32_t all = (gm ^ (gm >> 1)) & 1 ? 0x80008000u : 0u;
+    uint32_t h[4];                                    // c even, k without shared bits: dword d holds j = 2d, 2d + 1
 #pragma unroll
-    for (int h = 1; h < C; h *= 2)
+    for (int d = 0; d < 4; ++d) {
+      const uint32_t p = (m4 >> 1) & d & 1;           // j's bit 1 is d's bit 0
+      h[d] = 0x3F803F80u ^ all ^ (p ? 0x80008000u : 0u) ^ (m4 & 1 ? 0x80000000u : 0u);
+    }
 #pragma unroll
-      for (int i = 0; i < C; ++i)
-        if (!(i & h)) {
-          const float s = x[i] + x[i + h], d = x[i] - x[i + h];
-          x[i] = s;
-          x[i + h] = d;
-        }
-    const int lane = threadIdx.x & 63;
+    for (int c = 0; c < D / 16; ++c) {
+      x[c] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < C; ++i) {                    // channels C apart: lanes 16 apart; 2C: 32 apart
-      float a, b;
-      swap_pair<false>(x[i], a, b);
-      swap_pair<true>((lane & 16) ? a - b : a + b, a, b);
-      x[i] = (lane & 32) ? a - b : a + b;
+      for (int k = 0; k < D / 32; ++k) {
+        const int kc = k & (c >> 1);
+        const uint32_t lo = (kc ^ (kc >> 1)) & 1 ? 0x80008000u : 0u, hi = c & 1 ? lo ^ 0x80008000u : lo;
+        const u32x4 hm = {h[0] ^ lo, h[1] ^ lo, h[2] ^ hi, h[3] ^ hi};
+        x[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, hm), __builtin_bit_cast(bf16x8, f.x[k]), x[c], 0, 0, 0);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      const uint32_t a = f.x[c / 2][2 * (c & 1)], b = f.x[c / 2][2 * (c & 1) + 1];
+      x[c] = f32x4{__builtin_bit_cast(float, a << 16), __builtin_bit_cast(float, a & 0xFFFF0000u),
+                   __builtin_bit_cast(float, b << 16), __builtin_bit_cast(float, b & 0xFFFF0000u)};
     }
   }
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < C; ++i) m = max(m, __builtin_bit_cast(uint32_t, x[i]) & 0x7FFFFFFFu);
+  for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = max(m, __builtin_bit_cast(uint32_t, x[c][j]) & 0x7FFFFFFFu);
   m = row_max_u32(m);
   const uint32_t e = min(m >> 23, 253u);              // 2^(e-127) <= largest value, or smaller
   const float inv = __builtin_bit_cast(float, (254u - e) << 23);
   *rs = m >= 0x7F800000u ? NAN : e ? __builtin_bit_cast(float, e << 23) : 0x1p-127f;
 #pragma unroll
-  for (int i = 0; i < C / 8; ++i)
+  for (int c = 0; c < D / 16; ++c)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) out[i][j] = (_Float16)(x[8 * i + j] * inv);
+    for (int j = 0; j < 4; ++j) out[c / 2][4 * (c & 1) + j] = (_Float16)(x[c][j] * inv);
 }
 
 // 8 codes -> 8 fp16
@@ -312,10 +344,68 @@ __device__ __forceinline__ void finish_row(float* v, float l, bool rotate, float
   if (dst) *reinterpret_cast<u32x4*>(dst) = out;
 }
 
-__device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.0f : m; }
-
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+
+// Scores of 64 keys to weights: sc[n][i][j] is row lane % 16 of row tile n and key 16i + 4 (lane / 16) + j of the tile at
+// position t0.  The running maximum moves only when a score passes it by 2^8: weights up to 256 lose
+// nothing in fp16, and most tiles then need neither an exchange between lanes nor a rescaling.
+constexpr float kSlack = 8.0f;
+
+template <int D, int NB>
+__device__ __forceinline__ void soft_weights(const float* ks, const float* lv, const float* iv, int t0, bool whole, uint32_t held,
+                                             const float* rs, const int* lo, const int* hi, f32x4 (*sc)[4], float* M, float* l,
+                                             f32x4 (*o)[D / 16], f16x8 (*w)[2]) {
+  const int lane = threadIdx.x & 63, key = 4 * (lane >> 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f32x4 k = *reinterpret_cast<const f32x4*>(ks + 16 * i + key), v = *reinterpret_cast<const f32x4*>(lv + 16 * i + key);
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sc[n][i][j] = __builtin_fmaf(sc[n][i][j] * k[j], rs[n], v[j]);
+  }
+  if (!whole) {
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const int at = t0 + key - lo[n];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t len = (held >> i) & 1 ? (uint32_t)max(hi[n] - lo[n], 0) : 0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[n][i][j] = (uint32_t)(at + 16 * i + j) < len ? sc[n][i][j] : -INFINITY;
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mx = fmaxf(mx, sc[n][i][j]);
+    if (__any(mx > M[n] + kSlack)) {
+      const float rm = row_max(mx), m = rm > M[n] + kSlack ? rm : M[n];   // a row moves for its own scores alone
+      const float keep = __builtin_amdgcn_exp2f(M[n] - safe_max(m));
+      l[n] *= keep;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) o[n][c] *= keep;
+      M[n] = m;
+    }
+    const float ref = safe_max(M[n]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(iv + 16 * i + key);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float x = sc[n][i][j], p = __builtin_amdgcn_exp2f(x - ref);
+        // a masked key's 1 / vs may be NaN
+        l[n] = whole || x != -INFINITY ? __builtin_fmaf(p, v[j], l[n]) : l[n];
+        w[n][i >> 1][4 * (i & 1) + j] = (_Float16)p;
+      }
+    }
+  }
+}
 
 template <int D> struct Chunk;                        // a quarter of a row of codes
 template <> struct Chunk<128> { typedef u32x4 T; };
@@ -382,6 +472,14 @@ __global__ __launch_bounds__(64 * WV) void kv_attention_kernel(KvAttnArgs g, Spl
     const bool mine = more && tile < u.tiles.hi;
     TileRegs<D> nx;
     if (mine) pages = tile_pages<WV>(a, u.seq, tile);
+    Queries<D> fq[NB];
+    if (more) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const int r = u.row0 + 16 * n + (lane & 15);
+        fq[n] = fetch_queries<D>(g, sp, u.q, u.h, min(r, u.q.rows - 1), r < u.q.rows);
+      }
+    }
     if (have) {
       __syncthreads();
 #pragma unroll
@@ -450,11 +548,9 @@ __global__ __launch_bounds__(64 * WV) void kv_attention_kernel(KvAttnArgs g, Spl
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       const bool row = 16 * n + (lane & 15) < n_rows;
-      const int r = row ? row0 + 16 * n + (lane & 15) : row0, i = div_g(sp, r), h = r - i * sp.G;
-      const uint16_t* src = g.q + (int64_t)(q.t0 + i) * g.ldq + (kvh * sp.G + h) * D + (lane >> 4) * (D / 4);
-      load_queries<D>(row ? src : nullptr, a.rotate & 1, qf[n], &rs[n]);
+      convert_queries<D>(fq[n], a.rotate & 1, qf[n], &rs[n]);
       rs[n] *= c_scale;
-      const Range w = kv_range(q, i, g.causal, g.window);
+      const Range w = kv_range(q, div_g(sp, row ? row0 + 16 * n + (lane & 15) : row0), g.causal, g.window);
       lo[n] = w.lo;
       hi[n] = row ? w.hi : 0;
       M[n] = -INFINITY;
@@ -487,64 +583,18 @@ __global__ __launch_bounds__(64 * WV) void kv_attention_kernel(KvAttnArgs g, Spl
       // scores of 64 keys
       f32x4 sc[NB][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int k = 0; k < D / 32; ++k)
 #pragma unroll
-        for (int n = 0; n < NB; ++n) sc[n][i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
+        for (int i = 0; i < 4; ++i) {
           const f16x8 kf = e2m1_f16x8(cu.k[i][k]);
 #pragma unroll
           for (int n = 0; n < NB; ++n)
-            sc[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[n][k], sc[n][i], 0, 0, 0);
+            sc[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[n][k], k ? sc[n][i] : f32x4{0, 0, 0, 0}, 0, 0, 0);
         }
-      }
       __builtin_amdgcn_wave_barrier();
       const bool whole = cu.held == 15u && tile * kTile >= all_lo && tile * kTile + kTile <= all_hi;
-      f32x4 iv[4];
       f16x8 w[NB][2];
-      float mx[NB];
-#pragma unroll
-      for (int n = 0; n < NB; ++n) mx[n] = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x4 ks = *reinterpret_cast<const f32x4*>(&s.t.ks[wave][16 * i + 4 * (lane >> 4)]);
-        const f32x4 lv = *reinterpret_cast<const f32x4*>(&s.t.lv[wave][16 * i + 4 * (lane >> 4)]);
-        iv[i] = *reinterpret_cast<const f32x4*>(&s.t.iv[wave][16 * i + 4 * (lane >> 4)]);
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float x = __builtin_fmaf(sc[n][i][j] * ks[j], rs[n], lv[j]);
-            if (!whole) {
-              const int t = tile * kTile + 16 * i + 4 * (lane >> 4) + j;
-              x = t >= lo[n] && t < hi[n] && ((cu.held >> i) & 1) ? x : -INFINITY;
-            }
-            sc[n][i][j] = x;
-            mx[n] = fmaxf(mx[n], x);
-          }
-      }
-#pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        const float m = fmaxf(M[n], row_max(mx[n]));
-        if (__any(m > M[n])) {
-          const float keep = __builtin_amdgcn_exp2f(M[n] - safe_max(m));
-          l[n] *= keep;
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) o[n][c] *= keep;
-          M[n] = m;
-        }
-        const float ref = safe_max(M[n]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float x = sc[n][i][j];
-            const float p = __builtin_amdgcn_exp2f(x - ref);
-            // a masked key's 1 / vs may be NaN
-            l[n] = whole || x != -INFINITY ? __builtin_fmaf(p, iv[i][j], l[n]) : l[n];
-            w[n][i >> 1][4 * (i & 1) + j] = (_Float16)p;
-          }
-      }
+      soft_weights<D, NB>(s.t.ks[wave], s.t.lv[wave], s.t.iv[wave], tile * kTile, whole, cu.held, rs, lo, hi, sc, M, l, o, w);
       // values times weights, 16 channels at a time
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
@@ -568,15 +618,13 @@ __global__ __launch_bounds__(64 * WV) void kv_attention_kernel(KvAttnArgs g, Spl
 // Many query rows a sequence (prefill): a workgroup takes 4 x 16 NB rows of one key/value head, each wave its own,
 // and all four read the same key tiles.  A tile (64 keys: codes as they are, 8 KB, and the scales)
 // goes through LDS in two buffers with one barrier a tile, the next one's loads in flight meanwhile; each wave
-// converts what it multiplies.  The running maximum moves only when a score passes it by 2^8: weights up
-// to 256 lose nothing in fp16, and most tiles then need neither an exchange between lanes nor a rescaling.
-constexpr float kSlack = 8.0f;
+// converts what it multiplies.
 
 template <int D>
 struct PrefillLds {
   struct Buf {
-    uint8_t k[kTile * D / 2], v[kTile * D / 2];
-    float ks[kTile], lv[kTile], iv[kTile];
+    alignas(16) uint8_t k[kTile * D / 2], v[kTile * D / 2];
+    alignas(16) float ks[kTile], lv[kTile], iv[kTile];
     int held[4];
   } buf[2];
 };
@@ -638,11 +686,10 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
     for (int n = 0; n < NB; ++n) {
       const int rr = 16 * n + (lane & 15);
       const bool row = rr < w_rows;
-      const int r = row ? w0 + rr : r0, i = div_g(sp, r), h = r - i * sp.G;
-      const uint16_t* src = g.q + (int64_t)(q.t0 + i) * g.ldq + (kvh * sp.G + h) * D + (lane >> 4) * (D / 4);
-      load_queries<D>(row ? src : nullptr, a.rotate & 1, qf[n], &rs[n]);
+      const int r = row ? w0 + rr : r0;
+      convert_queries<D>(fetch_queries<D>(g, sp, q, kvh, r, row), a.rotate & 1, qf[n], &rs[n]);
       rs[n] *= c_scale;
-      const Range w = kv_range(q, i, g.causal, g.window);
+      const Range w = kv_range(q, div_g(sp, r), g.causal, g.window);
       lo[n] = w.lo;
       hi[n] = row ? w.hi : 0;
       M[n] = -INFINITY;
@@ -698,78 +745,23 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
       const int t0 = tile * kTile;
       if (t0 >= any.hi || t0 + kTile <= any.lo) continue;
       f32x4 sc[NB][4];
+      C kc[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const C kc = *reinterpret_cast<const C*>(B.k + (16 * i + (lane & 15)) * (D / 2) + ((lane >> 4) ^ ((lane >> 2) & 3)) * (D / 8));
+      for (int i = 0; i < 4; ++i)
+        kc[i] = *reinterpret_cast<const C*>(B.k + (16 * i + (lane & 15)) * (D / 2) + ((lane >> 4) ^ ((lane >> 2) & 3)) * (D / 8));
 #pragma unroll
-        for (int n = 0; n < NB; ++n) sc[n][i] = f32x4{0, 0, 0, 0};
+      for (int k = 0; k < D / 32; ++k)
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          const f16x8 kf = e2m1_f16x8(kc[k]);
+        for (int i = 0; i < 4; ++i) {
+          const f16x8 kf = e2m1_f16x8(kc[i][k]);
 #pragma unroll
           for (int n = 0; n < NB; ++n)
-            sc[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[n][k], sc[n][i], 0, 0, 0);
+            sc[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[n][k], k ? sc[n][i] : f32x4{0, 0, 0, 0}, 0, 0, 0);
         }
-      }
-      const int held4 = B.held[0] | B.held[1] << 1 | B.held[2] << 2 | B.held[3] << 3;
+      const uint32_t held4 = B.held[0] | B.held[1] << 1 | B.held[2] << 2 | B.held[3] << 3;
       const bool whole = held4 == 15 && t0 >= every.lo && t0 + kTile <= every.hi;
-      f32x4 iv[4];
       f16x8 w[NB][2];
-      float mx[NB];
-#pragma unroll
-      for (int n = 0; n < NB; ++n) mx[n] = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x4 ks = *reinterpret_cast<const f32x4*>(&B.ks[16 * i + 4 * (lane >> 4)]);
-        const f32x4 lv = *reinterpret_cast<const f32x4*>(&B.lv[16 * i + 4 * (lane >> 4)]);
-        iv[i] = *reinterpret_cast<const f32x4*>(&B.iv[16 * i + 4 * (lane >> 4)]);
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float x = __builtin_fmaf(sc[n][i][j] * ks[j], rs[n], lv[j]);
-            sc[n][i][j] = x;
-          }
-      }
-      if (!whole) {
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int t = t0 + 16 * i + 4 * (lane >> 4) + j;
-              if (!(t >= lo[n] && t < hi[n] && ((held4 >> i) & 1))) sc[n][i][j] = -INFINITY;
-            }
-      }
-#pragma unroll
-      for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) mx[n] = fmaxf(mx[n], sc[n][i][j]);
-#pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        if (__any(mx[n] > M[n] + kSlack)) {
-          const float m = fmaxf(M[n], row_max(mx[n]));
-          const float keep = __builtin_amdgcn_exp2f(M[n] - safe_max(m));
-          l[n] *= keep;
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) o[n][c] *= keep;
-          M[n] = m;
-        }
-        const float ref = safe_max(M[n]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float x = sc[n][i][j];
-            const float p = __builtin_amdgcn_exp2f(x - ref);
-            // a masked key's 1 / vs may be NaN
-            l[n] = whole || x != -INFINITY ? __builtin_fmaf(p, iv[i][j], l[n]) : l[n];
-            w[n][i >> 1][4 * (i & 1) + j] = (_Float16)p;
-          }
-      }
+      soft_weights<D, NB>(B.ks, B.lv, B.iv, t0, whole, held4, rs, lo, hi, sc, M, l, o, w);
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
         const int r = lane & 15, key = 16 * (r >> 2) + 4 * (lane >> 4) + (r & 3);
@@ -927,7 +919,7 @@ hipError_t launch_kv_attention(const KvAttnArgs& g, hipStream_t stream) {
   int64_t want = blocks;
   if (sp.split) {
     sp.min_units = 4;
-    sp.start_cost = rows == 128 ? 1 : 2;
+    sp.start_cost = rows == 128 ? 1 : 8;
     while (blocks * ((cap >> sp.shift) + 1 + sp.start_cost) >= 0x7FFFFFFF - kMaxGroups) ++sp.shift;
     want = blocks * ((cap >> sp.shift) + 1 + sp.start_cost);
     want = (want + sp.min_units - 1) / sp.min_units;
