@@ -21,7 +21,9 @@ namespace cbq {
 namespace {
 
 constexpr int kTile = 64;          // keys a wave takes at a time
-constexpr int kMaxGroups = 512;    // workgroups of a split call: two a CU
+constexpr int kWaves = 8;          // waves that share a decode row block
+// Workgroups of a split call, as many as the chip holds at once: 256 of eight waves, 512 of four.
+constexpr int max_groups(int rows) { return rows == 128 ? 512 : 256; }
 
 // A sequence's part of the step, all values uniform over the workgroup.
 struct Seq {
@@ -394,15 +396,31 @@ __device__ __forceinline__ void soft_weights(const float* ks, const float* lv, c
     }
     const float ref = safe_max(M[n]);
 #pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = __builtin_amdgcn_exp2f(sc[n][i][j] - ref);
+        sc[n][i][j] = p;
+        w[n][i >> 1][4 * (i & 1) + j] = (_Float16)p;
+      }
+  }
+  if (whole) {
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f32x4 v = *reinterpret_cast<const f32x4*>(iv + 16 * i + key);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float x = sc[n][i][j], p = __builtin_amdgcn_exp2f(x - ref);
-        // a masked key's 1 / vs may be NaN
-        l[n] = whole || x != -INFINITY ? __builtin_fmaf(p, v[j], l[n]) : l[n];
-        w[n][i >> 1][4 * (i & 1) + j] = (_Float16)p;
-      }
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) l[n] = __builtin_fmaf(sc[n][i][j], v[j], l[n]);
+    }
+  } else {                                            // a masked key's 1 / vs may be NaN
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(iv + 16 * i + key);
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) l[n] = sc[n][i][j] != 0.0f ? __builtin_fmaf(sc[n][i][j], v[j], l[n]) : l[n];
     }
   }
 }
@@ -450,7 +468,7 @@ __device__ __forceinline__ void load_tile(const KvArgs& a, int kvh, int tile, in
 }
 
 template <int D, int NB, int WV>
-__global__ __launch_bounds__(64 * WV) void kv_attention_kernel(KvAttnArgs g, SplitArgs sp) {
+__global__ __launch_bounds__(64 * WV, 2) void kv_attention_kernel(KvAttnArgs g, SplitArgs sp) {
   constexpr int ROWS = 16 * NB, NT = 64 * WV, P = Lds<D, NB, WV>::P, L = D / 8;
   __shared__ Lds<D, NB, WV> s;
   const KvArgs& a = g.kv;
@@ -472,14 +490,6 @@ __global__ __launch_bounds__(64 * WV) void kv_attention_kernel(KvAttnArgs g, Spl
     const bool mine = more && tile < u.tiles.hi;
     TileRegs<D> nx;
     if (mine) pages = tile_pages<WV>(a, u.seq, tile);
-    Queries<D> fq[NB];
-    if (more) {
-#pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        const int r = u.row0 + 16 * n + (lane & 15);
-        fq[n] = fetch_queries<D>(g, sp, u.q, u.h, min(r, u.q.rows - 1), r < u.q.rows);
-      }
-    }
     if (have) {
       __syncthreads();
 #pragma unroll
@@ -495,6 +505,14 @@ __global__ __launch_bounds__(64 * WV) void kv_attention_kernel(KvAttnArgs g, Spl
           *reinterpret_cast<f32x4*>(&s.o[wave][row * P + 16 * c + 4 * (lane >> 4)]) = o[n][c];
       }
       __syncthreads();
+    }
+    Queries<D> fq[NB];
+    if (more) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const int r = u.row0 + 16 * n + (lane & 15);
+        fq[n] = fetch_queries<D>(g, sp, u.q, u.h, min(r, u.q.rows - 1), r < u.q.rows);
+      }
     }
     if (mine) load_tile<D>(a, u.h, tile, pages, 0, nx);
     if (have) {
@@ -871,9 +889,9 @@ int row_block(int64_t T, int B, int G) {
   return rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
 }
 
-template <int D, int NB, int WV>
+template <int D, int NB>
 hipError_t launch_decode(const KvAttnArgs& g, SplitArgs sp, hipStream_t stream) {
-  kv_attention_kernel<D, NB, WV><<<sp.groups, 64 * WV, 0, stream>>>(g, sp);
+  kv_attention_kernel<D, NB, kWaves><<<sp.groups, 64 * kWaves, 0, stream>>>(g, sp);
   if (hipError_t e = hipGetLastError()) return e;
   if (!sp.split) return hipSuccess;
   kv_join_kernel<D, 16 * NB, 1><<<dim3(sp.groups, sp.join_rows), 256, 0, stream>>>(g, sp);
@@ -893,19 +911,19 @@ hipError_t launch_prefill(const KvAttnArgs& g, SplitArgs sp, hipStream_t stream)
 
 size_t kv_attention_workspace_bytes(int64_t T, int B, int n_q, int n_kv, int D) {
   const int rows = row_block(T, B, n_q / n_kv);
-  return (size_t)kMaxGroups * (sizeof(Desc) + 2 * rows * (sizeof(float2) + D * sizeof(float)));
+  return (size_t)max_groups(rows) * (sizeof(Desc) + 2 * rows * (sizeof(float2) + D * sizeof(float)));
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs& g, hipStream_t stream) {
   const KvArgs& a = g.kv;
-  const int G = g.n_q / a.n_kv, rows = row_block(a.T, a.B, G);
+  const int G = g.n_q / a.n_kv, rows = row_block(a.T, a.B, G), most = max_groups(rows);
   SplitArgs sp{};
   const float c = (float)(1.0 / std::sqrt((double)a.D));
   sp.c_q = a.rotate & 1 ? c : 1.0f;
   sp.c_v = a.rotate & 2 ? c : 1.0f;
   sp.desc = static_cast<Desc*>(g.ws);
-  sp.ml = reinterpret_cast<float2*>(sp.desc + kMaxGroups);
-  sp.o = reinterpret_cast<float*>(sp.ml + (size_t)2 * kMaxGroups * rows);
+  sp.ml = reinterpret_cast<float2*>(sp.desc + most);
+  sp.o = reinterpret_cast<float*>(sp.ml + (size_t)2 * most * rows);
   sp.G = G;
   const uint32_t lg = G > 1 ? 32 - __builtin_clz(G - 1) : 0;                // 2^lg >= G
   sp.g_shift = 31 + lg;
@@ -914,21 +932,20 @@ hipError_t launch_kv_attention(const KvAttnArgs& g, hipStream_t stream) {
   sp.join_rows = a.offsets || own > rows ? rows : (int)own;
   const int64_t blocks = ((a.T * G + rows - 1) / rows + a.B) * a.n_kv;      // row blocks at most
   const int64_t cap = ((int64_t)a.max_pages << a.logp) / kTile + 1;         // key tiles of one at most
-  sp.split = rows == 128 ? blocks < 3 * kMaxGroups && cap > 16 : cap > 32;
+  sp.split = rows == 128 ? blocks < 3 * most && cap > 16 : cap > 32;
   sp.min_units = 1;
   int64_t want = blocks;
   if (sp.split) {
     sp.min_units = 4;
-    sp.start_cost = rows == 128 ? 1 : 8;
-    while (blocks * ((cap >> sp.shift) + 1 + sp.start_cost) >= 0x7FFFFFFF - kMaxGroups) ++sp.shift;
-    want = blocks * ((cap >> sp.shift) + 1 + sp.start_cost);
-    want = (want + sp.min_units - 1) / sp.min_units;
+    sp.start_cost = rows == 128 ? 1 : 16;
+    while (blocks * ((cap >> sp.shift) + 1 + sp.start_cost) >= 0x7FFFFFFF - most) ++sp.shift;
+    want = (blocks * ((cap >> sp.shift) + 1 + sp.start_cost) + sp.min_units - 1) / sp.min_units;
   }
-  const int64_t most = rows == 128 && !sp.split ? 1 << 22 : kMaxGroups;
-  sp.groups = (int)(want < most ? want : most);
+  const int64_t limit = rows == 128 && !sp.split ? 1 << 22 : most;
+  sp.groups = (int)(want < limit ? want : limit);
   if (rows == 128) return a.D == 64 ? launch_prefill<64>(g, sp, stream) : launch_prefill<128>(g, sp, stream);
-  if (a.D == 64) return rows == 16 ? launch_decode<64, 1, 4>(g, sp, stream) : launch_decode<64, 2, 4>(g, sp, stream);
-  return rows == 16 ? launch_decode<128, 1, 4>(g, sp, stream) : launch_decode<128, 2, 4>(g, sp, stream);
+  if (a.D == 64) return rows == 16 ? launch_decode<64, 1>(g, sp, stream) : launch_decode<64, 2>(g, sp, stream);
+  return rows == 16 ? launch_decode<128, 1>(g, sp, stream) : launch_decode<128, 2>(g, sp, stream);
 }
 
 }  // namespace cbq
