@@ -276,13 +276,15 @@ __device__ __forceinline__ Queries<D> fetch_queries(const KvAttnArgs& g, const S
   return f;
 }
 
-// Rotated if asked, divided by a power of two near the row's largest value; *rs gets that power.  The rotation is a
+// Rotated if asked, times c, and, where the row's largest value is not within fp16's comfortable range (2^-4 ... 2^15: what
+// falls below 2^-14 there is off by at most 2^-25, as a part of a score nothing), divided by a power of two near
+// that value: *rs, else 1.  The rotation is a
 // product with the +-1 matrix on the matrix cores (bf16 inputs exact, fp32 sums): its row m of tile c
 // is output channel D/4 (m / 4) + 4c + m % 4, so that lane (row, g) gets the channels it needs.  An entry's sign is
 // the parity of the bits that input and output channel share; with input channel D/4 g + 8k + j
 // it falls into parities of j with (m % 4, c % 2), of k with c / 2, and of g with m / 4.
 template <int D>
-__device__ __forceinline__ void convert_queries(const Queries<D>& f, bool rotate, f16x8* out, float* rs) {
+__device__ __forceinline__ void convert_queries(const Queries<D>& f, bool rotate, float c_scale, f16x8* out, float* rs) {
   const int lane = threadIdx.x & 63;
   f32x4 x[D / 16];
   if (rotate) {
@@ -319,13 +321,16 @@ __device__ __forceinline__ void convert_queries(const Queries<D>& f, bool rotate
 #pragma unroll
     for (int j = 0; j < 4; ++j) m = max(m, __builtin_bit_cast(uint32_t, x[c][j]) & 0x7FFFFFFFu);
   m = row_max_u32(m);
+  const float top = __builtin_bit_cast(float, m) * fabsf(c_scale);
+  const bool unit = (top >= 0x1p-4f && top < 0x1p15f) || m == 0;
   const uint32_t e = min(m >> 23, 253u);              // 2^(e-127) <= largest value, or smaller
-  const float inv = __builtin_bit_cast(float, (254u - e) << 23);
-  *rs = m >= 0x7F800000u ? NAN : e ? __builtin_bit_cast(float, e << 23) : 0x1p-127f;
+  const float mul = unit ? c_scale : __builtin_bit_cast(float, (254u - e) << 23);
+  const float p = m >= 0x7F800000u ? NAN : e ? __builtin_bit_cast(float, e << 23) : 0x1p-127f;
+  *rs = unit ? 1.0f : p * c_scale;
 #pragma unroll
   for (int c = 0; c < D / 16; ++c)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) out[c / 2][4 * (c & 1) + j] = (_Float16)(x[c][j] * inv);
+    for (int j = 0; j < 4; ++j) out[c / 2][4 * (c & 1) + j] = (_Float16)(x[c][j] * mul);
 }
 
 // 8 codes -> 8 fp16
@@ -356,16 +361,22 @@ constexpr float kSlack = 8.0f;
 
 template <int D, int NB>
 __device__ __forceinline__ void soft_weights(const float* ks, const float* lv, const float* iv, int t0, bool whole, uint32_t held,
-                                             const float* rs, const int* lo, const int* hi, f32x4 (*sc)[4], float* M, float* l,
+                                             bool unit, const float* rs, const int* lo, const int* hi, f32x4 (*sc)[4], float* M, float* l,
                                              f32x4 (*o)[D / 16], f16x8 (*w)[2]) {
   const int lane = threadIdx.x & 63, key = 4 * (lane >> 4);
+  if (!unit) {
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc[n][i] *= rs[n];
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const f32x4 k = *reinterpret_cast<const f32x4*>(ks + 16 * i + key), v = *reinterpret_cast<const f32x4*>(lv + 16 * i + key);
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sc[n][i][j] = __builtin_fmaf(sc[n][i][j] * k[j], rs[n], v[j]);
+      for (int j = 0; j < 4; ++j) sc[n][i][j] = __builtin_fmaf(sc[n][i][j], k[j], v[j]);
   }
   if (!whole) {
 #pragma unroll
@@ -423,6 +434,15 @@ __device__ __forceinline__ void soft_weights(const float* ks, const float* lv, c
         for (int j = 0; j < 4; ++j) l[n] = sc[n][i][j] != 0.0f ? __builtin_fmaf(sc[n][i][j], v[j], l[n]) : l[n];
     }
   }
+}
+
+// 16 keys' codes of channel 16c + lane % 16: keys 16i + 4 (lane / 16) + j, nibble 4i + j.  v: the tile's codes by key,
+// quarters of a row swizzled by the key's i.
+template <int D>
+__device__ __forceinline__ i32x2 value_codes(const uint8_t* v, int c) {
+  const int lane = threadIdx.x & 63, r = lane & 15, key = 16 * (r >> 2) + 4 * (lane >> 4) + (r & 3);
+  const int chunk = c * 8 / (D / 8), in = c * 8 % (D / 8);
+  return __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2*)(v + key * (D / 2) + (chunk ^ (r >> 2)) * (D / 8) + in));
 }
 
 template <int D> struct Chunk;                        // a quarter of a row of codes
@@ -566,8 +586,7 @@ __global__ __launch_bounds__(64 * WV, 2) void kv_attention_kernel(KvAttnArgs g, 
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       const bool row = 16 * n + (lane & 15) < n_rows;
-      convert_queries<D>(fq[n], a.rotate & 1, qf[n], &rs[n]);
-      rs[n] *= c_scale;
+      convert_queries<D>(fq[n], a.rotate & 1, c_scale, qf[n], &rs[n]);
       const Range w = kv_range(q, div_g(sp, row ? row0 + 16 * n + (lane & 15) : row0), g.causal, g.window);
       lo[n] = w.lo;
       hi[n] = row ? w.hi : 0;
@@ -579,6 +598,9 @@ __global__ __launch_bounds__(64 * WV, 2) void kv_attention_kernel(KvAttnArgs g, 
     const int all_lo = kv_range(q, div_g(sp, row0 + n_rows - 1), g.causal, g.window).lo;   // positions that every row attends
     const int all_hi = kv_range(q, div_g(sp, row0), g.causal, g.window).hi;
     const int t_hi = u.tiles.hi;
+    bool unit = true;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) unit = unit && !__any(rs[n] != 1.0f);
     __syncthreads();                                  // the last part's sums have been read
 
     // ---- the wave's tiles
@@ -592,7 +614,7 @@ __global__ __launch_bounds__(64 * WV, 2) void kv_attention_kernel(KvAttnArgs g, 
         const float v = cu.vs < 0x1p-64f ? 0x1p-64f : cu.vs;
         s.t.ks[wave][lane] = cu.ks;
         s.t.lv[wave][lane] = __builtin_amdgcn_logf(v);
-        s.t.iv[wave][lane] = 1.0f / v;
+        s.t.iv[wave][lane] = __builtin_amdgcn_rcpf(v);
       }
       if (tile + WV < t_hi) {
         if (++at == 16) { pages = tile_pages<WV>(a, u.seq, tile + WV); at = 0; }
@@ -611,18 +633,23 @@ __global__ __launch_bounds__(64 * WV, 2) void kv_attention_kernel(KvAttnArgs g, 
         }
       __builtin_amdgcn_wave_barrier();
       const bool whole = cu.held == 15u && tile * kTile >= all_lo && tile * kTile + kTile <= all_hi;
+      i32x2 vc[D / 16];                               // early where registers allow
+      if constexpr (NB == 1) {
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) vc[c] = value_codes<D>(vl, c);
+      }
       f16x8 w[NB][2];
-      soft_weights<D, NB>(s.t.ks[wave], s.t.lv[wave], s.t.iv[wave], tile * kTile, whole, cu.held, rs, lo, hi, sc, M, l, o, w);
+      soft_weights<D, NB>(s.t.ks[wave], s.t.lv[wave], s.t.iv[wave], tile * kTile, whole, cu.held, unit, rs, lo, hi, sc, M, l, o, w);
+      if constexpr (NB > 1) {
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) vc[c] = value_codes<D>(vl, c);
+      }
       // values times weights, 16 channels at a time
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
-        const int r = lane & 15, key = 16 * (r >> 2) + 4 * (lane >> 4) + (r & 3);
-        const int chunk = c * 8 / (D / 8), in = c * 8 % (D / 8);
-        const uint8_t* src = vl + key * (D / 2) + (chunk ^ (r >> 2)) * (D / 8) + in;
-        const i32x2 x = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2*)src);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const f16x8 vf = e2m1_f16x8((uint32_t)x[k]);
+          const f16x8 vf = e2m1_f16x8((uint32_t)vc[c][k]);
 #pragma unroll
           for (int n = 0; n < NB; ++n) o[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, w[n][k], o[n][c], 0, 0, 0);
         }
@@ -705,8 +732,7 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
       const int rr = 16 * n + (lane & 15);
       const bool row = rr < w_rows;
       const int r = row ? w0 + rr : r0;
-      convert_queries<D>(fetch_queries<D>(g, sp, q, kvh, r, row), a.rotate & 1, qf[n], &rs[n]);
-      rs[n] *= c_scale;
+      convert_queries<D>(fetch_queries<D>(g, sp, q, kvh, r, row), a.rotate & 1, c_scale, qf[n], &rs[n]);
       const Range w = kv_range(q, div_g(sp, r), g.causal, g.window);
       lo[n] = w.lo;
       hi[n] = row ? w.hi : 0;
@@ -722,9 +748,13 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
       any = Range{r_first.lo, r_last.hi};
       every = Range{r_last.lo, r_first.hi};
     }
+    bool unit = true;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) unit = unit && !__any(rs[n] != 1.0f);
 
     // ---- the tiles: each wave brings 16 keys of each
     C kr, vr;
+    const float* scales = ((lane & 16) ? a.scales[1] : a.scales[0]) + (lane & 15);
     float scale = 0;
     int held = 0, pages = 0;
     auto fetch = [&](int tile, int at) {
@@ -734,7 +764,7 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
       const int64_t row = ((int64_t)(p * a.n_kv + kvh) << a.logp) + ((tile * kTile + 16 * wave) & mask);
       kr = *reinterpret_cast<const C*>(a.codes[0] + row * (D / 2) + lane * (D / 8));
       vr = *reinterpret_cast<const C*>(a.codes[1] + row * (D / 2) + lane * (D / 8));
-      scale = a.scales[(lane >> 4) & 1][row + (lane & 15)];
+      scale = scales[row];
     };
     auto page_batch = [&](int tile) { pages = kv_page(a, b, (int64_t)(tile + lane) * kTile + 16 * wave); };
     page_batch(t_lo);
@@ -747,11 +777,11 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
         const int key = 16 * wave + (lane >> 2);
         *reinterpret_cast<C*>(B.k + key * (D / 2) + ((lane & 3) ^ ((lane >> 4) & 3)) * (D / 8)) = kr;
         *reinterpret_cast<C*>(B.v + key * (D / 2) + ((lane & 3) ^ wave) * (D / 8)) = vr;
+        const float v = scale < 0x1p-64f ? 0x1p-64f : scale;
         if (lane < 16) B.ks[16 * wave + lane] = scale;
-        else if (lane < 32) {
-          const float v = scale < 0x1p-64f ? 0x1p-64f : scale;
+        if (lane >= 16 && lane < 32) {
           B.lv[16 * wave + lane - 16] = __builtin_amdgcn_logf(v);
-          B.iv[16 * wave + lane - 16] = 1.0f / v;
+          B.iv[16 * wave + lane - 16] = __builtin_amdgcn_rcpf(v);
         }
         if (lane == 0) B.held[wave] = held;
       }
@@ -778,17 +808,16 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
         }
       const uint32_t held4 = B.held[0] | B.held[1] << 1 | B.held[2] << 2 | B.held[3] << 3;
       const bool whole = held4 == 15 && t0 >= every.lo && t0 + kTile <= every.hi;
+      i32x2 vc[D / 16];
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) vc[c] = value_codes<D>(B.v, c);
       f16x8 w[NB][2];
-      soft_weights<D, NB>(B.ks, B.lv, B.iv, t0, whole, held4, rs, lo, hi, sc, M, l, o, w);
+      soft_weights<D, NB>(B.ks, B.lv, B.iv, t0, whole, held4, unit, rs, lo, hi, sc, M, l, o, w);
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
-        const int r = lane & 15, key = 16 * (r >> 2) + 4 * (lane >> 4) + (r & 3);
-        const int chunk = c * 8 / (D / 8), in = c * 8 % (D / 8);
-        const uint8_t* src = B.v + key * (D / 2) + (chunk ^ (r >> 2)) * (D / 8) + in;
-        const i32x2 x = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2*)src);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const f16x8 vf = e2m1_f16x8((uint32_t)x[k]);
+          const f16x8 vf = e2m1_f16x8((uint32_t)vc[c][k]);
 #pragma unroll
           for (int n = 0; n < NB; ++n) o[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, w[n][k], o[n][c], 0, 0, 0);
         }
@@ -825,6 +854,367 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
     }
     if (starts && !ends && tid == 0)
       sp.desc[blockIdx.x] = Desc{b, kvh, r0, u.following(sp)};
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Long prompts: 256 query rows of one key/value head a workgroup, 64 a wave.  With 64 rows behind each converted
+// code the vector instructions a score costs (the bound) are fewest: conversion, 2 of 7, halves.
+// Four waves hold the rows and go through the even key tiles, four more the same rows and the odd ones; the
+// two waves of a SIMD so share one set of queries, which does not fit the registers beside the 128 sums a
+// lane holds and lies in LDS in the order the matrix instructions read it (64 KB).  32x32x16 MFMA: keys
+// times queries, then channels times weights, in steps of 32 keys; lane (row r = lane % 32, h = lane / 32)
+// has the scores of keys 8b + 4h + j.  At the end the pairs of waves join their sums through LDS.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+template <int D>
+struct LongLds {
+  struct Buf {
+    alignas(16) uint8_t k[kTile * D / 2], v[kTile * D / 2];
+    alignas(16) float ks[kTile], lv[kTile], iv[kTile];
+    int held[4];
+  };
+  struct Main {
+    alignas(16) f16x8 q[4][2][D / 16][64];            // [rows' wave][row tile][step][lane]
+    Buf buf[2][2];                                    // [key group][double]
+  };
+  union {
+    Main t;
+    alignas(16) f32x4 o[8][D / 8][64];                // a wave's sums of the row tile that its partner finishes
+  };
+  float rs[256];
+  float m[8][32], l[8][32];
+};
+
+template <int D>
+__global__ __launch_bounds__(512, 2) void kv_long_kernel(KvAttnArgs g, SplitArgs sp) {
+  constexpr int ROWS = 256, CT = D / 32;
+  typedef typename Chunk<D>::T C;
+  __shared__ LongLds<D> s;
+  const KvArgs& a = g.kv;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int rg = wave & 3, kg = wave >> 2, h = lane >> 5;
+  const uint32_t mask = (1u << a.logp) - 1;
+  if (tid == 0 && sp.split) sp.desc[blockIdx.x].more = 0;
+  Walk<ROWS> u;
+  u.start(g, sp);
+  const float c_scale = g.scale * sp.c_q * 1.44269504088896341f;
+  while (u.next(g, sp)) {
+    const Seq q = u.q;
+    const int r0 = u.row0, kvh = u.h, b = u.seq;
+    const int t_lo = u.tiles.lo, t_hi = u.tiles.hi;
+    const int w0 = r0 + 64 * rg;                      // the wave's first row
+    const int w_rows = min(64, q.rows - w0);          // may be <= 0
+
+    // ---- the first keys on their way; the queries: each wave of a pair converts 32 rows
+    C kr, vr;
+    const float* scales = ((lane & 16) ? a.scales[1] : a.scales[0]) + (lane & 15);
+    float scale = 0;
+    int held = 0, pages = 0;
+    auto page_batch = [&](int tile) { pages = kv_page(a, b, (int64_t)(tile + 2 * lane) * kTile + 16 * rg); };
+    auto fetch = [&](int tile, int at) {              // 16 keys of the key group's tile
+      const int p0 = __builtin_amdgcn_readlane(pages, at);
+      held = p0 >= 0;
+      const int p = p0 >= 0 ? p0 : 0;                 // keys in no page: any page is read, and masked
+      const int64_t row = ((int64_t)(p * a.n_kv + kvh) << a.logp) + ((tile * kTile + 16 * rg) & mask);
+      kr = *reinterpret_cast<const C*>(a.codes[0] + row * (D / 2) + lane * (D / 8));
+      vr = *reinterpret_cast<const C*>(a.codes[1] + row * (D / 2) + lane * (D / 8));
+      scale = scales[row];
+    };
+    page_batch(t_lo + kg);
+    Queries<D> fq[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int rr = 32 * kg + 16 * n + (lane & 15);
+      fq[n] = fetch_queries<D>(g, sp, q, kvh, rr < w_rows ? w0 + rr : r0, rr < w_rows);
+    }
+    fetch(t_lo + kg, 0);
+    __syncthreads();                                  // the last row block's sums have been read
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      f16x8 qf[D / 32];
+      float r;
+      convert_queries<D>(fq[n], a.rotate & 1, c_scale, qf, &r);
+      if (lane < 16) s.rs[64 * rg + 32 * kg + 16 * n + lane] = r;
+      const int g4 = lane >> 4;                       // its channels: D/4 g4 + 8k ...
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k)
+        s.t.q[rg][kg][(g4 & 1) * (D / 32) + k][16 * n + (lane & 15) + 32 * (g4 >> 1)] = qf[k];
+    }
+    Range any{0, 0}, every{0, 0};                     // positions that some, that every row of the wave attends
+    float M[2], l[2];
+    f32x16 o[2][CT];
+    int lo[2], hi[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int rr = 32 * n + (lane & 31);
+      const Range w = kv_range(q, div_g(sp, rr < w_rows ? w0 + rr : r0), g.causal, g.window);
+      lo[n] = w.lo;
+      hi[n] = rr < w_rows ? w.hi : 0;
+      M[n] = -INFINITY;
+      l[n] = 0;
+#pragma unroll
+      for (int c = 0; c < CT; ++c) o[n][c] = (f32x16)(0.0f);
+    }
+    if (w_rows > 0) {
+      const Range r_first = kv_range(q, div_g(sp, w0), g.causal, g.window);
+      const Range r_last = kv_range(q, div_g(sp, w0 + w_rows - 1), g.causal, g.window);
+      any = Range{r_first.lo, r_last.hi};
+      every = Range{r_last.lo, r_first.hi};
+    }
+
+    // ---- the tiles, two at a time
+    int at = 0;
+    bool unit = true;                                 // no row of the wave needs its power
+    for (int pair = t_lo; pair < t_hi; pair += 2) {
+      const int tile = pair + kg;
+      auto& B = s.t.buf[kg][((pair - t_lo) >> 1) & 1];
+      {
+        const int key = 16 * rg + (lane >> 2);
+        // quarters of a row swizzled so that 16 lanes' reads fall into different banks
+        const int kx = D == 128 ? (key >> 2) & 3 : 2 * ((key >> 3) & 1), vx = D == 128 ? (key >> 3) & 3 : 2 * ((key >> 3) & 1);
+        *reinterpret_cast<C*>(B.k + key * (D / 2) + ((lane & 3) ^ kx) * (D / 8)) = kr;
+        *reinterpret_cast<C*>(B.v + key * (D / 2) + ((lane & 3) ^ vx) * (D / 8)) = vr;
+        const float v = scale < 0x1p-64f ? 0x1p-64f : scale;
+        if (lane < 16) B.ks[16 * rg + lane] = scale;
+        if (lane >= 16 && lane < 32) {
+          B.lv[16 * rg + lane - 16] = __builtin_amdgcn_logf(v);
+          B.iv[16 * rg + lane - 16] = __builtin_amdgcn_rcpf(v);
+        }
+        if (lane == 0) B.held[rg] = held;
+      }
+      lds_barrier();
+      if (pair + 2 < t_hi) {
+        if (++at == 64) { page_batch(tile + 2); at = 0; }
+        fetch(tile + 2, at);
+      }
+      if (pair == t_lo) unit = !__any(s.rs[64 * rg + lane] != 1.0f);
+      const int t0 = tile * kTile;
+      if (tile >= t_hi || t0 >= any.hi || t0 + kTile <= any.lo) continue;
+      const uint32_t held4 = B.held[0] | B.held[1] << 1 | B.held[2] << 2 | B.held[3] << 3;
+      const bool whole = held4 == 15 && t0 >= every.lo && t0 + kTile <= every.hi;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        // scores of 32 keys; the queries are read anew for each (an offset that the compiler cannot see through
+        // keeps it from holding all of them in registers)
+        __builtin_amdgcn_s_setprio(1);                // the matrix cores first: the other wave's vector work fills in
+        f32x16 sc[2];
+        {
+          const int key = 32 * half + (lane & 31);
+          uint32_t kc[D / 16];
+          if constexpr (D == 128) {
+            const int kx = (key >> 2) & 3;
+            const u32x4 x = *reinterpret_cast<const u32x4*>(B.k + key * 64 + ((2 * h) ^ kx) * 16);
+            const u32x4 y = *reinterpret_cast<const u32x4*>(B.k + key * 64 + ((2 * h + 1) ^ kx) * 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) { kc[i] = x[i]; kc[4 + i] = y[i]; }
+          } else {
+            const u32x4 x = *reinterpret_cast<const u32x4*>(B.k + key * 32 + (h ^ ((key >> 3) & 1)) * 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) kc[i] = x[i];
+          }
+          int ql = lane;
+          asm("" : "+v"(ql));
+          const f16x8* qp = &s.t.q[rg][0][0][ql];
+          f16x8 qf[2][2];                             // a step ahead
+#pragma unroll
+          for (int n = 0; n < 2; ++n) qf[0][n] = qp[n * (D / 16) * 64];
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            if (k + 1 < D / 16) {
+#pragma unroll
+              for (int n = 0; n < 2; ++n) qf[(k + 1) % 2][n] = qp[(n * (D / 16) + k + 1) * 64];
+            }
+            const f16x8 kf = e2m1_f16x8(kc[k]);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+              sc[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[k % 2][n], k ? sc[n] : (f32x16)(0.0f), 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+        i32x2 vc[CT];                                 // 32 channels at a time
+        {
+          const int r = lane & 15, key = 32 * half + 8 * (r >> 2) + 4 * h + (r & 3);
+#pragma unroll
+          for (int c = 0; c < CT; ++c) {
+            const int quarter = D == 128 ? c ^ (r >> 2) : c ^ ((r >> 2) & 1);  // 16 bytes hold 32 channels
+            vc[c] = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2*)(B.v + key * (D / 2) + quarter * 16 + ((lane >> 4) & 1) * 8));
+          }
+        }
+        // weights
+        __builtin_amdgcn_s_setprio(0);
+        f16x8 w[2][2];
+        const float *kp = &B.ks[32 * half + 4 * h], *lp = &B.lv[32 * half + 4 * h], *ip = &B.iv[32 * half + 4 * h];
+        if (!unit) {
+          sc[0] *= s.rs[64 * rg + (lane & 31)];
+          sc[1] *= s.rs[64 * rg + 32 + (lane & 31)];
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const f32x4 ks = *reinterpret_cast<const f32x4*>(kp + 8 * c), lv = *reinterpret_cast<const f32x4*>(lp + 8 * c);
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sc[n][4 * c + j] = __builtin_fmaf(sc[n][4 * c + j], ks[j], lv[j]);
+        }
+        if (!whole) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int from = t0 + 32 * half + 4 * h - lo[n];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t len = (held4 >> (2 * half + c / 2)) & 1 ? (uint32_t)max(hi[n] - lo[n], 0) : 0u;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) sc[n][4 * c + j] = (uint32_t)(from + 8 * c + j) < len ? sc[n][4 * c + j] : -INFINITY;
+            }
+          }
+        }
+        float mx[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          mx[n] = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) mx[n] = fmaxf(mx[n], sc[n][i]);
+        }
+        if (__any(mx[0] > M[0] + kSlack || mx[1] > M[1] + kSlack)) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            float x, y;
+            swap_pair<true>(mx[n], x, y);
+            const float rm = fmaxf(x, y), m = rm > M[n] + kSlack ? rm : M[n];   // a row moves for its own scores alone
+            const float keep = __builtin_amdgcn_exp2f(M[n] - safe_max(m));
+            l[n] *= keep;
+#pragma unroll
+            for (int c = 0; c < CT; ++c) o[n][c] *= keep;
+            M[n] = m;
+          }
+        }
+        const float ref[2] = {safe_max(M[0]), safe_max(M[1])};
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float p = __builtin_amdgcn_exp2f(sc[n][i] - ref[n]);
+            sc[n][i] = p;
+            w[n][i >> 3][i & 7] = (_Float16)p;
+          }
+        if (whole) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const f32x4 iv = *reinterpret_cast<const f32x4*>(ip + 8 * c);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) l[n] = __builtin_fmaf(sc[n][4 * c + j], iv[j], l[n]);
+          }
+        } else {                                      // a masked key's 1 / vs may be NaN
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const f32x4 iv = *reinterpret_cast<const f32x4*>(ip + 8 * c);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                l[n] = sc[n][4 * c + j] != 0.0f ? __builtin_fmaf(sc[n][4 * c + j], iv[j], l[n]) : l[n];
+          }
+        }
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const f16x8 vf = e2m1_f16x8((uint32_t)vc[c][k]);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) o[n][c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, w[n][k], o[n][c], 0, 0, 0);
+          }
+      }
+    }
+
+    // ---- the pairs' sums joined: a wave finishes row tile kg and hands the other one over
+    __syncthreads();
+    float sum[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      float x, y;
+      swap_pair<true>(l[n], x, y);
+      sum[n] = x + y;
+    }
+    if (lane < 32) {
+      s.m[wave][lane] = kg ? M[0] : M[1];
+      s.l[wave][lane] = kg ? sum[0] : sum[1];
+    }
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f32x4 x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = kg ? o[0][c][4 * e + j] : o[1][c][4 * e + j];
+        s.o[wave][4 * c + e][lane] = x;
+      }
+    __syncthreads();
+    const int other = wave ^ 4;
+    const float m0 = kg ? M[1] : M[0], m1 = s.m[other][lane & 31];
+    const float m = fmaxf(m0, m1), ref = safe_max(m);
+    const float f0 = __builtin_amdgcn_exp2f(m0 - ref), f1 = __builtin_amdgcn_exp2f(m1 - ref);
+    const float total = (kg ? sum[1] : sum[0]) * f0 + s.l[other][lane & 31] * f1;
+    f32x4 x[D / 8];                                   // channels 8i + 4h + j of row lane % 32
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const f32x4 y = s.o[other][4 * c + e][lane];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[4 * c + e][j] = (kg ? o[1][c][4 * e + j] : o[0][c][4 * e + j]) * f0 + y[j] * f1;
+      }
+    const bool starts = u.u0 == 0, ends = u.u1 == u.units;
+    const int64_t part = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
+    const int rr = 32 * kg + (lane & 31);
+    if (starts && ends) {
+      if (a.rotate & 2) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const f32x4 v = x[i];
+          const float p = v[0] + v[1], t = v[0] - v[1], d = v[2] + v[3], e = v[2] - v[3];
+          x[i] = f32x4{p + d, t + e, p - d, t - e};
+        }
+#pragma unroll
+        for (int k = 1; k < D / 8; k *= 2)
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+            if (!(i & k)) {
+              const f32x4 v = x[i], y = x[i + k];
+              x[i] = v + y;
+              x[i + k] = v - y;
+            }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float p, t;
+            swap_pair<true>(x[i][j], p, t);
+            x[i][j] = h ? p - t : p + t;
+          }
+      }
+      if (rr < w_rows) {
+        const float f = total != 0.0f ? sp.c_v / total : 0.0f;
+        const int r = w0 + rr, i = div_g(sp, r), head = r - i * sp.G;
+        uint16_t* dst = g.out + (int64_t)(q.t0 + i) * g.ldo + (kvh * sp.G + head) * D + 4 * h;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          u32x2 y;
+          y[0] = (uint32_t)f32_to_bf16_rne(x[k][0] * f) | ((uint32_t)f32_to_bf16_rne(x[k][1] * f) << 16);
+          y[1] = (uint32_t)f32_to_bf16_rne(x[k][2] * f) | ((uint32_t)f32_to_bf16_rne(x[k][3] * f) << 16);
+          *reinterpret_cast<u32x2*>(dst + 8 * k) = y;
+        }
+      }
+    } else if (rr < w_rows) {
+      const int64_t at_row = part * ROWS + 64 * rg + rr;
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) *reinterpret_cast<f32x4*>(sp.o + at_row * D + 8 * k + 4 * h) = x[k];
+      if (lane < 32) sp.ml[at_row] = float2{m, total};
+    }
+    if (starts && !ends && tid == 0) sp.desc[blockIdx.x] = Desc{b, kvh, r0, u.following(sp)};
   }
 }
 
@@ -886,7 +1276,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs g, SplitArgs sp
 // else 128, each wave its own 32.
 int row_block(int64_t T, int B, int G) {
   const int64_t rows = (T + B - 1) / B * G;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
 }
 
 template <int D, int NB>
@@ -904,6 +1294,15 @@ hipError_t launch_prefill(const KvAttnArgs& g, SplitArgs sp, hipStream_t stream)
   if (hipError_t e = hipGetLastError()) return e;
   if (!sp.split) return hipSuccess;
   kv_join_kernel<D, 128, 8><<<dim3(sp.groups, (sp.join_rows + 7) / 8), 256, 0, stream>>>(g, sp);
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_long(const KvAttnArgs& g, SplitArgs sp, hipStream_t stream) {
+  kv_long_kernel<D><<<sp.groups, 512, 0, stream>>>(g, sp);
+  if (hipError_t e = hipGetLastError()) return e;
+  if (!sp.split) return hipSuccess;
+  kv_join_kernel<D, 256, 8><<<dim3(sp.groups, (sp.join_rows + 7) / 8), 256, 0, stream>>>(g, sp);
   return hipGetLastError();
 }
 
@@ -932,17 +1331,18 @@ hipError_t launch_kv_attention(const KvAttnArgs& g, hipStream_t stream) {
   sp.join_rows = a.offsets || own > rows ? rows : (int)own;
   const int64_t blocks = ((a.T * G + rows - 1) / rows + a.B) * a.n_kv;      // row blocks at most
   const int64_t cap = ((int64_t)a.max_pages << a.logp) / kTile + 1;         // key tiles of one at most
-  sp.split = rows == 128 ? blocks < 3 * most && cap > 16 : cap > 32;
+  sp.split = rows >= 128 ? blocks < 3 * most && cap > 16 : cap > 32;
   sp.min_units = 1;
   int64_t want = blocks;
   if (sp.split) {
     sp.min_units = 4;
-    sp.start_cost = rows == 128 ? 1 : 16;
+    sp.start_cost = rows >= 128 ? 1 : 16;
     while (blocks * ((cap >> sp.shift) + 1 + sp.start_cost) >= 0x7FFFFFFF - most) ++sp.shift;
     want = (blocks * ((cap >> sp.shift) + 1 + sp.start_cost) + sp.min_units - 1) / sp.min_units;
   }
-  const int64_t limit = rows == 128 && !sp.split ? 1 << 22 : most;
+  const int64_t limit = rows >= 128 && !sp.split ? 1 << 22 : most;
   sp.groups = (int)(want < limit ? want : limit);
+  if (rows == 256) return a.D == 64 ? launch_long<64>(g, sp, stream) : launch_long<128>(g, sp, stream);
   if (rows == 128) return a.D == 64 ? launch_prefill<64>(g, sp, stream) : launch_prefill<128>(g, sp, stream);
   if (a.D == 64) return rows == 16 ? launch_decode<64, 1>(g, sp, stream) : launch_decode<64, 2>(g, sp, stream);
   return rows == 16 ? launch_decode<128, 1>(g, sp, stream) : launch_decode<128, 2>(g, sp, stream);
