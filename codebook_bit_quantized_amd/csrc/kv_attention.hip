@@ -210,17 +210,17 @@ struct Walk {
   }
 };
 
-template <int D, int NB, int WV>
+template <int D>
 struct Lds {
-  static constexpr int ROWS = 16 * NB, P = D + 4;    // padded row: 16 rows start in 16 different bank groups
+  static constexpr int P = D + 4;                     // padded row: 16 rows start in 16 different bank groups
   union {
     struct {
-      alignas(16) uint8_t v[WV][kTile * D / 2];                  // values' codes, 16-byte (8-byte) quarters of a row swizzled
-      alignas(16) float ks[WV][kTile], lv[WV][kTile], iv[WV][kTile];
+      alignas(16) uint8_t v[kWaves][kTile * D / 2];                  // values' codes, 16-byte (8-byte) quarters of a row swizzled
+      alignas(16) float ks[kWaves][kTile], lv[kWaves][kTile], iv[kWaves][kTile];
     } t;
-    alignas(16) float o[WV][ROWS * P];
+    alignas(16) float o[kWaves][16 * P];
   };
-  float m[WV][ROWS], l[WV][ROWS];
+  float m[kWaves][16], l[kWaves][16];
 };
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -487,10 +487,10 @@ __device__ __forceinline__ void load_tile(const KvArgs& a, int kvh, int tile, in
   r.held = held;
 }
 
-template <int D, int NB, int WV>
-__global__ __launch_bounds__(64 * WV, 2) void kv_attention_kernel(KvAttnArgs g, SplitArgs sp) {
-  constexpr int ROWS = 16 * NB, NT = 64 * WV, P = Lds<D, NB, WV>::P, L = D / 8;
-  __shared__ Lds<D, NB, WV> s;
+template <int D>
+__global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_kernel(KvAttnArgs g, SplitArgs sp) {
+  constexpr int ROWS = 16, WV = kWaves, P = Lds<D>::P, L = D / 8;
+  __shared__ Lds<D> s;
   const KvArgs& a = g.kv;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   if (tid == 0 && sp.split) sp.desc[blockIdx.x].more = 0;
@@ -501,8 +501,8 @@ __global__ __launch_bounds__(64 * WV, 2) void kv_attention_kernel(KvAttnArgs g, 
   Seq q;                                              // the part in hand
   int row0 = 0, n_rows = 0, kvh = 0;
   bool have = false, starts = false, ends = false;
-  float M[NB], l[NB];
-  f32x4 o[NB][D / 16];
+  float M[1], l[1];
+  f32x4 o[1][D / 16];
   for (;;) {
     // ---- the next part: its first keys are on their way before the last part's sums are joined
     const bool more = u.next(g, sp);
@@ -512,35 +512,28 @@ __global__ __launch_bounds__(64 * WV, 2) void kv_attention_kernel(KvAttnArgs g, 
     if (mine) pages = tile_pages<WV>(a, u.seq, tile);
     if (have) {
       __syncthreads();
-#pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        const int row = 16 * n + (lane & 15);
-        const float lsum = row_add(l[n]);
-        if (lane < 16) {
-          s.m[wave][row] = M[n];
-          s.l[wave][row] = lsum;
-        }
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c)
-          *reinterpret_cast<f32x4*>(&s.o[wave][row * P + 16 * c + 4 * (lane >> 4)]) = o[n][c];
+      const int row = lane & 15;
+      const float lsum = row_add(l[0]);
+      if (lane < 16) {
+        s.m[wave][row] = M[0];
+        s.l[wave][row] = lsum;
       }
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+        *reinterpret_cast<f32x4*>(&s.o[wave][row * P + 16 * c + 4 * (lane >> 4)]) = o[0][c];
       __syncthreads();
     }
-    Queries<D> fq[NB];
+    Queries<D> fq;
     if (more) {
-#pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        const int r = u.row0 + 16 * n + (lane & 15);
-        fq[n] = fetch_queries<D>(g, sp, u.q, u.h, min(r, u.q.rows - 1), r < u.q.rows);
-      }
+      const int r = u.row0 + (lane & 15);
+      fq = fetch_queries<D>(g, sp, u.q, u.h, min(r, u.q.rows - 1), r < u.q.rows);
     }
     if (mine) load_tile<D>(a, u.h, tile, pages, 0, nx);
     if (have) {
       const int64_t part = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
       const int sub = tid % L;
-      for (int b0 = 0; b0 < ROWS; b0 += NT / L) {
-        const int row = b0 + tid / L;
-        if (row >= n_rows) continue;                  // whole groups of L lanes
+      const int row = tid / L;
+      if (row < n_rows) {                             // whole groups of L lanes
         float m = -INFINITY, sum = 0, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < WV; ++w) m = fmaxf(m, s.m[w][row]);
@@ -580,27 +573,20 @@ __global__ __launch_bounds__(64 * WV, 2) void kv_attention_kernel(KvAttnArgs g, 
       sp.desc[blockIdx.x] = Desc{u.seq, kvh, row0, u.following(sp)};
 
     // ---- the queries, and what each row attends
-    f16x8 qf[NB][D / 32];
-    float rs[NB];
-    int lo[NB], hi[NB];
+    f16x8 qf[D / 32];
+    float rs[1];
+    convert_queries<D>(fq, a.rotate & 1, c_scale, qf, rs);
+    const bool row = (lane & 15) < n_rows;
+    const Range attended = kv_range(q, div_g(sp, row ? row0 + (lane & 15) : row0), g.causal, g.window);
+    const int lo[1] = {attended.lo}, hi[1] = {row ? attended.hi : 0};
+    M[0] = -INFINITY;
+    l[0] = 0;
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      const bool row = 16 * n + (lane & 15) < n_rows;
-      convert_queries<D>(fq[n], a.rotate & 1, c_scale, qf[n], &rs[n]);
-      const Range w = kv_range(q, div_g(sp, row ? row0 + 16 * n + (lane & 15) : row0), g.causal, g.window);
-      lo[n] = w.lo;
-      hi[n] = row ? w.hi : 0;
-      M[n] = -INFINITY;
-      l[n] = 0;
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) o[n][c] = f32x4{0, 0, 0, 0};
-    }
+    for (int c = 0; c < D / 16; ++c) o[0][c] = f32x4{0, 0, 0, 0};
     const int all_lo = kv_range(q, div_g(sp, row0 + n_rows - 1), g.causal, g.window).lo;   // positions that every row attends
     const int all_hi = kv_range(q, div_g(sp, row0), g.causal, g.window).hi;
     const int t_hi = u.tiles.hi;
-    bool unit = true;
-#pragma unroll
-    for (int n = 0; n < NB; ++n) unit = unit && !__any(rs[n] != 1.0f);
+    const bool unit = !__any(rs[0] != 1.0f);
     __syncthreads();                                  // the last part's sums have been read
 
     // ---- the wave's tiles
@@ -621,37 +607,28 @@ __global__ __launch_bounds__(64 * WV, 2) void kv_attention_kernel(KvAttnArgs g, 
         load_tile<D>(a, kvh, tile + WV, pages, at, nx);
       }
       // scores of 64 keys
-      f32x4 sc[NB][4];
+      f32x4 sc[1][4];
 #pragma unroll
       for (int k = 0; k < D / 32; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const f16x8 kf = e2m1_f16x8(cu.k[i][k]);
-#pragma unroll
-          for (int n = 0; n < NB; ++n)
-            sc[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[n][k], k ? sc[n][i] : f32x4{0, 0, 0, 0}, 0, 0, 0);
+          sc[0][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[k], k ? sc[0][i] : f32x4{0, 0, 0, 0}, 0, 0, 0);
         }
       __builtin_amdgcn_wave_barrier();
       const bool whole = cu.held == 15u && tile * kTile >= all_lo && tile * kTile + kTile <= all_hi;
-      i32x2 vc[D / 16];                               // early where registers allow
-      if constexpr (NB == 1) {
+      i32x2 vc[D / 16];
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) vc[c] = value_codes<D>(vl, c);
-      }
-      f16x8 w[NB][2];
-      soft_weights<D, NB>(s.t.ks[wave], s.t.lv[wave], s.t.iv[wave], tile * kTile, whole, cu.held, unit, rs, lo, hi, sc, M, l, o, w);
-      if constexpr (NB > 1) {
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) vc[c] = value_codes<D>(vl, c);
-      }
+      for (int c = 0; c < D / 16; ++c) vc[c] = value_codes<D>(vl, c);
+      f16x8 w[1][2];
+      soft_weights<D, 1>(s.t.ks[wave], s.t.lv[wave], s.t.iv[wave], tile * kTile, whole, cu.held, unit, rs, lo, hi, sc, M, l, o, w);
       // values times weights, 16 channels at a time
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const f16x8 vf = e2m1_f16x8((uint32_t)vc[c][k]);
-#pragma unroll
-          for (int n = 0; n < NB; ++n) o[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, w[n][k], o[n][c], 0, 0, 0);
+          o[0][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, w[0][k], o[0][c], 0, 0, 0);
         }
       }
       __builtin_amdgcn_wave_barrier();
@@ -1272,19 +1249,18 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs g, SplitArgs sp
   finish_row<D>(v, sum, g.kv.rotate & 2, sp.c_v, sub, g.out + (int64_t)(q.t0 + i) * g.ldo + (d.kvh * sp.G + h) * D + 8 * sub);
 }
 
-// Query rows of a row block: 16 or 32, all in every wave, for at most 32 rows a sequence on average;
-// else 128, each wave its own 32.
+// Query rows of a row block, by the rows a sequence has on average.
 int row_block(int64_t T, int B, int G) {
   const int64_t rows = (T + B - 1) / B * G;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
+  return rows <= 128 ? 16 : rows <= 256 ? 128 : 256;
 }
 
-template <int D, int NB>
+template <int D>
 hipError_t launch_decode(const KvAttnArgs& g, SplitArgs sp, hipStream_t stream) {
-  kv_attention_kernel<D, NB, kWaves><<<sp.groups, 64 * kWaves, 0, stream>>>(g, sp);
+  kv_attention_kernel<D><<<sp.groups, 64 * kWaves, 0, stream>>>(g, sp);
   if (hipError_t e = hipGetLastError()) return e;
   if (!sp.split) return hipSuccess;
-  kv_join_kernel<D, 16 * NB, 1><<<dim3(sp.groups, sp.join_rows), 256, 0, stream>>>(g, sp);
+  kv_join_kernel<D, 16, 1><<<dim3(sp.groups, sp.join_rows), 256, 0, stream>>>(g, sp);
   return hipGetLastError();
 }
 
@@ -1344,8 +1320,7 @@ hipError_t launch_kv_attention(const KvAttnArgs& g, hipStream_t stream) {
   sp.groups = (int)(want < limit ? want : limit);
   if (rows == 256) return a.D == 64 ? launch_long<64>(g, sp, stream) : launch_long<128>(g, sp, stream);
   if (rows == 128) return a.D == 64 ? launch_prefill<64>(g, sp, stream) : launch_prefill<128>(g, sp, stream);
-  if (a.D == 64) return rows == 16 ? launch_decode<64, 1>(g, sp, stream) : launch_decode<64, 2>(g, sp, stream);
-  return rows == 16 ? launch_decode<128, 1>(g, sp, stream) : launch_decode<128, 2>(g, sp, stream);
+  return a.D == 64 ? launch_decode<64>(g, sp, stream) : launch_decode<128>(g, sp, stream);
 }
 
 }  // namespace cbq

@@ -43,35 +43,56 @@ __device__ __forceinline__ f16x2 e2m1_pair(uint32_t x) {
   return __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(x, 1.0f, SEL));
 }
 
-// Butterfly stages of a D-channel transform whose channels lie 8 to a lane in D/8 lanes.
 template <int M, typename T>
 __device__ __forceinline__ T kv_xor_lane(T v) {
   if constexpr (sizeof(T) == 8) return xor_lane_f64<M>(v);
   else return xor_lane_f32<M>(v);
 }
 
-template <int M, typename T>
+// One butterfly stage of N values a lane with the lane M away: v + p in the lower lane, p - v in the
+// upper, as one fma by +-1 (an exact product; hidden from the compiler, which would select between two adds).
+template <int M, int N, typename T>
 __device__ __forceinline__ void kv_lane_stage(T* v, int lane) {
-  const T sgn = (lane & M) ? (T)-1 : (T)1;
+  T sgn = (lane & M) ? (T)-1 : (T)1;
+  asm("" : "+v"(sgn));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = v[i] * sgn + kv_xor_lane<M>(v[i]);   // exact product: one rounding
+  for (int i = 0; i < N; ++i) {
+    const T p = kv_xor_lane<M>(v[i]);
+    if constexpr (sizeof(T) == 8) v[i] = __builtin_fma(v[i], sgn, p);
+    else v[i] = __builtin_fmaf(v[i], sgn, p);
+  }
 }
 
-template <int D, typename T>
-__device__ __forceinline__ void kv_transform(T* v, int lane) {
+// Butterfly stages over the low bits of the index of N values in a lane, N = 2^k: strides from, 2 from, ... below to.
+template <int N, typename T>
+__device__ __forceinline__ void kv_reg_stages(T* v, int from, int to) {
 #pragma unroll
-  for (int h = 1; h < 8; h *= 2)
+  for (int h = 1; h < N; h *= 2) {
+    if (h < from || h >= to) continue;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < N; ++i)
       if (!(i & h)) {
         const T x = v[i], y = v[i + h];
         v[i] = x + y;
         v[i + h] = x - y;
       }
-  kv_lane_stage<1>(v, lane);
-  kv_lane_stage<2>(v, lane);
-  kv_lane_stage<4>(v, lane);
-  if constexpr (D >= 128) kv_lane_stage<8>(v, lane);
+  }
+}
+
+// The stages between L neighbouring lanes.
+template <int L, int N, typename T>
+__device__ __forceinline__ void kv_lane_stages(T* v, int lane) {
+  kv_lane_stage<1, N>(v, lane);
+  kv_lane_stage<2, N>(v, lane);
+  if constexpr (L > 4) kv_lane_stage<4, N>(v, lane);
+  if constexpr (L > 8) kv_lane_stage<8, N>(v, lane);
+}
+
+// Transform of D channels that lie 8 to a lane in D/8 lanes.
+template <int D, typename T>
+__device__ __forceinline__ void kv_transform(T* v, int lane) {
+  kv_reg_stages<8>(v, 1, 8);
+  kv_lane_stages<D / 8, 8>(v, lane);
 }
 
 }  // namespace cbq
