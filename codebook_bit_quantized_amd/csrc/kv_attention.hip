@@ -103,7 +103,7 @@ __device__ __forceinline__ int head_units(const KvAttnArgs& g, const SplitArgs& 
 }
 
 // The row blocks, or parts of them, that a workgroup works through.  All sequences' units in a row (a
-// sequence's in the order head, row block, key tile) are dealt out evenly, `per` to a workgroup; each
+// sequence's in the order head, row block, key tile; whole row blocks in the order row block, head) are dealt out evenly, `per` to a workgroup; each
 // wave counts them for itself, from the lengths, so the lengths stay on the device and the work is even
 // whatever they are.
 template <int ROWS>
@@ -166,17 +166,37 @@ struct Walk {
       q = get(a, sp, b);
       const int hu = head_units<ROWS>(g, sp, q);
       if (off < hu * a.n_kv) {
-        kvh = off / hu;
-        off -= kvh * hu;
+        if (sp.split) {
+          kvh = off / hu;
+          off -= kvh * hu;
+        } else {
+          r0 = off / a.n_kv * ROWS;
+          kvh = off % a.n_kv;
+        }
         break;
       }
       off -= hu * a.n_kv;
     }
-    if (!sp.split) { r0 = off * ROWS; off = 0; }
   }
 
   __device__ __forceinline__ bool next(const KvAttnArgs& g, const SplitArgs& sp) {
     if (left <= 0) return false;
+    if (!sp.split) {
+      while (r0 >= q.rows) {
+        if (++b >= g.kv.B) return false;
+        q = get(g.kv, sp, b);
+        r0 = 0;
+      }
+      tiles = kv_tiles(g, sp, q, r0, min(r0 + ROWS, q.rows) - 1);
+      seq = b;
+      h = kvh;
+      row0 = r0;
+      u0 = 0;
+      u1 = units = 1;
+      --left;
+      if (++kvh == g.kv.n_kv) { kvh = 0; r0 += ROWS; }
+      return true;
+    }
     for (;;) {
       if (r0 >= q.rows) {
         r0 = 0;
@@ -201,11 +221,10 @@ struct Walk {
     u1 = min(units, off + left);
     left -= u1 - u0;
     off = 0;
-    if (sp.split) {                                   // the units that count for the start hold no keys
-      const int lo = tiles.lo + (max(u0 - sp.start_cost, 0) << sp.shift);
-      tiles.hi = min(tiles.hi, tiles.lo + (max(u1 - sp.start_cost, 0) << sp.shift));
-      tiles.lo = lo;
-    }
+    // the units that count for the start hold no keys
+    const int lo = tiles.lo + (max(u0 - sp.start_cost, 0) << sp.shift);
+    tiles.hi = min(tiles.hi, tiles.lo + (max(u1 - sp.start_cost, 0) << sp.shift));
+    tiles.lo = lo;
     return true;
   }
 };
@@ -224,6 +243,9 @@ struct Lds {
 };
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// The bits of a value, by value: a bit cast of a vector's element reads the vector's first one.
+__device__ __forceinline__ uint32_t float_bits(float x) { return __builtin_bit_cast(uint32_t, x); }
 
 __device__ __forceinline__ float safe_max(float m) { return m == -INFINITY ? 0.0f : m; }
 
@@ -319,7 +341,7 @@ __device__ __forceinline__ void convert_queries(const Queries<D>& f, bool rotate
 #pragma unroll
   for (int c = 0; c < D / 16; ++c)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) m = max(m, __builtin_bit_cast(uint32_t, x[c][j]) & 0x7FFFFFFFu);
+    for (int j = 0; j < 4; ++j) m = max(m, float_bits(x[c][j]) & 0x7FFFFFFFu);
   m = row_max_u32(m);
   const float top = __builtin_bit_cast(float, m) * fabsf(c_scale);
   const bool unit = (top >= 0x1p-4f && top < 0x1p15f) || m == 0;
@@ -651,33 +673,45 @@ struct PrefillLds {
   } buf[2];
 };
 
-// A row's channels lie at 16c + 4g + j in o[c][j]: rotated over c and j in the lane, over g between lanes.
+// A row's channels lie at 16c + 4g + j in o[c][j] of lane group g: rotated over c and j in the lane and over g between
+// lanes, one of a pair of registers going to each lane (or, not rotated, only exchanged).  Four registers' exchange leaves
+// lane group g with channels 16 (4i + g) ... 16 (4i + g) + 15 in o[4i] ... o[4i + 3].
 template <int D>
-__device__ __forceinline__ void transform_tile(f32x4* o, int lane) {
+__device__ __forceinline__ void transform_tile(f32x4* o, bool rotate) {
+  if (rotate) {
 #pragma unroll
-  for (int c = 0; c < D / 16; ++c) {
-    const f32x4 x = o[c];
-    const float a = x[0] + x[1], b = x[0] - x[1], d = x[2] + x[3], e = x[2] - x[3];
-    o[c] = f32x4{a + d, b + e, a - d, b - e};
+    for (int c = 0; c < D / 16; ++c) {
+      const f32x4 x = o[c];
+      const float a = x[0] + x[1], b = x[0] - x[1], d = x[2] + x[3], e = x[2] - x[3];
+      o[c] = f32x4{a + d, b + e, a - d, b - e};
+    }
+#pragma unroll
+    for (int h = 1; h < D / 16; h *= 2)
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+        if (!(c & h)) {
+          const f32x4 x = o[c], y = o[c + h];
+          o[c] = x + y;
+          o[c + h] = x - y;
+        }
   }
+  // lane pairs 16 apart trade within (c, c + 1), pairs 32 apart within (c, c + 2)
 #pragma unroll
-  for (int h = 1; h < D / 16; h *= 2)
+  for (int far = 0; far < 2; ++far)
 #pragma unroll
     for (int c = 0; c < D / 16; ++c)
-      if (!(c & h)) {
-        const f32x4 x = o[c], y = o[c + h];
-        o[c] = x + y;
-        o[c + h] = x - y;
-      }
+      if (!(c & (1 << far)))
 #pragma unroll
-  for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float a, b;
-      swap_pair<false>(o[c][j], a, b);
-      swap_pair<true>((lane & 16) ? a - b : a + b, a, b);
-      o[c][j] = (lane & 32) ? a - b : a + b;
-    }
+        for (int j = 0; j < 4; ++j) {
+          const int d = c + (1 << far);
+          const uint32_t u = float_bits(o[c][j]), v = float_bits(o[d][j]);
+          u32x2 t;
+          if (far) { const auto r = __builtin_amdgcn_permlane32_swap(u, v, false, false); t = u32x2{r[0], r[1]}; }
+          else { const auto r = __builtin_amdgcn_permlane16_swap(u, v, false, false); t = u32x2{r[0], r[1]}; }
+          const float x = __builtin_bit_cast(float, (uint32_t)t[0]), y = __builtin_bit_cast(float, (uint32_t)t[1]);
+          o[c][j] = rotate ? x + y : x;
+          o[d][j] = rotate ? x - y : y;
+        }
 }
 
 template <int D, int NB>
@@ -770,6 +804,9 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
       const int t0 = tile * kTile;
       if (t0 >= any.hi || t0 + kTile <= any.lo) continue;
       f32x4 sc[NB][4];
+      // The softmax at a lower priority than the rest: what feeds the matrix cores goes first, and the other wave's
+      // vector work fills in (chunk of 512: 164 us; 180 without).
+      __builtin_amdgcn_s_setprio(1);
       C kc[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -783,6 +820,7 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
           for (int n = 0; n < NB; ++n)
             sc[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[n][k], k ? sc[n][i] : f32x4{0, 0, 0, 0}, 0, 0, 0);
         }
+      __builtin_amdgcn_s_setprio(0);
       const uint32_t held4 = B.held[0] | B.held[1] << 1 | B.held[2] << 2 | B.held[3] << 3;
       const bool whole = held4 == 15 && t0 >= every.lo && t0 + kTile <= every.hi;
       i32x2 vc[D / 16];
@@ -790,6 +828,7 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
       for (int c = 0; c < D / 16; ++c) vc[c] = value_codes<D>(B.v, c);
       f16x8 w[NB][2];
       soft_weights<D, NB>(B.ks, B.lv, B.iv, t0, whole, held4, unit, rs, lo, hi, sc, M, l, o, w);
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
 #pragma unroll
@@ -801,6 +840,8 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
       }
     }
 
+    __builtin_amdgcn_s_setprio(0);
+
     // ---- the rows, each in its wave
     const bool starts = u.u0 == 0, ends = u.u1 == u.units;
     const int64_t part = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
@@ -809,17 +850,20 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
       const int rr = 16 * n + (lane & 15);
       const float sum = row_add(l[n]);
       if (starts && ends) {
-        if (a.rotate & 2) transform_tile<D>(o[n], lane);
+        transform_tile<D>(o[n], a.rotate & 2);
         const float f = sum != 0.0f ? sp.c_v / sum : 0.0f;
         if (rr < w_rows) {
           const int r = w0 + rr, i = div_g(sp, r), h = r - i * sp.G;
-          uint16_t* dst = g.out + (int64_t)(q.t0 + i) * g.ldo + (kvh * sp.G + h) * D + 4 * (lane >> 4);
+          uint16_t* dst = g.out + (int64_t)(q.t0 + i) * g.ldo + (kvh * sp.G + h) * D + 16 * (lane >> 4);
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            u32x2 x;
-            x[0] = (uint32_t)f32_to_bf16_rne(o[n][c][0] * f) | ((uint32_t)f32_to_bf16_rne(o[n][c][1] * f) << 16);
-            x[1] = (uint32_t)f32_to_bf16_rne(o[n][c][2] * f) | ((uint32_t)f32_to_bf16_rne(o[n][c][3] * f) << 16);
-            *reinterpret_cast<u32x2*>(dst + 16 * c) = x;
+          for (int c = 0; c < D / 16; c += 2) {
+            u32x4 x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const f32x4 v = o[n][c + e / 2];
+              x[e] = (uint32_t)f32_to_bf16_rne(v[2 * (e & 1)] * f) | ((uint32_t)f32_to_bf16_rne(v[2 * (e & 1) + 1] * f) << 16);
+            }
+            *reinterpret_cast<u32x4*>(dst + 64 * (c / 4) + 4 * (c & 3)) = x;
           }
         }
       } else if (rr < w_rows) {
@@ -831,367 +875,6 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
     }
     if (starts && !ends && tid == 0)
       sp.desc[blockIdx.x] = Desc{b, kvh, r0, u.following(sp)};
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Long prompts: 256 query rows of one key/value head a workgroup, 64 a wave.  With 64 rows behind each converted
-// code the vector instructions a score costs (the bound) are fewest: conversion, 2 of 7, halves.
-// Four waves hold the rows and go through the even key tiles, four more the same rows and the odd ones; the
-// two waves of a SIMD so share one set of queries, which does not fit the registers beside the 128 sums a
-// lane holds and lies in LDS in the order the matrix instructions read it (64 KB).  32x32x16 MFMA: keys
-// times queries, then channels times weights, in steps of 32 keys; lane (row r = lane % 32, h = lane / 32)
-// has the scores of keys 8b + 4h + j.  At the end the pairs of waves join their sums through LDS.
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-template <int D>
-struct LongLds {
-  struct Buf {
-    alignas(16) uint8_t k[kTile * D / 2], v[kTile * D / 2];
-    alignas(16) float ks[kTile], lv[kTile], iv[kTile];
-    int held[4];
-  };
-  struct Main {
-    alignas(16) f16x8 q[4][2][D / 16][64];            // [rows' wave][row tile][step][lane]
-    Buf buf[2][2];                                    // [key group][double]
-  };
-  union {
-    Main t;
-    alignas(16) f32x4 o[8][D / 8][64];                // a wave's sums of the row tile that its partner finishes
-  };
-  float rs[256];
-  float m[8][32], l[8][32];
-};
-
-template <int D>
-__global__ __launch_bounds__(512, 2) void kv_long_kernel(KvAttnArgs g, SplitArgs sp) {
-  constexpr int ROWS = 256, CT = D / 32;
-  typedef typename Chunk<D>::T C;
-  __shared__ LongLds<D> s;
-  const KvArgs& a = g.kv;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int rg = wave & 3, kg = wave >> 2, h = lane >> 5;
-  const uint32_t mask = (1u << a.logp) - 1;
-  if (tid == 0 && sp.split) sp.desc[blockIdx.x].more = 0;
-  Walk<ROWS> u;
-  u.start(g, sp);
-  const float c_scale = g.scale * sp.c_q * 1.44269504088896341f;
-  while (u.next(g, sp)) {
-    const Seq q = u.q;
-    const int r0 = u.row0, kvh = u.h, b = u.seq;
-    const int t_lo = u.tiles.lo, t_hi = u.tiles.hi;
-    const int w0 = r0 + 64 * rg;                      // the wave's first row
-    const int w_rows = min(64, q.rows - w0);          // may be <= 0
-
-    // ---- the first keys on their way; the queries: each wave of a pair converts 32 rows
-    C kr, vr;
-    const float* scales = ((lane & 16) ? a.scales[1] : a.scales[0]) + (lane & 15);
-    float scale = 0;
-    int held = 0, pages = 0;
-    auto page_batch = [&](int tile) { pages = kv_page(a, b, (int64_t)(tile + 2 * lane) * kTile + 16 * rg); };
-    auto fetch = [&](int tile, int at) {              // 16 keys of the key group's tile
-      const int p0 = __builtin_amdgcn_readlane(pages, at);
-      held = p0 >= 0;
-      const int p = p0 >= 0 ? p0 : 0;                 // keys in no page: any page is read, and masked
-      const int64_t row = ((int64_t)(p * a.n_kv + kvh) << a.logp) + ((tile * kTile + 16 * rg) & mask);
-      kr = *reinterpret_cast<const C*>(a.codes[0] + row * (D / 2) + lane * (D / 8));
-      vr = *reinterpret_cast<const C*>(a.codes[1] + row * (D / 2) + lane * (D / 8));
-      scale = scales[row];
-    };
-    page_batch(t_lo + kg);
-    Queries<D> fq[2];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int rr = 32 * kg + 16 * n + (lane & 15);
-      fq[n] = fetch_queries<D>(g, sp, q, kvh, rr < w_rows ? w0 + rr : r0, rr < w_rows);
-    }
-    fetch(t_lo + kg, 0);
-    __syncthreads();                                  // the last row block's sums have been read
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      f16x8 qf[D / 32];
-      float r;
-      convert_queries<D>(fq[n], a.rotate & 1, c_scale, qf, &r);
-      if (lane < 16) s.rs[64 * rg + 32 * kg + 16 * n + lane] = r;
-      const int g4 = lane >> 4;                       // its channels: D/4 g4 + 8k ...
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k)
-        s.t.q[rg][kg][(g4 & 1) * (D / 32) + k][16 * n + (lane & 15) + 32 * (g4 >> 1)] = qf[k];
-    }
-    Range any{0, 0}, every{0, 0};                     // positions that some, that every row of the wave attends
-    float M[2], l[2];
-    f32x16 o[2][CT];
-    int lo[2], hi[2];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int rr = 32 * n + (lane & 31);
-      const Range w = kv_range(q, div_g(sp, rr < w_rows ? w0 + rr : r0), g.causal, g.window);
-      lo[n] = w.lo;
-      hi[n] = rr < w_rows ? w.hi : 0;
-      M[n] = -INFINITY;
-      l[n] = 0;
-#pragma unroll
-      for (int c = 0; c < CT; ++c) o[n][c] = (f32x16)(0.0f);
-    }
-    if (w_rows > 0) {
-      const Range r_first = kv_range(q, div_g(sp, w0), g.causal, g.window);
-      const Range r_last = kv_range(q, div_g(sp, w0 + w_rows - 1), g.causal, g.window);
-      any = Range{r_first.lo, r_last.hi};
-      every = Range{r_last.lo, r_first.hi};
-    }
-
-    // ---- the tiles, two at a time
-    int at = 0;
-    bool unit = true;                                 // no row of the wave needs its power
-    for (int pair = t_lo; pair < t_hi; pair += 2) {
-      const int tile = pair + kg;
-      auto& B = s.t.buf[kg][((pair - t_lo) >> 1) & 1];
-      {
-        const int key = 16 * rg + (lane >> 2);
-        // quarters of a row swizzled so that 16 lanes' reads fall into different banks
-        const int kx = D == 128 ? (key >> 2) & 3 : 2 * ((key >> 3) & 1), vx = D == 128 ? (key >> 3) & 3 : 2 * ((key >> 3) & 1);
-        *reinterpret_cast<C*>(B.k + key * (D / 2) + ((lane & 3) ^ kx) * (D / 8)) = kr;
-        *reinterpret_cast<C*>(B.v + key * (D / 2) + ((lane & 3) ^ vx) * (D / 8)) = vr;
-        const float v = scale < 0x1p-64f ? 0x1p-64f : scale;
-        if (lane < 16) B.ks[16 * rg + lane] = scale;
-        if (lane >= 16 && lane < 32) {
-          B.lv[16 * rg + lane - 16] = __builtin_amdgcn_logf(v);
-          B.iv[16 * rg + lane - 16] = __builtin_amdgcn_rcpf(v);
-        }
-        if (lane == 0) B.held[rg] = held;
-      }
-      lds_barrier();
-      if (pair + 2 < t_hi) {
-        if (++at == 64) { page_batch(tile + 2); at = 0; }
-        fetch(tile + 2, at);
-      }
-      if (pair == t_lo) unit = !__any(s.rs[64 * rg + lane] != 1.0f);
-      const int t0 = tile * kTile;
-      if (tile >= t_hi || t0 >= any.hi || t0 + kTile <= any.lo) continue;
-      const uint32_t held4 = B.held[0] | B.held[1] << 1 | B.held[2] << 2 | B.held[3] << 3;
-      const bool whole = held4 == 15 && t0 >= every.lo && t0 + kTile <= every.hi;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        // scores of 32 keys; the queries are read anew for each (an offset that the compiler cannot see through
-        // keeps it from holding all of them in registers)
-        __builtin_amdgcn_s_setprio(1);                // the matrix cores first: the other wave's vector work fills in
-        f32x16 sc[2];
-        {
-          const int key = 32 * half + (lane & 31);
-          uint32_t kc[D / 16];
-          if constexpr (D == 128) {
-            const int kx = (key >> 2) & 3;
-            const u32x4 x = *reinterpret_cast<const u32x4*>(B.k + key * 64 + ((2 * h) ^ kx) * 16);
-            const u32x4 y = *reinterpret_cast<const u32x4*>(B.k + key * 64 + ((2 * h + 1) ^ kx) * 16);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) { kc[i] = x[i]; kc[4 + i] = y[i]; }
-          } else {
-            const u32x4 x = *reinterpret_cast<const u32x4*>(B.k + key * 32 + (h ^ ((key >> 3) & 1)) * 16);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) kc[i] = x[i];
-          }
-          int ql = lane;
-          asm("" : "+v"(ql));
-          const f16x8* qp = &s.t.q[rg][0][0][ql];
-          f16x8 qf[2][2];                             // a step ahead
-#pragma unroll
-          for (int n = 0; n < 2; ++n) qf[0][n] = qp[n * (D / 16) * 64];
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            if (k + 1 < D / 16) {
-#pragma unroll
-              for (int n = 0; n < 2; ++n) qf[(k + 1) % 2][n] = qp[(n * (D / 16) + k + 1) * 64];
-            }
-            const f16x8 kf = e2m1_f16x8(kc[k]);
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-              sc[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[k % 2][n], k ? sc[n] : (f32x16)(0.0f), 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-          }
-        }
-        i32x2 vc[CT];                                 // 32 channels at a time
-        {
-          const int r = lane & 15, key = 32 * half + 8 * (r >> 2) + 4 * h + (r & 3);
-#pragma unroll
-          for (int c = 0; c < CT; ++c) {
-            const int quarter = D == 128 ? c ^ (r >> 2) : c ^ ((r >> 2) & 1);  // 16 bytes hold 32 channels
-            vc[c] = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2*)(B.v + key * (D / 2) + quarter * 16 + ((lane >> 4) & 1) * 8));
-          }
-        }
-        // weights
-        __builtin_amdgcn_s_setprio(0);
-        f16x8 w[2][2];
-        const float *kp = &B.ks[32 * half + 4 * h], *lp = &B.lv[32 * half + 4 * h], *ip = &B.iv[32 * half + 4 * h];
-        if (!unit) {
-          sc[0] *= s.rs[64 * rg + (lane & 31)];
-          sc[1] *= s.rs[64 * rg + 32 + (lane & 31)];
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const f32x4 ks = *reinterpret_cast<const f32x4*>(kp + 8 * c), lv = *reinterpret_cast<const f32x4*>(lp + 8 * c);
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sc[n][4 * c + j] = __builtin_fmaf(sc[n][4 * c + j], ks[j], lv[j]);
-        }
-        if (!whole) {
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int from = t0 + 32 * half + 4 * h - lo[n];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t len = (held4 >> (2 * half + c / 2)) & 1 ? (uint32_t)max(hi[n] - lo[n], 0) : 0u;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) sc[n][4 * c + j] = (uint32_t)(from + 8 * c + j) < len ? sc[n][4 * c + j] : -INFINITY;
-            }
-          }
-        }
-        float mx[2];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          mx[n] = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) mx[n] = fmaxf(mx[n], sc[n][i]);
-        }
-        if (__any(mx[0] > M[0] + kSlack || mx[1] > M[1] + kSlack)) {
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            float x, y;
-            swap_pair<true>(mx[n], x, y);
-            const float rm = fmaxf(x, y), m = rm > M[n] + kSlack ? rm : M[n];   // a row moves for its own scores alone
-            const float keep = __builtin_amdgcn_exp2f(M[n] - safe_max(m));
-            l[n] *= keep;
-#pragma unroll
-            for (int c = 0; c < CT; ++c) o[n][c] *= keep;
-            M[n] = m;
-          }
-        }
-        const float ref[2] = {safe_max(M[0]), safe_max(M[1])};
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float p = __builtin_amdgcn_exp2f(sc[n][i] - ref[n]);
-            sc[n][i] = p;
-            w[n][i >> 3][i & 7] = (_Float16)p;
-          }
-        if (whole) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const f32x4 iv = *reinterpret_cast<const f32x4*>(ip + 8 * c);
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) l[n] = __builtin_fmaf(sc[n][4 * c + j], iv[j], l[n]);
-          }
-        } else {                                      // a masked key's 1 / vs may be NaN
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const f32x4 iv = *reinterpret_cast<const f32x4*>(ip + 8 * c);
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                l[n] = sc[n][4 * c + j] != 0.0f ? __builtin_fmaf(sc[n][4 * c + j], iv[j], l[n]) : l[n];
-          }
-        }
-        __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const f16x8 vf = e2m1_f16x8((uint32_t)vc[c][k]);
-#pragma unroll
-            for (int n = 0; n < 2; ++n) o[n][c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, w[n][k], o[n][c], 0, 0, 0);
-          }
-      }
-    }
-
-    // ---- the pairs' sums joined: a wave finishes row tile kg and hands the other one over
-    __syncthreads();
-    float sum[2];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      float x, y;
-      swap_pair<true>(l[n], x, y);
-      sum[n] = x + y;
-    }
-    if (lane < 32) {
-      s.m[wave][lane] = kg ? M[0] : M[1];
-      s.l[wave][lane] = kg ? sum[0] : sum[1];
-    }
-#pragma unroll
-    for (int c = 0; c < CT; ++c)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        f32x4 x;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = kg ? o[0][c][4 * e + j] : o[1][c][4 * e + j];
-        s.o[wave][4 * c + e][lane] = x;
-      }
-    __syncthreads();
-    const int other = wave ^ 4;
-    const float m0 = kg ? M[1] : M[0], m1 = s.m[other][lane & 31];
-    const float m = fmaxf(m0, m1), ref = safe_max(m);
-    const float f0 = __builtin_amdgcn_exp2f(m0 - ref), f1 = __builtin_amdgcn_exp2f(m1 - ref);
-    const float total = (kg ? sum[1] : sum[0]) * f0 + s.l[other][lane & 31] * f1;
-    f32x4 x[D / 8];                                   // channels 8i + 4h + j of row lane % 32
-#pragma unroll
-    for (int c = 0; c < CT; ++c)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const f32x4 y = s.o[other][4 * c + e][lane];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[4 * c + e][j] = (kg ? o[1][c][4 * e + j] : o[0][c][4 * e + j]) * f0 + y[j] * f1;
-      }
-    const bool starts = u.u0 == 0, ends = u.u1 == u.units;
-    const int64_t part = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
-    const int rr = 32 * kg + (lane & 31);
-    if (starts && ends) {
-      if (a.rotate & 2) {
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const f32x4 v = x[i];
-          const float p = v[0] + v[1], t = v[0] - v[1], d = v[2] + v[3], e = v[2] - v[3];
-          x[i] = f32x4{p + d, t + e, p - d, t - e};
-        }
-#pragma unroll
-        for (int k = 1; k < D / 8; k *= 2)
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-            if (!(i & k)) {
-              const f32x4 v = x[i], y = x[i + k];
-              x[i] = v + y;
-              x[i + k] = v - y;
-            }
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float p, t;
-            swap_pair<true>(x[i][j], p, t);
-            x[i][j] = h ? p - t : p + t;
-          }
-      }
-      if (rr < w_rows) {
-        const float f = total != 0.0f ? sp.c_v / total : 0.0f;
-        const int r = w0 + rr, i = div_g(sp, r), head = r - i * sp.G;
-        uint16_t* dst = g.out + (int64_t)(q.t0 + i) * g.ldo + (kvh * sp.G + head) * D + 4 * h;
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k) {
-          u32x2 y;
-          y[0] = (uint32_t)f32_to_bf16_rne(x[k][0] * f) | ((uint32_t)f32_to_bf16_rne(x[k][1] * f) << 16);
-          y[1] = (uint32_t)f32_to_bf16_rne(x[k][2] * f) | ((uint32_t)f32_to_bf16_rne(x[k][3] * f) << 16);
-          *reinterpret_cast<u32x2*>(dst + 8 * k) = y;
-        }
-      }
-    } else if (rr < w_rows) {
-      const int64_t at_row = part * ROWS + 64 * rg + rr;
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k) *reinterpret_cast<f32x4*>(sp.o + at_row * D + 8 * k + 4 * h) = x[k];
-      if (lane < 32) sp.ml[at_row] = float2{m, total};
-    }
-    if (starts && !ends && tid == 0) sp.desc[blockIdx.x] = Desc{b, kvh, r0, u.following(sp)};
   }
 }
 
@@ -1252,7 +935,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs g, SplitArgs sp
 // Query rows of a row block, by the rows a sequence has on average.
 int row_block(int64_t T, int B, int G) {
   const int64_t rows = (T + B - 1) / B * G;
-  return rows <= 128 ? 16 : rows <= 256 ? 128 : 256;
+  return rows <= 128 ? 16 : 128;
 }
 
 template <int D>
@@ -1270,15 +953,6 @@ hipError_t launch_prefill(const KvAttnArgs& g, SplitArgs sp, hipStream_t stream)
   if (hipError_t e = hipGetLastError()) return e;
   if (!sp.split) return hipSuccess;
   kv_join_kernel<D, 128, 8><<<dim3(sp.groups, (sp.join_rows + 7) / 8), 256, 0, stream>>>(g, sp);
-  return hipGetLastError();
-}
-
-template <int D>
-hipError_t launch_long(const KvAttnArgs& g, SplitArgs sp, hipStream_t stream) {
-  kv_long_kernel<D><<<sp.groups, 512, 0, stream>>>(g, sp);
-  if (hipError_t e = hipGetLastError()) return e;
-  if (!sp.split) return hipSuccess;
-  kv_join_kernel<D, 256, 8><<<dim3(sp.groups, (sp.join_rows + 7) / 8), 256, 0, stream>>>(g, sp);
   return hipGetLastError();
 }
 
@@ -1307,18 +981,17 @@ hipError_t launch_kv_attention(const KvAttnArgs& g, hipStream_t stream) {
   sp.join_rows = a.offsets || own > rows ? rows : (int)own;
   const int64_t blocks = ((a.T * G + rows - 1) / rows + a.B) * a.n_kv;      // row blocks at most
   const int64_t cap = ((int64_t)a.max_pages << a.logp) / kTile + 1;         // key tiles of one at most
-  sp.split = rows >= 128 ? blocks < 3 * most && cap > 16 : cap > 32;
+  sp.split = rows == 128 ? blocks < 3 * most && cap > 16 : cap > 32;
   sp.min_units = 1;
   int64_t want = blocks;
   if (sp.split) {
     sp.min_units = 4;
-    sp.start_cost = rows >= 128 ? 1 : 16;
+    sp.start_cost = rows == 128 ? 1 : 16;
     while (blocks * ((cap >> sp.shift) + 1 + sp.start_cost) >= 0x7FFFFFFF - most) ++sp.shift;
     want = (blocks * ((cap >> sp.shift) + 1 + sp.start_cost) + sp.min_units - 1) / sp.min_units;
   }
-  const int64_t limit = rows >= 128 && !sp.split ? 1 << 22 : most;
+  const int64_t limit = rows == 128 && !sp.split ? 1 << 22 : most;
   sp.groups = (int)(want < limit ? want : limit);
-  if (rows == 256) return a.D == 64 ? launch_long<64>(g, sp, stream) : launch_long<128>(g, sp, stream);
   if (rows == 128) return a.D == 64 ? launch_prefill<64>(g, sp, stream) : launch_prefill<128>(g, sp, stream);
   return a.D == 64 ? launch_decode<64>(g, sp, stream) : launch_decode<128>(g, sp, stream);
 }
