@@ -15,6 +15,8 @@
 // product wants 8 keys of one channel in a lane: the values go to LDS as they are, and
 // ds_read_b64_tr_b4 hands each lane 16 keys' codes of its channel.  Codes become fp16 by
 // v_cvt_scalef32_pk_f16_fp4, two at a time.
+#include <algorithm>
+
 #include "kv_device.hpp"
 
 namespace cbq {
@@ -34,8 +36,9 @@ struct Seq {
 
 struct Range { int lo, hi; };      // [lo, hi)
 
-// What the workgroups of a split call leave for the join: a row block that starts in group w and goes on in the next `more`.
-struct Desc { int b, kvh, r0, more; };
+// What the workgroups of a split call leave for the join: a row block that starts in group w and goes on in the next `more`:
+// its sequence's first token, its head, its first row and its rows.
+struct alignas(32) Desc { int t0, kvh, r0, rows, more; };
 
 struct SplitArgs {
   int groups;                      // workgroups
@@ -89,64 +92,97 @@ __device__ __forceinline__ Range kv_tiles(const KvAttnArgs& g, const SplitArgs& 
   return Range{lo, max(hi, lo + 1)};
 }
 
-__device__ __forceinline__ int block_units(const SplitArgs& sp, Range t) {
-  return sp.split ? ((t.hi - t.lo - 1) >> sp.shift) + 1 + sp.start_cost : 1;
+// Units of row block rb of a sequence.
+template <int ROWS>
+__device__ __forceinline__ int rb_units(const KvAttnArgs& g, const SplitArgs& sp, const Seq& q, int rb) {
+  if (rb >= (q.rows + ROWS - 1) / ROWS) return 0;
+  if (!sp.split) return 1;
+  const Range t = kv_tiles(g, sp, q, rb * ROWS, min((rb + 1) * ROWS, q.rows) - 1);
+  return ((t.hi - t.lo - 1) >> sp.shift) + 1 + sp.start_cost;
 }
 
-// Units of one key/value head of a sequence: its row blocks' key tiles, or its row blocks.
-template <int ROWS>
-__device__ __forceinline__ int head_units(const KvAttnArgs& g, const SplitArgs& sp, const Seq& q) {
-  if (!sp.split) return (int)((uint32_t)(q.rows + ROWS - 1) / ROWS);
-  int n = 0;
-  for (int r0 = 0; r0 < q.rows; r0 += ROWS) n += block_units(sp, kv_tiles(g, sp, q, r0, min(r0 + ROWS, q.rows) - 1));
-  return n;
+// Inclusive sums over the lanes of a wave.
+__device__ __forceinline__ int wave_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);   // lane 15 of a row into the next row
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);   // lane 31 into the upper half
+  return x;
 }
 
 // The row blocks, or parts of them, that a workgroup works through.  All sequences' units in a row (a
-// sequence's in the order head, row block, key tile; whole row blocks in the order row block, head) are dealt out evenly, `per` to a workgroup; each
-// wave counts them for itself, from the lengths, so the lengths stay on the device and the work is even
-// whatever they are.
+// sequence's in the order head, row block, key tile; whole row blocks in the order row block, head) are dealt out evenly,
+// `per` to a workgroup; each wave counts them for itself, from the lengths, so the lengths stay on the device and the
+// work is even whatever they are.  A lane counts its sequences' row blocks where they are few, else
+// the wave does it together.
 template <int ROWS>
 struct Walk {
   Seq q;
   int b, kvh, r0, off, left, per;  // r0: the next row block, off: units of it that are not this workgroup's
+  // the current part: units [u0, u1) of `units` of row block `row0` of head `h` of sequence `seq`
+  int seq, h, row0, u0, u1, units;
+  Range tiles;                     // its key tiles
+  Seq lane_q;                      // up to 64 sequences: the lane's own, so that no start waits for a length
+
   // whether and for how many groups the current part goes on: only the last part of a group does
   __device__ __forceinline__ int following(const SplitArgs& sp) const {
     const uint32_t n = ((uint32_t)(units - u1) + per - 1) / (uint32_t)per;
     return (int)min(n, (uint32_t)sp.groups - 1 - blockIdx.x);
   }
-  // the current part: units [u0, u1) of `units` of row block `row0` of head `h` of sequence `seq`
-  int seq, h, row0, u0, u1, units;
-  Range tiles;                     // its key tiles
-
-  Seq lane_q;                      // up to 64 sequences: the lane's own, so that no start waits for a length
 
   __device__ __forceinline__ Seq get(const KvArgs& a, const SplitArgs& sp, int i) const {
-    if (a.B > 64) return kv_seq(a, i, sp.G);
-    return Seq{__builtin_amdgcn_readlane(lane_q.t0, i), __builtin_amdgcn_readlane(lane_q.rows, i),
-               __builtin_amdgcn_readlane(lane_q.pos0, i), __builtin_amdgcn_readlane(lane_q.len, i)};
+    return a.B > 64 ? kv_seq(a, i, sp.G) : lane_seq(lane_q, i);
+  }
+  static __device__ __forceinline__ Seq lane_seq(const Seq& s, int i) {
+    return Seq{__builtin_amdgcn_readlane(s.t0, i), __builtin_amdgcn_readlane(s.rows, i),
+               __builtin_amdgcn_readlane(s.pos0, i), __builtin_amdgcn_readlane(s.len, i)};
+  }
+
+  // Units of one key/value head, by the whole wave; with at: the row block that holds unit *at, and what of it comes before.
+  static __device__ __forceinline__ int head_units(const KvAttnArgs& g, const SplitArgs& sp, const Seq& s, int* at, int* row) {
+    const int lane = threadIdx.x & 63;
+    int n = 0;
+    for (int rb = 0; rb * ROWS < s.rows; rb += 64) {
+      const int mine = rb_units<ROWS>(g, sp, s, rb + lane), inc = wave_scan(mine);
+      const int all = __builtin_amdgcn_readlane(inc, 63);
+      if (at && *at < n + all) {
+        const int l = (int)__builtin_ctzll(__ballot(*at < n + inc));
+        *row = (rb + l) * ROWS;
+        *at -= n + __builtin_amdgcn_readlane(inc - mine, l);
+        return n;
+      }
+      n += all;
+    }
+    return n;
   }
 
   __device__ __forceinline__ void start(const KvAttnArgs& g, const SplitArgs& sp) {
     const KvArgs& a = g.kv;
     const int lane = threadIdx.x & 63;
     const int each = (a.B + 63) >> 6;                 // sequences a lane counts
-    int mine = 0;
+    constexpr int kFew = 4;
+    int mine = 0, head = 0;
     for (int k = 0; k < each; ++k) {
-      const int s = lane * each + k;
-      if (s < a.B) {
-        lane_q = kv_seq(a, s, sp.G);
-        mine += head_units<ROWS>(g, sp, lane_q) * a.n_kv;
+      const int i = lane * each + k;
+      lane_q = Seq{0, 0, 0, 0};
+      if (i < a.B) lane_q = kv_seq(a, i, sp.G);
+      const int blocks = (int)((uint32_t)(lane_q.rows + ROWS - 1) / ROWS);
+      head = blocks;
+      if (sp.split) {
+        head = 0;
+        if (blocks <= kFew)
+          for (int rb = 0; rb < blocks; ++rb) head += rb_units<ROWS>(g, sp, lane_q, rb);
+        for (uint64_t many = __ballot(blocks > kFew); many; many &= many - 1) {
+          const int l = (int)__builtin_ctzll(many);
+          const int n = head_units(g, sp, lane_seq(lane_q, l), nullptr, nullptr);
+          if (lane == l) head = n;
+        }
       }
+      mine += head * a.n_kv;
     }
-    int inc = mine;                                   // inclusive sums over the lanes
-    inc += __builtin_amdgcn_update_dpp(0, inc, 0x111, 0xF, 0xF, false);
-    inc += __builtin_amdgcn_update_dpp(0, inc, 0x112, 0xF, 0xF, false);
-    inc += __builtin_amdgcn_update_dpp(0, inc, 0x114, 0xF, 0xF, false);
-    inc += __builtin_amdgcn_update_dpp(0, inc, 0x118, 0xF, 0xF, false);
-    inc += __builtin_amdgcn_update_dpp(0, inc, 0x142, 0xA, 0xF, false);   // lane 15 of a row into the next row
-    inc += __builtin_amdgcn_update_dpp(0, inc, 0x143, 0xC, 0xF, false);   // lane 31 into the upper half
-    const int total = __builtin_amdgcn_readlane(inc, 63);
+    const int inc = wave_scan(mine), total = __builtin_amdgcn_readlane(inc, 63);
     per = max((int)(((uint32_t)total + sp.groups - 1) / (uint32_t)sp.groups), sp.min_units);
     // unsplit calls start with the last units: a sequence's last rows attend the most keys
     const int64_t at = sp.split ? (int64_t)blockIdx.x : (int64_t)sp.groups - 1 - blockIdx.x;
@@ -164,16 +200,18 @@ struct Walk {
     for (;; ++b) {                                    // at most `each` times
       if (b >= a.B) { left = 0; return; }             // offsets that do not ascend
       q = get(a, sp, b);
-      const int hu = head_units<ROWS>(g, sp, q);
+      const int hu = each == 1 ? __builtin_amdgcn_readlane(head, f) : head_units(g, sp, q, nullptr, nullptr);
       if (off < hu * a.n_kv) {
-        if (sp.split) {
-          kvh = off / hu;
-          off -= kvh * hu;
-        } else {
+        if (!sp.split) {
           r0 = off / a.n_kv * ROWS;
           kvh = off % a.n_kv;
+          off = 0;
+        } else {
+          kvh = off / hu;
+          off -= kvh * hu;
+          head_units(g, sp, q, &off, &r0);
         }
-        break;
+        return;
       }
       off -= hu * a.n_kv;
     }
@@ -197,24 +235,20 @@ struct Walk {
       if (++kvh == g.kv.n_kv) { kvh = 0; r0 += ROWS; }
       return true;
     }
-    for (;;) {
-      if (r0 >= q.rows) {
-        r0 = 0;
-        if (++kvh >= g.kv.n_kv) {
-          kvh = 0;
-          do {
-            if (++b >= g.kv.B) return false;
-            q = get(g.kv, sp, b);
-          } while (q.rows == 0);
-        }
+    if (r0 >= q.rows) {
+      r0 = 0;
+      if (++kvh >= g.kv.n_kv) {
+        kvh = 0;
+        do {
+          if (++b >= g.kv.B) return false;
+          q = get(g.kv, sp, b);
+        } while (q.rows == 0);
       }
-      tiles = kv_tiles(g, sp, q, r0, min(r0 + ROWS, q.rows) - 1);
-      units = block_units(sp, tiles);
-      row0 = r0;
-      r0 += ROWS;
-      if (off < units) break;
-      off -= units;
     }
+    tiles = kv_tiles(g, sp, q, r0, min(r0 + ROWS, q.rows) - 1);
+    units = ((tiles.hi - tiles.lo - 1) >> sp.shift) + 1 + sp.start_cost;
+    row0 = r0;
+    r0 += ROWS;
     seq = b;
     h = kvh;
     u0 = off;
@@ -592,7 +626,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_kernel(KvAttnArgs
     ends = u.u1 == u.units;
     have = true;
     if (starts && !ends && tid == 0)
-      sp.desc[blockIdx.x] = Desc{u.seq, kvh, row0, u.following(sp)};
+      sp.desc[blockIdx.x] = Desc{q.t0, kvh, row0, n_rows, u.following(sp)};
 
     // ---- the queries, and what each row attends
     f16x8 qf[D / 32];
@@ -874,7 +908,7 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
       }
     }
     if (starts && !ends && tid == 0)
-      sp.desc[blockIdx.x] = Desc{b, kvh, r0, u.following(sp)};
+      sp.desc[blockIdx.x] = Desc{q.t0, kvh, r0, min(ROWS, q.rows - r0), u.following(sp)};
   }
 }
 
@@ -887,8 +921,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs g, SplitArgs sp
   const int w = blockIdx.x, row = blockIdx.y * RB + rb;
   const Desc d = sp.desc[w];
   if (d.more == 0) return;
-  const Seq q = kv_seq(g.kv, d.b, sp.G);
-  const bool mine = d.r0 + row < q.rows;
+  const bool mine = row < d.rows;
   if (RB == 1 && !mine) return;
   __shared__ float so[RB][NG][D], sm[RB][NG], sl[RB][NG];
   // part 0 is the block's start (second slot of w), part p the first slot of w + p
@@ -929,13 +962,30 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs g, SplitArgs sp
   }
   if (!mine) return;                                  // whole groups of lanes
   const int r = d.r0 + row, i = div_g(sp, r), h = r - i * sp.G;
-  finish_row<D>(v, sum, g.kv.rotate & 2, sp.c_v, sub, g.out + (int64_t)(q.t0 + i) * g.ldo + (d.kvh * sp.G + h) * D + 8 * sub);
+  finish_row<D>(v, sum, g.kv.rotate & 2, sp.c_v, sub, g.out + (int64_t)(d.t0 + i) * g.ldo + (d.kvh * sp.G + h) * D + 8 * sub);
 }
 
 // Query rows of a row block, by the rows a sequence has on average.
 int row_block(int64_t T, int B, int G) {
   const int64_t rows = (T + B - 1) / B * G;
   return rows <= 128 ? 16 : 128;
+}
+
+// Whether row blocks are cut, for a second launch that joins them (about 4 us and the parts' traffic).
+//  16 rows: no below 1024 positions (4 heads, one sequence of 1000: 11 against 11.4 us; of 512: 9.4 against 11.7; of
+//  2048: 14.4 against 11.9, of 4096: 21.6 against 12.5), nor below 2048 with 64 row blocks (16 sequences of 2048: 14.8
+//  against 15.6; of 4096: 22.6 against 18.9).
+//  128 rows: whole blocks take 8 us and 1.75 a key tile, in rounds of 512 where the longest go first; cut ones 22 us and
+//  half as much again, evenly (64 new tokens, 8 heads, one sequence of 1024: 35.5 against 25 us; 16 of them: 37 against 51;
+//  a prompt of 2048: 70 against 91).
+bool split_pays(const KvAttnArgs& g, int rows, int64_t blocks, int64_t cap) {
+  if (rows == 16) return cap > (blocks >= 64 ? 33 : 17);
+  const KvArgs& a = g.kv;
+  const int64_t G = g.n_q / a.n_kv;
+  const double n = (double)a.n_kv * (a.offsets ? (double)(a.T * G / rows) + 0.5 * a.B : (double)a.B * ((a.per_seq * G + rows - 1) / rows));
+  const double mean = g.causal ? std::max((double)cap - (double)(a.T / a.B) / (2 * kTile), 0.5 * cap) : (double)cap;
+  const double whole = std::max(8 + 1.75 * cap, n * (8 + 1.75 * mean) / 512);
+  return 22 + 1.5 * n * 1.75 * mean / 512 < whole;
 }
 
 template <int D>
@@ -980,13 +1030,14 @@ hipError_t launch_kv_attention(const KvAttnArgs& g, hipStream_t stream) {
   const int64_t own = (int64_t)a.per_seq * G;
   sp.join_rows = a.offsets || own > rows ? rows : (int)own;
   const int64_t blocks = ((a.T * G + rows - 1) / rows + a.B) * a.n_kv;      // row blocks at most
-  const int64_t cap = ((int64_t)a.max_pages << a.logp) / kTile + 1;         // key tiles of one at most
-  sp.split = rows == 128 ? blocks < 3 * most && cap > 16 : cap > 32;
+  int64_t cap = ((int64_t)a.max_pages << a.logp) / kTile + 1;               // key tiles of one at most
+  if (g.window) cap = std::min(cap, ((int64_t)g.window + rows / G + 1) / kTile + 2);
+  sp.split = split_pays(g, rows, blocks, cap);
   sp.min_units = 1;
   int64_t want = blocks;
   if (sp.split) {
     sp.min_units = 4;
-    sp.start_cost = rows == 128 ? 1 : 16;
+    sp.start_cost = rows == 128 ? 1 : 24;
     while (blocks * ((cap >> sp.shift) + 1 + sp.start_cost) >= 0x7FFFFFFF - most) ++sp.shift;
     want = (blocks * ((cap >> sp.shift) + 1 + sp.start_cost) + sp.min_units - 1) / sp.min_units;
   }
