@@ -2,11 +2,13 @@
 //
 // The mathematics.  With a_j = scale <q, k_j> the result is sum_j exp(a_j) v_j / sum_j exp(a_j), in one
 // pass over the keys with a running maximum.  A key is its scale ks_j times E2M1 codes, so
-// a_j = ks_j <q', codes_j> with the rotated query q' in fp16 (its row divided by a power of two); codes are
-// exact in fp16 and the products' sums are fp32.  A value's scale vs_j joins the weight:
+// a_j = ks_j <q', codes_j> with q' the rotated query times scale in fp16 (11 bits, where q came in 8: its rounding
+// is far below that of q itself, and the range is seen to in convert_queries); codes are exact in fp16 and the
+// products' sums are fp32.  A value's scale vs_j joins the weight:
 //     b_j = a_j log2 e + log2 vs_j,   w_j = 2^(b_j - M),   M the running maximum of b,
 //     result = sum_j w_j codes_j / sum_j (w_j / vs_j),
-// so w_j in fp16 is always relative to its row's largest contribution, whatever the scales' range.
+// so w_j in fp16 (11 bits, and what lies 2^-24 below the largest contribution is lost) is always relative to its row's
+// largest contribution, whatever the scales' range; the sum of weights takes them before that rounding.
 //
 // The tiles.  A wave takes 64 keys at a time.  Scores are computed transposed, keys times queries
 // (16x16x32 MFMA: 16 keys, 16 query rows), so that lane (row r = lane % 16, g = lane / 16) ends
@@ -29,7 +31,7 @@ constexpr int max_groups(int rows) { return rows == 128 ? 512 : 256; }
 
 // A sequence's part of the step, all values uniform over the workgroup.
 struct Seq {
-  int t0, rows;                    // its first token; tokens * G
+  int t0, rows;                    // its first token; tokens * G (-1: see kv_seq)
   int pos0;                        // position of the first token
   int len;                         // positions that can hold anything
 };
@@ -38,7 +40,7 @@ struct Range { int lo, hi; };      // [lo, hi)
 
 // What the workgroups of a split call leave for the join: a row block that starts in group w and goes on in the next `more`:
 // its sequence's first token, its head, its first row and its rows.
-struct alignas(32) Desc { int t0, kvh, r0, rows, more; };
+struct alignas(16) Desc { int t0, kvh, r0, rows, more; };
 
 struct SplitArgs {
   int groups;                      // workgroups
@@ -67,7 +69,7 @@ __device__ __forceinline__ Seq kv_seq(const KvArgs& a, int b, int G) {
   const int s = max(o0, 0), e = min(o1, T);
   Seq q;
   q.t0 = s;
-  q.rows = e > s ? (e - s) * G : 0;                   // T * n_q < 2^31
+  q.rows = e > s ? (e - s) * G : o1 < o0 ? -1 : 0;    // T * n_q < 2^31; -1: offsets that do not ascend
   const int64_t pos0 = (int64_t)len - o1 + s;         // pos0 + i < len for its tokens i: no sum below leaves 32 bits
   q.pos0 = (int)max(pos0, (int64_t)-0x80000000LL);
   q.len = min(max(len, 0), cap);
@@ -164,10 +166,12 @@ struct Walk {
     const int each = (a.B + 63) >> 6;                 // sequences a lane counts
     constexpr int kFew = 4;
     int mine = 0, head = 0;
+    bool ascending = true;
     for (int k = 0; k < each; ++k) {
       const int i = lane * each + k;
       lane_q = Seq{0, 0, 0, 0};
       if (i < a.B) lane_q = kv_seq(a, i, sp.G);
+      ascending = ascending && lane_q.rows >= 0;
       const int blocks = (int)((uint32_t)(lane_q.rows + ROWS - 1) / ROWS);
       head = blocks;
       if (sp.split) {
@@ -188,7 +192,8 @@ struct Walk {
     const int64_t at = sp.split ? (int64_t)blockIdx.x : (int64_t)sp.groups - 1 - blockIdx.x;
     left = 0;
     b = a.B;
-    if (at * per >= total) return;
+    // sequences whose tokens overlap could have more row blocks than the host has counted: nothing is done
+    if (__any(!ascending) || at * per >= total) return;
     const int first = (int)at * per;
     left = min(total - first, per);
     const uint64_t past = __ballot(first < inc);
@@ -197,8 +202,7 @@ struct Walk {
     off = first - (__builtin_amdgcn_readlane(inc, f) - __builtin_amdgcn_readlane(mine, f));
     kvh = 0;
     r0 = 0;
-    for (;; ++b) {                                    // at most `each` times
-      if (b >= a.B) { left = 0; return; }             // offsets that do not ascend
+    for (; b < a.B; ++b) {                            // at most `each` times
       q = get(a, sp, b);
       const int hu = each == 1 ? __builtin_amdgcn_readlane(head, f) : head_units(g, sp, q, nullptr, nullptr);
       if (off < hu * a.n_kv) {
@@ -215,6 +219,7 @@ struct Walk {
       }
       off -= hu * a.n_kv;
     }
+    left = 0;
   }
 
   __device__ __forceinline__ bool next(const KvAttnArgs& g, const SplitArgs& sp) {
@@ -332,10 +337,10 @@ __device__ __forceinline__ Queries<D> fetch_queries(const KvAttnArgs& g, const S
   return f;
 }
 
-// Rotated if asked, times c, and, where the row's largest value is not within fp16's comfortable range (2^-4 ... 2^15: what
-// falls below 2^-14 there is off by at most 2^-25, as a part of a score nothing), divided by a power of two near
-// that value: *rs, else 1.  The rotation is a
-// product with the +-1 matrix on the matrix cores (bf16 inputs exact, fp32 sums): its row m of tile c
+// Rotated if asked, times c_scale in fp16.  A row whose largest value is then within 2^-4 ... 2^15 stays as it is (what
+// lies below 2^-14 is off by at most 2^-25 there, 2^-21 of the largest); another is divided by a power of two near that
+// value instead of times c_scale, and *rs, which its scores are multiplied by, makes up for both.
+// The rotation is a product with the +-1 matrix on the matrix cores (bf16 inputs exact, fp32 sums): its row m of tile c
 // is output channel D/4 (m / 4) + 4c + m % 4, so that lane (row, g) gets the channels it needs.  An entry's sign is
 // the parity of the bits that input and output channel share; with input channel D/4 g + 8k + j
 // it falls into parities of j with (m % 4, c % 2), of k with c / 2, and of g with m / 4.
@@ -404,7 +409,7 @@ __device__ __forceinline__ void finish_row(float* v, float l, bool rotate, float
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     out[i] = (uint32_t)f32_to_bf16_rne(v[2 * i] * f) | ((uint32_t)f32_to_bf16_rne(v[2 * i + 1] * f) << 16);
-  if (dst) *reinterpret_cast<u32x4*>(dst) = out;
+  *reinterpret_cast<u32x4*>(dst) = out;
 }
 
 typedef int i32x2 __attribute__((ext_vector_type(2)));
@@ -748,9 +753,9 @@ __device__ __forceinline__ void transform_tile(f32x4* o, bool rotate) {
         }
 }
 
-template <int D, int NB>
+template <int D>
 __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitArgs sp) {
-  constexpr int ROWS = 64 * NB;
+  constexpr int NB = 2, ROWS = 64 * NB;               // tiles of 16 query rows a wave; rows of a workgroup
   typedef typename Chunk<D>::T C;
   __shared__ PrefillLds<D> s;
   const KvArgs& a = g.kv;
@@ -873,7 +878,6 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
         }
       }
     }
-
     __builtin_amdgcn_s_setprio(0);
 
     // ---- the rows, each in its wave
@@ -978,7 +982,9 @@ int row_block(int64_t T, int B, int G) {
 //  128 rows: whole blocks take 8 us and 1.75 a key tile, in rounds of 512 where the longest go first; cut ones 22 us and
 //  half as much again, evenly (64 new tokens, 8 heads, one sequence of 1024: 35.5 against 25 us; 16 of them: 37 against 51;
 //  a prompt of 2048: 70 against 91).
+// So many row blocks that there is work for each compute unit many times over are not cut.
 bool split_pays(const KvAttnArgs& g, int rows, int64_t blocks, int64_t cap) {
+  if (blocks >= 1 << 24) return false;                // (so that the units of all fit 31 bits)
   if (rows == 16) return cap > (blocks >= 64 ? 33 : 17);
   const KvArgs& a = g.kv;
   const int64_t G = g.n_q / a.n_kv;
@@ -999,7 +1005,7 @@ hipError_t launch_decode(const KvAttnArgs& g, SplitArgs sp, hipStream_t stream) 
 
 template <int D>
 hipError_t launch_prefill(const KvAttnArgs& g, SplitArgs sp, hipStream_t stream) {
-  kv_prefill_kernel<D, 2><<<sp.groups, 256, 0, stream>>>(g, sp);
+  kv_prefill_kernel<D><<<sp.groups, 256, 0, stream>>>(g, sp);
   if (hipError_t e = hipGetLastError()) return e;
   if (!sp.split) return hipSuccess;
   kv_join_kernel<D, 128, 8><<<dim3(sp.groups, (sp.join_rows + 7) / 8), 256, 0, stream>>>(g, sp);

@@ -499,7 +499,8 @@ int cbq_codebook_adapter_gemm(const uint8_t* codes, const float* scales, int32_t
  *  k_codes, v_codes   : [n_pages][n_kv][page][D/2] bytes, 16-byte aligned; channel 2j in the
  *                       low nibble of byte j.  Nibble: sign (bit 3), then the value's index above.
  *  k_scales, v_scales : fp32 [n_pages][n_kv][page].
- *  n_pages >= 1, n_pages * n_kv < 2^31; 1 <= n_kv <= 1024 key/value heads; page: tokens a page holds, a power of two, 16 to 1024.
+ *  n_pages >= 1, n_pages * n_kv < 2^31; 1 <= n_kv <= 1024 key/value heads; page: tokens a page
+ *             holds, a power of two, 16 to 1024.
  *  D        : 64 or 128.
  *  rotate   : CBQ_KV_ROTATE_K | CBQ_KV_ROTATE_V, or fewer: which of the two are rotated (a
  *             Sylvester Hadamard transform over the D channels, orthonormal with the scale).
@@ -529,7 +530,9 @@ typedef struct {
  *                sequence b's last ones, the i-th at position lens[b] - (offsets[b+1] -
  *                offsets[b]) + i (a negative position is as in no page).  Tokens before offsets[0] and
  *                from offsets[B] on belong to no sequence: outputs leave their rows as they
- *                were.  NULL: each sequence has T / B tokens (T a multiple of B).
+ *                were.  NULL: each sequence has T / B tokens (T a multiple of B).  With offsets that
+ *                do not ascend cbq_kv_attention writes nothing, and the other two calls what each
+ *                token's sequence is found to be, within the cache and the tensors.
  *  0 <= B <= 65536, max_pages * page <= 2^30.  All three are device memory, so a captured graph
  *  replays with the lengths and pages of the day.
  */
@@ -581,9 +584,10 @@ int cbq_kv_cache_read(const cbq_kv_cache* cache, const cbq_kv_seqs* seqs, uint16
  *  window : 0, or (causal only) how many positions a token attends, its own the last of them.
  *  out    : bf16 [T][ldo] (as q): sum_j softmax(a)_j v_j, rounded once.  A token that attends
  *           nothing gets zeros.
- *  The rotated queries and the weights softmax(a)_j * scale_j enter the matrix cores as fp16
- *  relative to their own largest value; scores, softmax statistics and sums are fp32.  A
- *  value scale below 2^-64 counts as 2^-64 in the weights.  What a token does not attend (other pages,
+ *  The rotated queries times scale enter the matrix cores as fp16 (a head whose largest value is
+ *  outside 2^-4 ... 2^15, relative to that), and so do the weights softmax(a)_j * scale_j,
+ *  relative to the largest of their row; scores, softmax statistics and sums are fp32.  Value
+ *  scales are at most 2^126; one below 2^-64 counts as 2^-64.  What a token does not attend (other pages,
  *  masked positions, rows of other sequences) reaches its result in no way, whatever it holds.
  *  Deterministic: no result depends on the order of atomics.
  *  ws, ws_bytes : device workspace of cbq_kv_attention_workspace(...) bytes, 16-byte aligned;

@@ -163,6 +163,39 @@ def test_long_axes_split_over_the_chip(n_q, n_kv, D, lens, new):
     check_attention(Step(sum(lens), lens, new, n_kv, D, 64).device(), n_q)
 
 
+@pytest.mark.parametrize("new", [15, 16, 17, 31, 32, 33, 63, 65])
+@pytest.mark.parametrize("n_q,n_kv,D,length", [(8, 1, 64, 200), (8, 2, 128, 2500), (3, 1, 64, 4200)])
+def test_row_blocks(new, n_q, n_kv, D, length):
+    """Around 128 query rows a sequence, where the form changes, in blocks that end inside a token's heads; whole and cut."""
+    check_attention(Step(new + length, [length, 70], [new, new], n_kv, D, 64).device(), n_q)
+
+
+def test_long_prompts_in_many_row_blocks():
+    check_attention(Step(31, [700, 130], [700, 130], 2, 64, 32).device(), 8)          # self-attention, whole blocks
+    check_attention(Step(32, [1500], [1200], 1, 64, 64).device(), 2, window=200)
+    check_attention(Step(33, [6000, 40], [200, 40], 1, 128, 64).device(), 4, causal=False)
+
+
+def test_one_prompt_among_decoding_sequences():
+    """Few rows a sequence on average, one with many row blocks, which a wave counts together."""
+    check_attention(Step(34, [3000] + [60] * 20, [1500] + [1] * 20, 1, 64, 64).device(), 1)
+    lens = [50, 0, 2300] + [7] * 90 + [1200, 33]
+    new = [1, 0, 300] + [1] * 90 + [120, 2]
+    check_attention(Step(35, lens, new, 2, 64, 64).device(), 4)                       # more than 64 sequences
+
+
+def test_a_table_for_2_to_the_30_positions():
+    """Units of several key tiles: the count of a call's key tiles would pass 31 bits."""
+    B, page = 150, 1024
+    rng = np.random.default_rng(3)
+    lens = rng.integers(1, 3000, B).tolist()
+    st = Step(36, lens, [1] * B, 2, 64, page).device()
+    table = torch.full((B, (1 << 30) // page), -1, dtype=torch.int32, device=DEV)
+    table[:, :st.max_pages] = st.at["block_table"]
+    st.at["block_table"] = table
+    check_attention(st, 4)
+
+
 def test_many_sequences():
     rng = np.random.default_rng(5)
     lens = rng.integers(0, 90, 700).tolist()
