@@ -17,6 +17,13 @@
 // product wants 8 keys of one channel in a lane: the values go to LDS as they are, and
 // ds_read_b64_tr_b4 hands each lane 16 keys' codes of its channel.  Codes become fp16 by
 // v_cvt_scalef32_pk_f16_fp4, two at a time.
+//
+// What bounds it.  Up to 128 query rows a sequence (decode, drafted tokens) the cache is read once and the bytes count: the
+// kernel reads at 5.9 TB/s once under way, on top of 3.5 us until the first keys are there (length, schedule, page, key: four
+// dependent loads), some 3 us in which the last workgroups end, and 4 us for the launch that joins.  64 ragged
+// sequences of up to 32768 tokens: 48 us, 187 MB; one of 131072: 38 us, 143 MB.  Beyond that the vector instructions
+// count: 64 keys by 32 rows take 387 of them (weights, conversions of codes) next to 64 matrix instructions, which are busy
+// 29 to 41 % of the time.  The last 512 tokens of 16384: 159 us, 850 TFLOP/s; four prompts: 289 us, 820 TFLOP/s.
 #include <algorithm>
 
 #include "kv_device.hpp"
@@ -25,8 +32,11 @@ namespace cbq {
 namespace {
 
 constexpr int kTile = 64;          // keys a wave takes at a time
-constexpr int kWaves = 8;          // waves that share a decode row block
-// Workgroups of a split call, as many as the chip holds at once: 256 of eight waves, 512 of four.
+// Waves that share a row block of 16 rows.  Four, two workgroups on a compute unit, leave more parts to join: one sequence of
+// 131072 tokens 38.8 against 38.1 us, 16 of 4000 36.1 against 34.3; 32 windows of 4096 23.5 against 25.5.
+constexpr int kWaves = 8;
+// Workgroups of a split call, as many as the chip holds at once (with the registers of a wave at their most): 256 of eight
+// waves, 512 of four.
 constexpr int max_groups(int rows) { return rows == 128 ? 512 : 256; }
 
 // A sequence's part of the step, all values uniform over the workgroup.
@@ -94,13 +104,26 @@ __device__ __forceinline__ Range kv_tiles(const KvAttnArgs& g, const SplitArgs& 
   return Range{lo, max(hi, lo + 1)};
 }
 
+// ceil(x / y) for 0 <= x, 0 < y, quotients up to 2^16, by a reciprocal: what its rounding may miss is one step.
+__device__ __forceinline__ int div_up(int x, int y) {
+  const int q = (int)((float)x * __builtin_amdgcn_rcpf((float)y));
+  return (int64_t)q * y < x ? q + 1 : q;
+}
+
+// How units are counted: `start` of them for a row block's start, and each row block rounded up to a multiple of `whole`.
+struct Count { int start, whole; };
+
+__device__ __forceinline__ int units_of(const SplitArgs& sp, const Count& c, const Range& t) {
+  const int n = ((t.hi - t.lo - 1) >> sp.shift) + 1 + c.start;
+  return c.whole > 1 ? div_up(n, c.whole) * c.whole : n;
+}
+
 // Units of row block rb of a sequence.
 template <int ROWS>
-__device__ __forceinline__ int rb_units(const KvAttnArgs& g, const SplitArgs& sp, const Seq& q, int rb) {
+__device__ __forceinline__ int rb_units(const KvAttnArgs& g, const SplitArgs& sp, const Count& c, const Seq& q, int rb) {
   if (rb >= (q.rows + ROWS - 1) / ROWS) return 0;
   if (!sp.split) return 1;
-  const Range t = kv_tiles(g, sp, q, rb * ROWS, min((rb + 1) * ROWS, q.rows) - 1);
-  return ((t.hi - t.lo - 1) >> sp.shift) + 1 + sp.start_cost;
+  return units_of(sp, c, kv_tiles(g, sp, q, rb * ROWS, min((rb + 1) * ROWS, q.rows) - 1));
 }
 
 // Inclusive sums over the lanes of a wave.
@@ -126,6 +149,7 @@ struct Walk {
   // the current part: units [u0, u1) of `units` of row block `row0` of head `h` of sequence `seq`
   int seq, h, row0, u0, u1, units;
   Range tiles;                     // its key tiles
+  Count count;
   Seq lane_q;                      // up to 64 sequences: the lane's own, so that no start waits for a length
 
   // whether and for how many groups the current part goes on: only the last part of a group does
@@ -143,11 +167,11 @@ struct Walk {
   }
 
   // Units of one key/value head, by the whole wave; with at: the row block that holds unit *at, and what of it comes before.
-  static __device__ __forceinline__ int head_units(const KvAttnArgs& g, const SplitArgs& sp, const Seq& s, int* at, int* row) {
+  __device__ __forceinline__ int head_units(const KvAttnArgs& g, const SplitArgs& sp, const Seq& s, int* at, int* row) const {
     const int lane = threadIdx.x & 63;
     int n = 0;
     for (int rb = 0; rb * ROWS < s.rows; rb += 64) {
-      const int mine = rb_units<ROWS>(g, sp, s, rb + lane), inc = wave_scan(mine);
+      const int mine = rb_units<ROWS>(g, sp, count, s, rb + lane), inc = wave_scan(mine);
       const int all = __builtin_amdgcn_readlane(inc, 63);
       if (at && *at < n + all) {
         const int l = (int)__builtin_ctzll(__ballot(*at < n + inc));
@@ -164,30 +188,49 @@ struct Walk {
     const KvArgs& a = g.kv;
     const int lane = threadIdx.x & 63;
     const int each = (a.B + 63) >> 6;                 // sequences a lane counts
-    constexpr int kFew = 4;
-    int mine = 0, head = 0;
+    constexpr int kFew = 4;                           // row blocks that a lane counts by itself
+    int mine, head = 0, inc, total, blocks;
     bool ascending = true;
-    for (int k = 0; k < each; ++k) {
-      const int i = lane * each + k;
-      lane_q = Seq{0, 0, 0, 0};
-      if (i < a.B) lane_q = kv_seq(a, i, sp.G);
-      ascending = ascending && lane_q.rows >= 0;
-      const int blocks = (int)((uint32_t)(lane_q.rows + ROWS - 1) / ROWS);
-      head = blocks;
-      if (sp.split) {
-        head = 0;
-        if (blocks <= kFew)
-          for (int rb = 0; rb < blocks; ++rb) head += rb_units<ROWS>(g, sp, lane_q, rb);
-        for (uint64_t many = __ballot(blocks > kFew); many; many &= many - 1) {
-          const int l = (int)__builtin_ctzll(many);
-          const int n = head_units(g, sp, lane_seq(lane_q, l), nullptr, nullptr);
-          if (lane == l) head = n;
+    count = Count{sp.start_cost, 1};
+    per = 0;
+    for (;;) {
+      mine = blocks = 0;
+      for (int k = 0; k < each; ++k) {
+        const int i = lane * each + k;
+        if (each > 1 || per == 0) {
+          lane_q = Seq{0, 0, 0, 0};
+          if (i < a.B) lane_q = kv_seq(a, i, sp.G);
         }
+        ascending = ascending && lane_q.rows >= 0;
+        const int n = (int)((uint32_t)(lane_q.rows + ROWS - 1) / ROWS);
+        head = n;
+        if (sp.split) {
+          head = 0;
+          if (n <= kFew)
+            for (int rb = 0; rb < n; ++rb) head += rb_units<ROWS>(g, sp, count, lane_q, rb);
+          for (uint64_t many = __ballot(n > kFew); many; many &= many - 1) {
+            const int l = (int)__builtin_ctzll(many);
+            const int u = head_units(g, sp, lane_seq(lane_q, l), nullptr, nullptr);
+            if (lane == l) head = u;
+          }
+        }
+        mine += head * a.n_kv;
+        blocks += n * a.n_kv;
       }
-      mine += head * a.n_kv;
+      inc = wave_scan(mine);
+      total = __builtin_amdgcn_readlane(inc, 63);
+      if (per) break;
+      const int n = ROWS == 16 ? __builtin_amdgcn_readlane(wave_scan(blocks), 63) : 0;
+      per = max((int)(((uint32_t)total + sp.groups - 1) / (uint32_t)sp.groups), sp.min_units);
+      // Where it takes no longer, a workgroup takes units of one row block only (the sum of the rounded-up quotients is at
+      // most groups): a second row block in it would cost 1 to 3 us (4 heads, one sequence of 1200: 12.2 against 14.1 us, of
+      // 4096, where the even split happens to fit, 13.6 against 12.7; 8 heads, 8 of 3000: 16.2 against 18.5).
+      if (ROWS > 16 || !sp.split || n >= sp.groups) break;
+      const int own = max((int)(((uint32_t)(total - n * sp.start_cost) + sp.groups - n - 1) / (uint32_t)(sp.groups - n)), sp.min_units);
+      if (own > per) break;
+      per = own;
+      count = Count{0, own};
     }
-    const int inc = wave_scan(mine), total = __builtin_amdgcn_readlane(inc, 63);
-    per = max((int)(((uint32_t)total + sp.groups - 1) / (uint32_t)sp.groups), sp.min_units);
     // unsplit calls start with the last units: a sequence's last rows attend the most keys
     const int64_t at = sp.split ? (int64_t)blockIdx.x : (int64_t)sp.groups - 1 - blockIdx.x;
     left = 0;
@@ -251,7 +294,7 @@ struct Walk {
       }
     }
     tiles = kv_tiles(g, sp, q, r0, min(r0 + ROWS, q.rows) - 1);
-    units = ((tiles.hi - tiles.lo - 1) >> sp.shift) + 1 + sp.start_cost;
+    units = units_of(sp, count, tiles);
     row0 = r0;
     r0 += ROWS;
     seq = b;
@@ -261,8 +304,8 @@ struct Walk {
     left -= u1 - u0;
     off = 0;
     // the units that count for the start hold no keys
-    const int lo = tiles.lo + (max(u0 - sp.start_cost, 0) << sp.shift);
-    tiles.hi = min(tiles.hi, tiles.lo + (max(u1 - sp.start_cost, 0) << sp.shift));
+    const int lo = tiles.lo + (max(u0 - count.start, 0) << sp.shift);
+    tiles.hi = min(tiles.hi, tiles.lo + (max(u1 - count.start, 0) << sp.shift));
     tiles.lo = lo;
     return true;
   }
@@ -415,13 +458,23 @@ __device__ __forceinline__ void finish_row(float* v, float l, bool rotate, float
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
 
+// A key's scales as soft_weights takes them.
+__device__ __forceinline__ void stage_key(float ks, bool some, float* at) { *at = some ? ks : 0.0f; }
+__device__ __forceinline__ void stage_value(float vs, bool some, float* lv, float* iv) {
+  const float v = vs < 0x1p-64f ? 0x1p-64f : vs;
+  *lv = some ? __builtin_amdgcn_logf(v) : -INFINITY;
+  *iv = some ? __builtin_amdgcn_rcpf(v) : 0.0f;
+}
+
 // Scores of 64 keys to weights: sc[n][i][j] is row lane % 16 of row tile n and key 16i + 4 (lane / 16) + j of the tile at
-// position t0.  The running maximum moves only when a score passes it by 2^8: weights up to 256 lose
-// nothing in fp16, and most tiles then need neither an exchange between lanes nor a rescaling.
+// position t0.  Keys that no row attends come with ks = 0, lv = -inf and iv = 0 (stage_key, stage_value), which masks them at no
+// cost here; same: all rows attend the same of the others.  The running maximum moves only when a score passes it by
+// 2^8: weights up to 256 lose nothing in fp16, and most tiles then need neither an exchange between lanes nor a
+// rescaling.
 constexpr float kSlack = 8.0f;
 
 template <int D, int NB>
-__device__ __forceinline__ void soft_weights(const float* ks, const float* lv, const float* iv, int t0, bool whole, uint32_t held,
+__device__ __forceinline__ void soft_weights(const float* ks, const float* lv, const float* iv, int t0, bool same,
                                              bool unit, const float* rs, const int* lo, const int* hi, f32x4 (*sc)[4], float* M, float* l,
                                              f32x4 (*o)[D / 16], f16x8 (*w)[2]) {
   const int lane = threadIdx.x & 63, key = 4 * (lane >> 4);
@@ -439,13 +492,13 @@ __device__ __forceinline__ void soft_weights(const float* ks, const float* lv, c
 #pragma unroll
       for (int j = 0; j < 4; ++j) sc[n][i][j] = __builtin_fmaf(sc[n][i][j], k[j], v[j]);
   }
-  if (!whole) {
+  if (!same) {
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       const int at = t0 + key - lo[n];
+      const uint32_t len = (uint32_t)max(hi[n] - lo[n], 0);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t len = (held >> i) & 1 ? (uint32_t)max(hi[n] - lo[n], 0) : 0u;
 #pragma unroll
         for (int j = 0; j < 4; ++j) sc[n][i][j] = (uint32_t)(at + 16 * i + j) < len ? sc[n][i][j] : -INFINITY;
       }
@@ -476,7 +529,7 @@ __device__ __forceinline__ void soft_weights(const float* ks, const float* lv, c
         w[n][i >> 1][4 * (i & 1) + j] = (_Float16)p;
       }
   }
-  if (whole) {
+  if (same) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f32x4 v = *reinterpret_cast<const f32x4*>(iv + 16 * i + key);
@@ -485,7 +538,7 @@ __device__ __forceinline__ void soft_weights(const float* ks, const float* lv, c
 #pragma unroll
         for (int j = 0; j < 4; ++j) l[n] = __builtin_fmaf(sc[n][i][j], v[j], l[n]);
     }
-  } else {                                            // a masked key's 1 / vs may be NaN
+  } else {                                            // 1 / vs of a key that the row does not attend may be NaN
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f32x4 v = *reinterpret_cast<const f32x4*>(iv + 16 * i + key);
@@ -644,8 +697,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_kernel(KvAttnArgs
     l[0] = 0;
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) o[0][c] = f32x4{0, 0, 0, 0};
-    const int all_lo = kv_range(q, div_g(sp, row0 + n_rows - 1), g.causal, g.window).lo;   // positions that every row attends
-    const int all_hi = kv_range(q, div_g(sp, row0), g.causal, g.window).hi;
+    // positions that some row attends, and that every row does
+    const Range first = kv_range(q, div_g(sp, row0), g.causal, g.window), last = kv_range(q, div_g(sp, row0 + n_rows - 1), g.causal, g.window);
+    const Range any{first.lo, last.hi}, every{last.lo, first.hi};
     const int t_hi = u.tiles.hi;
     const bool unit = !__any(rs[0] != 1.0f);
     __syncthreads();                                  // the last part's sums have been read
@@ -657,16 +711,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_kernel(KvAttnArgs
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<typename Chunk<D>::T*>(vl + (16 * i + (lane >> 2)) * (D / 2) + ((lane & 3) ^ i) * (D / 8)) = cu.v[i];
-      {
-        const float v = cu.vs < 0x1p-64f ? 0x1p-64f : cu.vs;
-        s.t.ks[wave][lane] = cu.ks;
-        s.t.lv[wave][lane] = __builtin_amdgcn_logf(v);
-        s.t.iv[wave][lane] = __builtin_amdgcn_rcpf(v);
-      }
+      const int t0 = tile * kTile;
+      const bool some = ((cu.held >> (lane >> 4)) & 1) && t0 + lane >= any.lo && t0 + lane < any.hi;
+      stage_key(cu.ks, some, &s.t.ks[wave][lane]);
+      stage_value(cu.vs, some, &s.t.lv[wave][lane], &s.t.iv[wave][lane]);
       if (tile + WV < t_hi) {
         if (++at == 16) { pages = tile_pages<WV>(a, u.seq, tile + WV); at = 0; }
         load_tile<D>(a, kvh, tile + WV, pages, at, nx);
       }
+      if (!__ballot(some)) continue;                  // (a row that attends nothing gets zeros, whatever its query)
       // scores of 64 keys
       f32x4 sc[1][4];
 #pragma unroll
@@ -677,12 +730,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_kernel(KvAttnArgs
           sc[0][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[k], k ? sc[0][i] : f32x4{0, 0, 0, 0}, 0, 0, 0);
         }
       __builtin_amdgcn_wave_barrier();
-      const bool whole = cu.held == 15u && tile * kTile >= all_lo && tile * kTile + kTile <= all_hi;
+      const bool same = (t0 >= every.lo || any.lo == every.lo) && (t0 + kTile <= every.hi || any.hi == every.hi);
       i32x2 vc[D / 16];
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) vc[c] = value_codes<D>(vl, c);
       f16x8 w[1][2];
-      soft_weights<D, 1>(s.t.ks[wave], s.t.lv[wave], s.t.iv[wave], tile * kTile, whole, cu.held, unit, rs, lo, hi, sc, M, l, o, w);
+      soft_weights<D, 1>(s.t.ks[wave], s.t.lv[wave], s.t.iv[wave], t0, same, unit, rs, lo, hi, sc, M, l, o, w);
       // values times weights, 16 channels at a time
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
@@ -698,7 +751,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_kernel(KvAttnArgs
 }
 
 // ---------------------------------------------------------------------------
-// Many query rows a sequence (prefill): a workgroup takes 4 x 16 NB rows of one key/value head, each wave its own,
+// Many query rows a sequence (prefill): a workgroup takes 128 rows of one key/value head, each wave 32 of its own,
 // and all four read the same key tiles.  A tile (64 keys: codes as they are, 8 KB, and the scales)
 // goes through LDS in two buffers with one barrier a tile, the next one's loads in flight meanwhile; each wave
 // converts what it multiplies.
@@ -708,7 +761,7 @@ struct PrefillLds {
   struct Buf {
     alignas(16) uint8_t k[kTile * D / 2], v[kTile * D / 2];
     alignas(16) float ks[kTile], lv[kTile], iv[kTile];
-    int held[4];
+    int held[4];                                      // whether each 16 keys lie in a page
   } buf[2];
 };
 
@@ -791,7 +844,10 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) o[n][c] = f32x4{0, 0, 0, 0};
     }
-    Range any{0, 0}, every{0, 0};                 // positions that some, that every row of the wave attends
+    // positions that some row of the block attends, that some and that every row of the wave does
+    const Range block{kv_range(q, div_g(sp, r0), g.causal, g.window).lo,
+                      kv_range(q, div_g(sp, min(r0 + ROWS, q.rows) - 1), g.causal, g.window).hi};
+    Range any{0, 0}, every{0, 0};
     if (w_rows > 0) {
       const Range r_first = kv_range(q, div_g(sp, w0), g.causal, g.window);
       const Range r_last = kv_range(q, div_g(sp, w0 + w_rows - 1), g.causal, g.window);
@@ -827,12 +883,10 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
         const int key = 16 * wave + (lane >> 2);
         *reinterpret_cast<C*>(B.k + key * (D / 2) + ((lane & 3) ^ ((lane >> 4) & 3)) * (D / 8)) = kr;
         *reinterpret_cast<C*>(B.v + key * (D / 2) + ((lane & 3) ^ wave) * (D / 8)) = vr;
-        const float v = scale < 0x1p-64f ? 0x1p-64f : scale;
-        if (lane < 16) B.ks[16 * wave + lane] = scale;
-        if (lane >= 16 && lane < 32) {
-          B.lv[16 * wave + lane - 16] = __builtin_amdgcn_logf(v);
-          B.iv[16 * wave + lane - 16] = __builtin_amdgcn_rcpf(v);
-        }
+        const int at16 = 16 * wave + (lane & 15), pos = tile * kTile + at16;
+        const bool some = held && pos >= block.lo && pos < block.hi;
+        if (lane < 16) stage_key(scale, some, &B.ks[at16]);
+        if (lane >= 16 && lane < 32) stage_value(scale, some, &B.lv[at16], &B.iv[at16]);
         if (lane == 0) B.held[wave] = held;
       }
       lds_barrier();
@@ -860,13 +914,13 @@ __global__ __launch_bounds__(256, 2) void kv_prefill_kernel(KvAttnArgs g, SplitA
             sc[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[n][k], k ? sc[n][i] : f32x4{0, 0, 0, 0}, 0, 0, 0);
         }
       __builtin_amdgcn_s_setprio(0);
-      const uint32_t held4 = B.held[0] | B.held[1] << 1 | B.held[2] << 2 | B.held[3] << 3;
-      const bool whole = held4 == 15 && t0 >= every.lo && t0 + kTile <= every.hi;
+      if (!(B.held[0] | B.held[1] | B.held[2] | B.held[3])) continue;
+      const bool same = t0 >= every.lo && t0 + kTile <= every.hi;
       i32x2 vc[D / 16];
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) vc[c] = value_codes<D>(B.v, c);
       f16x8 w[NB][2];
-      soft_weights<D, NB>(B.ks, B.lv, B.iv, t0, whole, held4, unit, rs, lo, hi, sc, M, l, o, w);
+      soft_weights<D, NB>(B.ks, B.lv, B.iv, t0, same, unit, rs, lo, hi, sc, M, l, o, w);
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
@@ -969,7 +1023,9 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs g, SplitArgs sp
   finish_row<D>(v, sum, g.kv.rotate & 2, sp.c_v, sub, g.out + (int64_t)(d.t0 + i) * g.ldo + (d.kvh * sp.G + h) * D + 8 * sub);
 }
 
-// Query rows of a row block, by the rows a sequence has on average.
+// Query rows of a row block, by the rows a sequence has on average.  16 rows share keys among eight waves, 128 rows read them
+// once for all.  Both: 8 sequences of 4096, 64 rows each 32 against 39 us, 96 49 against 44, 128 56 against 48; one of 16384,
+// 96 rows 29 against 48, 128 32 against 52, 256 51 against 53; 32 of 1000, 128 rows 37.5 against 37.9, 192 53 against 46.
 int row_block(int64_t T, int B, int G) {
   const int64_t rows = (T + B - 1) / B * G;
   return rows <= 128 ? 16 : 128;
@@ -1042,7 +1098,10 @@ hipError_t launch_kv_attention(const KvAttnArgs& g, hipStream_t stream) {
   sp.min_units = 1;
   int64_t want = blocks;
   if (sp.split) {
+    // Fewer than 4 key tiles to a workgroup only make more parts: one head, one sequence of 4096, at least 1: 19 us, 4: 13, 16: 16.
     sp.min_units = 4;
+    // Queries, sums over the waves and results of a row block against key tiles.  64 ragged sequences: 48 us; counted as 8
+    // 56, as 64 54; drafted tokens 30, 35 and 33.  128 rows: 0 and 4 take what 1 does, within 1 %.
     sp.start_cost = rows == 128 ? 1 : 24;
     while (blocks * ((cap >> sp.shift) + 1 + sp.start_cost) >= 0x7FFFFFFF - most) ++sp.shift;
     want = (blocks * ((cap >> sp.shift) + 1 + sp.start_cost) + sp.min_units - 1) / sp.min_units;

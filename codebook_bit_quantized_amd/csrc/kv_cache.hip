@@ -8,6 +8,10 @@
 // sums; reading back needs fp32 only, as sums of at most 128 multiples of 1/2 up to 6 are exact there.
 // A workgroup takes the heads of some consecutive tokens; their places (sequence, length, page: four dependent
 // loads) are looked up once, by a lane each, and handed over in LDS.
+//
+// What bounds it.  Writing: vector instructions, most of them the transform's in fp64 (790 a wave; 30 us for a step of 8
+// prompts, 75 MB, of which the bytes would take 15).  Reading: HBM (65536 tokens of 4 heads: 170 MB in 40 us, 4.3 TB/s).  A
+// call for one token takes 3 us, the chain of its loads.
 #include "kv_device.hpp"
 
 namespace cbq {
@@ -184,7 +188,9 @@ hipError_t over_tokens(const KvArgs& a, F launch) {
   return hipSuccess;
 }
 
-// Few heads: a lane holds 8 channels of one.
+// Few heads: a lane holds 8 channels of one, else 4 lanes hold it (see the top).  16 and 4 lanes, D = 128, tokens of 8 heads:
+// write 1 token 3.4 and 4.2 us, 1024 5.5 and 5.6, 2048 8.2 and 6.1, 4096 13.6 and 9.6; read 1 3.0 and 3.7, 1024 4.9 and
+// 5.2, 2048 7.0 and 5.6.
 bool few_heads(const KvArgs& a) { return a.T * a.n_kv <= 8192; }
 
 }  // namespace
