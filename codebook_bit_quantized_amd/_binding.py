@@ -786,6 +786,8 @@ def kv_attention(cache: KVCache, q: torch.Tensor, lens: torch.Tensor, block_tabl
     ldo = n_q * D if out is None else _kv_heads("out", out, dev, T, n_q, D)
     s = _kv_seqs(cache, dev, lens, block_table, offsets)
     _tensor("ws", ws, dev, torch.uint8, contiguous=True)
+    if not 0 <= window < 1 << 31:
+        raise ValueError(f"window must be in [0, 2^31) (got {window})")
     if scale is None:
         scale = D ** -0.5
 

@@ -25,7 +25,7 @@ def _seqs(table=0x1000, ld=4, max_pages=4, lens=0x1000, offsets=0x1000, B=3):
     return ctypes.byref(cbq._binding.cbq_kv_seqs(table, ld, max_pages, lens, offsets, B))
 
 
-CACHE = [(dict(n_pages=0), "EINVAL"), (dict(n_kv=0), "EINVAL"), (dict(n_kv=1025), "EUNSUPPORTED"), (dict(page=8), "EINVAL"),
+CACHE = [(dict(n_pages=0), "EINVAL"), (dict(n_kv=0), "EINVAL"), (dict(n_kv=1025), "EUNSUPPORTED"), (dict(n_pages=1 << 30), "EUNSUPPORTED"), (dict(page=8), "EINVAL"),
          (dict(page=48), "EINVAL"), (dict(page=0), "EINVAL"), (dict(page=-16), "EINVAL"), (dict(page=2048), "EINVAL"),
          (dict(D=96), "EUNSUPPORTED"), (dict(D=0), "EUNSUPPORTED"), (dict(D=256), "EUNSUPPORTED"), (dict(rotate=4), "EINVAL"),
          (dict(rotate=-1), "EINVAL"), (dict(kc=None), "EINVAL"), (dict(vc=None), "EINVAL"), (dict(ks=None), "EINVAL"),
@@ -76,6 +76,7 @@ def test_attention_refusals(lib):
         assert lib.cbq_last_error()
     assert f(n_q=1026, ldq=1 << 20, ldo=1 << 20) == cbq.CBQ_EUNSUPPORTED
     assert f(ldq=1 << 62) == cbq.CBQ_EUNSUPPORTED and f(ldo=(1 << 31) + 8) == cbq.CBQ_EUNSUPPORTED
+    assert f(T=(1 << 30), n_q=2, seqs=_seqs(B=3)) == cbq.CBQ_EUNSUPPORTED            # T * n_q = 2^31
     assert f(ws=None) == cbq.CBQ_EWORKSPACE and f(n=need - 1) == cbq.CBQ_EWORKSPACE
 
 

@@ -184,6 +184,90 @@ def test_one_prompt_among_decoding_sequences():
     check_attention(Step(35, lens, new, 2, 64, 64).device(), 4)                       # more than 64 sequences
 
 
+@pytest.mark.parametrize("lens,new", [([90], [70]), ([2600], [70])])         # whole row blocks, and cut ones
+@pytest.mark.parametrize("rotate", [0, 1, 2, 3])
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompts_rotations_and_windows(lens, new, rotate, D):
+    st = Step(D + rotate + lens[0], lens, new, 1, D, 32, rotate).device()
+    check_attention(st, 4)
+    check_attention(st, 4, window=50)
+    check_attention(st, 4, causal=False)
+
+
+@pytest.mark.parametrize("spread,scale", [(0.0, None), (1e-3, None), (30.0, None), (1.0, -0.2), (1.0, 0.0), (1e30, 1e-30), (1e-30, 1e30)])
+def test_prompts_spreads_and_scales(spread, scale):
+    check_attention(Step(41, [150], [90], 2, 64, 16).device(), 4, q_spread=spread, scale=scale)
+
+
+def test_prompts_scales_of_the_cache_far_apart():
+    st = Step(42, [200], [130], 1, 64, 16, garbage=False)
+    rng = np.random.default_rng(1)
+    st.scales[1] = np.ldexp(st.scales[1], rng.integers(-40, 60, st.scales[1].shape)).astype(np.float32)
+    st.scales[0] = np.ldexp(st.scales[0], rng.integers(-20, 3, st.scales[0].shape)).astype(np.float32)
+    check_attention(st.device(), 2)
+
+
+@pytest.mark.parametrize("n_q,n_kv,new", [(1024, 1, 1), (1024, 1, 2), (1024, 1024, 1), (1024, 512, 3), (1000, 8, 1), (7, 7, 40), (96, 1, 2)])
+def test_many_heads(n_q, n_kv, new):
+    check_attention(Step(n_q + new, [40], [new], n_kv, 64, 16).device(), n_q)
+
+
+def test_padding_queries_that_are_not_finite():
+    """Rows that attend nothing get zeros whatever their queries hold: empty sequences, pages given back, tokens before the
+    start; in both forms, with few and many key tiles."""
+    for new, long in ((1, 40), (1, 5000), (100, 140), (100, 5000)):
+        st = Step(new + long, [long, 0, 200, -3], [new, new, new, new], 1, 64, 16)
+        st.table[2, :] = -1
+        st.device()
+        q = torch.randn((st.T, 4, 64), device=DEV).to(torch.bfloat16)
+        want = cbq.kv_attention(st.cache, q, st.d_lens, **st.at)
+        assert bool(want[:new].any()) and not bool(want[new:].any())
+        for bad in (float("nan"), float("inf")):
+            q[new:] = bad
+            got = cbq.kv_attention(st.cache, q, st.d_lens, **st.at)
+            assert torch.equal(got, want)
+
+
+def test_offsets_that_do_not_ascend():
+    """Nothing is written, in either form."""
+    for new in (1, 100):
+        st = Step(new, [200, 300, 150], [new] * 3, 2, 64, 16).device()
+        q = torch.randn((st.T, 8, 64), device=DEV).to(torch.bfloat16)
+        for o in ([0, 2 * new, new, 3 * new], [3 * new, 0, 0, 3 * new], [0, 3 * new, -7, 2 ** 31 - 1], [0, 2 ** 31 - 1, -2 ** 31, 5]):
+            out = torch.full_like(q, 7.0)
+            cbq.kv_attention(st.cache, q, st.d_lens, st.at["block_table"], torch.tensor(o, dtype=torch.int32, device=DEV), out=out)
+            assert bool((out == 7).all())
+
+
+def test_the_most_sequences():
+    B, at = 65536, {0: 5, 1000: 70, 30000: 1, 30001: 16, 65535: 33}
+    lens = [at.get(b, 0) for b in range(B)]
+    check_attention(Step(43, lens, [min(n, 3) for n in lens], 1, 64, 16).device(), 2)
+
+
+def test_two_graphs_that_share_a_workspace():
+    """Replayed in turn, each with its own results."""
+    steps = [Step(44, [2500, 80], [1, 1], 2, 64, 64).device(), Step(45, [3000], [150], 2, 64, 64).device()]
+    qs = [torch.randn((s.T, 8, 64), device=DEV).to(torch.bfloat16) for s in steps]
+    want = [cbq.kv_attention(s.cache, q, s.d_lens, **s.at) for s, q in zip(steps, qs)]
+    n = max(cbq.kv_attention_workspace(s.cache, s.T, len(s.lens), 8) for s in steps)
+    ws = torch.empty((n,), dtype=torch.uint8, device=DEV)
+    outs = [torch.empty_like(q) for q in qs]
+    graphs = []
+    for s, q, o in zip(steps, qs, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            cbq.kv_attention(s.cache, q, s.d_lens, out=o, ws=ws, **s.at)
+        graphs.append(g)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
 def test_a_table_for_2_to_the_30_positions():
     """Units of several key tiles: the count of a call's key tiles would pass 31 bits."""
     B, page = 150, 1024

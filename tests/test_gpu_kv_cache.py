@@ -159,6 +159,68 @@ def test_extreme_rows():
         assert np.array_equal(got_s[~bad], s[~bad]) and np.array_equal(got_c[~bad], oracle.kv_pack(q)[~bad])
 
 
+@pytest.mark.parametrize("lens,n_kv,D,page,rotate", [
+    ([1024], 8, 128, 64, 3), ([1025], 8, 128, 64, 3),    # 8192 heads, and more: four lanes a head
+    ([700, 400], 8, 64, 16, 3), ([300, 9, 800], 9, 128, 32, 0), ([9, 11], 1024, 64, 16, 3), ([6, 3], 1000, 128, 16, 2)])
+def test_many_heads(lens, n_kv, D, page, rotate):
+    """Each form of the kernels against the oracle; read back in one call as sequence by sequence."""
+    st = Step(sum(lens) + D, lens, lens, n_kv, D, page, rotate, garbage=False).device()
+    (k, k64), (v, v64) = bf16_values(st.rng, (st.T, n_kv, D), 3), bf16_values(st.rng, (st.T, n_kv, D), 0.2)
+    k[0, 0, ::3] = -0.0                                   # a zero's sign stays
+    k64[0, 0, ::3] = -0.0
+    before = _host(st.cache)
+    cbq.kv_cache_write(st.cache, k.to(DEV), v.to(DEV), st.d_lens, **st.at)
+    _check_write(st, (k64, v64), before, rotate)
+    whole = cbq.kv_cache_read(st.cache, st.d_lens, st.T, **st.at)
+    for b, n in enumerate(lens):
+        for t in range(0, n, 8000 // n_kv):               # positions t ... of sequence b
+            m = min(8000 // n_kv, n - t)
+            part = cbq.kv_cache_read(st.cache, torch.tensor([t + m], dtype=torch.int32, device=DEV), m, st.at["block_table"][b:b + 1])
+            for i in range(2):
+                assert torch.equal(whole[i][st.offsets[b] + t:st.offsets[b] + t + m], part[i])
+    host = _host(st.cache)
+    place = st.places()
+    for i in range(2):
+        x = oracle.kv_dequantise(oracle.kv_unpack(host[i][place[:, 2], :, place[:, 3]]), host[2 + i][place[:, 2], :, place[:, 3]],
+                                 bool(rotate >> i & 1))
+        assert np.all(np.abs(whole[i].double().cpu().numpy() - x) <= (2.0 ** -8 + 2.0 ** -22) * np.abs(x) + 1e-40)
+
+
+def test_arguments_are_checked():
+    cache = cbq.KVCache.empty(4, 2, 16, 64)
+    x = torch.zeros((3, 2, 64), dtype=torch.bfloat16, device=DEV)
+    lens = torch.tensor([3], dtype=torch.int32, device=DEV)
+    table = torch.zeros((1, 4), dtype=torch.int32, device=DEV)
+    offsets = torch.tensor([0, 3], dtype=torch.int32, device=DEV)
+    bad = [dict(k=x.half()), dict(k=x[:, :1]), dict(k=x[:2]), dict(k=x[:, :, :32]), dict(k=x.transpose(1, 2)), dict(k=x.cpu()),
+           dict(k=x[..., None]), dict(lens=lens.long()), dict(lens=lens[None]), dict(lens=lens.cpu()), dict(block_table=table[0]),
+           dict(block_table=table.long()), dict(block_table=table.expand(2, 4)), dict(offsets=offsets[:1]), dict(offsets=offsets.float()),
+           dict(offsets=offsets.cpu())]
+    for b in bad:
+        a = dict(k=x, lens=lens, block_table=table, offsets=offsets)
+        a.update(b)
+        with pytest.raises((ValueError, RuntimeError)):
+            cbq.kv_cache_write(cache, a["k"], x, a["lens"], a["block_table"], a["offsets"])
+        with pytest.raises((ValueError, RuntimeError)):
+            cbq.kv_cache_write(cache, x, a["k"], a["lens"], a["block_table"], a["offsets"] if "k" not in b else offsets[:1])
+        with pytest.raises((ValueError, RuntimeError)):
+            cbq.kv_cache_read(cache, a["lens"], 3, a["block_table"], a["offsets"], k=a["k"], v=x)
+        if b.get("k") is None or b["k"].shape[0] != 2 and tuple(b["k"].shape[1:]) != (1, 64):
+            with pytest.raises((ValueError, RuntimeError)):
+                cbq.kv_attention(cache, a["k"], a["lens"], a["block_table"], a["offsets"])
+    for b in (dict(window=-1), dict(window=1 << 32), dict(window=3, causal=False), dict(scale=float("nan")), dict(out=x[:2]),
+              dict(out=x.float()), dict(ws=torch.empty((16,), dtype=torch.uint8, device=DEV)), dict(ws=x)):
+        with pytest.raises((ValueError, RuntimeError)):
+            cbq.kv_attention(cache, x, lens, table, offsets, **b)
+    for i, t in enumerate((cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales)):
+        for other in (t[:3], t.cpu(), t.double(), t.transpose(1, 2)):
+            parts = [cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales]
+            parts[i] = other
+            with pytest.raises((ValueError, RuntimeError)):
+                cbq.kv_cache_write(cbq.KVCache(*parts), x, x, lens, table, offsets)
+    assert not bool(cache.k_codes.any())
+
+
 def test_codes_are_those_of_the_same_token_in_any_batch():
     n_kv, D = 4, 128
     st = Step(11, [500], [500], n_kv, D, 64).device()
