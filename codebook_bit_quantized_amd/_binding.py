@@ -671,44 +671,54 @@ class KVCache:
 
     def _c_checked(self, dev: torch.device) -> cbq_kv_cache:
         """The C struct of tensors that are as it describes them: on dev, packed, of these sizes."""
-        if self.k_codes.dim() != 4:
-            raise ValueError(f"k_codes must have four dimensions (got shape {tuple(self.k_codes.shape)})")
-        n, h, p, half = self.k_codes.shape
-        _tensor("k_codes", self.k_codes, dev, torch.uint8, contiguous=True)
-        _tensor("v_codes", self.v_codes, dev, torch.uint8, (n, h, p, half), contiguous=True)
-        _tensor("k_scales", self.k_scales, dev, torch.float32, (n, h, p), contiguous=True)
-        _tensor("v_scales", self.v_scales, dev, torch.float32, (n, h, p), contiguous=True)
-        return cbq_kv_cache(self.k_codes.data_ptr(), self.v_codes.data_ptr(), self.k_scales.data_ptr(),
-                            self.v_scales.data_ptr(), n, h, p, 2 * half, self.rotate)
+        kc, vc, ks, vs = self.k_codes, self.v_codes, self.k_scales, self.v_scales
+        codes, scales = kc.shape, ks.shape
+        if len(codes) != 4:
+            raise ValueError(f"k_codes must have four dimensions (got shape {tuple(codes)})")
+        n, h, p, half = codes
+        # the usual case in one expression: the calls' checks are most of a small call's time on the host
+        if not (kc.dtype is vc.dtype is torch.uint8 and ks.dtype is vs.dtype is torch.float32
+                and kc.device == vc.device == ks.device == vs.device == dev
+                and vc.shape == codes and scales == codes[:3] and vs.shape == scales
+                and kc.is_contiguous() and vc.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+            for name, t, dtype, shape in (("k_codes", kc, torch.uint8, codes), ("v_codes", vc, torch.uint8, codes),
+                                          ("k_scales", ks, torch.float32, codes[:3]), ("v_scales", vs, torch.float32, codes[:3])):
+                _tensor(name, t, dev, dtype, shape, contiguous=True)
+        return cbq_kv_cache(kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), n, h, p, 2 * half, self.rotate)
 
 
 def _kv_seqs(cache: KVCache, dev, lens, block_table, offsets) -> cbq_kv_seqs:
     if lens.dim() != 1:
         raise ValueError(f"lens must have one dimension (got shape {tuple(lens.shape)})")
     B = lens.shape[0]
-    _tensor("lens", lens, dev, torch.int32, contiguous=True)
-    _tensor("offsets", offsets, dev, torch.int32, (B + 1,), contiguous=True)
+    _tensor("lens", lens, dev, torch.int32, None, False, True)
+    if offsets is not None:
+        _tensor("offsets", offsets, dev, torch.int32, (B + 1,), False, True)
+        offsets = offsets.data_ptr()
     if block_table is None:
-        return cbq_kv_seqs(None, 0, cache.n_pages // max(B, 1), lens.data_ptr(), _opt_ptr(offsets), B)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table must have shape ({B}, pages) (got {tuple(block_table.shape)})")
-    _tensor("block_table", block_table, dev, torch.int32, rows=True)
-    ld = block_table.stride(0) if B > 1 else block_table.shape[1]
-    if ld < block_table.shape[1]:
+        return cbq_kv_seqs(None, 0, cache.n_pages // max(B, 1), lens.data_ptr(), offsets, B)
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != B:
+        raise ValueError(f"block_table must have shape ({B}, pages) (got {tuple(shape)})")
+    _tensor("block_table", block_table, dev, torch.int32, None, True)
+    pages = shape[1]
+    ld = block_table.stride(0) if B > 1 else pages
+    if ld < pages:
         raise ValueError("block_table's rows must not overlap")
-    return cbq_kv_seqs(block_table.data_ptr(), ld, block_table.shape[1], lens.data_ptr(), _opt_ptr(offsets), B)
+    return cbq_kv_seqs(block_table.data_ptr(), ld, pages, lens.data_ptr(), offsets, B)
 
 
 def _kv_heads(name: str, t: torch.Tensor, dev, T: Optional[int], heads: Optional[int], D: int) -> int:
     """Checks a bf16 [T][heads*D] or [T][heads][D] tensor (rows may be strided) and returns its row stride."""
-    shape = tuple(t.shape)
-    if t.dim() not in (2, 3) or (t.dim() == 3 and shape[2] != D) or (t.dim() == 2 and shape[1] % D):
-        raise ValueError(f"{name} must have shape (T, heads, {D}) or (T, heads * {D}) (got {shape})")
-    n = shape[1] if t.dim() == 3 else shape[1] // D
+    shape = t.shape
+    three = len(shape) == 3
+    if shape[2] != D if three else len(shape) != 2 or shape[1] % D:
+        raise ValueError(f"{name} must have shape (T, heads, {D}) or (T, heads * {D}) (got {tuple(shape)})")
+    n = shape[1] if three else shape[1] // D
     if (T is not None and shape[0] != T) or (heads is not None and n != heads):
-        raise ValueError(f"{name} must hold {T} tokens of {heads} heads (got shape {shape})")
-    _tensor(name, t, dev, torch.bfloat16, rows=True)
-    if t.dim() == 3 and t.numel() > 0 and n > 1 and t.stride(1) != D:
+        raise ValueError(f"{name} must hold {T} tokens of {heads} heads (got shape {tuple(shape)})")
+    _tensor(name, t, dev, torch.bfloat16, None, True)
+    if three and n > 1 and t.stride(1) != D and t.numel() > 0:
         raise ValueError(f"{name}: a token's heads must be contiguous")
     return t.stride(0) if shape[0] > 1 else max(n * D, 8)
 
