@@ -186,6 +186,35 @@ def test_many_heads(lens, n_kv, D, page, rotate):
         assert np.all(np.abs(whole[i].double().cpu().numpy() - x) <= (2.0 ** -8 + 2.0 ** -22) * np.abs(x) + 1e-40)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_heads_of_all_magnitudes(D):
+    """Rotated rows whose values lie within or beyond 8 and 17 binades of their largest, near the ends of the exponent range, or are
+    zero, neighbours in the kernel's groups of 16: codes and scales bit for bit the oracle's, which sums in fp64."""
+    n_kv, T = 8, 1100
+    st = Step(D, [T], [T], n_kv, D, 64, 3, garbage=False).device()
+    rng = np.random.default_rng(D)
+    depth = np.array([0, 1, 7, 8, 9, 10, 16, 17, 18, 25, 30])[rng.integers(0, 11, (T, n_kv, 1))]     # binades down to the least
+    x = np.ldexp(1 + rng.integers(0, 128, (T, n_kv, D)) / 128, -rng.integers(0, 31, (T, n_kv, D)) % (depth + 1))
+    x *= np.where(rng.random(x.shape) < 0.5, -1, 1) * (rng.random(x.shape) > 0.1)
+    x[: T // 4] = np.abs(x[: T // 4])                     # sums as large as they get
+    x = np.ldexp(x, np.array([0, 0, 0, 0, 100, -60, -90, -115])[rng.integers(0, 8, (T, n_kv, 1))])
+    x[rng.random((T, n_kv)) < 0.05] = 0
+    x[rng.random((T, n_kv)) < 0.02] = -0.0
+    x[::50, 3] = np.sign(x[::50, 3]) * 1.0                # all of one magnitude
+    x[1::50, 2] = np.ldexp(np.sign(x[1::50, 2]), -133)    # bf16's smallest
+    y = torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16)
+    x = y.double().numpy()                                # some have become subnormal or zero
+    cbq.kv_cache_write(st.cache, y.to(DEV), (-y).to(DEV), st.d_lens, **st.at)
+    place = st.places()
+    for i, v in enumerate((x, -x)):
+        q, want = oracle.kv_quantise(v, True)
+        codes, scales = (_host(st.cache)[j][place[:, 2], :, place[:, 3]] for j in (i, 2 + i))
+        fine = np.isfinite(want)                          # sums beyond fp32 leave a row that is not finite
+        assert fine.mean() > 0.9 and not np.isfinite(scales[~fine]).any()
+        assert np.array_equal(scales[fine].view(np.uint32), want[fine].view(np.uint32))
+        assert np.array_equal(codes[fine], oracle.kv_pack(q)[fine])
+
+
 def test_arguments_are_checked():
     cache = cbq.KVCache.empty(4, 2, 16, 64)
     x = torch.zeros((3, 2, 64), dtype=torch.bfloat16, device=DEV)
