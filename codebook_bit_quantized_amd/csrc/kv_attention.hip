@@ -18,7 +18,7 @@
 // ds_read_b64_tr_b4 hands each lane 16 keys' codes of its channel.  Codes become fp16 by
 // v_cvt_scalef32_pk_f16_fp4, two at a time.
 //
-// What bounds it.  Up to 128 query rows a sequence (decode, drafted tokens) the cache is read once and the bytes count: the
+// What bounds it.  With few query rows (decode, drafted tokens) the cache is read once and the bytes count: the
 // kernel reads at 5.9 TB/s once under way, on top of 3.5 us until the first keys are there (length, schedule, page, key: four
 // dependent loads), some 3 us in which the last workgroups end, and 4 us for the launch that joins.  64 ragged
 // sequences of up to 32768 tokens: 48 us, 187 MB; one of 131072: 38 us, 143 MB.  Beyond that the vector instructions
@@ -751,7 +751,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_kernel(KvAttnArgs
 }
 
 // ---------------------------------------------------------------------------
-// Many query rows a sequence (prefill): a workgroup takes 128 rows of one key/value head, each wave 32 of its own,
+// Many query rows (prefill): a workgroup takes 128 rows of one key/value head, each wave 32 of its own,
 // and all four read the same key tiles.  A tile (64 keys: codes as they are, 8 KB, and the scales)
 // goes through LDS in two buffers with one barrier a tile, the next one's loads in flight meanwhile; each wave
 // converts what it multiplies.
@@ -1023,25 +1023,31 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs g, SplitArgs sp
   finish_row<D>(v, sum, g.kv.rotate & 2, sp.c_v, sub, g.out + (int64_t)(d.t0 + i) * g.ldo + (d.kvh * sp.G + h) * D + 8 * sub);
 }
 
-// Query rows of a row block, by the rows a sequence has on average.  16 rows share keys among eight waves, 128 rows read them
-// once for all.  Both: 8 sequences of 4096, 64 rows each 32 against 39 us, 96 49 against 44, 128 56 against 48; one of 16384,
-// 96 rows 29 against 48, 128 32 against 52, 256 51 against 53; 32 of 1000, 128 rows 37.5 against 37.9, 192 53 against 46.
-int row_block(int64_t T, int B, int G) {
-  const int64_t rows = (T + B - 1) / B * G;
-  return rows <= 128 ? 16 : 128;
+// Query rows of a row block, by the rows a sequence has on average and all rows together.  16 rows share keys among eight
+// waves and start sooner, 128 rows read them once for all.  Which is faster goes by rows times keys, about 25 million
+// of them; the keys' number stays on the device.  Both forms, 8 key/value heads, rows a sequence:
+//   1 sequence  of  1000: 512 rows 12 and 28 us; of 4096: 256 24 and 31, 512 35 and 40; of 16384: 256 47 and 54, 512 78 and 66
+//   2 sequences of  8192: 256 43 and 48, 384 68 and 56
+//   4 sequences of  2048: 128 16 and 32, 256 28 and 40, 512 50 and 48; of 8192: 96 46 and 44, 128 54 and 49, 256 95 and 65
+//   8 sequences of  4096: 64 32 and 40, 96 49 and 44, 128 57 and 48, 256 100 and 65
+//   16 sequences of 2048: 96 39 and 43, 128 52 and 48, 256 97 and 67
+int row_block(int64_t T, int B, int n_q, int n_kv) {
+  const int64_t rows = (T + B - 1) / B * (n_q / n_kv);
+  return rows <= 128 || T * n_q <= 4096 ? 16 : 128;
 }
 
 // Whether row blocks are cut, for a second launch that joins them (about 4 us and the parts' traffic).
-//  16 rows: no below 1024 positions (4 heads, one sequence of 1000: 11 against 11.4 us; of 512: 9.4 against 11.7; of
-//  2048: 14.4 against 11.9, of 4096: 21.6 against 12.5), nor below 2048 with 64 row blocks (16 sequences of 2048: 14.8
-//  against 15.6; of 4096: 22.6 against 18.9).
+//  16 rows: a whole block takes 7.5 us and 0.23 a key tile, cutting pays from 1536 positions (8 heads, one sequence of
+//  1203: 11.3 against 12.3 us; of 2011: 14.4 against 12.7, of 4096: 22 against 13), with more row blocks later: 64 of
+//  them from 2560 (16 heads, 4 of 2011: 12.2 against 12.9; of 4096: 17.8 against 15.0), 128 from 4096 (8 heads, 16 of 2011: 15.9
+//  against 19.2; of 4096: the same; of 16384: 68 against 54).
 //  128 rows: whole blocks take 8 us and 1.75 a key tile, in rounds of 512 where the longest go first; cut ones 22 us and
 //  half as much again, evenly (64 new tokens, 8 heads, one sequence of 1024: 35.5 against 25 us; 16 of them: 37 against 51;
 //  a prompt of 2048: 70 against 91).
 // So many row blocks that there is work for each compute unit many times over are not cut.
 bool split_pays(const KvAttnArgs& g, int rows, int64_t blocks, int64_t cap) {
   if (blocks >= 1 << 24) return false;                // (so that the units of all fit 31 bits)
-  if (rows == 16) return cap > (blocks >= 64 ? 33 : 17);
+  if (rows == 16) return cap > (blocks >= 128 ? 65 : blocks >= 64 ? 41 : 25);
   const KvArgs& a = g.kv;
   const int64_t G = g.n_q / a.n_kv;
   const double n = (double)a.n_kv * (a.offsets ? (double)(a.T * G / rows) + 0.5 * a.B : (double)a.B * ((a.per_seq * G + rows - 1) / rows));
@@ -1071,13 +1077,13 @@ hipError_t launch_prefill(const KvAttnArgs& g, SplitArgs sp, hipStream_t stream)
 }  // namespace
 
 size_t kv_attention_workspace_bytes(int64_t T, int B, int n_q, int n_kv, int D) {
-  const int rows = row_block(T, B, n_q / n_kv);
+  const int rows = row_block(T, B, n_q, n_kv);
   return (size_t)max_groups(rows) * (sizeof(Desc) + 2 * rows * (sizeof(float2) + D * sizeof(float)));
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs& g, hipStream_t stream) {
   const KvArgs& a = g.kv;
-  const int G = g.n_q / a.n_kv, rows = row_block(a.T, a.B, G), most = max_groups(rows);
+  const int G = g.n_q / a.n_kv, rows = row_block(a.T, a.B, g.n_q, a.n_kv), most = max_groups(rows);
   SplitArgs sp{};
   const float c = (float)(1.0 / std::sqrt((double)a.D));
   sp.c_q = a.rotate & 1 ? c : 1.0f;
@@ -1091,7 +1097,8 @@ hipError_t launch_kv_attention(const KvAttnArgs& g, hipStream_t stream) {
   sp.g_mul = (uint32_t)(((uint64_t(1) << sp.g_shift) + G - 1) / G);
   const int64_t own = (int64_t)a.per_seq * G;
   sp.join_rows = a.offsets || own > rows ? rows : (int)own;
-  const int64_t blocks = ((a.T * G + rows - 1) / rows + a.B) * a.n_kv;      // row blocks at most
+  // row blocks at most
+  const int64_t blocks = (a.offsets ? (a.T * G + rows - 1) / rows + a.B : a.B * ((own + rows - 1) / rows)) * a.n_kv;
   int64_t cap = ((int64_t)a.max_pages << a.logp) / kTile + 1;               // key tiles of one at most
   if (g.window) cap = std::min(cap, ((int64_t)g.window + rows / G + 1) / kTile + 2);
   sp.split = split_pays(g, rows, blocks, cap);

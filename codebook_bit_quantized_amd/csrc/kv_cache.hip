@@ -9,9 +9,11 @@
 // A workgroup takes the heads of some consecutive tokens; their places (sequence, length, page: four dependent
 // loads) are looked up once, by a lane each, and handed over in LDS.
 //
-// What bounds it.  Writing: vector instructions, most of them the transform's in fp64 (790 a wave; 30 us for a step of 8
-// prompts, 75 MB, of which the bytes would take 15).  Reading: HBM (65536 tokens of 4 heads: 170 MB in 40 us, 4.3 TB/s).  A
-// call for one token takes 3 us, the chain of its loads.
+// What bounds it.  Writing: 16384 tokens of 8 heads take 26 us, 17 not rotated, and 25 as torch's copy of the same rows;
+// 65536 take 92, 84 and 101.  Rotated on the matrix cores (two products of exact fp32 sums, the values that lie 8 binades below
+// their head's largest apart) they took 27 and 96: what it saved in fp64 instructions went into the exchange of lanes and
+// fewer waves.  Reading: HBM (65536 tokens of 4 heads, 170 MB in 43 us, 4.0 TB/s of which four fifths are written).  A call
+// for one token takes 3 us, the chain of its loads.
 #include "kv_device.hpp"
 
 namespace cbq {
