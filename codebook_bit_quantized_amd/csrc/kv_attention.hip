@@ -226,7 +226,8 @@ struct Walk {
       // most groups): a second row block in it would cost 1 to 3 us (4 heads, one sequence of 1200: 12.2 against 14.1 us, of
       // 4096, where the even split happens to fit, 13.6 against 12.7; 8 heads, 8 of 3000: 16.2 against 18.5).
       if (ROWS > 16 || !sp.split || n >= sp.groups) break;
-      const int own = max((int)(((uint32_t)(total - n * sp.start_cost) + sp.groups - n - 1) / (uint32_t)(sp.groups - n)), sp.min_units);
+      const int rest = total - n * sp.start_cost, free = sp.groups - n;
+      const int own = max((int)(((uint32_t)rest + free - 1) / (uint32_t)free), sp.min_units);
       if (own > per) break;
       per = own;
       count = Count{0, own};
@@ -698,7 +699,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_kernel(KvAttnArgs
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) o[0][c] = f32x4{0, 0, 0, 0};
     // positions that some row attends, and that every row does
-    const Range first = kv_range(q, div_g(sp, row0), g.causal, g.window), last = kv_range(q, div_g(sp, row0 + n_rows - 1), g.causal, g.window);
+    const Range first = kv_range(q, div_g(sp, row0), g.causal, g.window);
+    const Range last = kv_range(q, div_g(sp, row0 + n_rows - 1), g.causal, g.window);
     const Range any{first.lo, last.hi}, every{last.lo, first.hi};
     const int t_hi = u.tiles.hi;
     const bool unit = !__any(rs[0] != 1.0f);
@@ -1040,17 +1042,24 @@ int row_block(int64_t T, int B, int n_q, int n_kv) {
 //  16 rows: a whole block takes 7.5 us and 0.23 a key tile, cutting pays from 1536 positions (8 heads, one sequence of
 //  1203: 11.3 against 12.3 us; of 2011: 14.4 against 12.7, of 4096: 22 against 13), with more row blocks later: 64 of
 //  them from 2560 (16 heads, 4 of 2011: 12.2 against 12.9; of 4096: 17.8 against 15.0), 128 from 4096 (8 heads, 16 of 2011: 15.9
-//  against 19.2; of 4096: the same; of 16384: 68 against 54).
+//  against 19.2; of 4096: the same; of 16384: 68 against 54).  With a window the row blocks are alike, and whole ones lose
+//  only what the last 256 leave idle (8 heads of 64, window 4096, 16 sequences: 18.2 against 21.0; 32: 19.3 against 27.3, 40: 32.1
+//  against 30.9, 48: 32.4 against 34.4; window 8192: 28.6 and 25.9, 29.3 and 34.2, 52.7 and 40.4, 52.7 and 44.4).
 //  128 rows: whole blocks take 8 us and 1.75 a key tile, in rounds of 512 where the longest go first; cut ones 22 us and
 //  half as much again, evenly (64 new tokens, 8 heads, one sequence of 1024: 35.5 against 25 us; 16 of them: 37 against 51;
 //  a prompt of 2048: 70 against 91).
 // So many row blocks that there is work for each compute unit many times over are not cut.
 bool split_pays(const KvAttnArgs& g, int rows, int64_t blocks, int64_t cap) {
   if (blocks >= 1 << 24) return false;                // (so that the units of all fit 31 bits)
-  if (rows == 16) return cap > (blocks >= 128 ? 65 : blocks >= 64 ? 41 : 25);
   const KvArgs& a = g.kv;
+  if (rows == 16) {
+    const int64_t idle = -blocks & (max_groups(16) - 1);
+    if (g.window && !a.offsets && blocks >= 128 && idle <= (cap > 80 ? 64 : 128)) return false;
+    return cap > (blocks >= 128 ? 65 : blocks >= 64 ? 41 : 25);
+  }
   const int64_t G = g.n_q / a.n_kv;
-  const double n = (double)a.n_kv * (a.offsets ? (double)(a.T * G / rows) + 0.5 * a.B : (double)a.B * ((a.per_seq * G + rows - 1) / rows));
+  const double n = a.n_kv * (a.offsets ? (double)(a.T * G / rows) + 0.5 * a.B
+                                       : (double)a.B * ((a.per_seq * G + rows - 1) / rows));
   const double mean = g.causal ? std::max((double)cap - (double)(a.T / a.B) / (2 * kTile), 0.5 * cap) : (double)cap;
   const double whole = std::max(8 + 1.75 * cap, n * (8 + 1.75 * mean) / 512);
   return 22 + 1.5 * n * 1.75 * mean / 512 < whole;

@@ -170,6 +170,16 @@ def test_row_blocks(new, n_q, n_kv, D, length):
     check_attention(Step(new + length, [length, 70], [new, new], n_kv, D, 64).device(), n_q)
 
 
+@pytest.mark.parametrize("lens,n_kv,window", [([5000, 3000, 40], 1, 2500), ([4400, 100] * 8, 8, 4200), ([2600, 70] * 12, 8, 2000),
+                                              ([900] * 40, 8, 300)])
+def test_windows_over_many_key_tiles(lens, n_kv, window):
+    """Whole and cut row blocks, as the host takes them by the window and their number."""
+    st = Step(len(lens) + window, lens, [1] * len(lens), n_kv, 64, 64).device()
+    check_attention(st, 2 * n_kv, window=window)
+    st.at = dict(block_table=st.at["block_table"])        # one token a sequence: no offsets needed
+    check_attention(st, 2 * n_kv, window=window)
+
+
 def test_long_prompts_in_many_row_blocks():
     check_attention(Step(31, [700, 130], [700, 130], 2, 64, 32).device(), 8)          # self-attention, whole blocks
     check_attention(Step(32, [1500], [1200], 1, 64, 64).device(), 2, window=200)
