@@ -1039,23 +1039,26 @@ int row_block(int64_t T, int B, int n_q, int n_kv) {
 }
 
 // Whether row blocks are cut, for a second launch that joins them (about 4 us and the parts' traffic).
-//  16 rows: a whole block takes 7.5 us and 0.23 a key tile, cutting pays from 1536 positions (8 heads, one sequence of
-//  1203: 11.3 against 12.3 us; of 2011: 14.4 against 12.7, of 4096: 22 against 13), with more row blocks later: 64 of
-//  them from 2560 (16 heads, 4 of 2011: 12.2 against 12.9; of 4096: 17.8 against 15.0), 128 from 4096 (8 heads, 16 of 2011: 15.9
-//  against 19.2; of 4096: the same; of 16384: 68 against 54).  With a window the row blocks are alike, and whole ones lose
-//  only what the last 256 leave idle (8 heads of 64, window 4096, 16 sequences: 18.2 against 21.0; 32: 19.3 against 27.3, 40: 32.1
-//  against 30.9, 48: 32.4 against 34.4; window 8192: 28.6 and 25.9, 29.3 and 34.2, 52.7 and 40.4, 52.7 and 44.4).
+//  16 rows: a whole block takes 7.5 us and 0.23 a key tile; cutting pays
+//   - from 1536 positions (8 heads, one sequence of 1203: 11.3 against 12.3 us; of 2011: 14.4 against 12.7, of 4096: 22
+//     against 13);
+//   - with 64 row blocks from 2560 (16 heads, 4 of 2011: 12.2 against 12.9; of 4096: 17.8 against 15.0);
+//   - with 128 from 4096 (8 heads, 16 of 2011: 15.9 against 19.2; of 4096: the same; of 16384: 68 against 54);
+//   - beyond 256 from 2048 (8 heads, 40 of 8 to 1500: 21.9 against 23.3; to 3000: 33 against 27; 256 of 8 to 1500: 79
+//     against 75, to 4000: 164 against 127).
+//   With a window the row blocks are alike, and whole ones lose only what the last 256 leave idle (8 heads of 64, window
+//   4096, 16 sequences: 18.2 against 21.0; 32: 19.3 against 27.3, 40: 32.1 against 30.9, 48: 32.4 against 34.4; window
+//   8192: 28.6 against 25.9, 29.3 against 34.2, 52.7 against 40.4, 52.7 against 44.4).
 //  128 rows: whole blocks take 8 us and 1.75 a key tile, in rounds of 512 where the longest go first; cut ones 22 us and
 //  half as much again, evenly (64 new tokens, 8 heads, one sequence of 1024: 35.5 against 25 us; 16 of them: 37 against 51;
 //  a prompt of 2048: 70 against 91).
-// So many row blocks that there is work for each compute unit many times over are not cut.
 bool split_pays(const KvAttnArgs& g, int rows, int64_t blocks, int64_t cap) {
-  if (blocks >= 1 << 24) return false;                // (so that the units of all fit 31 bits)
+  if (blocks >= 1 << 24) return false;                // enough work for any chip, and the units of fewer fit 31 bits
   const KvArgs& a = g.kv;
   if (rows == 16) {
     const int64_t idle = -blocks & (max_groups(16) - 1);
     if (g.window && !a.offsets && blocks >= 128 && idle <= (cap > 80 ? 64 : 128)) return false;
-    return cap > (blocks >= 128 ? 65 : blocks >= 64 ? 41 : 25);
+    return cap > (blocks > 256 ? 33 : blocks >= 128 ? 65 : blocks >= 64 ? 41 : 25);
   }
   const int64_t G = g.n_q / a.n_kv;
   const double n = a.n_kv * (a.offsets ? (double)(a.T * G / rows) + 0.5 * a.B
