@@ -136,3 +136,12 @@ def test_strides_streams_repetition_and_graphs():
             torch.cuda.synchronize()
             assert torch.equal(out, cbq.kv_attention(st.cache, q, st.d_lens, **st.at).view(out.shape))
         assert torch.equal(out, want)
+
+
+def test_equal_prompts_without_offsets_or_a_table():
+    st = Step(50, [200, 150, 70], [70] * 3, 1, 64, 64, table=False, max_pages=4).device()
+    st.at = {}
+    check_attention(st, _many(210, 32))
+    st = Step(51, [2500, 1900], [66] * 2, 2, 128, 64).device()
+    st.at = dict(block_table=st.at["block_table"])
+    check_attention(st, _many(132, 32), window=900)
