@@ -1,18 +1,20 @@
 // The 4-bit key/value cache: a step's keys and values quantised into it, and read back.
 //
-// L lanes hold a head: channel 8Lj + 8l + i is value 8j + i of lane l, so that for each j the lanes' 16 bytes
-// of bf16 are contiguous, and the transform is the stages of i and j in registers and log2(L) stages
-// between lanes, DPP moves and swizzles: no LDS memory.  Four lanes for many heads, as a stage between lanes costs
-// three instructions a value and one in registers one; D/8 lanes for few, as a lane's chain is then shorter.  The transform
-// to be quantised is in fp64, as in cbq_rotate_quantize: exact, so a code does not depend on the order of its
-// sums; reading back needs fp32 only, as sums of at most 128 multiples of 1/2 up to 6 are exact there.
+// L lanes hold a head: channel 8Lj + 8l + i is value 8j + i of lane l, so that for each j the lanes' 16 bytes of bf16 are
+// contiguous, and the transform is the stages of i and j in registers and log2(L) stages between lanes, DPP moves and
+// swizzles: no LDS memory.  Four lanes for many heads, as a stage between lanes costs three instructions a value and one
+// in registers one; D/8 lanes for few, as a lane's chain is then shorter.  Reading D = 128 takes eight lanes for many heads:
+// each store then fills lines of 128 bytes (65536 tokens of 4 heads 31 us a call, with four lanes 44; writing the cache with
+// eight 28 against 26 us, 16384 tokens of 8 heads).  The transform to be quantised is in fp64, as in cbq_rotate_quantize:
+// exact, so a code does not depend on the order of its sums; reading back needs fp32 only, as sums of at most 128
+// multiples of 1/2 up to 6 are exact there.
 // A workgroup takes the heads of some consecutive tokens; their places (sequence, length, page: four dependent
 // loads) are looked up once, by a lane each, and handed over in LDS.
 //
 // What bounds it.  Writing: 16384 tokens of 8 heads take 26 us, 17 not rotated, and 25 as torch's copy of the same rows;
 // 65536 take 92, 84 and 101.  Rotated on the matrix cores (two products of exact fp32 sums, the values that lie 8 binades below
 // their head's largest apart) they took 27 and 96: what it saved in fp64 instructions went into the exchange of lanes and
-// fewer waves.  Reading: HBM (65536 tokens of 4 heads, 170 MB in 43 us, 4.0 TB/s of which four fifths are written).  A call
+// fewer waves.  Reading: HBM (65536 tokens of 4 heads, 170 MB in 31 us, 5.5 TB/s of which four fifths are written).  A call
 // for one token takes 3 us, the chain of its loads.
 #include "kv_device.hpp"
 
@@ -170,7 +172,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvArgs a, uint16_t* k, int
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           x[i] = (uint32_t)f32_to_bf16_rne(f[8 * j + 2 * i] * s) | ((uint32_t)f32_to_bf16_rne(f[8 * j + 2 * i + 1] * s) << 16);
-      __builtin_nontemporal_store(x, reinterpret_cast<u32x4*>(dst + 8 * L * j));   // 41.6 against 54.4 us a call, 65536 tokens
+      __builtin_nontemporal_store(x, reinterpret_cast<u32x4*>(dst + 8 * L * j));   // past the caches: 54 us a call with ordinary stores, 65536 tokens, 42 so
     }
   }
 }
@@ -190,9 +192,9 @@ hipError_t over_tokens(const KvArgs& a, F launch) {
   return hipSuccess;
 }
 
-// Few heads: a lane holds 8 channels of one, else 4 lanes hold it (see the top).  16 and 4 lanes, D = 128, tokens of 8 heads:
-// write 1 token 3.4 and 4.2 us, 1024 5.5 and 5.6, 2048 8.2 and 6.1, 4096 13.6 and 9.6; read 1 3.0 and 3.7, 1024 4.9 and
-// 5.2, 2048 7.0 and 5.6.
+// Few heads: a lane holds 8 channels of one, else 4 or 8 lanes hold it (see the top).  Few and many lanes, D = 128, tokens of 8
+// heads: write 1 token 3.4 and 4.3 us, 1024 5.5 and 5.5, 2048 8.1 and 6.0, 4096 13.6 and 9.7; read 1 3.0 and 3.1, 512 4.0 and
+// 4.2, 1024 4.9 and 4.6, 2048 7.0 and 5.6, 16384 25.8 and 18.8.
 bool few_heads(const KvArgs& a) { return a.T * a.n_kv <= 8192; }
 
 }  // namespace
@@ -210,7 +212,7 @@ hipError_t launch_kv_write(const KvArgs& a, const uint16_t* k, int64_t ldk, cons
 hipError_t launch_kv_read(const KvArgs& a, uint16_t* k, int64_t ldk, uint16_t* v, int64_t ldv, hipStream_t stream) {
   const float c_b = (float)(1.0 / std::sqrt((double)a.D));
   auto f = a.D == 64 ? few_heads(a) ? kv_read_kernel<64, 8> : kv_read_kernel<64, 4>
-                     : few_heads(a) ? kv_read_kernel<128, 16> : kv_read_kernel<128, 4>;
+                     : few_heads(a) ? kv_read_kernel<128, 16> : kv_read_kernel<128, 8>;
   return over_tokens(a, [&](int64_t t0, int per, uint32_t blocks) {
     f<<<dim3(blocks, k && v ? 2 : 1), 256, 0, stream>>>(a, k, ldk, v, ldv, k ? 0 : 1, t0, per, c_b);
   });

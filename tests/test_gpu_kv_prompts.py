@@ -145,3 +145,20 @@ def test_equal_prompts_without_offsets_or_a_table():
     st = Step(51, [2500, 1900], [66] * 2, 2, 128, 64).device()
     st.at = dict(block_table=st.at["block_table"])
     check_attention(st, _many(132, 32), window=900)
+
+
+def test_a_query_that_is_not_finite_stays_alone():
+    """Rows of the same wave included."""
+    for length in (200, 2600):
+        st = Step(length + 7, [length, 60], [131, 10], 2, 64, 16).device()
+        q = torch.randn((st.T, _many(141, 32), 64), device=DEV).to(torch.bfloat16)
+        want = cbq.kv_attention(st.cache, q, st.d_lens, **st.at)
+        for bad in (float("nan"), float("inf"), 3e38):
+            q2 = q.clone()
+            q2[17, 5, 3] = bad
+            got = cbq.kv_attention(st.cache, q2, st.d_lens, **st.at)
+            keep = torch.ones(got.shape[:2], dtype=torch.bool, device=DEV)
+            keep[17, 5] = False
+            assert torch.equal(got[keep], want[keep])
+            if bad != 3e38:
+                assert not bool(torch.isfinite(got[17, 5].float()).all())
