@@ -5,10 +5,10 @@
 // a_j = ks_j <q', codes_j> with q' the rotated query times scale in fp16 (11 bits, where q came in 8: its rounding
 // is far below that of q itself, and the range is seen to in convert_queries); codes are exact in fp16 and the
 // products' sums are fp32.  A value's scale vs_j joins the weight:
-//     b_j = a_j log2 e + log2 vs_j,   w_j = 2^(b_j - M),   M the running maximum of b,
+//     b_j = a_j log2 e + log2 vs_j,   w_j = 2^(b_j - M),   M 2^7 below the running maximum of b,
 //     result = sum_j w_j codes_j / sum_j (w_j / vs_j),
-// so w_j in fp16 (11 bits, and what lies 2^-24 below the largest contribution is lost) is always relative to its row's
-// largest contribution, whatever the scales' range; the sum of weights takes them before that rounding.
+// so w_j in fp16 is always relative to its row's largest contribution, whatever the scales' range: 11 bits down to 2^-21 of
+// it, fewer below, none below 2^-32.  The sum of weights takes them before that rounding, down to 2^-133 of the largest.
 //
 // The tiles.  A wave takes 64 keys at a time.  Scores are computed transposed, keys times queries
 // (16x16x32 MFMA: 16 keys, 16 query rows), so that lane (row r = lane % 16, g = lane / 16) ends
@@ -470,9 +470,10 @@ __device__ __forceinline__ void stage_value(float vs, bool some, float* lv, floa
 // Scores of 64 keys to weights: sc[n][i][j] is row lane % 16 of row tile n and key 16i + 4 (lane / 16) + j of the tile at
 // position t0.  Keys that no row attends come with ks = 0, lv = -inf and iv = 0 (stage_key, stage_value), which masks them at no
 // cost here, but for scores that are NaN; same: all rows attend the same of the others, at least one of them.  The running
-// maximum moves only when a score passes it by 2^8: weights up to 256 lose nothing in fp16, and most tiles then need neither
-// an exchange between lanes nor a rescaling.
-constexpr float kSlack = 8.0f;
+// maximum moves only when a score passes it by 2^kSlack: most tiles then need neither an exchange between lanes nor a
+// rescaling.  M lies kTop below the maximum, so that weights use fp16's range to 2^15: with M the maximum itself they were
+// lost from 2^-25 of the largest on, and 2^20 keys that far below another lost 2 % of the row's sum.
+constexpr float kSlack = 8.0f, kTop = 7.0f;
 
 template <int D, int NB>
 __device__ __forceinline__ void soft_weights(const float* ks, const float* lv, const float* iv, int t0, bool same,
@@ -525,8 +526,8 @@ __device__ __forceinline__ void soft_weights(const float* ks, const float* lv, c
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) mx = fmaxf(mx, sc[n][i][j]);
-    if (__any(mx > M[n] + kSlack)) {
-      const float rm = row_max(mx), m = rm > M[n] + kSlack ? rm : M[n];   // a row moves for its own scores alone
+    if (__any(mx > M[n] + (kTop + kSlack))) {
+      const float rm = row_max(mx), m = rm > M[n] + (kTop + kSlack) ? rm - kTop : M[n];   // a row moves for its own scores alone
       const float keep = __builtin_amdgcn_exp2f(M[n] - safe_max(m));
       l[n] *= keep;
 #pragma unroll

@@ -586,8 +586,10 @@ int cbq_kv_cache_read(const cbq_kv_cache* cache, const cbq_kv_seqs* seqs, uint16
  *           nothing gets zeros.
  *  The rotated queries times scale enter the matrix cores as fp16 (a head whose largest value is
  *  outside 2^-4 ... 2^15, relative to that), and so do the weights softmax(a)_j * scale_j,
- *  relative to the largest of their row; scores, softmax statistics and sums are fp32.  Value
- *  scales are at most 2^126; one below 2^-64 counts as 2^-64.  What a token does not attend (other pages,
+ *  relative to the largest of their row: 11 bits of those down to 2^-21 of it, fewer of smaller
+ *  ones, none below 2^-32.  Scores, softmax statistics and sums are fp32; the softmax's sum takes
+ *  the weights before they are rounded, down to 2^-133 of the largest.  Value scales are at most
+ *  2^126; one below 2^-64 counts as 2^-64.  What a token does not attend (other pages,
  *  masked positions, rows of other sequences) reaches its result in no way, whatever it holds.
  *  Deterministic: no result depends on the order of atomics.
  *  ws, ws_bytes : device workspace of cbq_kv_attention_workspace(...) bytes, 16-byte aligned;
