@@ -770,7 +770,7 @@ def kv_cache_read(cache: KVCache, lens: torch.Tensor, T: int, block_table: Optio
 
 
 def kv_attention_workspace(cache: KVCache, T: int, B: int, n_q: int) -> int:
-    """Bytes of device workspace kv_attention needs (cbq_kv_attention_workspace)."""
+    """Bytes of device workspace that kv_attention needs for T tokens, or fewer, of any batch (cbq_kv_attention_workspace)."""
     c = cbq_kv_cache(None, None, None, None, cache.n_pages, cache.n_kv, cache.page, cache.D, cache.rotate)
     return int(load_library().cbq_kv_attention_workspace(ctypes.byref(c), T, B, n_q))
 

@@ -639,7 +639,7 @@ CBQ_EXPORT size_t cbq_kv_attention_workspace(const cbq_kv_cache* cache, int64_t 
   if (!cache || T <= 0 || T > 0x7FFFFFFF || B < 1 || B > 65536 || cache->n_kv < 1 || n_q < cache->n_kv || n_q > 1024 ||
       n_q % cache->n_kv || (cache->D != 64 && cache->D != 128))
     return 0;
-  return cbq::kv_attention_workspace_bytes(T, B, n_q, cache->n_kv, cache->D);
+  return cbq::kv_attention_workspace_most(T, n_q, cache->D);
 }
 
 CBQ_EXPORT int cbq_kv_attention(const cbq_kv_cache* cache, const cbq_kv_seqs* seqs, const uint16_t* q, int64_t ldq,

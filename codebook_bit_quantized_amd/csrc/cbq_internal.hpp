@@ -161,7 +161,8 @@ struct KvAttnArgs {
   int64_t ldo;
   void* ws;
 };
-size_t kv_attention_workspace_bytes(int64_t T, int B, int n_q, int n_kv, int D);
+size_t kv_attention_workspace_bytes(int64_t T, int B, int n_q, int n_kv, int D);   // of one call
+size_t kv_attention_workspace_most(int64_t T, int n_q, int D);                     // of any with at most T tokens
 hipError_t launch_kv_attention(const KvAttnArgs& a, hipStream_t stream);
 
 // Compute units of the current device (cached per device after the first query).

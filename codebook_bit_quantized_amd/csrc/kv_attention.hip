@@ -1047,9 +1047,14 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs g, SplitArgs sp
 //   4 sequences of  2048: 128 16 and 32, 256 28 and 40, 512 50 and 48; of 8192: 96 46 and 44, 128 54 and 49, 256 95 and 65
 //   8 sequences of  4096: 64 32 and 40, 96 49 and 44, 128 57 and 48, 256 100 and 65
 //   16 sequences of 2048: 96 39 and 43, 128 52 and 48, 256 97 and 67
+bool few_rows(int64_t T, int n_q) { return T * n_q <= 4096; }
 int row_block(int64_t T, int B, int n_q, int n_kv) {
   const int64_t rows = (T + B - 1) / B * (n_q / n_kv);
-  return rows <= 128 || T * n_q <= 4096 ? 16 : 128;
+  return rows <= 128 || few_rows(T, n_q) ? 16 : 128;
+}
+
+size_t workspace_of(int rows, int D) {
+  return (size_t)max_groups(rows) * (sizeof(Desc) + 2 * rows * (sizeof(float2) + D * sizeof(float)));
 }
 
 // Whether row blocks are cut, for a second launch that joins them (about 4 us and the parts' traffic).
@@ -1103,9 +1108,10 @@ hipError_t launch_prefill(const KvAttnArgs& g, SplitArgs sp, hipStream_t stream)
 }  // namespace
 
 size_t kv_attention_workspace_bytes(int64_t T, int B, int n_q, int n_kv, int D) {
-  const int rows = row_block(T, B, n_q, n_kv);
-  return (size_t)max_groups(rows) * (sizeof(Desc) + 2 * rows * (sizeof(float2) + D * sizeof(float)));
+  return workspace_of(row_block(T, B, n_q, n_kv), D);
 }
+
+size_t kv_attention_workspace_most(int64_t T, int n_q, int D) { return workspace_of(few_rows(T, n_q) ? 16 : 128, D); }
 
 hipError_t launch_kv_attention(const KvAttnArgs& g, hipStream_t stream) {
   const KvArgs& a = g.kv;

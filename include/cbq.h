@@ -593,7 +593,9 @@ int cbq_kv_cache_read(const cbq_kv_cache* cache, const cbq_kv_seqs* seqs, uint16
  *  masked positions, rows of other sequences) reaches its result in no way, whatever it holds.
  *  Deterministic: no result depends on the order of atomics.
  *  ws, ws_bytes : device workspace of cbq_kv_attention_workspace(...) bytes, 16-byte aligned;
- *           rewritten by every call; calls that overlap in time need one each.
+ *           rewritten by every call; calls that overlap in time need one each.  The query's size
+ *           does not depend on B and does not shrink as T grows, so a buffer for the most tokens of
+ *           a step serves every smaller step (D = 128: 4.3 MB up to T * n_q = 4096, then 68 MB).
  *  out overlaps no input, nor ws.  n_q <= 1024, T * n_q < 2^31.
  */
 size_t cbq_kv_attention_workspace(const cbq_kv_cache* cache, int64_t T, int32_t B, int32_t n_q);
