@@ -1065,9 +1065,10 @@ size_t workspace_of(int rows, int D) {
 //   - with 128 from 4096 (8 heads, 16 of 2011: 15.9 against 19.2; of 4096: the same; of 16384: 68 against 54);
 //   - beyond 256 from 2048 (8 heads, 40 of 8 to 1500: 21.9 against 23.3; to 3000: 33 against 27; 256 of 8 to 1500: 79
 //     against 75, to 4000: 164 against 127).
-//   With a window the row blocks are alike, and whole ones lose only what the last 256 leave idle (8 heads of 64, window
-//   4096, 16 sequences: 18.2 against 21.0; 32: 19.3 against 27.3, 40: 32.1 against 30.9, 48: 32.4 against 34.4; window
-//   8192: 28.6 against 25.9, 29.3 against 34.2, 52.7 against 40.4, 52.7 against 44.4).
+//   With a window, and as many tokens in each sequence (no offsets, or one each), row blocks are alike but for sequences
+//   shorter than it, and whole ones lose only what the last 256 leave idle (8 heads of 64, window 4096, 16 sequences: 18.2
+//   against 21.0; 32: 19.3 against 27.3, of which any are as short as 200: 17.5 against 23.5; 40: 32.1 against 30.9, 48:
+//   32.4 against 34.4; window 8192: 28.6 against 25.9, 29.3 against 34.2, 52.7 against 40.4, 52.7 against 44.4).
 //  128 rows: whole blocks take 8 us and 1.75 a key tile, in rounds of 512 where the longest go first; cut ones 22 us and
 //  half as much again, evenly (64 new tokens, 8 heads, one sequence of 1024: 35.5 against 25 us; 16 of them: 37 against 51;
 //  a prompt of 2048: 70 against 91).
@@ -1076,7 +1077,7 @@ bool split_pays(const KvAttnArgs& g, int rows, int64_t blocks, int64_t cap) {
   const KvArgs& a = g.kv;
   if (rows == 16) {
     const int64_t idle = -blocks & (max_groups(16) - 1);
-    if (g.window && !a.offsets && blocks >= 128 && idle <= (cap > 80 ? 64 : 128)) return false;
+    if (g.window && (!a.offsets || a.T == a.B) && blocks >= 128 && idle <= (cap > 80 ? 64 : 128)) return false;
     return cap > (blocks > 256 ? 33 : blocks >= 128 ? 65 : blocks >= 64 ? 41 : 25);
   }
   const int64_t G = g.n_q / a.n_kv;
@@ -1129,8 +1130,10 @@ hipError_t launch_kv_attention(const KvAttnArgs& g, hipStream_t stream) {
   sp.g_mul = (uint32_t)(((uint64_t(1) << sp.g_shift) + G - 1) / G);
   const int64_t own = (int64_t)a.per_seq * G;
   sp.join_rows = a.offsets || own > rows ? rows : (int)own;
-  // row blocks at most
-  const int64_t blocks = (a.offsets ? (a.T * G + rows - 1) / rows + a.B : a.B * ((own + rows - 1) / rows)) * a.n_kv;
+  // Row blocks at most.  With offsets: a sequence of n tokens has ceil(n G / rows) <= n ceil(G / rows), and its last block
+  // lacks rows - 1 rows at most; with one token a sequence that is the number without offsets, so the call is the same.
+  const int64_t ragged = std::min(a.T * ((G + rows - 1) / rows), (a.T * G + (rows - 1) * std::min<int64_t>(a.T, a.B)) / rows);
+  const int64_t blocks = (a.offsets ? ragged : a.B * ((own + rows - 1) / rows)) * a.n_kv;
   int64_t cap = ((int64_t)a.max_pages << a.logp) / kTile + 1;               // key tiles of one at most
   if (g.window) cap = std::min(cap, ((int64_t)g.window + rows / G + 1) / kTile + 2);
   sp.split = split_pays(g, rows, blocks, cap);
