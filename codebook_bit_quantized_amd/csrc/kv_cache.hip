@@ -40,9 +40,11 @@ __device__ __forceinline__ void find_places(const KvArgs& a, int64_t t0, int tok
   }
 }
 
-// v / s as IEEE division rounds it, from y = RN(1 / s): the quotient's remainder is exact, and one step of it
-// corrects the rounding (Markstein).  y: one such step from the hardware's reciprocal, correctly rounded for every
-// fp32 mantissa.  For s and v / s away from the ends of the exponent range.
+// v / s from y = RN(1 / s): the quotient's remainder is exact, and one step of it corrects the rounding (Markstein).  So it
+// is v / s rounded to nearest for every mantissa of s and every v whose quotient lies next to a border of the codes, which is what
+// they depend on.  y: one such step from the hardware's reciprocal, which is within one step of 1 / s.  That gives RN(1 / s) from
+// any such start, but for a mantissa of ones: there from RN(1 / s) alone, which is what the hardware returns for it.  (All of it
+// checked for every mantissa.)  For s and v / s away from the ends of the exponent range.
 __device__ __forceinline__ float div_by(float v, float s, float y) {
   const float q = v * y;
   return __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-q, s, v), y, q), v);   // -0 stays -0
