@@ -746,24 +746,29 @@ def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, lens: torch
 
 def kv_cache_read(cache: KVCache, lens: torch.Tensor, T: int, block_table: Optional[torch.Tensor] = None,
                   offsets: Optional[torch.Tensor] = None, k: Optional[torch.Tensor] = None,
-                  v: Optional[torch.Tensor] = None, stream=None):
+                  v: Optional[torch.Tensor] = None, stream=None, want_k: bool = True, want_v: bool = True):
     """The cached keys and values of a step's T tokens as bf16 [T][n_kv][D], rotated back: what
-    kv_cache_write of the same arguments stored (cbq_kv_cache_read).  Returns (k, v); rows that
-    belong to no sequence are left as they were (unwritten in tensors made here)."""
+    kv_cache_write of the same arguments stored (cbq_kv_cache_read).  Returns (k, v), None for
+    one that is not wanted; rows that belong to no sequence are left as they were (unwritten in
+    tensors made here)."""
     lib = load_library()
     _require_gpu(cache.k_codes)
     dev = cache.k_codes.device
     c = cache._c_checked(dev)
+    if not (want_k or want_v):
+        raise ValueError("want_k or want_v must be true")
+    if k is not None and not want_k or v is not None and not want_v:
+        raise ValueError("k and v must be None where they are not wanted")
     ldk = 0 if k is None else _kv_heads("k", k, dev, T, c.n_kv, c.D)
     ldv = 0 if v is None else _kv_heads("v", v, dev, T, c.n_kv, c.D)
     s = _kv_seqs(cache, dev, lens, block_table, offsets)
 
     def call(st):
         shape = (T, c.n_kv, c.D)
-        ko = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
-        vo = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
-        _check(lib.cbq_kv_cache_read(ctypes.byref(c), ctypes.byref(s), ko.data_ptr(), ldk or c.n_kv * c.D, vo.data_ptr(),
-                                     ldv or c.n_kv * c.D, T, st))
+        ko = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None and want_k else k
+        vo = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None and want_v else v
+        _check(lib.cbq_kv_cache_read(ctypes.byref(c), ctypes.byref(s), ko.data_ptr() if want_k else None,
+                                     ldk or c.n_kv * c.D, vo.data_ptr() if want_v else None, ldv or c.n_kv * c.D, T, st))
         return ko, vo
 
     return _on_stream(dev, stream, call)
