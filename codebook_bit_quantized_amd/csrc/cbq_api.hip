@@ -652,7 +652,7 @@ CBQ_EXPORT int cbq_kv_attention(const cbq_kv_cache* cache, const cbq_kv_seqs* se
     return fail(CBQ_EINVAL, "n_q must be a positive multiple of n_kv = %d (got %d)", cache->n_kv, n_q);
   if (n_q > 1024) return fail(CBQ_EUNSUPPORTED, "n_q must be <= 1024 (got %d)", n_q);
   if (T * n_q > 0x7FFFFFFF) return fail(CBQ_EUNSUPPORTED, "T * n_q must be < 2^31");
-  if (!std::isfinite(scale)) return fail(CBQ_EINVAL, "scale must be finite");
+  if (!(std::fabs(scale) <= 0x1p127f)) return fail(CBQ_EINVAL, "scale must be finite and at most 2^127");   // times log2(e) in fp32
   if (causal != 0 && causal != 1) return fail(CBQ_EINVAL, "causal must be 0 or 1");
   if (window < 0) return fail(CBQ_EINVAL, "window must be >= 0 (got %d)", window);
   if (window > 0 && !causal) return fail(CBQ_EINVAL, "a window needs causal = 1");
