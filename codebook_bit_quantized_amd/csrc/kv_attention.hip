@@ -526,8 +526,10 @@ __device__ __forceinline__ void soft_weights(const float* ks, const float* lv, c
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) mx = fmaxf(mx, sc[n][i][j]);
-    if (__any(mx > M[n] + (kTop + kSlack))) {
-      const float rm = row_max(mx), m = rm > M[n] + (kTop + kSlack) ? rm - kTop : M[n];   // a row moves for its own scores alone
+    // by differences, as the weights' arguments: M + 15 is rounded by more where scores pass 2^24, and a weight past 2^16 is
+    // infinite in fp16
+    if (__any(mx - M[n] > kTop + kSlack)) {
+      const float rm = row_max(mx), m = rm - M[n] > kTop + kSlack ? rm - kTop : M[n];   // a row moves for its own scores alone
       const float keep = __builtin_amdgcn_exp2f(M[n] - safe_max(m));
       l[n] *= keep;
 #pragma unroll

@@ -1,5 +1,5 @@
 """Weights far below their row's largest: one key takes nearly all of the softmax, and many others far below it add up in channels
-where that key's value is zero; keys whose values are zeros beside large ones."""
+where that key's value is zero; keys whose values are zeros beside large ones.  Scores of any size."""
 import math
 
 import numpy as np
@@ -76,3 +76,33 @@ def test_a_zero_value_beside_large_ones(new, n_q, power):
     # the exponential and the sums in fp32, 2^-18 at most; fp16's and bf16's half steps
     off = float((np.abs(got - want[:, None, None]) / want[:, None, None]).max())
     assert off <= 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -18
+
+
+@pytest.mark.parametrize("length,new,n_q", [(1300, 1, 2), (700, 130, 32), (4000, 1, 2)])
+@pytest.mark.parametrize("power", [10, 20, 23, 24, 25, 26, 28, 40])
+def test_scores_of_any_size(length, new, n_q, power):
+    """Scores near 2^power binades: key 0's, and the largest of the later tiles', which lies two steps of fp32 (of 8 binades, if these
+    are smaller) above.  All are exact, so weights are powers of two: finite, and right to a step of bf16 and of fp16."""
+    step = max(8.0, 2 * 2.0 ** (power - 23))
+    st = Step(power + new, [length], [new], 1, 64, 64, rotate=0, garbage=False)
+    for c in st.codes:
+        c[:] = 0
+    for s in st.scales:
+        s[:] = 1
+    j = np.arange(0, length - new, 64)                       # a key in each tile has a score
+    st.codes[0][st.table[0, j // 64], 0, 0, 0] = 0x02         # 1 in channel 0
+    st.scales[0][st.table[0, j // 64], 0, 0] = 2.0 ** power + step
+    st.scales[0][st.table[0, 0], 0, 0] = 2.0 ** power
+    st.codes[1][st.table[0, j // 64], 0, 0, :] = 0x77
+    st.codes[1][st.table[0, 0], 0, 0, :] = 0x22              # 1, and 6 in the others
+    st.device()
+    scale = float(np.float32(math.log(2) / 16))
+    while float(np.float32(np.float32(scale) * np.float32(1.44269504088896341))) != 2.0 ** -4:
+        scale = float(np.nextafter(np.float32(scale), np.float32(1 if scale * 1.4426950408889634 < 2.0 ** -4 else 0)))
+    q = torch.zeros((new, n_q, 64), dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 16
+    got = cbq.kv_attention(st.cache, q, st.d_lens, scale=scale, **st.at).double().cpu().numpy()
+    n, w = len(j) - 1, 2.0 ** -step
+    want = (6 * n + w) / (n + w)
+    bad = int((~(np.abs(got / want - 1) <= 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -18)).sum())
+    assert bad == 0, f"{bad} of {got.size} values, {int((~np.isfinite(got)).sum())} of them not finite"
