@@ -480,11 +480,30 @@ __device__ __forceinline__ void soft_weights(const float* ks, const float* lv, c
                                              bool unit, const float* rs, const int* lo, const int* hi, f32x4 (*sc)[4], float* M, float* l,
                                              f32x4 (*o)[D / 16], f16x8 (*w)[2]) {
   const int lane = threadIdx.x & 63, key = 4 * (lane >> 4);
+  // A query that is not finite has an rs that is not 1, and scores that are NaN: they would survive lv = -inf, and a row may
+  // attend none of the tile's keys that are held.  Called where its code costs the other calls least: with one row tile
+  // before the masks (windows of 4096 19.8 us behind the scaling or at the masks, 19.1 in it), with two at the masks of rows
+  // that attend different keys (four prompts 286 us; in the scaling 290, for every key's mask 293).  by: what the scores are
+  // multiplied by besides, or null.
+  auto clear_unheld = [&](const float* by) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool held = lv[16 * i + key + j] != -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) sc[n][i][j] = held ? sc[n][i][j] * (by ? by[n] : 1.0f) : by ? 0.0f : -INFINITY;
+      }
+  };
   if (!unit) {
+    if constexpr (NB == 1) {
+      clear_unheld(rs);
+    } else {
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
+      for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sc[n][i] *= rs[n];
+        for (int i = 0; i < 4; ++i) sc[n][i] *= rs[n];
+    }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -505,19 +524,7 @@ __device__ __forceinline__ void soft_weights(const float* ks, const float* lv, c
         for (int j = 0; j < 4; ++j) sc[n][i][j] = (uint32_t)(at + 16 * i + j) < len ? sc[n][i][j] : -INFINITY;
       }
     }
-    // A row may attend none of the tile's keys that are held, though positions among the others: scores that are NaN, as a
-    // query that is not finite gives (its rs is then not 1), would survive lv = -inf there.  Selected here and not above,
-    // where it costs every call (four prompts 293 against 286 us).
-    if (!unit) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bool held = lv[16 * i + key + j] != -INFINITY;
-#pragma unroll
-          for (int n = 0; n < NB; ++n) sc[n][i][j] = held ? sc[n][i][j] : -INFINITY;
-        }
-    }
+    if (NB > 1 && !unit) clear_unheld(nullptr);
   }
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
