@@ -1050,7 +1050,9 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs g, SplitArgs sp
 
 // Query rows of a row block, by the rows a sequence has on average and all rows together.  16 rows share keys among eight
 // waves and start sooner, 128 rows read them once for all.  Which is faster goes by rows times keys, about 25 million
-// of them; the keys' number stays on the device.  Both forms, 8 key/value heads, rows a sequence:
+// of them; the keys' number stays on the device, so long sequences just within the limits take the slower form (8 of 4096 with
+// 128 rows, one of 16384 with 512), and so do sequences whose rows are far from the average (512 tokens of 16384 among 63 single
+// tokens of 1000 to 4000: 306 us in one call, 160 and 41 in two).  Both forms, 8 key/value heads, rows a sequence:
 //   1 sequence  of  1000: 512 rows 12 and 28 us; of 4096: 256 24 and 31, 512 35 and 40; of 16384: 256 47 and 54, 512 78 and 66
 //   2 sequences of  8192: 256 43 and 48, 384 68 and 56
 //   4 sequences of  2048: 128 16 and 32, 256 28 and 40, 512 50 and 48; of 8192: 96 46 and 44, 128 54 and 49, 256 95 and 65
@@ -1073,7 +1075,11 @@ size_t workspace_of(int rows, int D) {
 //   - with 64 row blocks from 2560 (16 heads, 4 of 2011: 12.2 against 12.9; of 4096: 17.8 against 15.0);
 //   - with 128 from 4096 (8 heads, 16 of 2011: 15.9 against 19.2; of 4096: the same; of 16384: 68 against 54);
 //   - beyond 256 from 2048 (8 heads, 40 of 8 to 1500: 21.9 against 23.3; to 3000: 33 against 27; 256 of 8 to 1500: 79
-//     against 75, to 4000: 164 against 127).
+//     against 75, to 4000: 164 against 127).  Sequences of equal length lose by that, less than ragged ones gain (8 heads, 64
+//     of 2500: 35.8 against 38.3, of 3100: 42.8 against 44.5; 16 heads of 64, 64 of 2500: 43.0 against 46.1).
+//   All of it by the table's width, which is what the host knows of the lengths: under a table for far longer ones short
+//   sequences are cut too (16 of 1203 under one for 131072 positions 14.6 instead of 11.7, with 5 tokens each 21.8 instead of
+//   12.6; 16 of 300 with 64 tokens each 35 instead of 19).
 //   With a window, and as many tokens in each sequence (no offsets, or one each), row blocks are alike but for sequences
 //   shorter than it, and whole ones lose only what the last 256 leave idle (8 heads of 64, window 4096, 16 sequences: 18.2
 //   against 21.0; 32: 19.3 against 27.3, of which any are as short as 200: 17.5 against 23.5; 40: 32.1 against 30.9, 48:

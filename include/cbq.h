@@ -597,6 +597,10 @@ int cbq_kv_cache_read(const cbq_kv_cache* cache, const cbq_kv_seqs* seqs, uint16
  *           rewritten by every call; calls that overlap in time need one each.  The query's size
  *           does not depend on B and does not shrink as T grows, so a buffer for the most tokens of
  *           a step serves every smaller step (D = 128: 4.3 MB up to T * n_q = 4096, then 68 MB).
+ *  Speed: the host chooses the kernels by T, B and max_pages alone, as lengths and offsets are on
+ *           the device.  A block table (or a view of its first columns) no wider than the longest
+ *           sequence needs is faster for short sequences, and a long chunk among many single
+ *           tokens is faster in a call of its own.
  *  out overlaps no input, nor ws.  n_q <= 1024, T * n_q < 2^31.
  */
 size_t cbq_kv_attention_workspace(const cbq_kv_cache* cache, int64_t T, int32_t B, int32_t n_q);
