@@ -23,7 +23,7 @@
 // dependent loads), some 3 us in which the last workgroups end, and 4 us for the launch that joins.  64 ragged
 // sequences of up to 32768 tokens: 48 us, 187 MB; one of 131072: 38 us, 143 MB.  Beyond that the vector instructions
 // count: 64 keys by 32 rows take 387 of them (weights, conversions of codes) next to 64 matrix instructions, which are busy
-// 29 to 41 % of the time.  The last 512 tokens of 16384: 159 us, 850 TFLOP/s; four prompts: 289 us, 820 TFLOP/s.
+// 29 to 41 % of the time.  The last 512 tokens of 16384: 159 us, 850 TFLOP/s; four prompts: 287 us, 824 TFLOP/s.
 #include <algorithm>
 
 #include "kv_device.hpp"
