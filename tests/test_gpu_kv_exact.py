@@ -79,3 +79,9 @@ def test_pages_given_back():
         st = ExactStep(8, lens, new, n_q, 1, 64, 16, 0)
         st.table[0, 3:7], st.table[0, 30] = -1, st.n_pages + 9
         _check(st)
+
+
+def test_windows_cut_among_many_sequences():
+    """Two tokens a sequence, so that the window's rule for whole row blocks does not apply."""
+    assert _check(ExactStep(4, [4400, 100] * 8, [2] * 16, 16, 8, 64, 64, 0), window=4200)
+    assert _check(ExactStep(5, [5000, 4300, 20] * 6, [3, 1, 0] * 6, 16, 8, 64, 64), window=4200)
