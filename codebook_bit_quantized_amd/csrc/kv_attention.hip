@@ -1082,7 +1082,7 @@ size_t workspace_of(int rows, int D) {
 //   12.6; 16 of 300 with 64 tokens each 35 instead of 19).
 //   With a window, and as many tokens in each sequence (no offsets, or one each), row blocks are alike but for sequences
 //   shorter than it, and whole ones lose only what the last 256 leave idle (8 heads of 64, window 4096, 16 sequences: 18.2
-//   against 21.0; 32: 19.3 against 27.3, of which any are as short as 200: 17.5 against 23.5; 40: 32.1 against 30.9, 48:
+//   against 21.0; 32: 19.3 against 27.3, some of them as short as 200: 17.5 against 23.5; 40: 32.1 against 30.9, 48:
 //   32.4 against 34.4; window 8192: 28.6 against 25.9, 29.3 against 34.2, 52.7 against 40.4, 52.7 against 44.4).
 //  128 rows: whole blocks take 8 us and 1.75 a key tile, in rounds of 512 where the longest go first; cut ones 22 us and
 //  half as much again, evenly (64 new tokens, 8 heads, one sequence of 1024: 35.5 against 25 us; 16 of them: 37 against 51;

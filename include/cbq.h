@@ -580,7 +580,7 @@ int cbq_kv_cache_read(const cbq_kv_cache* cache, const cbq_kv_seqs* seqs, uint16
  *  q      : bf16 [T][ldq]: token t's n_q heads of D channels (ldq >= n_q*D, % 8, 16-byte aligned).
  *  n_q    : query heads, a multiple of n_kv; query head h reads key/value head h / (n_q / n_kv).
  *  scale  : |scale| <= 2^127; a_j = scale * <q, k_j> over the dequantised keys.  A row whose
- *           rotated query or scores pass fp32's range is not finite.
+ *           rotated query or scores pass fp32's range may not be finite.
  *  causal : 1: a token attends positions up to its own; 0: all lens[b].
  *  window : 0, or (causal only) how many positions a token attends, its own the last of them.
  *  out    : bf16 [T][ldo] (as q): sum_j softmax(a)_j v_j, rounded once.  A token that attends
